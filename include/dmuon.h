@@ -62,6 +62,9 @@ typedef enum dmuon_status {
 /* Gradient dtypes. */
 enum { DMUON_DTYPE_F32 = 0, DMUON_DTYPE_BF16 = 1 };
 
+/* Token id and target dtypes. */
+enum { DMUON_INDEX_I32 = 0, DMUON_INDEX_I64 = 1 };
+
 /* dmuon_muon_step flags. */
 enum {
   DMUON_FLAG_NESTEROV = 1u, /* u = g + mu*buf (else u = buf)                      */
@@ -365,10 +368,119 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
                               int32_t n_groups, void* stream);
 
 /*
+ * The two ends of a language model: its vocabulary-sized parameters (embedding
+ * table, output head) take the AdamW routes ("Pure DMuon 路由"), and these
+ * entries compute the loss and the gradients that dmuon_adamw_step reads for
+ * them.  The pages have no counterpart: there the gradients come from the
+ * training framework.
+ *
+ * dmuon_cross_entropy -- softmax cross entropy of hidden states against a head.
+ *
+ *   z_iv   = logit_scale * (x_i . w_v)              v in [0, vocab)
+ *   lse_i  = log sum_v exp(z_iv)
+ *   loss_i = lse_i - z_{i, t_i}                     (0 where t_i < 0)
+ *   L      = sum_i a_i loss_i / (MEAN: sum_i a_i, else 1),  a_i = weights[i]
+ *            (1 if NULL) for t_i >= 0, else 0; a zero sum of weights gives 0
+ *   dx_i   = grad_scale * dL/dx_i,   dw_v = grad_scale * dL/dw_v
+ *
+ * The logits are never stored: their maxima, sums and, for the gradients, one
+ * 16-bit fixed-point log per entry leave the product's epilogue, for as many
+ * tokens at a time as tuning key 14 allows.
+ * Rounding: products of bf16 operands with fp32 sums; softmax statistics, the
+ * loss and L in fp32 (L's sum in fp64); d logits are rounded to bf16 once,
+ * before the gradient products; dx and dw once on output (fp32 outputs thus
+ * carry the d logits' bf16 rounding too).  dW of several passes, and
+ * DMUON_CE_ADD_DW, add in fp32 before the one rounding.
+ *
+ *   x        bf16, n_tokens x dim, rows ld_x elements apart
+ *   w        bf16, vocab x dim, rows ld_w elements apart
+ *   targets  n_tokens ids of target_dtype; below zero: not counted (loss and
+ *            lse 0, no gradient, whatever x holds there); at or above vocab:
+ *            not counted either, and dmuon_sync reports DMUON_ERR_INVALID_ARG
+ *   weights  fp32 per token, or NULL
+ *   loss, lse  fp32 per token (written); total  one fp32: L (written)
+ *   dx, dw   bf16 or fp32, row pitches ld_dx and ld_dw (written; dw is added to
+ *            with DMUON_CE_ADD_DW)
+ * Each of loss, lse, total, dx and dw may be NULL (not all of them).  Rows on
+ * 16-byte boundaries (pointer and pitch) are read and written in place by TMA;
+ * other x and w are copied first, and other dx and dw go through a partial
+ * buffer, as does a bf16 dw that is added to.  n_tokens = 0: total is 0, and
+ * dw is zeroed unless it is added to.
+ * Errors: DMUON_ERR_INVALID_ARG (null or overlapping memory, no output, bad
+ * scale or flags), DMUON_ERR_SHAPE (n_tokens >= 2^31, vocab outside
+ * [1, 2^24], dim outside [1, 2^20], a pitch below dim), DMUON_ERR_DTYPE,
+ * DMUON_ERR_NOMEM, DMUON_ERR_CUDA, DMUON_ERR_UNSUPPORTED.
+ */
+enum {
+  DMUON_CE_MEAN = 1u,   /* divide by the counted weights' sum */
+  DMUON_CE_ADD_DW = 2u  /* dw += ... instead of dw = ...      */
+};
+
+typedef struct dmuon_ce {
+  int64_t n_tokens, vocab, dim;
+  const uint16_t* x;
+  const uint16_t* w;
+  int64_t ld_x, ld_w;
+  const void* targets;
+  const float* weights;
+  float* loss;
+  float* lse;
+  float* total;
+  void* dx;
+  void* dw;
+  int64_t ld_dx, ld_dw;
+  int32_t x_dtype, w_dtype;   /* DMUON_DTYPE_BF16 */
+  int32_t target_dtype;       /* DMUON_INDEX_*    */
+  int32_t dx_dtype, dw_dtype; /* DMUON_DTYPE_*    */
+  float logit_scale, grad_scale;
+  uint32_t flags;
+} dmuon_ce;
+
+DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream);
+
+/*
+ * dmuon_embed_forward  -- rows[i] = scale * table[ids[i]]
+ * dmuon_embed_backward -- table[v] = scale * sum of rows[i] over ids[i] = v,
+ *                         for every v of the vocabulary (rows that no id names
+ *                         become zeros); with DMUON_EMBED_ADD the sums are
+ *                         added to what table holds and other rows stay.
+ * Backward's `table` is the gradient (written) and its `rows` the gradient of
+ * the lookup's output (read).  ids below zero are padding: zero rows forward,
+ * no gradient backward; ids at or above vocab likewise, and dmuon_sync reports
+ * DMUON_ERR_INVALID_ARG.  Rows of equal ids are added in the order of their
+ * positions, in fp32, and the result is rounded once.  Both arrays are bf16 or
+ * fp32 each, at any row pitch >= dim; rows on 16-byte boundaries with
+ * dim % 8 = 0 move as 16-byte vectors.  Errors as dmuon_cross_entropy.
+ *
+ * The vocabulary operators share scratch of the context, apart from the Muon
+ * step's: a call on another stream than the last one's waits for that one.
+ * A call whose scratch has its size already (any earlier call of the sizes) can
+ * be captured into a CUDA graph; captured calls and their replays must not
+ * overlap other calls of these entries on the context.
+ */
+enum { DMUON_EMBED_ADD = 1u };
+
+typedef struct dmuon_embed {
+  int64_t n_tokens, vocab, dim;
+  const void* ids;
+  void* table;
+  void* rows;
+  int64_t ld_table, ld_rows;
+  int32_t id_dtype;               /* DMUON_INDEX_* */
+  int32_t table_dtype, row_dtype; /* DMUON_DTYPE_* */
+  float scale;
+  uint32_t flags;                 /* backward: DMUON_EMBED_ADD or 0; forward: 0 */
+} dmuon_embed;
+
+DMUON_API int dmuon_embed_forward(dmuon_context* ctx, const dmuon_embed* args, void* stream);
+DMUON_API int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stream);
+
+/*
  * dmuon_sync -- wait for the stream and report device-side errors.
  * Synchronises `stream`, then reads and clears the context's device error
  * word.  Returns DMUON_ERR_TIMEOUT if a bounded wait ran out since the last
- * call, DMUON_ERR_CUDA if the stream reported an error, else DMUON_OK.
+ * call, DMUON_ERR_INVALID_ARG if a token id or target past the vocabulary was
+ * met (whichever came first), DMUON_ERR_CUDA if the stream reported an error, else DMUON_OK.
  */
 DMUON_API int dmuon_sync(dmuon_context* ctx, void* stream);
 
@@ -420,6 +532,10 @@ DMUON_API int dmuon_selftest_wait_timeout(dmuon_context* ctx, int32_t timeout_us
  *          tiles average at least `value` 64-deep k-blocks runs 256 x 512
  *          tiles wherever two adjacent column blocks exist (0..1e6, default
  *          128; 0 = never).  Results do not depend on the setting.
+ *   key 14: dmuon_cross_entropy with gradients: the block of 16-bit logs that
+ *          is held at a time is at most `value` MiB (1..65536, default 2048;
+ *          at least 256 tokens' worth).  A call whose tokens do not fit runs
+ *          in passes; their number only moves the rounding of dW's fp32 sums.
  * Results never depend on keys 3, 4, 6, 8, 9, 10, 11 and 12 (bit for bit);
  * key 2 changes the kernel and key 7 the rounding points, both within the
  * documented tolerances.

@@ -5,6 +5,8 @@ of ``include/dmuon.h``); this package is its thin Python binding:
 
 * ``capi``       ctypes wrappers named after the C entry points;
 * ``optim``      ``OwnerStep``, a context plus cached descriptor arrays;
+* ``vocab``      ``VocabOps``: embedding lookup and cross entropy over the
+  output head, each with its gradient (the tensors of the AdamW routes);
 * ``workloads``  seeded synthetic inputs and work accounting;
 * ``build``      the nvcc build of the library.
 
@@ -13,8 +15,11 @@ raises if it has not been built.
 """
 
 from .capi import (  # noqa: F401
+    DMUON_CE_ADD_DW,
+    DMUON_CE_MEAN,
     DMUON_DTYPE_BF16,
     DMUON_DTYPE_F32,
+    DMUON_EMBED_ADD,
     DMUON_FLAG_FP32_NS,
     DMUON_FLAG_NESTEROV,
     DmuonError,
@@ -22,6 +27,9 @@ from .capi import (  # noqa: F401
     dmuon_context_create,
     dmuon_context_destroy,
     dmuon_context_set_tuning,
+    dmuon_cross_entropy,
+    dmuon_embed_backward,
+    dmuon_embed_forward,
     dmuon_kernel_launches,
     dmuon_lpt_assign,
     dmuon_lpt_assign_layered,
@@ -38,3 +46,4 @@ from .capi import (  # noqa: F401
     load_library,
 )
 from .optim import OwnerStep, adamw_shard_ranges, adamw_shard_views, owner_partition  # noqa: F401
+from .vocab import VocabOps  # noqa: F401

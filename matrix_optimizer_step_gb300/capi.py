@@ -33,12 +33,20 @@ DMUON_DTYPE_BF16 = 1
 DMUON_FLAG_NESTEROV = 1
 DMUON_FLAG_FP32_NS = 2
 
+DMUON_INDEX_I32 = 0
+DMUON_INDEX_I64 = 1
+
+DMUON_CE_MEAN = 1
+DMUON_CE_ADD_DW = 2
+DMUON_EMBED_ADD = 1
+
 EXPORTED = (
     "dmuon_status_string", "dmuon_last_error", "dmuon_lpt_assign", "dmuon_context_create",
     "dmuon_context_destroy", "dmuon_muon_step", "dmuon_adamw_step", "dmuon_sync",
     "dmuon_selftest_wait_timeout", "dmuon_set_tuning", "dmuon_kernel_launches", "dmuon_profile",
     "dmuon_profile_read", "dmuon_muon_step_noalloc", "dmuon_lpt_assign_layered", "dmuon_step_host",
     "dmuon_muon_step_noalloc_sync", "dmuon_profile_host_timeline", "dmuon_context_set_tuning",
+    "dmuon_cross_entropy", "dmuon_embed_forward", "dmuon_embed_backward",
 )
 
 KERNEL_KINDS = ("momentum", "norm", "ns_gram", "ns_poly", "ns_combine", "update", "adamw")
@@ -94,6 +102,32 @@ class DmuonAdamwHparams(ctypes.Structure):
     ]
 
 
+class DmuonCe(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("w", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+        ("targets", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("total", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("ld_dw", ctypes.c_int64),
+        ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("target_dtype", ctypes.c_int32),
+        ("dx_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+        ("logit_scale", ctypes.c_float), ("grad_scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class DmuonEmbed(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+        ("ids", ctypes.c_void_p), ("table", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64), ("ld_rows", ctypes.c_int64),
+        ("id_dtype", ctypes.c_int32), ("table_dtype", ctypes.c_int32), ("row_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
 _lib = None
 
 
@@ -132,6 +166,9 @@ def load_library(path=LIB_PATH):
         "dmuon_muon_step_noalloc_sync": (ctypes.c_int, [vp]),
         "dmuon_profile_host_timeline": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_double), i32,
                                                        ctypes.POINTER(i32)]),
+        "dmuon_cross_entropy": (ctypes.c_int, [vp, ctypes.POINTER(DmuonCe), vp]),
+        "dmuon_embed_forward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
+        "dmuon_embed_backward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
         "dmuon_step_host": (ctypes.c_int, [vp, ctypes.POINTER(DmuonMatrix), ctypes.POINTER(DmuonHostIO), i32,
                                            ctypes.POINTER(DmuonMuonHparams), ctypes.POINTER(DmuonVector),
                                            ctypes.POINTER(DmuonHostIO), i32, ctypes.POINTER(DmuonAdamwHparams),
@@ -368,3 +405,18 @@ def dmuon_step_host(ctx, mats, mat_io, muon, vecs=None, vec_io=None, adamw=None,
     _check(lib.dmuon_step_host(ctx, mats, mat_io, n_m, ctypes.byref(muon) if muon is not None else None,
                                vecs, vec_io, n_v, ctypes.byref(adamw) if adamw is not None else None,
                                int(n_groups), _stream_handle(stream)))
+
+
+def dmuon_cross_entropy(ctx, args, stream=None):
+    """``args``: one DmuonCe."""
+    _check(load_library().dmuon_cross_entropy(ctx, ctypes.byref(args), _stream_handle(stream)))
+
+
+def dmuon_embed_forward(ctx, args, stream=None):
+    """``args``: one DmuonEmbed."""
+    _check(load_library().dmuon_embed_forward(ctx, ctypes.byref(args), _stream_handle(stream)))
+
+
+def dmuon_embed_backward(ctx, args, stream=None):
+    """``args``: one DmuonEmbed (``table``: the gradient, ``rows``: the lookup output's)."""
+    _check(load_library().dmuon_embed_backward(ctx, ctypes.byref(args), _stream_handle(stream)))

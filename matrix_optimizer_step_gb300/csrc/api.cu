@@ -49,6 +49,11 @@ int apply_tuning(Tuning& t, int32_t key, int32_t value) {
         return set_error(DMUON_ERR_INVALID_ARG, "set_tuning: key 12 value outside [0, 1e6]");
       t.wide_min_kb = value;
       return DMUON_OK;
+    case 14:
+      if (value < 1 || value > 65536)
+        return set_error(DMUON_ERR_INVALID_ARG, "set_tuning: key 14 value outside [1, 65536]");
+      t.ce_block_bytes = int64_t(value) << 20;
+      return DMUON_OK;
     default:
       return set_error(DMUON_ERR_INVALID_ARG, "set_tuning: unknown key");
   }
@@ -408,6 +413,10 @@ int dmuon_context_destroy(dmuon_context* ctx) {
     if (ctx->d2h) cudaStreamDestroy(ctx->d2h);
     ctx->h2d = ctx->d2h = nullptr;
     ctx->prof.release();
+    if (ctx->vocab_done) cudaEventDestroy(ctx->vocab_done);
+    ctx->vocab_done = nullptr;
+    ctx->vocab_ws.release();
+    ctx->vocab_ticket.release();
     ctx->ws.release();
     ctx->err.release();
   }
@@ -466,6 +475,8 @@ int dmuon_sync(dmuon_context* ctx, void* stream) {
   DM_CUDA(cudaMemcpy(&word, ctx->err.p, sizeof(int), cudaMemcpyDeviceToHost));
   if (word != kErrNone) {
     DM_CUDA(cudaMemset(ctx->err.p, 0, sizeof(int)));
+    if (word == kErrBadIndex)
+      return set_error(DMUON_ERR_INVALID_ARG, "a token id or target past the vocabulary (the entry was not counted)");
     char buf[96];
     snprintf(buf, sizeof buf, "a bounded device-side wait ran out (site %d)", word);
     return set_error(DMUON_ERR_TIMEOUT, buf);

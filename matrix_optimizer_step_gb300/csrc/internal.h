@@ -16,6 +16,7 @@ enum : int {
   kErrTimeoutEpilogue = 3,
   kErrTimeoutDrain = 4,
   kErrTimeoutSelftest = 5,
+  kErrBadIndex = 6,  // a token id or target past the vocabulary (the entry was skipped)
 };
 
 // One 2-D slice (m x n, row-major, contiguous) of a Muon tensor, as the two

@@ -1,0 +1,487 @@
+// The three products of the cross entropy over a head matrix, on CTA pairs
+// (tcgen05, cta_group::2):
+//   logits   Z  = X W^T     (tokens x vocabulary, K = width)
+//   dX       dX = dZ W      (tokens x width,      K = vocabulary)
+//   dW       dW = dZ^T X    (vocabulary x width,  K = tokens)
+// bf16 operands, fp32 accumulation in TMEM.  Each output tile is 256 x 256
+// and belongs to a cluster of two CTAs: CTA r loads rows [128r, 128r + 128)
+// of the tile's A operand and of its B operand into a 4-stage ring, one
+// thread of CTA 0 issues M = 256, N = 256, K = 16 MMAs that read both CTAs'
+// shared memory, and each CTA's TMEM receives 128 rows of the accumulator.
+// The accumulator is double-buffered (2 x 256 of the 512 TMEM columns), so
+// the epilogue of a tile runs under the main loop of the next.
+//
+// The logits' epilogue never stores a logit.  Each thread owns one row and
+// 128 columns: it keeps the 128 accumulators in registers (and hands the TMEM
+// back at once), takes their maximum m and the sum of 2^(z - m), with
+// z = logit * log2(e), and writes that pair.  For the gradient it also leaves
+// round((m - z) * 1024) as 16 bits: the exponential's argument in fixed point
+// is within 2^-11 octaves, i.e. a relative error of at most 3.4e-4 in the
+// probability, a quarter of the rounding to bf16 that d logits get anyway,
+// where the logit itself rounded to 16 bits would be off by its size times
+// 2^-9.  The logs turn into d logits once the row's sum is known
+// (k_vocab_ce.cu), so the gradient needs no second logits product.
+//
+// Every wait is bounded; after a timeout the CTA records the error, stops
+// issuing, and both CTAs meet at the final cluster barrier before the pair
+// frees its TMEM.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "vocab.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int TILE = 256;
+constexpr int BK = 64;
+constexpr int STAGES = 4;
+constexpr int EPI = 8;  // epilogue warps: two per TMEM lane quarter, 128 columns each
+constexpr int kThreads = (3 + EPI) * 32;
+constexpr uint32_t HALF_BYTES = 128 * BK * 2;
+constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
+constexpr uint32_t MN_BOX_BYTES = 64 * 64 * 2;
+constexpr uint32_t kStaging = 2 * 4096;  // two boxes of 32 rows x 128 bytes per epilogue warp
+constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1;
+constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + EPI * kStaging + kNumBars * 8 + 16;
+constexpr uint32_t kTmemCols = 512;
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+// Every CTA takes all of its SM's TMEM, so no second one may share the SM.
+static_assert(kSmem > 114 * 1024, "one CTA per SM");
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) {
+  return smem_desc_sw128(base + 32u * kk, 16u, 1024u);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {
+  return smem_desc_sw128(base + 2048u * kk, MN_BOX_BYTES, 1024u);
+}
+
+struct Tile {
+  int m0, n0, kb0, kb1, split;
+};
+
+// Tiles of one split in groups of group_m row tiles, the row tile fastest: the
+// tiles that run at the same time share the group's A rows and a few B blocks.
+__device__ __forceinline__ Tile tile_at(const VocabGemm& G, int t) {
+  const int per_split = G.tiles_m * G.tiles_n;
+  Tile T;
+  T.split = t / per_split;
+  int r = t - T.split * per_split;
+  const int per_group = G.group_m * G.tiles_n;
+  const int g = r / per_group;
+  r -= g * per_group;
+  const int gm = min(G.group_m, G.tiles_m - g * G.group_m);
+  const int n = r / gm;
+  T.m0 = (g * G.group_m + (r - n * gm)) * TILE;
+  T.n0 = n * TILE;
+  T.kb0 = static_cast<int>(static_cast<int64_t>(G.kb_total) * T.split / G.splits);
+  T.kb1 = static_cast<int>(static_cast<int64_t>(G.kb_total) * (T.split + 1) / G.splits);
+  return T;
+}
+
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// This thread's 128 accumulator columns.
+__device__ __forceinline__ void load_columns(uint32_t t_lane, uint32_t (&r)[4][32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(t_lane + 32u * i, r[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld_wait_regs(r[i]);
+}
+
+// Box `buf` of the warp's staging (32 rows of 128 bytes, 128-byte swizzle):
+// 16-byte piece j of row `lane`.
+__device__ __forceinline__ uint32_t piece(uint32_t buf, int lane, int j) {
+  return buf + static_cast<uint32_t>(lane) * 128u + (static_cast<uint32_t>(j ^ (lane & 7)) << 4);
+}
+
+__device__ __forceinline__ void logits_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int row, int col0,
+                                                int warp_row0, uint32_t staging, int lane) {
+  const float c = G.logit_scale_log2;
+  const float minus_inf = __int_as_float(0xff800000);
+  if (col0 + kCeBlock > G.N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + 32 * i + j >= G.N) r[i][j] = __float_as_uint(minus_inf);
+  }
+  float m4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m4[i] = __uint_as_float(r[i][0]);
+#pragma unroll
+    for (int j = 1; j < 32; ++j) m4[i] = fmaxf(m4[i], __uint_as_float(r[i][j]));
+  }
+  float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;  // c > 0
+  // Above every z by more than the rounding of the products below, so that no
+  // distance comes out negative.
+  m += fabsf(m) * 2.4e-7f;
+  if (m == minus_inf) m = 0.f;  // only NaN and -inf: the sum below is then NaN or 0
+  const bool row_ok = row < G.M;
+  bool bad = false;
+  const int target = row_ok ? load_id(G.targets, row, &bad) : -1;
+  const int at = target - col0;
+  const bool hit = target >= 0 && at >= 0 && at < kCeBlock;
+  if (__any_sync(0xffffffffu, hit)) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (at == 32 * i + j) z = __uint_as_float(r[i][j]);
+    if (hit) G.target_z[row] = z * c;
+  }
+  float s4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s4[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float d = fmaf(__uint_as_float(r[i][j]), c, -m);
+      s4[i] += ex2(d);
+      r[i][j] = __float_as_uint(d);
+    }
+  }
+  if (row_ok)
+    G.stats[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+  if (!G.store_logs) return;
+  // Rounded to the nearest unit by adding 2^23, whose low mantissa bits then
+  // are the integer; distances past 64 octaves stay at the largest.
+  const float magic = 8388608.f, most = magic + 65535.f;
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const uint32_t buf = staging + 4096u * b;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = 64 * b + 8 * p + 2 * k;
+        const float lo = fminf(fmaf(__uint_as_float(r[j >> 5][j & 31]), -kCeLogUnits, magic), most);
+        const float hi = fminf(fmaf(__uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]), -kCeLogUnits, magic), most);
+        w[k] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+      }
+      st_shared_16(piece(buf, lane, p), w[0], w[1], w[2], w[3]);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
+    if (col0 + 64 < G.N) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
+    bulk_commit_group();
+  }
+}
+
+__device__ __forceinline__ void bf16_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int col0, int warp_row0,
+                                              uint32_t staging, int lane) {
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const uint32_t buf = staging + 4096u * b;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = 64 * b + 8 * p + 2 * k;
+        w[k] = pack_bf16x2(__uint_as_float(r[j >> 5][j & 31]), __uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]));
+      }
+      st_shared_16(piece(buf, lane, p), w[0], w[1], w[2], w[3]);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
+    if (col0 + 64 < G.N) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
+    bulk_commit_group();
+  }
+}
+
+__device__ __forceinline__ void f32_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int col0, int warp_row0,
+                                             int split, uint32_t staging, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (col0 + 32 * i >= G.N) break;
+    const uint32_t buf = staging + 4096u * (i & 1);
+    if (lane == 0) {
+      if (i == 0)
+        bulk_wait_group_read<0>();
+      else
+        bulk_wait_group_read<1>();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      st_shared_16(piece(buf, lane, p), r[i][4 * p], r[i][4 * p + 1], r[i][4 * p + 2], r[i][4 * p + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (G.add)
+        tma_add_3d(&G.map_out, buf, col0 + 32 * i, warp_row0, split);
+      else
+        tma_store_3d(&G.map_out, buf, col0 + 32 * i, warp_row0, split);
+      bulk_commit_group();
+    }
+  }
+}
+
+template <int MODE, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    vocab_gemm_kernel(const __grid_constant__ VocabGemm G) {
+  constexpr int kProducerBWarp = 2 + EPI;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t staging = ring + STAGES * STAGE_BYTES;
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + EPI * kStaging);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_mem + kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bar_mem);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain = bar0 + 8u * (2 * STAGES + 4);
+
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int n_pairs = gridDim.x >> 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 2);  // one arrival per operand producer of the leader
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 2 * EPI);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_tiles = G.tiles_m * G.tiles_n * G.splits;
+
+  if ((warp == 0 || warp == kProducerBWarp) && lane == 0) {
+    // ------------------------------------ producers (A: warp 0, B: the last)
+    const bool is_b = warp != 0;
+    const bool mn = is_b ? B_MN : A_MN;
+    const CUtensorMap* map = is_b ? &G.map_b : &G.map_a;
+    tma_prefetch_map(map);
+    const uint32_t dst_off = is_b ? HALF_BYTES : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    int fills[STAGES] = {};
+    bool ok = true;
+    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      const Tile T = tile_at(G, t);
+      const int row0 = (is_b ? T.n0 : T.m0) + 128 * static_cast<int>(rank);
+      for (int kb = T.kb0; kb < T.kb1; ++kb) {
+        if (!mbar_wait_bounded_cluster(empty(stage), phase ^ 1u, abort_flag, G.err, kErrTimeoutProducer)) {
+          ok = false;
+          break;
+        }
+        const uint32_t leader_full = mapa_shared(full(stage), 0);
+        if (leader) mbar_expect_tx(full(stage), 2 * HALF_BYTES);
+        ++fills[stage];
+        const uint32_t dst = ring + stage * STAGE_BYTES + dst_off;
+        if (!mn) {
+          tma_load_3d_pair(dst, map, leader_full, kb * BK, row0, 0);
+        } else {
+          tma_load_3d_pair(dst, map, leader_full, row0, kb * BK, 0);
+          tma_load_3d_pair(dst + MN_BOX_BYTES, map, leader_full, row0 + 64, kb * BK, 0);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && leader) {
+      // The leader's barriers count both CTAs' bytes: let every armed phase
+      // land before the pair tears down.
+      for (int s = 0; s < STAGES; ++s) {
+        if (fills[s] > 0) {
+          volatile int no_abort = 0;
+          mbar_wait_bounded_cluster(full(s), static_cast<uint32_t>(fills[s] - 1) & 1u, &no_abort, nullptr, 0,
+                                    100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------- MMA issuer (leader only)
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(TILE, TILE, A_MN, B_MN);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int use = 0;
+      for (int t = pair; t < n_tiles && ok; t += n_pairs, ++use) {
+        const Tile T = tile_at(G, t);
+        if (!mbar_wait_bounded_cluster(tempty(use & 1), (static_cast<uint32_t>(use >> 1) & 1u) ^ 1u, abort_flag, G.err,
+                                       kErrTimeoutMma))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((use & 1) * TILE);
+        for (int kb = T.kb0; kb < T.kb1; ++kb) {
+          if (!mbar_wait_bounded_cluster(full(stage), phase, abort_flag, G.err, kErrTimeoutMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = ring + stage * STAGE_BYTES;
+          const uint32_t sb = sa + HALF_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = A_MN ? desc_mn(sa, kk) : desc_k(sa, kk);
+            const uint64_t bd = B_MN ? desc_mn(sb, kk) : desc_k(sb, kk);
+            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != T.kb0 || kk != 0) ? 1u : 0u);
+          }
+          umma_commit_pair_multicast(empty(stage), 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) umma_commit_pair_multicast(tfull(use & 1), 0x3);
+      }
+      umma_commit_pair_multicast(drain, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait_bounded_cluster(drain, 0, &no_abort, G.err, kErrTimeoutDrain);
+    }
+  } else if (warp >= 2 && warp < 2 + EPI) {
+    // ------------------------------------------------------------ epilogue
+    // A warp reaches the TMEM lanes of its warp index mod 4; the two warps of
+    // a lane quarter take 128 columns each.
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const uint32_t my_staging = staging + static_cast<uint32_t>(warp - 2) * kStaging;
+    int use = 0;
+    for (int t = pair; t < n_tiles; t += n_pairs, ++use) {
+      const Tile T = tile_at(G, t);
+      const int acc = use & 1;
+      if (!mbar_wait_bounded_cluster(tfull(acc), static_cast<uint32_t>(use >> 1) & 1u, abort_flag, G.err,
+                                     kErrTimeoutEpilogue))
+        break;
+      tc_fence_after();
+      const int warp_row0 = T.m0 + 128 * static_cast<int>(rank) + 32 * quarter;
+      const int col0 = T.n0 + 128 * half;
+      const bool any = warp_row0 < G.M && col0 < G.N;  // warp-uniform
+      uint32_t r[4][32];
+      if (any)
+        load_columns(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * TILE + 128 * half),
+                     r);
+      // The registers hold the accumulator: the next tile may use the TMEM.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(tempty(acc));
+        else
+          mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+      }
+      if (!any) continue;
+      if (MODE == kVgLogits)
+        logits_epilogue(G, r, warp_row0 + lane, col0, warp_row0, my_staging, lane);
+      else if (MODE == kVgBf16)
+        bf16_epilogue(G, r, col0, warp_row0, my_staging, lane);
+      else
+        f32_epilogue(G, r, col0, warp_row0, T.split, my_staging, lane);
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // all MMAs drained, no more cross-CTA traffic
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+template <int MODE, bool A_MN, bool B_MN>
+cudaError_t launch_variant(const VocabGemm& G, int n_pairs, cudaStream_t st) {
+  static unsigned long long attr_mask = 0;
+  if (attr_needed_on_current_device(&attr_mask)) {
+    cudaError_t e = cudaFuncSetAttribute(vocab_gemm_kernel<MODE, A_MN, B_MN>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    attr_note_current_device(&attr_mask);
+  }
+  const int64_t tiles = static_cast<int64_t>(G.tiles_m) * G.tiles_n * G.splits;
+  const int pairs = static_cast<int>(tiles < n_pairs ? tiles : n_pairs);
+  vocab_gemm_kernel<MODE, A_MN, B_MN><<<2 * pairs, kThreads, kSmem, st>>>(G);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_vocab_gemm(int mode, bool a_mn, bool b_mn, const VocabGemm& G, int n_pairs, cudaStream_t st) {
+  if (G.M <= 0 || G.N <= 0 || n_pairs <= 0) return cudaErrorInvalidValue;
+  if (mode == kVgLogits && !a_mn && !b_mn) return launch_variant<kVgLogits, false, false>(G, n_pairs, st);
+  if (mode == kVgBf16 && !a_mn && b_mn) return launch_variant<kVgBf16, false, true>(G, n_pairs, st);
+  if (mode == kVgBf16 && a_mn && b_mn) return launch_variant<kVgBf16, true, true>(G, n_pairs, st);
+  if (mode == kVgF32 && !a_mn && b_mn) return launch_variant<kVgF32, false, true>(G, n_pairs, st);
+  if (mode == kVgF32 && a_mn && b_mn) return launch_variant<kVgF32, true, true>(G, n_pairs, st);
+  return cudaErrorInvalidValue;  // not built
+}
+
+// CTA pairs that can be resident at once.
+int vocab_gemm_max_pairs() {
+  auto kernel = vocab_gemm_kernel<kVgLogits, false, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};  // the cluster shape comes from __cluster_dims__
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
+}
+
+}  // namespace dmuon

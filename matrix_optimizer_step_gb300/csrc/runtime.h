@@ -62,6 +62,9 @@ struct Tuning {
   int64_t group_min_elems = int64_t(1) << 30;
   // Host-buffer step: smallest group (elements).
   int64_t host_group_min_elems = int64_t(1) << 25;
+  // Cross entropy with gradients: largest block of fixed-point logs (2 bytes
+  // per token and vocabulary entry) that is held at a time.
+  int64_t ce_block_bytes = int64_t(2) << 30;
 };
 
 // Apply one (key, value) pair of dmuon_set_tuning to `t`; DMUON_ERR_INVALID_ARG
@@ -339,6 +342,14 @@ struct dmuon_context {
   dmuon::AdamPlan adam;
   dmuon::StagedTable vec_table;
   dmuon::Profiler prof;
+  // Vocabulary operators (vocab.cu): their scratch, the ticket of their last-block
+  // sums, the end of the last call that used them and its stream, and the number
+  // of CTA pairs their products run on.
+  dmuon::DevBuf vocab_ws, vocab_ticket;
+  cudaEvent_t vocab_done = nullptr;
+  cudaStream_t vocab_stream = nullptr;
+  bool vocab_used = false;
+  int vocab_pairs = 0;
   // AdamW descriptor array whose pointers last passed the reachability check.
   std::vector<uint8_t> checked_vecs;
   // Descriptor arrays (Muon, AdamW) that last passed the overlap check.
@@ -391,6 +402,7 @@ inline void keep_bytes(std::vector<uint8_t>& v, const T* a, int n) {
 
 // ---- api.cu
 int ensure_device(dmuon_context* ctx);
+int check_reachable(const dmuon_context* ctx, const void* p, const char* what, int idx);
 int check_matrices_reachable(dmuon_context* ctx, std::vector<uint8_t>& checked, const dmuon_matrix* mats,
                              int n);
 int check_vectors_reachable(dmuon_context* ctx, const dmuon_vector* ts, int n);

@@ -1,0 +1,151 @@
+"""User-facing wrapper of the vocabulary operators: embedding lookup and softmax
+cross entropy over the output head, each with its gradient.
+
+``VocabOps`` keeps a library context; its methods check and marshal torch
+tensors, and everything runs in the CUDA library through the C ABI.  The
+gradients have the dtypes ``OwnerStep.set_adamw`` takes, so an embedding table
+or head goes from here straight to its AdamW step.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import capi
+
+_FLOATS = {torch.bfloat16: capi.DMUON_DTYPE_BF16, torch.float32: capi.DMUON_DTYPE_F32}
+_INDEX = {torch.int32: capi.DMUON_INDEX_I32, torch.int64: capi.DMUON_INDEX_I64}
+
+
+class VocabOps:
+    """Embedding and cross entropy on one GPU.
+
+    Matrices are (rows, width) tensors with contiguous rows (any row pitch);
+    lists are contiguous.  Work is enqueued on ``stream`` (a torch stream or
+    handle; None: the current one) and returns without waiting; ``sync``
+    reports device-side errors, an id past the vocabulary among them."""
+
+    def __init__(self, device=0):
+        self.device = int(device)
+        self.ctx = capi.dmuon_context_create(self.device)
+        self._lib = capi.load_library()
+
+    def _matrix(self, t, name, dtypes, rows=None, cols=None):
+        """(pointer, row pitch) of a checked matrix."""
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != self.device:
+            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+        if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'*' if rows is None else rows}, "
+                             f"{'*' if cols is None else cols})")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        if pitch < t.shape[1]:
+            raise ValueError(f"{name} has overlapping rows (stride {pitch})")
+        return t.data_ptr(), pitch
+
+    def _list(self, t, name, dtypes, n):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != self.device:
+            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: expected {n} contiguous elements")
+        return t.data_ptr()
+
+    # ----------------------------------------------------------- embedding
+    def _embed(self, fn, ids, table, rows, scale, flags, stream):
+        a = capi.DmuonEmbed()
+        a.table, a.ld_table = self._matrix(table, "table", _FLOATS)
+        a.vocab, a.dim = table.shape
+        a.n_tokens = ids.numel()
+        a.ids = self._list(ids, "ids", _INDEX, a.n_tokens)
+        a.rows, a.ld_rows = self._matrix(rows, "rows", _FLOATS, a.n_tokens, a.dim)
+        a.id_dtype, a.table_dtype, a.row_dtype = _INDEX[ids.dtype], _FLOATS[table.dtype], _FLOATS[rows.dtype]
+        a.scale, a.flags = scale, flags
+        capi._check(fn(self.ctx, ctypes.byref(a), capi._stream_handle(stream)))
+
+    def embed(self, ids, table, out=None, scale=1.0, stream=None):
+        """out[i] = scale * table[ids[i]] (zeros for ids below zero); returns
+        ``out`` (allocated in the table's dtype if None)."""
+        if out is None:
+            out = torch.empty(ids.numel(), table.shape[1], device=table.device, dtype=table.dtype)
+        self._embed(self._lib.dmuon_embed_forward, ids, table, out, scale, 0, stream)
+        return out
+
+    def embed_grad(self, ids, dout, dtable, scale=1.0, accumulate=False, stream=None):
+        """dtable[v] = scale * sum of dout[i] over ids[i] = v, for the whole
+        table; with ``accumulate`` added to what ``dtable`` holds."""
+        self._embed(self._lib.dmuon_embed_backward, ids, dtable, dout, scale,
+                    capi.DMUON_EMBED_ADD if accumulate else 0, stream)
+        return dtable
+
+    # ------------------------------------------------------- cross entropy
+    def cross_entropy(self, x, w, targets, weights=None, mean=True, logit_scale=1.0, grad_scale=1.0,
+                      loss=None, lse=None, total=None, dx=None, dw=None, accumulate_dw=False, stream=None):
+        """Softmax cross entropy of logits ``logit_scale * x @ w.T`` against
+        ``targets`` (below zero: not counted), without storing the logits.
+
+        Writes whichever outputs are given: ``loss`` and ``lse`` (fp32 per
+        token), ``total`` (one fp32: the weighted sum of losses, over the sum
+        of weights with ``mean``), and the gradients of ``grad_scale * total``
+        in ``dx`` (like x) and ``dw`` (like w; added to with
+        ``accumulate_dw``), bf16 or fp32.  With none given, ``loss`` is
+        allocated.  Returns ``loss``."""
+        a = capi.DmuonCe()
+        bf16 = (torch.bfloat16,)
+        a.x, a.ld_x = self._matrix(x, "x", bf16)
+        a.n_tokens, a.dim = x.shape
+        a.w, a.ld_w = self._matrix(w, "w", bf16, cols=a.dim)
+        a.vocab = w.shape[0]
+        n, f32 = a.n_tokens, (torch.float32,)
+        a.targets = self._list(targets, "targets", _INDEX, n)
+        if loss is None and lse is None and total is None and dx is None and dw is None:
+            loss = torch.empty(n, device=x.device, dtype=torch.float32)
+        if weights is not None:
+            a.weights = self._list(weights, "weights", f32, n)
+        if loss is not None:
+            a.loss = self._list(loss, "loss", f32, n)
+        if lse is not None:
+            a.lse = self._list(lse, "lse", f32, n)
+        if total is not None:
+            a.total = self._list(total, "total", f32, 1)
+        if dx is not None:
+            a.dx, a.ld_dx = self._matrix(dx, "dx", _FLOATS, n, a.dim)
+            a.dx_dtype = _FLOATS[dx.dtype]
+        if dw is not None:
+            a.dw, a.ld_dw = self._matrix(dw, "dw", _FLOATS, a.vocab, a.dim)
+            a.dw_dtype = _FLOATS[dw.dtype]
+        a.x_dtype = a.w_dtype = capi.DMUON_DTYPE_BF16
+        a.target_dtype = _INDEX[targets.dtype]
+        a.logit_scale, a.grad_scale = logit_scale, grad_scale
+        a.flags = (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0)
+        capi._check(self._lib.dmuon_cross_entropy(self.ctx, ctypes.byref(a), capi._stream_handle(stream)))
+        return loss
+
+    # ---------------------------------------------------------------- misc
+    def sync(self, stream=None):
+        """Wait for ``stream`` and raise DmuonError for device-side errors."""
+        capi.dmuon_sync(self.ctx, stream)
+
+    def set_tuning(self, key, value):
+        """One tuning key of this context (dmuon_context_set_tuning)."""
+        capi.dmuon_context_set_tuning(self.ctx, key, value)
+
+    def kernel_launches(self):
+        return capi.dmuon_kernel_launches(self.ctx)
+
+    def close(self):
+        if self.ctx is not None:
+            capi.dmuon_context_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
