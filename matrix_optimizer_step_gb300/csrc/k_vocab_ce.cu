@@ -33,42 +33,39 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
 }
 
 // --------------------------------------------------------------- operand copy
-// One warp per row; VEC: rows start on 16 bytes in both arrays and cols % 8 == 0.
+// One warp per row; VEC: source rows start on 16 bytes and cols % 8 == 0.
 template <bool VEC>
-__global__ void ce_copy_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
-                               int cols, IdList targets, int has_targets, const float* weights, float* inv_norm) {
-  if (inv_norm && blockIdx.x == 0) {
-    __shared__ double smem[32];
-    double s = 0.0;
-    bool bad = false;
-    for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) s += weight_of(targets, weights, i, &bad);
-    s = block_sum(s, smem);
-    if (threadIdx.x == 0) *inv_norm = s != 0.0 ? static_cast<float>(1.0 / s) : 0.f;
-  }
-  if (!dst) return;  // only the norm is wanted
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps) {
-    bool bad = false;
-    const bool keep = !has_targets || load_id(targets, row, &bad) >= 0;
-    const uint16_t* s = src + row * ld_src;
-    uint16_t* d = dst + row * ld_dst;
-    if (VEC) {
-      for (int c = lane * 8; c < cols; c += 256)
-        *reinterpret_cast<uint4*>(d + c) = keep ? __ldg(reinterpret_cast<const uint4*>(s + c)) : make_uint4(0, 0, 0, 0);
-    } else {
-      for (int c = lane; c < ld_dst; c += 32) d[c] = keep && c < cols ? s[c] : uint16_t(0);
-    }
+__device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int cols, int ld_dst, bool keep, int lane) {
+  if (VEC) {
+    for (int c = lane * 8; c < cols; c += 256)
+      *reinterpret_cast<uint4*>(d + c) = keep ? __ldg(reinterpret_cast<const uint4*>(s + c)) : make_uint4(0, 0, 0, 0);
+  } else {
+    for (int c = lane; c < ld_dst; c += 32) d[c] = keep && c < cols ? s[c] : uint16_t(0);
   }
 }
 
+template <bool VEC>
+__global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
+                                                      int64_t rows, int cols) {
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps)
+    copy_row<VEC>(src + row * ld_src, dst + row * ld_dst, cols, static_cast<int>(ld_dst), true, threadIdx.x & 31);
+}
+
 // ------------------------------------------------------------------- row sums
-// Joins a row's (maximum, sum) pairs of all column blocks:
-//   M = max m_b,  S = sum_b s_b 2^(m_b - M),  log2 sum = M + log2 S,
-//   loss = ln2 ((M - z_t) + log2 S).
-// A block takes 32 rows (one per lane, so a warp reads 32 neighbouring pairs)
-// and its 32 warps take every 32nd column block; the warps' pairs are joined
-// in a fixed order.  The last block of the last pass sums the losses.
+// Joins a row's (maximum, sum) pairs of all vocabulary blocks:
+//   M = max m_b,  S = sum_b s_b 2^(m_b - M),
+// and from them the row's loss.  The product's fp32 sums may truncate, which
+// shows where one logit is large: the target's.  So the target's logit is
+// summed again here (one dot product a row) and takes the place of the
+// product's in S: with rest = S - 2^(z_t - M) and the new z_t,
+//   loss = ln((rest + 2^(z_t - M)) / 2^(z_t - M)),
+// as log1p where the target holds more than half of the sum.
+//
+// A block takes up to 32 rows and its 32 warps share their vocabulary blocks:
+// with fewer rows than lanes, a warp's lanes also take several blocks at once.
+// Then warp w finishes row w.  All joins run in a fixed order.  The blocks after
+// those copy dW's operand.  The last of the row blocks sums the losses.
 constexpr int kRowWarps = 32;
 
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
@@ -81,55 +78,126 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
-__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R) {
+// Joined over lanes `step`, 2 step, ... 16 apart.
+__device__ __forceinline__ void join_lanes(float& m, float& s, int step) {
+  for (int o = step; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    join(m, s, m2, s2);
+  }
+}
+
+// Dot product of two bf16 rows by one warp, in fp32; the same in every lane.
+__device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, int n, int lane) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
+    const int n8 = n >> 3;
+#pragma unroll 4
+    for (int c = lane; c < n8; c += 32) {
+      const uint4 p = __ldg(reinterpret_cast<const uint4*>(a) + c), q = __ldg(reinterpret_cast<const uint4*>(b) + c);
+      const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), acc[i]);
+        acc[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc[i]);
+      }
+    }
+    a += n8 * 8;
+    b += n8 * 8;
+    n &= 7;
+  }
+  for (int c = lane; c < n; c += 32) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
+  float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks, int width) {
   __shared__ float sm[kRowWarps][33], ss[kRowWarps][33];
   __shared__ double red[32];
   __shared__ uint32_t last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float m = __int_as_float(0xff800000), s = 0.f;
-  if (r < R.rows) {
-    const float2* p = R.stats + r;
-    int b = warp;
-    for (; b + 3 * kRowWarps < R.n_blocks; b += 4 * kRowWarps) {
-      float2 q[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = __ldg(p + static_cast<int64_t>(b + k * kRowWarps) * R.stats_ld);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) join(m, s, q[k].x, q[k].y);
+  if (static_cast<int>(blockIdx.x) >= row_blocks) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x - row_blocks) * kRowWarps;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x - row_blocks) * kRowWarps + warp; r < R.rows; r += warps) {
+      bool bad = false;
+      const bool keep = load_id(R.targets, R.row0 + r, &bad) >= 0;
+      for (int k = 0; k < R.copies; ++k)
+        copy_row<VEC>(R.x + r * R.ld_x, R.x_copy + (r + k * R.rows) * R.ld_copy, R.dim, static_cast<int>(R.ld_copy), keep, lane);
     }
-    for (; b < R.n_blocks; b += kRowWarps) {
-      const float2 q = __ldg(p + static_cast<int64_t>(b) * R.stats_ld);
-      join(m, s, q.x, q.y);
-    }
+    return;
   }
-  sm[warp][lane] = m;
-  ss[warp][lane] = s;
+  // width: rows of a block, a power of two up to 32.
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * width;
+  {
+    const int64_t r = base + (lane & (width - 1));
+    const int per_warp = 32 / width, stride = kRowWarps * per_warp;
+    float m = __int_as_float(0xff800000), s = 0.f;
+    if (r < R.rows) {
+      const float2* p = R.stats + r;
+      int b = warp * per_warp + lane / width;
+      for (; b + 3 * stride < R.n_blocks; b += 4 * stride) {
+        float2 q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) join(m, s, q[k].x, q[k].y);
+      }
+      for (; b < R.n_blocks; b += stride) {
+        const float2 q = __ldg(p + static_cast<int64_t>(b) * R.stats_ld);
+        join(m, s, q.x, q.y);
+      }
+    }
+    join_lanes(m, s, width);
+    sm[warp][lane] = m;
+    ss[warp][lane] = s;
+  }
   __syncthreads();
-  if (warp == 0 && r < R.rows) {
-    const int warps = min(kRowWarps, R.n_blocks);
-    for (int w = 1; w < warps; ++w) join(m, s, sm[w][lane], ss[w][lane]);
+  const int64_t r = base + warp;
+  if (warp < width && r < R.rows) {
+    float m = sm[lane][warp], s = ss[lane][warp];
+    join_lanes(m, s, 1);
     const int64_t i = R.row0 + r;
     bool bad = false;
     const int t = load_id(R.targets, i, &bad);
-    if (bad) atomicCAS(R.err, 0, kErrBadIndex);
-    const float l2 = log2f(s), lse2 = m + l2;
-    const float gap = t >= 0 ? (m - R.target_z[r]) + l2 : 0.f;  // log2(1 / p_target), octaves
-    R.loss[i] = t >= 0 ? kLn2 * gap : 0.f;
-    if (R.lse) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;
-    if (R.out) {
-      CeRow o;
-      o.lse2 = lse2;
-      o.coef = t < 0 ? 0.f : R.grad_scale * (R.weights ? R.weights[i] : 1.f) * (R.inv_norm ? *R.inv_norm : 1.f);
-      o.target_dz = o.coef * expm1f(-kLn2 * gap);
-      o.target = t;
-      R.out[r] = o;
+    if (bad && lane == 0) atomicCAS(R.err, 0, kErrBadIndex);
+    float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
+    if (t >= 0) {
+      const float z = warp_dot(R.x + r * R.ld_x, R.w + t * R.ld_w, R.dim, lane) * R.logit_scale_log2;
+      float rest = s - exp2f(R.target_z[r] - m);
+      if (rest < 0.f) rest = 0.f;  // (a NaN stays)
+      const float own = exp2f(z - m), sum = rest + own, l2 = log2f(sum);
+      loss = own > rest ? log1pf(rest / own) : kLn2 * ((m - z) + l2);
+      lse2 = m + l2;
+      share = rest / sum;
     }
+    if (lane == 0) {
+      R.loss[i] = loss;
+      if (R.lse) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;
+      if (R.out) {
+        CeRow o;
+        o.lse2 = lse2;
+        o.weight = t < 0 ? 0.f : R.weights ? R.weights[i] : 1.f;
+        o.target_dz = -o.weight * share;
+        o.target = t;
+        R.out[r] = o;
+      }
+    }
+  }
+  if (R.alpha && blockIdx.x == 0) {
+    double norm = 0.0;
+    bool bad = false;
+    if (R.mean) {
+      for (int64_t i = threadIdx.x; i < R.n; i += blockDim.x) norm += weight_of(R.targets, R.weights, i, &bad);
+      norm = block_sum(norm, red);
+    }
+    if (threadIdx.x == 0) *R.alpha = !R.mean ? R.scale : norm != 0.0 ? static_cast<float>(R.scale / norm) : 0.f;
   }
   if (!R.total) return;
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(R.ticket, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) last = atomicAdd(R.ticket, 1u) == static_cast<uint32_t>(row_blocks) - 1u;
   __syncthreads();
   if (!last) return;
   __threadfence();
@@ -149,8 +217,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R)
 }
 
 // ------------------------------------------------------------------- d logits
-//   dz = coef (2^(m_b - lse - q / 1024) - [v = target])
-// with the factor folded into the exponent.  Eight columns (16 bytes) a thread.
+//   dz = weight (2^(m_b - lse - q / 1024) - [v = target])
+// with the weight folded into the exponent; the factor common to all rows stays
+// out, so that without weights a target's dz is rounded next to 1, not next to
+// 1 / (number of tokens).  Eight entries (16 bytes) a thread, four at a time.
+// LO: also the rest of the rounding, for the rows below.
 constexpr int kDlThreads = 256;
 constexpr int kDlCols = kDlThreads * 8 * 4;
 
@@ -160,16 +231,17 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-__global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block, int64_t ld, int vocab,
+template <bool LO>
+__global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block, int64_t ld, int vocab, int stats_shift,
                                                                 const float2* stats, int64_t stats_ld,
-                                                                const CeRow* row_info) {
+                                                                const CeRow* row_info, int64_t lo_rows) {
   const int64_t row = blockIdx.y;
   const CeRow R = row_info[row];
   uint16_t* p = block + row * ld;
   const int c0 = blockIdx.x * kDlCols + threadIdx.x * 8;
-  const bool counted = R.coef != 0.f;  // else zeros, whatever the row's logits are
-  const float lift = log2f(fabsf(R.coef)) - R.lse2;
-  const uint32_t sign = __float_as_uint(R.coef) & 0x80000000u;
+  const bool counted = R.weight != 0.f;  // else zeros, whatever the row's logits are
+  const float lift = log2f(fabsf(R.weight)) - R.lse2;
+  const uint32_t sign = __float_as_uint(R.weight) & 0x80000000u;
   uint4 q[4];
   float m[4];
 #pragma unroll
@@ -177,7 +249,7 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
     const int c = c0 + k * kDlThreads * 8;
     if (c < vocab) {
       q[k] = *reinterpret_cast<const uint4*>(p + c);
-      m[k] = __ldg(&stats[static_cast<int64_t>(c / kCeBlock) * stats_ld + row].x);
+      m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld + row].x);
     }
   }
 #pragma unroll
@@ -198,32 +270,60 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
       if (c + j == R.target) v[j] = R.target_dz;
       if (!counted) v[j] = 0.f;
     }
-    uint4 o;
-    o.x = pack_bf16x2(v[0], v[1]);
-    o.y = pack_bf16x2(v[2], v[3]);
-    o.z = pack_bf16x2(v[4], v[5]);
-    o.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4*>(p + c) = o;
+    *reinterpret_cast<uint4*>(p + c) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    if (LO)
+      *reinterpret_cast<uint4*>(p + lo_rows * ld + c) =
+          make_uint4(pack_bf16x2_remainder(v[0], v[1]), pack_bf16x2_remainder(v[2], v[3]),
+                     pack_bf16x2_remainder(v[4], v[5]), pack_bf16x2_remainder(v[6], v[7]));
   }
 }
 
 // ------------------------------------------------------------- partial sums
-__global__ void ce_finish_kernel(const float* part, int64_t ld_part, int64_t part_stride, int parts, void* out,
-                                 int64_t ld_out, int out_bf16, int accumulate, int64_t rows, int cols) {
-  const int64_t n = rows * cols;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+// One thread per four columns (VEC) or one.
+template <int VEC>
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64_t ld_part, int64_t part_stride, int parts,
+                                                        int64_t fold, void* out, int64_t ld_out, int out_bf16,
+                                                        int accumulate, const float* alpha, int64_t rows, int cols) {
+  const int64_t per_row = cols / VEC;
+  const float f = alpha ? __ldg(alpha) : 1.f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * per_row;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / cols, c = i - r * cols;
+    const int64_t r = i / per_row, c = (i - r * per_row) * VEC;
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = 0.f;
+    auto add = [&](const float* p) {
+      if (VEC == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        s[0] += q.x;
+        s[1 % VEC] += q.y;
+        s[2 % VEC] += q.z;
+        s[3 % VEC] += q.w;
+      } else {
+        s[0] += p[0];
+      }
+    };
     const float* p = part + r * ld_part + c;
-    float s = p[0];
-    for (int k = 1; k < parts; ++k) s += p[k * part_stride];
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      add(p + k * part_stride);
+      if (fold > 0) add(p + k * part_stride + fold * ld_part);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] *= f;
     if (out_bf16) {
       uint16_t* o = static_cast<uint16_t*>(out) + r * ld_out + c;
-      if (accumulate) s += bf16_bits_to_f32(*o);
-      *o = to_bf16_bits(s);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if (accumulate) s[j] += bf16_bits_to_f32(o[j]);
+        if (VEC == 1) o[j] = to_bf16_bits(s[j]);
+      }
+      if (VEC == 4) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s[0], s[1 % VEC]), pack_bf16x2(s[2 % VEC], s[3 % VEC]));
     } else {
       float* o = static_cast<float*>(out) + r * ld_out + c;
-      *o = accumulate ? *o + s : s;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = accumulate ? o[j] + s[j] : s[j];
     }
   }
 }
@@ -231,42 +331,62 @@ __global__ void ce_finish_kernel(const float* part, int64_t ld_part, int64_t par
 }  // namespace
 
 cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
-                           int32_t cols, const IdList* targets, const float* weights, float* inv_norm,
-                           cudaStream_t st) {
-  const bool vec = cols % 8 == 0 && ld_src % 8 == 0 && ld_dst % 8 == 0 && cols == ld_dst &&
-                   (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+                           int32_t cols, cudaStream_t st) {
+  const bool vec = cols % 8 == 0 && ld_src % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
   const int64_t blocks = (rows + 7) / 8;
-  const int grid = !dst ? 1 : static_cast<int>(blocks < 152 * 16 ? blocks : 152 * 16);
-  const IdList ids = targets ? *targets : IdList{nullptr, 0, 0};
+  const int grid = static_cast<int>(blocks < 152 * 16 ? blocks : 152 * 16);
   if (vec)
-    ce_copy_kernel<true><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols, ids, targets != nullptr, weights, inv_norm);
+    ce_copy_kernel<true><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols);
   else
-    ce_copy_kernel<false><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols, ids, targets != nullptr, weights, inv_norm);
+    ce_copy_kernel<false><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols);
   return cudaGetLastError();
 }
 
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st) {
-  ce_rows_kernel<<<static_cast<unsigned>((R.rows + 31) / 32), kRowWarps * 32, 0, st>>>(R);
+  // About 256 blocks before a block takes a full warp's width of rows: the way
+  // through a row's blocks is latency (24 rows: 44 us with one block, 9 with 24).
+  int width = 1;
+  while (width < 32 && width * 512 <= R.rows) width <<= 1;
+  const int64_t row_blocks = (R.rows + width - 1) / width;
+  int64_t copy_blocks = 0;
+  if (R.x_copy) copy_blocks = (R.rows + kRowWarps - 1) / kRowWarps;
+  const bool vec = R.dim % 8 == 0 && R.ld_x % 8 == 0 && (reinterpret_cast<uintptr_t>(R.x) & 15u) == 0;
+  const unsigned grid = static_cast<unsigned>(row_blocks + copy_blocks);
+  if (vec)
+    ce_rows_kernel<true><<<grid, kRowWarps * 32, 0, st>>>(R, static_cast<int>(row_blocks), width);
+  else
+    ce_rows_kernel<false><<<grid, kRowWarps * 32, 0, st>>>(R, static_cast<int>(row_blocks), width);
   return cudaGetLastError();
 }
 
-cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, const float2* stats,
-                              int64_t stats_ld, const CeRow* row_info, cudaStream_t st) {
+cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_block,
+                              const float2* stats, int64_t stats_ld, const CeRow* row_info, int64_t lo_rows,
+                              cudaStream_t st) {
+  const int shift = stats_block == kCeThinBlock ? 5 : 7;
+  static_assert(kCeThinBlock == 32 && kCeBlock == 128, "block shifts");
   const int64_t per_launch = 65535;  // the grid's second dimension
   for (int64_t r = 0; r < rows; r += per_launch) {
     const int64_t n = rows - r < per_launch ? rows - r : per_launch;
     const dim3 grid(static_cast<unsigned>((vocab + kDlCols - 1) / kDlCols), static_cast<unsigned>(n));
-    ce_dlogits_kernel<<<grid, kDlThreads, 0, st>>>(block + r * ld, ld, vocab, stats + r, stats_ld, row_info + r);
+    if (lo_rows > 0)
+      ce_dlogits_kernel<true><<<grid, kDlThreads, 0, st>>>(block + r * ld, ld, vocab, shift, stats + r, stats_ld, row_info + r, lo_rows);
+    else
+      ce_dlogits_kernel<false><<<grid, kDlThreads, 0, st>>>(block + r * ld, ld, vocab, shift, stats + r, stats_ld, row_info + r, 0);
   }
   return cudaGetLastError();
 }
 
-cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, void* out,
-                             int64_t ld_out, int out_bf16, int accumulate, int64_t rows, int32_t cols,
-                             cudaStream_t st) {
-  const int64_t blocks = (rows * cols + 255) / 256;
+cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, int64_t fold,
+                             void* out, int64_t ld_out, int out_bf16, int accumulate, const float* alpha,
+                             int64_t rows, int32_t cols, cudaStream_t st) {
+  // Partials have pitches of four; the output's rows must start on four bf16.
+  const bool vec = cols % 4 == 0 && ld_out % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
+  const int64_t blocks = (rows * (vec ? cols / 4 : cols) + 255) / 256;
   const int grid = static_cast<int>(blocks < 152 * 32 ? blocks : 152 * 32);
-  ce_finish_kernel<<<grid, 256, 0, st>>>(part, ld_part, part_stride, parts, out, ld_out, out_bf16, accumulate, rows, cols);
+  if (vec)
+    ce_finish_kernel<4><<<grid, 256, 0, st>>>(part, ld_part, part_stride, parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, cols);
+  else
+    ce_finish_kernel<1><<<grid, 256, 0, st>>>(part, ld_part, part_stride, parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, cols);
   return cudaGetLastError();
 }
 

@@ -12,8 +12,7 @@
 // the epilogue of a tile runs under the main loop of the next.
 //
 // The logits' epilogue never stores a logit.  Each thread owns one row and
-// 128 columns: it keeps the 128 accumulators in registers (and hands the TMEM
-// back at once), takes their maximum m and the sum of 2^(z - m), with
+// 128 columns: it takes their maximum m and the sum of 2^(z - m), with
 // z = logit * log2(e), and writes that pair.  For the gradient it also leaves
 // round((m - z) * 1024) as 16 bits: the exponential's argument in fixed point
 // is within 2^-11 octaves, i.e. a relative error of at most 3.4e-4 in the
@@ -60,25 +59,62 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {
 }
 
 struct Tile {
+  int product;           // index into VocabGrad::p; -1: no more
   int m0, n0, kb0, kb1, split;
 };
 
 // Tiles of one split in groups of group_m row tiles, the row tile fastest: the
 // tiles that run at the same time share the group's A rows and a few B blocks.
-__device__ __forceinline__ Tile tile_at(const VocabGemm& G, int t) {
-  const int per_split = G.tiles_m * G.tiles_n;
-  Tile T;
-  T.split = t / per_split;
-  int r = t - T.split * per_split;
-  const int per_group = G.group_m * G.tiles_n;
+__device__ __forceinline__ void place(Tile& T, int r, int tiles_m, int tiles_n, int group_m) {
+  const int per_group = group_m * tiles_n;
   const int g = r / per_group;
   r -= g * per_group;
-  const int gm = min(G.group_m, G.tiles_m - g * G.group_m);
+  const int gm = min(group_m, tiles_m - g * group_m);
   const int n = r / gm;
-  T.m0 = (g * G.group_m + (r - n * gm)) * TILE;
+  T.m0 = (g * group_m + (r - n * gm)) * TILE;
   T.n0 = n * TILE;
-  T.kb0 = static_cast<int>(static_cast<int64_t>(G.kb_total) * T.split / G.splits);
-  T.kb1 = static_cast<int>(static_cast<int64_t>(G.kb_total) * (T.split + 1) / G.splits);
+}
+
+// The i-th tile of CTA pair `pair` of `pairs`.
+__device__ __forceinline__ Tile tile_at(const VocabLogits& G, int pair, int pairs, int i) {
+  Tile T;
+  const int t = pair + i * pairs;
+  T.product = t < G.tiles_m * G.tiles_n ? 0 : -1;
+  if (T.product < 0) return T;
+  place(T, t, G.tiles_m, G.tiles_n, G.group_m);
+  T.split = 0;
+  T.kb0 = 0;
+  T.kb1 = G.kb_total;
+  return T;
+}
+
+__device__ __forceinline__ Tile tile_at(const VocabGrad& G, int pair, int pairs, int i) {
+  Tile T;
+  int t = pair + i * pairs;
+  T.product = 0;
+  if (t >= G.n_units[0]) {
+    T.product = 1;
+    // Pairs from `heavy` on have one tile of the first product fewer.
+    const int heavy = G.n_units[0] % pairs;
+    const int light = pairs - heavy;
+    const int extras = min(light * G.extra, G.n_units[1]);
+    i -= G.n_units[0] / pairs + (pair < heavy ? 1 : 0);
+    const int mine = pair >= heavy && pair - heavy < extras ? (extras - (pair - heavy) + light - 1) / light : 0;
+    if (i < mine)
+      t = pair - heavy + i * light;
+    else
+      t = extras + pair + (i - mine) * pairs;
+    if (t >= G.n_units[1]) {
+      T.product = -1;
+      return T;
+    }
+  }
+  const VgProduct& P = G.p[T.product];
+  const int per_split = P.tiles_m * P.tiles_n;
+  T.split = t / per_split;
+  place(T, t - T.split * per_split, P.tiles_m, P.tiles_n, P.group_m);
+  T.kb0 = static_cast<int>(static_cast<int64_t>(P.kb_total) * T.split / P.splits);
+  T.kb1 = static_cast<int>(static_cast<int64_t>(P.kb_total) * (T.split + 1) / P.splits);
   return T;
 }
 
@@ -113,60 +149,117 @@ __device__ __forceinline__ uint32_t piece(uint32_t buf, int lane, int j) {
   return buf + static_cast<uint32_t>(lane) * 128u + (static_cast<uint32_t>(j ^ (lane & 7)) << 4);
 }
 
-__device__ __forceinline__ void logits_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int row, int col0,
-                                                int warp_row0, uint32_t staging, int lane) {
+// Columns past the vocabulary in a 32-column chunk starting at `col` do not count.
+__device__ __forceinline__ void mask_columns(uint32_t (&r)[32], int col, int n) {
+  if (col + 32 <= n) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (col + j >= n) r[j] = 0xff800000u;  // -inf
+}
+
+__device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = __uint_as_float(r[k]);
+#pragma unroll
+    for (int j = k + 4; j < 32; j += 4) m[k] = fmaxf(m[k], __uint_as_float(r[j]));
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// The accumulator is read twice, 32 columns at a time: once for the maximum
+// and once for the sums and logs.  Holding all 128 columns in registers
+// spills (168 registers a thread with 11 warps) and measured 2.1 times the
+// time of the whole product at 4096 x 50257 x 768.
+// `target`: of this thread's row, -1 for none.  Calls `release` once the last
+// column has left the TMEM.
+template <class Release>
+__device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t_lane, int row, int target, int col0,
+                                                int warp_row0, uint32_t staging, int lane, Release release) {
   const float c = G.logit_scale_log2;
   const float minus_inf = __int_as_float(0xff800000);
-  if (col0 + kCeBlock > G.N) {
+  const int n = G.N;
+  uint32_t ra[32], rb[32];
+  float m = minus_inf;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (col0 + 32 * i + j >= G.N) r[i][j] = __float_as_uint(minus_inf);
+  for (int i = 0; i < 4; i += 2) {
+    tmem_ld_32x32b_x32(t_lane + 32u * i, ra);
+    tmem_ld_32x32b_x32(t_lane + 32u * (i + 1), rb);
+    tmem_ld_wait_regs(ra);
+    tmem_ld_wait_regs(rb);
+    mask_columns(ra, col0 + 32 * i, n);
+    mask_columns(rb, col0 + 32 * (i + 1), n);
+    m = fmaxf(m, fmaxf(max_of(ra), max_of(rb)));
   }
-  float m4[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m4[i] = __uint_as_float(r[i][0]);
-#pragma unroll
-    for (int j = 1; j < 32; ++j) m4[i] = fmaxf(m4[i], __uint_as_float(r[i][j]));
-  }
-  float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;  // c > 0
+  m *= c;  // c > 0
   // Above every z by more than the rounding of the products below, so that no
   // distance comes out negative.
   m += fabsf(m) * 2.4e-7f;
   if (m == minus_inf) m = 0.f;  // only NaN and -inf: the sum below is then NaN or 0
   const bool row_ok = row < G.M;
-  bool bad = false;
-  const int target = row_ok ? load_id(G.targets, row, &bad) : -1;
   const int at = target - col0;
-  const bool hit = target >= 0 && at >= 0 && at < kCeBlock;
-  if (__any_sync(0xffffffffu, hit)) {
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+  const bool store = G.store_logs != 0;
+  if (store) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+  // A distance is rounded to the nearest unit by adding 2^23, whose low
+  // mantissa bits then are the integer; past 64 octaves it stays at the largest.
+  const float magic = 8388608.f, most = magic + 65535.f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  auto chunk = [&](uint32_t (&q)[32], int i) {
+    if (__any_sync(0xffffffffu, target >= 0 && (at >> 5) == i)) {
+      float z = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (at == 32 * i + j) z = __uint_as_float(r[i][j]);
-    if (hit) G.target_z[row] = z * c;
-  }
-  float s4[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s4[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float d = fmaf(__uint_as_float(r[i][j]), c, -m);
-      s4[i] += ex2(d);
-      r[i][j] = __float_as_uint(d);
+        if (at == 32 * i + j) z = __uint_as_float(q[j]);
+      if (target >= 0 && (at >> 5) == i) G.target_z[row] = z * c;
     }
-  }
+    mask_columns(q, col0 + 32 * i, n);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float lo = fmaf(__uint_as_float(q[8 * p + 2 * k]), c, -m);
+        const float hi = fmaf(__uint_as_float(q[8 * p + 2 * k + 1]), c, -m);
+        s[k] += ex2(lo);
+        s[k] += ex2(hi);
+        w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),
+                           __float_as_uint(fminf(fmaf(hi, -kCeLogUnits, magic), most)), 0x5410);
+      }
+      if (store) st_shared_16(piece(staging + 4096u * (i >> 1), lane, 4 * (i & 1) + p), w[0], w[1], w[2], w[3]);
+    }
+  };
+  // The next chunk's load is in flight while one is worked on.
+  tmem_ld_32x32b_x32(t_lane, ra);
+  tmem_ld_wait_regs(ra);
+  tmem_ld_32x32b_x32(t_lane + 32u, rb);
+  chunk(ra, 0);
+  tmem_ld_wait_regs(rb);
+  tmem_ld_32x32b_x32(t_lane + 64u, ra);
+  chunk(rb, 1);
+  tmem_ld_wait_regs(ra);
+  tmem_ld_32x32b_x32(t_lane + 96u, rb);
+  chunk(ra, 2);
+  tmem_ld_wait_regs(rb);
+  release();
+  chunk(rb, 3);
   if (row_ok)
-    G.stats[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
-  if (!G.store_logs) return;
-  // Rounded to the nearest unit by adding 2^23, whose low mantissa bits then
-  // are the integer; distances past 64 octaves stay at the largest.
-  const float magic = 8388608.f, most = magic + 65535.f;
+    G.stats[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+  if (!store) return;
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
+    if (col0 + 64 < n) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
+    bulk_commit_group();
+  }
+}
+
+__device__ __forceinline__ void bf16_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0,
+                                              int warp_row0, uint32_t staging, int lane) {
   if (lane == 0) bulk_wait_group_read<0>();
   __syncwarp();
 #pragma unroll
@@ -178,9 +271,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabGemm& G, uint32_t (&r
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int j = 64 * b + 8 * p + 2 * k;
-        const float lo = fminf(fmaf(__uint_as_float(r[j >> 5][j & 31]), -kCeLogUnits, magic), most);
-        const float hi = fminf(fmaf(__uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]), -kCeLogUnits, magic), most);
-        w[k] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+        w[k] = pack_bf16x2(alpha * __uint_as_float(r[j >> 5][j & 31]), alpha * __uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]));
       }
       st_shared_16(piece(buf, lane, p), w[0], w[1], w[2], w[3]);
     }
@@ -188,44 +279,17 @@ __device__ __forceinline__ void logits_epilogue(const VocabGemm& G, uint32_t (&r
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
-    if (col0 + 64 < G.N) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
+    tma_store_3d(&P.map_out, staging, col0, warp_row0, 0);
+    if (col0 + 64 < P.N) tma_store_3d(&P.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
     bulk_commit_group();
   }
 }
 
-__device__ __forceinline__ void bf16_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int col0, int warp_row0,
-                                              uint32_t staging, int lane) {
-  if (lane == 0) bulk_wait_group_read<0>();
-  __syncwarp();
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const uint32_t buf = staging + 4096u * b;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = 64 * b + 8 * p + 2 * k;
-        w[k] = pack_bf16x2(__uint_as_float(r[j >> 5][j & 31]), __uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]));
-      }
-      st_shared_16(piece(buf, lane, p), w[0], w[1], w[2], w[3]);
-    }
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
-    if (col0 + 64 < G.N) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
-    bulk_commit_group();
-  }
-}
-
-__device__ __forceinline__ void f32_epilogue(const VocabGemm& G, uint32_t (&r)[4][32], int col0, int warp_row0,
-                                             int split, uint32_t staging, int lane) {
+__device__ __forceinline__ void f32_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0,
+                                             int warp_row0, int split, uint32_t staging, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (col0 + 32 * i >= G.N) break;
+    if (col0 + 32 * i >= P.N) break;
     const uint32_t buf = staging + 4096u * (i & 1);
     if (lane == 0) {
       if (i == 0)
@@ -235,23 +299,38 @@ __device__ __forceinline__ void f32_epilogue(const VocabGemm& G, uint32_t (&r)[4
     }
     __syncwarp();
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-      st_shared_16(piece(buf, lane, p), r[i][4 * p], r[i][4 * p + 1], r[i][4 * p + 2], r[i][4 * p + 3]);
+    for (int p = 0; p < 8; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(alpha * __uint_as_float(r[i][4 * p + k]));
+      st_shared_16(piece(buf, lane, p), w[0], w[1], w[2], w[3]);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (G.add)
-        tma_add_3d(&G.map_out, buf, col0 + 32 * i, warp_row0, split);
+      if (P.add)
+        tma_add_3d(&P.map_out, buf, col0 + 32 * i, warp_row0, split);
       else
-        tma_store_3d(&G.map_out, buf, col0 + 32 * i, warp_row0, split);
+        tma_store_3d(&P.map_out, buf, col0 + 32 * i, warp_row0, split);
       bulk_commit_group();
     }
   }
 }
 
-template <int MODE, bool A_MN, bool B_MN>
+// The parts of a tile's product that differ between the two kernels.
+__device__ __forceinline__ const CUtensorMap* operand_map(const VocabLogits& G, int, bool b) { return b ? &G.map_b : &G.map_a; }
+__device__ __forceinline__ const CUtensorMap* operand_map(const VocabGrad& G, int p, bool b) {
+  return b ? &G.p[p].map_b : &G.p[p].map_a;
+}
+__device__ __forceinline__ bool a_is_mn(const VocabLogits&, int) { return false; }
+__device__ __forceinline__ bool a_is_mn(const VocabGrad& G, int p) { return G.p[p].a_mn != 0; }
+
+// Args: VocabLogits (B is vocabulary x width, K-contiguous) or VocabGrad (B is
+// N-contiguous).
+template <class Args, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    vocab_gemm_kernel(const __grid_constant__ VocabGemm G) {
+    vocab_gemm_kernel(const __grid_constant__ Args G) {
+  constexpr bool LOGITS = !B_MN;
   constexpr int kProducerBWarp = 2 + EPI;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -297,21 +376,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int n_tiles = G.tiles_m * G.tiles_n * G.splits;
 
   if ((warp == 0 || warp == kProducerBWarp) && lane == 0) {
     // ------------------------------------ producers (A: warp 0, B: the last)
     const bool is_b = warp != 0;
-    const bool mn = is_b ? B_MN : A_MN;
-    const CUtensorMap* map = is_b ? &G.map_b : &G.map_a;
-    tma_prefetch_map(map);
     const uint32_t dst_off = is_b ? HALF_BYTES : 0u;
-    int stage = 0;
+    int stage = 0, filled = 0;
     uint32_t phase = 0;
-    int fills[STAGES] = {};
     bool ok = true;
-    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
-      const Tile T = tile_at(G, t);
+    for (int i = 0; ok; ++i) {
+      const Tile T = tile_at(G, pair, n_pairs, i);
+      if (T.product < 0) break;
+      const CUtensorMap* map = operand_map(G, T.product, is_b);
+      const bool mn = is_b ? B_MN : a_is_mn(G, T.product);
       const int row0 = (is_b ? T.n0 : T.m0) + 128 * static_cast<int>(rank);
       for (int kb = T.kb0; kb < T.kb1; ++kb) {
         if (!mbar_wait_bounded_cluster(empty(stage), phase ^ 1u, abort_flag, G.err, kErrTimeoutProducer)) {
@@ -320,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint32_t leader_full = mapa_shared(full(stage), 0);
         if (leader) mbar_expect_tx(full(stage), 2 * HALF_BYTES);
-        ++fills[stage];
+        ++filled;
         const uint32_t dst = ring + stage * STAGE_BYTES + dst_off;
         if (!mn) {
           tma_load_3d_pair(dst, map, leader_full, kb * BK, row0, 0);
@@ -335,26 +412,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && leader) {
-      // The leader's barriers count both CTAs' bytes: let every armed phase
-      // land before the pair tears down.
-      for (int s = 0; s < STAGES; ++s) {
-        if (fills[s] > 0) {
-          volatile int no_abort = 0;
-          mbar_wait_bounded_cluster(full(s), static_cast<uint32_t>(fills[s] - 1) & 1u, &no_abort, nullptr, 0,
-                                    100000000ull);
-        }
+      // The leader's barriers count both CTAs' bytes: let every armed phase land
+      // before the pair tears down.  Stage s was armed ceil((filled - s) / STAGES) times.
+      for (int s = 0; s < STAGES && s < filled; ++s) {
+        volatile int no_abort = 0;
+        const int uses = (filled - s + STAGES - 1) / STAGES;
+        mbar_wait_bounded_cluster(full(s), static_cast<uint32_t>(uses - 1) & 1u, &no_abort, nullptr, 0, 100000000ull);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (leader only)
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(TILE, TILE, A_MN, B_MN);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       int use = 0;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs, ++use) {
-        const Tile T = tile_at(G, t);
+      for (; ok; ++use) {
+        const Tile T = tile_at(G, pair, n_pairs, use);
+        if (T.product < 0) break;
+        const bool a_mn = a_is_mn(G, T.product);
+        const uint32_t idesc = idesc_bf16_f32(TILE, TILE, a_mn, B_MN);
         if (!mbar_wait_bounded_cluster(tempty(use & 1), (static_cast<uint32_t>(use >> 1) & 1u) ^ 1u, abort_flag, G.err,
                                        kErrTimeoutMma))
           break;
@@ -370,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sb = sa + HALF_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = A_MN ? desc_mn(sa, kk) : desc_k(sa, kk);
+            const uint64_t ad = a_mn ? desc_mn(sa, kk) : desc_k(sa, kk);
             const uint64_t bd = B_MN ? desc_mn(sb, kk) : desc_k(sb, kk);
             umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != T.kb0 || kk != 0) ? 1u : 0u);
           }
@@ -394,36 +471,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;
     const uint32_t my_staging = staging + static_cast<uint32_t>(warp - 2) * kStaging;
     int use = 0;
-    for (int t = pair; t < n_tiles; t += n_pairs, ++use) {
-      const Tile T = tile_at(G, t);
+    float alpha = 1.f;
+    if constexpr (!LOGITS) alpha = G.alpha ? __ldg(G.alpha) : 1.f;
+    for (;; ++use) {
+      const Tile T = tile_at(G, pair, n_pairs, use);
+      if (T.product < 0) break;
       const int acc = use & 1;
+      const int warp_row0 = T.m0 + 128 * static_cast<int>(rank) + 32 * quarter;
+      const int col0 = T.n0 + 128 * half;
+      int target = -1, rows, cols;
+      if constexpr (LOGITS) {
+        rows = G.M;
+        cols = G.N;
+        bool bad = false;
+        if (warp_row0 + lane < rows) target = load_id(G.targets, warp_row0 + lane, &bad);
+      } else {
+        rows = G.p[T.product].M;
+        cols = G.p[T.product].N;
+      }
       if (!mbar_wait_bounded_cluster(tfull(acc), static_cast<uint32_t>(use >> 1) & 1u, abort_flag, G.err,
                                      kErrTimeoutEpilogue))
         break;
       tc_fence_after();
-      const int warp_row0 = T.m0 + 128 * static_cast<int>(rank) + 32 * quarter;
-      const int col0 = T.n0 + 128 * half;
-      const bool any = warp_row0 < G.M && col0 < G.N;  // warp-uniform
-      uint32_t r[4][32];
-      if (any)
-        load_columns(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * TILE + 128 * half),
-                     r);
-      // The registers hold the accumulator: the next tile may use the TMEM.
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader)
-          mbar_arrive(tempty(acc));
-        else
-          mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+      const uint32_t t_lane =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * TILE + 128 * half);
+      // Hands the accumulator back: its columns have been read.
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(tempty(acc));
+          else
+            mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+        }
+      };
+      if (warp_row0 >= rows || col0 >= cols) {  // warp-uniform
+        release();
+        continue;
       }
-      if (!any) continue;
-      if (MODE == kVgLogits)
-        logits_epilogue(G, r, warp_row0 + lane, col0, warp_row0, my_staging, lane);
-      else if (MODE == kVgBf16)
-        bf16_epilogue(G, r, col0, warp_row0, my_staging, lane);
-      else
-        f32_epilogue(G, r, col0, warp_row0, T.split, my_staging, lane);
+      if constexpr (LOGITS) {
+        logits_epilogue(G, t_lane, warp_row0 + lane, target, col0, warp_row0, my_staging, lane, release);
+      } else {
+        const VgProduct& P = G.p[T.product];
+        uint32_t r[4][32];
+        load_columns(t_lane, r);
+        release();
+        if (P.out_bf16)
+          bf16_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);
+        else
+          f32_epilogue(P, r, alpha, col0, warp_row0, T.split, my_staging, lane);
+      }
     }
     if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
@@ -438,36 +536,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int MODE, bool A_MN, bool B_MN>
-cudaError_t launch_variant(const VocabGemm& G, int n_pairs, cudaStream_t st) {
+template <class Args, bool B_MN>
+cudaError_t launch(const Args& G, int64_t tiles, int n_pairs, cudaStream_t st) {
   static unsigned long long attr_mask = 0;
   if (attr_needed_on_current_device(&attr_mask)) {
-    cudaError_t e = cudaFuncSetAttribute(vocab_gemm_kernel<MODE, A_MN, B_MN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    cudaError_t e = cudaFuncSetAttribute(vocab_gemm_kernel<Args, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
     attr_note_current_device(&attr_mask);
   }
-  const int64_t tiles = static_cast<int64_t>(G.tiles_m) * G.tiles_n * G.splits;
+  if (tiles <= 0 || n_pairs <= 0) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < n_pairs ? tiles : n_pairs);
-  vocab_gemm_kernel<MODE, A_MN, B_MN><<<2 * pairs, kThreads, kSmem, st>>>(G);
+  vocab_gemm_kernel<Args, B_MN><<<2 * pairs, kThreads, kSmem, st>>>(G);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_vocab_gemm(int mode, bool a_mn, bool b_mn, const VocabGemm& G, int n_pairs, cudaStream_t st) {
-  if (G.M <= 0 || G.N <= 0 || n_pairs <= 0) return cudaErrorInvalidValue;
-  if (mode == kVgLogits && !a_mn && !b_mn) return launch_variant<kVgLogits, false, false>(G, n_pairs, st);
-  if (mode == kVgBf16 && !a_mn && b_mn) return launch_variant<kVgBf16, false, true>(G, n_pairs, st);
-  if (mode == kVgBf16 && a_mn && b_mn) return launch_variant<kVgBf16, true, true>(G, n_pairs, st);
-  if (mode == kVgF32 && !a_mn && b_mn) return launch_variant<kVgF32, false, true>(G, n_pairs, st);
-  if (mode == kVgF32 && a_mn && b_mn) return launch_variant<kVgF32, true, true>(G, n_pairs, st);
-  return cudaErrorInvalidValue;  // not built
+cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st) {
+  return launch<VocabLogits, false>(G, static_cast<int64_t>(G.tiles_m) * G.tiles_n, n_pairs, st);
+}
+
+cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st) {
+  return launch<VocabGrad, true>(G, static_cast<int64_t>(G.n_units[0]) + G.n_units[1], n_pairs, st);
 }
 
 // CTA pairs that can be resident at once.
 int vocab_gemm_max_pairs() {
-  auto kernel = vocab_gemm_kernel<kVgLogits, false, false>;
+  auto kernel = vocab_gemm_kernel<VocabLogits, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess) {
     cudaGetLastError();
     return 0;

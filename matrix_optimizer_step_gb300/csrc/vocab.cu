@@ -153,22 +153,29 @@ bool tma_rows(const void* p, int64_t ld, int elem) { return aligned16(p) && ld *
 
 constexpr int kVgTile = 256;
 
-// Parts that the K axis of an M x N product is cut into: few output tiles leave
-// pairs idle, and every part costs a pass of its fp32 partial through memory.
-// Unit: one k-block of one tile (256 x 256 x 64, about 0.27 us on a pair);
-// 12 units is what a tile's pipeline fill and epilogue measured, and 24 KB
-// of partial traffic take a unit at the copy rate.
-int choose_splits(int64_t m, int64_t n, int64_t k, int pairs, bool need_partial) {
-  const int64_t tiles = ((m + kVgTile - 1) / kVgTile) * ((n + kVgTile - 1) / kVgTile);
+int64_t tiles_of(int64_t n) { return (n + kVgTile - 1) / kVgTile; }
+
+// Costs in k-blocks of one 256 x 256 tile (about 0.27 us on a pair): what a
+// tile adds to its main loop, a further launch, and the way of a partial's
+// bytes through memory (written, read).
+constexpr double kTileCost = 6.0, kLaunchCost = 12.0, kPartialBytesPerUnit = 1.8e6;
+
+// Parts that the K axis of an M x N product is cut into.  Few output tiles
+// leave pairs idle, and `other` k-blocks of further tiles share the launch;
+// every part costs a pass of its fp32 partial through memory.
+int choose_splits(int64_t m, int64_t n, int64_t k, double other, int pairs, bool need_partial) {
+  const int64_t tiles = tiles_of(m) * tiles_of(n);
   const int64_t kb = (k + 63) / 64;
-  if (tiles >= 4 * pairs) return 1;
   double best = 0.0;
   int parts = 1;
   for (int s = 1; s <= 64 && s <= kb; ++s) {
-    const int64_t waves = (tiles * s + pairs - 1) / pairs;
-    double cost = static_cast<double>(waves) * (static_cast<double>((kb + s - 1) / s) + 12.0);
-    if (s > 1 || need_partial) cost += 10.0 + static_cast<double>(m) * static_cast<double>(n) * 4.0 * (2.0 * s + 1.0) / 1.8e6;
-    if (s == 1 || cost < best * 0.95) {
+    const double unit = static_cast<double>((kb + s - 1) / s) + kTileCost;
+    const double units = static_cast<double>(tiles * s);
+    // The pairs finish together, but not before the longest column of whole units.
+    const double waves = std::ceil(units / pairs);
+    double cost = other > 0 ? std::max((units * unit + other) / pairs, std::max(1.0, std::floor(units / pairs)) * unit) : waves * unit;
+    if (s > 1 || need_partial) cost += kLaunchCost + static_cast<double>(m) * static_cast<double>(n) * 4.0 * (2.0 * s + 1.0) / kPartialBytesPerUnit;
+    if (s == 1 || cost < best * 0.97) {
       best = cost;
       parts = s;
     }
@@ -176,75 +183,53 @@ int choose_splits(int64_t m, int64_t n, int64_t k, int pairs, bool need_partial)
   return parts;
 }
 
-struct Product {
-  int64_t m, n, k;
-  bool a_mn;
-  const void* a;
-  int64_t ld_a;  // rows x inner: m x k (or k x m when a_mn)
-  const void* b;
-  int64_t ld_b;  // k x n
-  void* out;
-  int64_t ld_out;
-  bool out_bf16;
-  bool keep;     // add to what `out` holds
-  // fp32 partials, or null where the product writes `out` itself
-  float* part;
-  int64_t ld_part;
-  int splits;
-  bool first, last;  // first and last pass over the rows (dW)
-};
-
 int encode_2d(EncodeTiledFn enc, CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t ld, uint32_t box_inner,
               uint32_t box_rows) {
   return make_map_typed(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, inner, rows, 1, ld, rows * ld, box_inner, box_rows);
 }
 
-void set_tiles(VocabGemm& G, int64_t m, int64_t n, int64_t k, int splits) {
-  G.M = static_cast<int32_t>(m);
-  G.N = static_cast<int32_t>(n);
-  G.K = static_cast<int32_t>(k);
-  G.tiles_m = static_cast<int32_t>((m + kVgTile - 1) / kVgTile);
-  G.tiles_n = static_cast<int32_t>((n + kVgTile - 1) / kVgTile);
-  G.kb_total = static_cast<int32_t>((k + 63) / 64);
-  G.splits = splits;
-  G.group_m = 8;
+// A gradient's way out: written by its product, or as fp32 partials that a
+// further kernel joins (several parts of K, rows that TMA cannot write, two
+// halves to fold, or a bf16 sum over passes or onto what is there).
+struct Target {
+  void* out = nullptr;
+  int64_t ld = 0;
+  bool bf16 = false, keep = false;
+  int splits = 1;
+  float* part = nullptr;
+  int64_t ld_part = 0;
+};
+
+bool writes_out(const void* out, int64_t ld, bool bf16, bool keep, bool one_pass) {
+  return tma_rows(out, ld, bf16 ? 2 : 4) && (!bf16 || (one_pass && !keep));
 }
 
-int run_product(dmuon_context* ctx, EncodeTiledFn enc, const Product& P, cudaStream_t s) {
-  VocabGemm G = {};
-  set_tiles(G, P.m, P.n, P.k, P.splits);
-  G.err = static_cast<int*>(ctx->err.p);
-  if (P.a_mn)
-    DM_TRY(encode_2d(enc, &G.map_a, P.a, P.m, P.k, P.ld_a, 64, 64));
+// Product D (m x n) = A B into T; `first`: first pass over the rows.
+int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_t k, bool a_mn, const void* a, int64_t ld_a,
+                   const void* b, int64_t ld_b, const Target& T, int splits, int group_m, bool first) {
+  P->M = static_cast<int32_t>(m);
+  P->N = static_cast<int32_t>(n);
+  P->tiles_m = static_cast<int32_t>(tiles_of(m));
+  P->tiles_n = static_cast<int32_t>(tiles_of(n));
+  P->splits = splits;
+  P->kb_total = static_cast<int32_t>((k + 63) / 64);
+  P->group_m = group_m;
+  P->a_mn = a_mn;
+  if (a_mn)
+    DM_TRY(encode_2d(enc, &P->map_a, a, m, k, ld_a, 64, 64));
   else
-    DM_TRY(encode_2d(enc, &G.map_a, P.a, P.k, P.m, P.ld_a, 64, 128));
-  DM_TRY(encode_2d(enc, &G.map_b, P.b, P.n, P.k, P.ld_b, 64, 64));
-  int mode = kVgF32;
-  if (P.part) {
-    DM_TRY(make_map_typed(enc, &G.map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, P.part, P.n, P.m, P.splits, P.ld_part,
-                          P.m * P.ld_part, 32, 32));
-    G.add = P.first ? 0 : 1;
-  } else if (P.out_bf16) {
-    mode = kVgBf16;
-    DM_TRY(encode_2d(enc, &G.map_out, P.out, P.n, P.m, P.ld_out, 64, 32));
-  } else {
-    DM_TRY(make_map_typed(enc, &G.map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, P.out, P.n, P.m, 1, P.ld_out,
-                          P.m * P.ld_out, 32, 32));
-    G.add = P.keep || !P.first ? 1 : 0;
+    DM_TRY(encode_2d(enc, &P->map_a, a, k, m, ld_a, 64, 128));
+  DM_TRY(encode_2d(enc, &P->map_b, b, n, k, ld_b, 64, 64));
+  if (T.part) {
+    P->add = !first;
+    return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.part, n, m, splits, T.ld_part, m * T.ld_part, 32, 32);
   }
-  DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_gemm(mode, P.a_mn, true, G, ctx->vocab_pairs, s); }));
-  if (P.part && P.last)
-    DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_finish(P.part, P.ld_part, P.m * P.ld_part, P.splits, P.out, P.ld_out, P.out_bf16, P.keep, P.m,
-                              static_cast<int32_t>(P.n), s);
-    }));
-  return DMUON_OK;
-}
-
-// Whether a product of these properties may write its output itself.
-bool writes_out(const void* out, int64_t ld, bool bf16, bool keep, bool one_pass, int splits) {
-  if (splits > 1 || !tma_rows(out, ld, bf16 ? 2 : 4)) return false;
-  return bf16 ? one_pass && !keep : true;
+  if (T.bf16) {
+    P->out_bf16 = 1;
+    return encode_2d(enc, &P->map_out, T.out, n, m, T.ld, 64, 32);
+  }
+  P->add = T.keep || !first;
+  return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.out, n, m, 1, T.ld, m * T.ld, 32, 32);
 }
 
 int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
@@ -275,13 +260,23 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     rows = passes == 1 ? n : round_up((n + passes - 1) / passes, kVgTile);
   }
   const bool one_pass = rows >= n;
-  const int n_blocks = static_cast<int>((v + kCeBlock - 1) / kCeBlock);
-  const int64_t stats_ld = round_up(rows, 32);
 
-  // Operand copies: rows that are not counted must read as zeros in dW's
-  // product whatever they hold, and TMA needs rows on 16 bytes.
-  const bool copy_x = C.dw != nullptr || !tma_rows(C.x, C.ld_x, 2);
-  const bool copy_w = !tma_rows(C.w, C.ld_w, 2);
+  // Few tokens: a 256-row tile has room for d logits in two bf16 halves (value
+  // and the rounding's rest), so they come at no cost, and with as few terms in
+  // the gradients' sums one rounding would not average out.  Up to half of
+  // that, the products that read W have it as the long operand.
+  const bool halves = grads && n <= kThinRows;
+  const int64_t token_rows = halves ? 2 * n : rows;
+  const bool thin = n <= kThinRows / 2;
+  const int stats_block = thin ? kCeThinBlock : kCeBlock;
+  const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
+  int64_t stats_ld = round_up(rows, 32);
+  if (rows < 32)
+    for (stats_ld = 1; stats_ld < rows;) stats_ld *= 2;
+
+  // Operand copies: TMA needs rows on 16 bytes, and rows that are not counted
+  // must read as zeros in dW's product whatever they hold.
+  const bool copy_x = !tma_rows(C.x, C.ld_x, 2), copy_w = !tma_rows(C.w, C.ld_w, 2);
   const int64_t ld8 = round_up(d, 8), ld4 = round_up(d, 4);
   Layout L;
   const size_t off_x = copy_x ? L.take(static_cast<size_t>(n * ld8) * 2) : 0;
@@ -289,53 +284,68 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const size_t off_stats = L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float2));
   const size_t off_z = L.take(static_cast<size_t>(rows) * 4);
   const size_t off_loss = C.loss ? 0 : L.take(static_cast<size_t>(n) * 4);
-  const size_t off_norm = L.take(4);
-  size_t off_block = 0, off_rows = 0, off_dx = 0, off_dw = 0;
-  int dx_splits = 1, dw_splits = 1;
-  bool dx_part = false, dw_part = false;
+  size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
+  Target dx, dw;
   if (grads) {
-    off_block = L.take(static_cast<size_t>(rows * ld_block) * 2);
+    off_block = L.take(static_cast<size_t>(token_rows * ld_block) * 2);
     off_rows = L.take(static_cast<size_t>(rows) * sizeof(CeRow));
-    if (C.dx) {
-      dx_splits = choose_splits(rows, d, v, pairs, !writes_out(C.dx, C.ld_dx, dx_bf16, false, true, 1));
-      dx_part = !writes_out(C.dx, C.ld_dx, dx_bf16, false, true, dx_splits);
-      if (dx_part) off_dx = L.take(static_cast<size_t>(dx_splits * rows * ld4) * 4);
-    }
+    off_alpha = L.take(4);
+    bool dx_part = false, dw_part = false;
     if (C.dw) {
-      dw_splits = choose_splits(v, d, rows, pairs, !writes_out(C.dw, C.ld_dw, dw_bf16, add_dw, one_pass, 1));
-      dw_part = !writes_out(C.dw, C.ld_dw, dw_bf16, add_dw, one_pass, dw_splits);
-      if (dw_part) off_dw = L.take(static_cast<size_t>(dw_splits * v * ld4) * 4);
+      off_masked = L.take(static_cast<size_t>(token_rows * ld8) * 2);
+      dw.out = C.dw;
+      dw.ld = C.ld_dw;
+      dw.bf16 = dw_bf16;
+      dw.keep = add_dw;
+      dw_part = !writes_out(C.dw, C.ld_dw, dw_bf16, add_dw, one_pass);
+      dw.splits = choose_splits(v, d, token_rows, 0.0, pairs, dw_part);
+      dw_part = dw_part || dw.splits > 1;
+      dw.ld_part = ld4;
+      if (dw_part) off_dw = L.take(static_cast<size_t>(dw.splits * v * ld4) * 4);
     }
+    if (C.dx) {
+      dx.bf16 = dx_bf16;
+      dx.ld = C.ld_dx;
+      dx_part = halves || !writes_out(C.dx, C.ld_dx, dx_bf16, false, true);
+      if (thin) {
+        // Tiles of 128 columns; parts of the vocabulary for a few tiles per SM.
+        const int64_t tiles = (d + 127) / 128, kb = (v + 63) / 64;
+        int64_t parts = (2 * ctx->num_sms + tiles - 1) / tiles;
+        // Whole waves of CTAs, but at least 8 k-blocks in a part.
+        if (parts * tiles > ctx->num_sms) parts = std::max<int64_t>(1, (2 * ctx->num_sms) / tiles);
+        dx.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(parts, kb / 8)));
+      } else {
+        const double other = C.dw ? static_cast<double>(tiles_of(v) * tiles_of(d) * dw.splits) *
+                                        (static_cast<double>((token_rows + 63) / 64) / dw.splits + kTileCost)
+                                  : 0.0;
+        dx.splits = choose_splits(token_rows, d, v, other, pairs, dx_part);
+      }
+      dx_part = dx_part || dx.splits > 1;
+      dx.ld_part = ld4;
+      if (dx_part) off_dx = L.take(static_cast<size_t>(dx.splits * token_rows * ld4) * 4);
+    }
+    DM_TRY(vocab_workspace(ctx, L.bytes, s));
+    char* ws = static_cast<char*>(ctx->vocab_ws.p);
+    if (dx_part) dx.part = reinterpret_cast<float*>(ws + off_dx);
+    if (dw_part) dw.part = reinterpret_cast<float*>(ws + off_dw);
+  } else {
+    DM_TRY(vocab_workspace(ctx, L.bytes, s));
   }
-  DM_TRY(vocab_workspace(ctx, L.bytes, s));
   char* ws = static_cast<char*>(ctx->vocab_ws.p);
+  int* err = static_cast<int*>(ctx->err.p);
   const IdList ids{C.targets, C.target_dtype == DMUON_INDEX_I64, static_cast<int32_t>(v)};
-  auto ids_from = [&](int64_t row) {
-    IdList q = ids;
-    q.p = static_cast<const char*>(ids.p) + row * (ids.is64 ? 8 : 4);
-    return q;
-  };
   const uint16_t* x = C.x;
   const uint16_t* w = C.w;
   int64_t ld_x = C.ld_x, ld_w = C.ld_w;
-  float* inv_norm = grads && mean ? reinterpret_cast<float*>(ws + off_norm) : nullptr;
   if (copy_x) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + off_x);
-    DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_copy(C.x, C.ld_x, to, ld8, n, static_cast<int32_t>(d), &ids, C.weights, inv_norm, s);
-    }));
+    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.x, C.ld_x, to, ld8, n, static_cast<int32_t>(d), s); }));
     x = to;
     ld_x = ld8;
-  } else if (inv_norm) {
-    DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_copy(nullptr, 0, nullptr, 0, n, static_cast<int32_t>(d), &ids, C.weights, inv_norm, s);
-    }));
   }
   if (copy_w) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + off_w);
-    DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_copy(C.w, C.ld_w, to, ld8, v, static_cast<int32_t>(d), nullptr, nullptr, nullptr, s);
-    }));
+    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.w, C.ld_w, to, ld8, v, static_cast<int32_t>(d), s); }));
     w = to;
     ld_w = ld8;
   }
@@ -344,23 +354,55 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   float* loss = C.loss ? C.loss : reinterpret_cast<float*>(ws + off_loss);
   uint16_t* block = reinterpret_cast<uint16_t*>(ws + off_block);
   CeRow* row_info = reinterpret_cast<CeRow*>(ws + off_rows);
+  float* alpha = reinterpret_cast<float*>(ws + off_alpha);
+  uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
+  const float scale_log2 = C.logit_scale * 1.4426950408889634f;
 
   for (int64_t r0 = 0; r0 < n; r0 += rows) {
     const int64_t nr = std::min(rows, n - r0);
     const bool first = r0 == 0, last = r0 + rows >= n;
-    VocabGemm G = {};
-    set_tiles(G, nr, v, d, 1);
-    G.err = static_cast<int*>(ctx->err.p);
-    DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
-    DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
-    if (grads) DM_TRY(encode_2d(enc, &G.map_out, block, v, nr, ld_block, 64, 32));
-    G.logit_scale_log2 = C.logit_scale * 1.4426950408889634f;
-    G.store_logs = grads;
-    G.stats = stats;
-    G.stats_ld = stats_ld;
-    G.target_z = target_z;
-    G.targets = ids_from(r0);
-    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_gemm(kVgLogits, false, false, G, pairs, s); }));
+    const int64_t k_rows = halves ? 2 * nr : nr;  // rows of d logits
+    IdList here = ids;
+    here.p = static_cast<const char*>(ids.p) + r0 * (ids.is64 ? 8 : 4);
+    if (thin) {
+      VocabThin G = {};
+      G.M = static_cast<int32_t>(v);
+      G.tokens = static_cast<int32_t>(nr);
+      G.np = static_cast<int32_t>(round_up(nr, 16));
+      G.tiles_m = static_cast<int32_t>((v + 127) / 128);
+      G.splits = 1;
+      G.kb_total = static_cast<int32_t>((d + 63) / 64);
+      G.err = err;
+      DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
+      DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
+      G.logit_scale_log2 = scale_log2;
+      G.logs = grads ? block : nullptr;
+      G.ld_logs = ld_block;
+      G.stats = stats;
+      G.stats_ld = stats_ld;
+      G.target_z = target_z;
+      G.targets = here;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
+    } else {
+      VocabLogits G = {};
+      G.M = static_cast<int32_t>(nr);
+      G.N = static_cast<int32_t>(v);
+      G.tiles_m = static_cast<int32_t>(tiles_of(nr));
+      G.tiles_n = static_cast<int32_t>(tiles_of(v));
+      G.kb_total = static_cast<int32_t>((d + 63) / 64);
+      G.group_m = 8;
+      G.err = err;
+      DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
+      DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
+      if (grads) DM_TRY(encode_2d(enc, &G.map_out, block, v, nr, ld_block, 64, 32));
+      G.logit_scale_log2 = scale_log2;
+      G.store_logs = grads;
+      G.stats = stats;
+      G.stats_ld = stats_ld;
+      G.target_z = target_z;
+      G.targets = here;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_logits(G, pairs, s); }));
+    }
 
     CeRows R = {};
     R.stats = stats;
@@ -372,59 +414,79 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     R.target_z = target_z;
     R.targets = ids;
     R.weights = C.weights;
-    R.inv_norm = inv_norm;
-    R.grad_scale = C.grad_scale * C.logit_scale;
+    R.x = x + r0 * ld_x;
+    R.w = w;
+    R.ld_x = ld_x;
+    R.ld_w = ld_w;
+    R.dim = static_cast<int32_t>(d);
+    R.logit_scale_log2 = scale_log2;
     R.out = grads ? row_info : nullptr;
     R.loss = loss;
     R.lse = C.lse;
+    R.x_copy = C.dw ? masked : nullptr;
+    R.ld_copy = ld8;
+    R.copies = halves ? 2 : 1;
+    R.alpha = grads && first ? alpha : nullptr;
+    R.scale = C.grad_scale * C.logit_scale;
     R.total = last ? C.total : nullptr;
     R.mean = mean;
     R.ticket = static_cast<uint32_t*>(ctx->vocab_ticket.p);
-    R.err = static_cast<int*>(ctx->err.p);
+    R.err = err;
     DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_rows(R, s); }));
     if (!grads) continue;
 
     DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats, stats_ld, row_info, s);
+      return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_block, stats, stats_ld, row_info,
+                               halves ? nr : 0, s);
     }));
-    if (C.dx) {
-      Product P = {};
-      P.m = nr; P.n = d; P.k = v;
-      P.a = block; P.ld_a = ld_block;
-      P.b = w; P.ld_b = ld_w;
-      P.out = static_cast<char*>(C.dx) + r0 * C.ld_dx * (dx_bf16 ? 2 : 4);
-      P.ld_out = C.ld_dx;
-      P.out_bf16 = dx_bf16;
-      P.part = dx_part ? reinterpret_cast<float*>(ws + off_dx) : nullptr;
-      P.ld_part = ld4;
-      P.splits = dx_splits;
-      P.first = P.last = true;
-      DM_TRY(run_product(ctx, enc, P, s));
+    if (C.dx) dx.out = static_cast<char*>(C.dx) + r0 * C.ld_dx * (dx_bf16 ? 2 : 4);
+    VocabGrad G = {};
+    G.alpha = alpha;
+    G.err = err;
+    if (C.dx && thin) {
+      VocabThin T = {};
+      T.M = static_cast<int32_t>(d);
+      T.tokens = static_cast<int32_t>(k_rows);
+      T.np = static_cast<int32_t>(round_up(k_rows, 16));
+      T.tiles_m = static_cast<int32_t>((d + 127) / 128);
+      T.splits = dx.splits;
+      T.kb_total = static_cast<int32_t>((v + 63) / 64);
+      T.err = err;
+      DM_TRY(encode_2d(enc, &T.map_a, w, d, v, ld_w, 64, 64));
+      DM_TRY(encode_2d(enc, &T.map_b, block, v, k_rows, ld_block, 64, static_cast<uint32_t>(T.np)));
+      T.part = dx.part;
+      T.ld_part = dx.ld_part;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(false, T, ctx->num_sms, s); }));
+    } else if (C.dx) {
+      DM_TRY(encode_product(enc, &G.p[0], k_rows, d, v, false, block, ld_block, w, ld_w, dx, dx.splits, 8, true));
+      G.n_units[0] = G.p[0].tiles_m * G.p[0].tiles_n * G.p[0].splits;
     }
     if (C.dw) {
-      Product P = {};
-      P.m = v; P.n = d; P.k = nr;
-      P.a_mn = true;
-      P.a = block; P.ld_a = ld_block;
-      P.b = x + r0 * ld_x; P.ld_b = ld_x;
-      P.out = C.dw;
-      P.ld_out = C.ld_dw;
-      P.out_bf16 = dw_bf16;
-      P.keep = add_dw;
-      P.part = dw_part ? reinterpret_cast<float*>(ws + off_dw) : nullptr;
-      P.ld_part = ld4;
       // The last pass may be shorter: every part needs a k-block of its own,
-      // and its other parts already hold the earlier passes' sums.
-      P.splits = static_cast<int>(std::min<int64_t>(dw_splits, (nr + 63) / 64));
-      P.first = first;
-      P.last = false;
-      DM_TRY(run_product(ctx, enc, P, s));
-      if (dw_part && last)
-        DM_TRY(timed_launch(ctx, -1, s, [&] {
-          return launch_ce_finish(P.part, ld4, v * ld4, dw_splits, C.dw, C.ld_dw, dw_bf16, add_dw, v,
-                                  static_cast<int32_t>(d), s);
-        }));
+      // and the parts it leaves out hold the earlier passes' sums.
+      const int splits = static_cast<int>(std::min<int64_t>(dw.splits, (k_rows + 63) / 64));
+      // Short main loops are bound by the stores: whole rows of tiles then go out together.
+      DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked, ld8, dw, splits, 8, first));
+      G.n_units[1] = G.p[1].tiles_m * G.p[1].tiles_n * G.p[1].splits;
     }
+    if (G.n_units[0] > 0 && G.n_units[0] % pairs != 0 && G.n_units[1] > 0) {
+      const double u0 = static_cast<double>(G.p[0].kb_total) / G.p[0].splits + kTileCost;
+      const double u1 = static_cast<double>(G.p[1].kb_total) / G.p[1].splits + kTileCost;
+      G.extra = static_cast<int32_t>(u0 / u1 + 0.5);
+    }
+    if (G.n_units[0] + G.n_units[1] > 0)
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_grad(G, pairs, s); }));
+    if (dx.part)
+      DM_TRY(timed_launch(ctx, -1, s, [&] {
+        // The tile kernel has applied alpha already.
+        return launch_ce_finish(dx.part, dx.ld_part, k_rows * dx.ld_part, dx.splits, halves ? nr : 0, dx.out, dx.ld, dx.bf16, 0,
+                                thin ? alpha : nullptr, nr, static_cast<int32_t>(d), s);
+      }));
+    if (dw.part && last)
+      DM_TRY(timed_launch(ctx, -1, s, [&] {
+        return launch_ce_finish(dw.part, dw.ld_part, v * dw.ld_part, dw.splits, 0, C.dw, C.ld_dw, dw_bf16, add_dw, nullptr, v,
+                                static_cast<int32_t>(d), s);
+      }));
   }
   return vocab_used(ctx, s);
 }

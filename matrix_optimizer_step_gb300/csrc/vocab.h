@@ -16,72 +16,119 @@ struct IdList {
   int32_t vocab;
 };
 
-// Columns that one epilogue warp reduces: the softmax statistics of a row
-// come as one (maximum, sum) pair for each block of this many columns.
-constexpr int kCeBlock = 128;
+// Softmax statistics of a row come as one (maximum, sum) pair for each block
+// of this many vocabulary entries: what one epilogue warp reduces.
+constexpr int kCeBlock = 128;     // 256 x 256 tiles (k_vocab_gemm.cu)
+constexpr int kCeThinBlock = 32;  // few tokens (k_vocab_thin.cu)
 
-// Fixed-point logs: a logit of the block is kept as the 16-bit distance to
-// the block's maximum in units of 2^-10 octaves, cut off at 64 octaves.
+// Fixed-point logs: a logit is kept as the 16-bit distance to its block's
+// maximum in units of 2^-10 octaves, cut off at 64 octaves.
 constexpr float kCeLogUnits = 1024.f;
 
-// One product D (M x N) = A (M x K) B (K x N) of the cross entropy, on CTA
-// pairs with 256 x 256 tiles.
-enum VocabGemmMode : int {
-  kVgLogits = 0,  // softmax statistics of each row, optionally the logits' fixed-point logs
-  kVgBf16 = 1,    // D as bf16
-  kVgF32 = 2,     // D as fp32, stored or added; with splits > 1 one partial D for each split
-};
-
-struct VocabGemm {
-  CUtensorMap map_a, map_b, map_out;
-  int32_t M, N, K;
-  int32_t tiles_m, tiles_n, splits;
-  int32_t kb_total;      // 64-deep k-blocks of K
-  int32_t group_m;       // row tiles that are walked together (operand reuse in L2)
-  int32_t add;           // kVgF32: add to what `out` holds
+// Z = X W^T on 256 x 256 tiles of CTA pairs: statistics, optionally logs.
+struct VocabLogits {
+  CUtensorMap map_a, map_b, map_out;  // X, W, logs
+  int32_t M, N;                       // tokens, vocabulary
+  int32_t tiles_m, tiles_n;
+  int32_t kb_total;                   // 64-deep k-blocks
+  int32_t group_m;                    // row tiles that are walked together (operand reuse in L2)
   int* err;
-  // kVgLogits
-  float logit_scale_log2;  // logit scale times log2(e)
+  float logit_scale_log2;             // logit scale times log2(e)
   int32_t store_logs;
-  float2* stats;           // [column block][row]: maximum and sum of 2^(z - maximum), z in octaves
+  float2* stats;                      // [block][row]: maximum and sum of 2^(z - maximum), z in octaves
   int64_t stats_ld;
-  float* target_z;         // [row]: the target's z
-  IdList targets;          // of row 0 of this product
+  float* target_z;                    // [row]: the target's z
+  IdList targets;                     // of row 0 of this product
+};
+cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st);
+
+// One gradient product D (M x N) = alpha A B: B is k x n with contiguous
+// columns, A is m x k, or k x m with a_mn.
+struct VgProduct {
+  CUtensorMap map_a, map_b, map_out;
+  int32_t M, N;
+  int32_t tiles_m, tiles_n, splits;   // splits > 1: fp32 partials, one per part of K
+  int32_t kb_total;
+  int32_t group_m;
+  int32_t a_mn;
+  int32_t out_bf16;                   // else fp32
+  int32_t add;                        // fp32: add to what `out` holds
 };
 
-cudaError_t launch_vocab_gemm(int mode, bool a_mn, bool b_mn, const VocabGemm& G, int n_pairs, cudaStream_t st);
+// One launch for up to two products.  Tiles go to the pairs in turn, the
+// first product's first; the pairs that get one tile fewer of those take
+// `extra` more of the second's.
+struct VocabGrad {
+  VgProduct p[2];
+  int32_t n_units[2];
+  int32_t extra;
+  const float* alpha;
+  int* err;
+};
+cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st);
 int vocab_gemm_max_pairs();
 
+// The products that read W, for few tokens (k_vocab_thin.cu).
+constexpr int kThinRows = 128;        // token rows at most
+struct VocabThin {
+  CUtensorMap map_a, map_b;           // W; X or dZ
+  int32_t M;                          // vocabulary (logits) or width (dX)
+  int32_t tokens, np;                 // token rows, and those rounded up to 16
+  int32_t tiles_m, splits, kb_total;
+  int* err;
+  // logits
+  float logit_scale_log2;
+  uint16_t* logs;                     // [token][ld_logs], or null
+  int64_t ld_logs;
+  float2* stats;
+  int64_t stats_ld;
+  float* target_z;
+  IdList targets;
+  // dX: fp32 partials [split][token][ld_part]
+  float* part;
+  int64_t ld_part;
+};
+cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaStream_t st);
+
 // ---- k_vocab_ce.cu
-// Copy of `rows` x `cols` bf16 values into rows of pitch ld_dst (the columns
-// up to ld_dst are zeros).  With targets, rows whose target is not counted
-// become zeros; with norm, block 0 also writes 1 / (sum of the counted weights).
+// Copy of rows x cols bf16 values into rows of pitch ld_dst (a multiple of 8;
+// the columns up to ld_dst become zeros).
 cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
-                           int32_t cols, const IdList* targets, const float* weights, float* inv_norm,
-                           cudaStream_t st);
+                           int32_t cols, cudaStream_t st);
 
 // Per-row outcome of the statistics, as the gradient pass reads it.
 struct CeRow {
   float lse2;       // log2 of the softmax's sum, in octaves
-  float coef;       // factor of (p - onehot) in d logits, 0 for a row that is not counted
-  float target_dz;  // coef * (p_target - 1)
+  float weight;     // 0 for a row that is not counted
+  float target_dz;  // weight * (p_target - 1)
   int32_t target;   // -1: none
 };
 
 struct CeRows {
   const float2* stats;
   int64_t stats_ld;
-  int32_t n_blocks;        // column blocks
+  int32_t n_blocks;        // vocabulary blocks
   int64_t row0, rows;      // rows of this pass, as part of n
   int64_t n;
-  const float* target_z;   // of row row0
+  const float* target_z;   // of row row0: the target's z as the product summed it
   IdList targets;          // of row 0
   const float* weights;    // of row 0, or null
-  const float* inv_norm;   // or null: 1
-  float grad_scale;        // upstream factor times logit scale
+  const uint16_t* x;       // of row row0
+  const uint16_t* w;
+  int64_t ld_x, ld_w;
+  int32_t dim;
+  float logit_scale_log2;
   CeRow* out;              // of row row0, or null
   float* loss;             // of row 0, never null
   float* lse;              // of row 0, or null
+  // dW's operand: this pass's rows of x, zeros where the row is not counted; twice
+  // (copies rows apart) for a gradient in two halves.  Null: not wanted.
+  uint16_t* x_copy;
+  int64_t ld_copy;
+  int32_t copies;
+  // Factor of both gradients, written by the first pass: scale [/ sum(weight)].  Null: not wanted.
+  float* alpha;
+  float scale;
   // The last pass sums the losses: total = sum(weight * loss) [/ sum(weight)].
   float* total;            // null: not in this pass
   int32_t mean;
@@ -90,15 +137,17 @@ struct CeRows {
 };
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st);
 
-// Fixed-point logs -> bf16 d logits, in place.
-cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, const float2* stats,
-                              int64_t stats_ld, const CeRow* row_info, cudaStream_t st);
+// Fixed-point logs -> bf16 d logits (before the factor alpha), in place.  With
+// lo_rows > 0 the rounding's rest goes, as bf16, to the row lo_rows below.
+cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_block,
+                              const float2* stats, int64_t stats_ld, const CeRow* row_info, int64_t lo_rows,
+                              cudaStream_t st);
 
 // out (rows x cols, pitch ld_out) = sum over `parts` partials (pitch ld_part,
-// part_stride elements apart) [+ out].
-cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, void* out,
-                             int64_t ld_out, int out_bf16, int accumulate, int64_t rows, int32_t cols,
-                             cudaStream_t st);
+// part_stride elements apart), with fold > 0 of their rows r and r + fold [+ out].
+cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, int64_t fold,
+                             void* out, int64_t ld_out, int out_bf16, int accumulate, const float* alpha,
+                             int64_t rows, int32_t cols, cudaStream_t st);
 
 // ---- k_embed.cu
 struct EmbedForward {

@@ -32,42 +32,52 @@ class VocabOps:
         self.ctx = capi.dmuon_context_create(self.device)
         self._lib = capi.load_library()
 
+    # These run on every call: the checks are ordered so that a good tensor
+    # takes few attribute reads (a small lookup is bound by this code).
     def _matrix(self, t, name, dtypes, rows=None, cols=None):
         """(pointer, row pitch) of a checked matrix."""
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != self.device:
-            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-        if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'*' if rows is None else rows}, "
+        self._on_device(t, name, dtypes)
+        shape = t.shape
+        if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected ({'*' if rows is None else rows}, "
                              f"{'*' if cols is None else cols})")
-        if t.shape[1] > 1 and t.stride(1) != 1:
+        pitch, step = t.stride()
+        if step != 1 and shape[1] > 1:
             raise ValueError(f"{name} must have contiguous rows")
-        pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-        if pitch < t.shape[1]:
+        if shape[0] <= 1:
+            pitch = shape[1]
+        elif pitch < shape[1]:
             raise ValueError(f"{name} has overlapping rows (stride {pitch})")
         return t.data_ptr(), pitch
 
     def _list(self, t, name, dtypes, n):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != self.device:
-            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+        self._on_device(t, name, dtypes)
         if t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name}: expected {n} contiguous elements")
         return t.data_ptr()
 
+    def _on_device(self, t, name, dtypes):
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.device or not t.is_cuda:
+            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+
+    def _call(self, fn, args, stream):
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        status = fn(self.ctx, ctypes.byref(args), getattr(stream, "cuda_stream", stream))
+        if status:
+            capi._check(status)
+
     # ----------------------------------------------------------- embedding
     def _embed(self, fn, ids, table, rows, scale, flags, stream):
-        a = capi.DmuonEmbed()
-        a.table, a.ld_table = self._matrix(table, "table", _FLOATS)
-        a.vocab, a.dim = table.shape
-        a.n_tokens = ids.numel()
-        a.ids = self._list(ids, "ids", _INDEX, a.n_tokens)
-        a.rows, a.ld_rows = self._matrix(rows, "rows", _FLOATS, a.n_tokens, a.dim)
-        a.id_dtype, a.table_dtype, a.row_dtype = _INDEX[ids.dtype], _FLOATS[table.dtype], _FLOATS[rows.dtype]
-        a.scale, a.flags = scale, flags
-        capi._check(fn(self.ctx, ctypes.byref(a), capi._stream_handle(stream)))
+        table_p, ld_table = self._matrix(table, "table", _FLOATS)
+        vocab, dim = table.shape
+        n = ids.numel()
+        rows_p, ld_rows = self._matrix(rows, "rows", _FLOATS, n, dim)
+        self._call(fn, capi.DmuonEmbed(n, vocab, dim, self._list(ids, "ids", _INDEX, n), table_p, rows_p, ld_table,
+                                       ld_rows, _INDEX[ids.dtype], _FLOATS[table.dtype], _FLOATS[rows.dtype], scale, flags),
+                   stream)
 
     def embed(self, ids, table, out=None, scale=1.0, stream=None):
         """out[i] = scale * table[ids[i]] (zeros for ids below zero); returns
@@ -124,7 +134,7 @@ class VocabOps:
         a.target_dtype = _INDEX[targets.dtype]
         a.logit_scale, a.grad_scale = logit_scale, grad_scale
         a.flags = (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0)
-        capi._check(self._lib.dmuon_cross_entropy(self.ctx, ctypes.byref(a), capi._stream_handle(stream)))
+        self._call(self._lib.dmuon_cross_entropy, a, stream)
         return loss
 
     # ---------------------------------------------------------------- misc
