@@ -16,6 +16,7 @@ enum : int {
   kErrTimeoutEpilogue = 3,
   kErrTimeoutDrain = 4,
   kErrTimeoutSelftest = 5,
+  kErrTimeoutMailbox = 7,
   kErrBadIndex = 6,  // a token id or target past the vocabulary (the entry was skipped)
 };
 

@@ -47,6 +47,8 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int col
 template <bool VEC>
 __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
                                                       int64_t rows, int cols) {
+  pdl_launch();
+  pdl_wait();
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps)
     copy_row<VEC>(src + row * ld_src, dst + row * ld_dst, cols, static_cast<int>(ld_dst), true, threadIdx.x & 31);
@@ -62,11 +64,13 @@ __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64
 //   loss = ln((rest + 2^(z_t - M)) / 2^(z_t - M)),
 // as log1p where the target holds more than half of the sum.
 //
-// A block takes up to 32 rows and its 32 warps share their vocabulary blocks:
-// with fewer rows than lanes, a warp's lanes also take several blocks at once.
-// Then warp w finishes row w.  All joins run in a fixed order.  The blocks after
-// those copy dW's operand.  The last of the row blocks sums the losses.
-constexpr int kRowWarps = 32;
+// A block takes `width` rows (1, or 4: then a warp reads whole 32-byte sectors
+// of pairs) and its 8 warps share their vocabulary blocks and their dot
+// products; what is left is a chain of memory latencies, so each is taken by
+// as many threads as there are.  All joins run in a fixed order.  The blocks
+// after those copy dW's operand.  The last of the row blocks joins the blocks'
+// sums of losses and weights.
+constexpr int kRowWarps = 8;
 
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
@@ -86,13 +90,16 @@ __device__ __forceinline__ void join_lanes(float& m, float& s, int step) {
   }
 }
 
-// Dot product of two bf16 rows by one warp, in fp32; the same in every lane.
-__device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, int n, int lane) {
+// This warp's share (of `shares`) of the dot product of two bf16 rows, in fp32;
+// the same in every lane.
+__device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int start = share * 32 + lane, step = shares * 32;
+  int done = 0;
   if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
-    const int n8 = n >> 3;
+    done = n & ~7;
 #pragma unroll 4
-    for (int c = lane; c < n8; c += 32) {
+    for (int c = start; c < n >> 3; c += step) {
       const uint4 p = __ldg(reinterpret_cast<const uint4*>(a) + c), q = __ldg(reinterpret_cast<const uint4*>(b) + c);
       const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -101,11 +108,8 @@ __device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, 
         acc[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc[i]);
       }
     }
-    a += n8 * 8;
-    b += n8 * 8;
-    n &= 7;
   }
-  for (int c = lane; c < n; c += 32) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
+  for (int c = done + start; c < n; c += step) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
   float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -113,11 +117,13 @@ __device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, 
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks, int width) {
-  __shared__ float sm[kRowWarps][33], ss[kRowWarps][33];
+__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks) {
+  __shared__ float sm[kRowWarps][4], ss[kRowWarps][4], dots[kRowWarps];
   __shared__ double red[32];
   __shared__ uint32_t last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = R.width;
+  pdl_launch();
+  pdl_wait();
   if (static_cast<int>(blockIdx.x) >= row_blocks) {
     const int64_t warps = static_cast<int64_t>(gridDim.x - row_blocks) * kRowWarps;
     for (int64_t r = static_cast<int64_t>(blockIdx.x - row_blocks) * kRowWarps + warp; r < R.rows; r += warps) {
@@ -128,8 +134,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
     }
     return;
   }
-  // width: rows of a block, a power of two up to 32.
+  if (blockIdx.x == 0 && threadIdx.x < 2) R.counters[threadIdx.x] = 0u;
   const int64_t base = static_cast<int64_t>(blockIdx.x) * width;
+  const int shares = kRowWarps / width;
+  const int64_t dot_row = base + warp / shares;
+  bool bad = false;
+  const int dot_target = dot_row < R.rows ? load_id(R.targets, R.row0 + dot_row, &bad) : -1;
   {
     const int64_t r = base + (lane & (width - 1));
     const int per_warp = 32 / width, stride = kRowWarps * per_warp;
@@ -137,12 +147,19 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
     if (r < R.rows) {
       const float2* p = R.stats + r;
       int b = warp * per_warp + lane / width;
-      for (; b + 3 * stride < R.n_blocks; b += 4 * stride) {
-        float2 q[4];
+      for (; b + 7 * stride < R.n_blocks; b += 8 * stride) {
+        float2 q[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld);
+        for (int k = 0; k < 8; ++k) q[k] = __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld);
+        float top = m;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) join(m, s, q[k].x, q[k].y);
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, q[k].x);
+        if (top != __int_as_float(0xff800000)) {
+          s *= exp2f(m - top);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s += q[k].y * exp2f(q[k].x - top);
+          m = top;
+        }
       }
       for (; b < R.n_blocks; b += stride) {
         const float2 q = __ldg(p + static_cast<int64_t>(b) * R.stats_ld);
@@ -150,68 +167,87 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
       }
     }
     join_lanes(m, s, width);
-    sm[warp][lane] = m;
-    ss[warp][lane] = s;
+    if (lane < width) {
+      sm[warp][lane] = m;
+      ss[warp][lane] = s;
+    }
+  }
+  if (dot_target >= 0) {
+    const float d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
+    if (lane == 0) dots[warp] = d;
   }
   __syncthreads();
-  const int64_t r = base + warp;
-  if (warp < width && r < R.rows) {
-    float m = sm[lane][warp], s = ss[lane][warp];
-    join_lanes(m, s, 1);
-    const int64_t i = R.row0 + r;
-    bool bad = false;
-    const int t = load_id(R.targets, i, &bad);
-    if (bad && lane == 0) atomicCAS(R.err, 0, kErrBadIndex);
-    float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
-    if (t >= 0) {
-      const float z = warp_dot(R.x + r * R.ld_x, R.w + t * R.ld_w, R.dim, lane) * R.logit_scale_log2;
-      float rest = s - exp2f(R.target_z[r] - m);
-      if (rest < 0.f) rest = 0.f;  // (a NaN stays)
-      const float own = exp2f(z - m), sum = rest + own, l2 = log2f(sum);
-      loss = own > rest ? log1pf(rest / own) : kLn2 * ((m - z) + l2);
-      lse2 = m + l2;
-      share = rest / sum;
-    }
-    if (lane == 0) {
-      R.loss[i] = loss;
+  if (warp == 0) {
+    const int64_t r = base + lane;
+    double weighted = 0.0, weight_sum = 0.0;
+    if (lane < width && r < R.rows) {
+      float m = sm[0][lane], s = ss[0][lane];
+#pragma unroll
+      for (int w = 1; w < kRowWarps; ++w) join(m, s, sm[w][lane], ss[w][lane]);
+      const int64_t i = R.row0 + r;
+      const int t = load_id(R.targets, i, &bad);
+      if (bad) atomicCAS(R.err, 0, kErrBadIndex);
+      const float weight = t < 0 ? 0.f : R.weights ? __ldg(R.weights + i) : 1.f;
+      float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
+      if (t >= 0) {
+        float z = 0.f;
+        for (int k = 0; k < shares; ++k) z += dots[lane * shares + k];
+        z *= R.logit_scale_log2;
+        float rest = s - exp2f(R.target_z[r] - m);
+        if (rest < 0.f) rest = 0.f;  // (a NaN stays)
+        const float own = exp2f(z - m), sum = rest + own, l2 = log2f(sum);
+        loss = own > rest ? log1pf(rest / own) : kLn2 * ((m - z) + l2);
+        lse2 = m + l2;
+        share = rest / sum;
+      }
+      if (R.loss) R.loss[i] = loss;
       if (R.lse) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;
       if (R.out) {
         CeRow o;
         o.lse2 = lse2;
-        o.weight = t < 0 ? 0.f : R.weights ? R.weights[i] : 1.f;
-        o.target_dz = -o.weight * share;
+        o.weight = weight;
+        o.target_dz = -weight * share;
         o.target = t;
         R.out[r] = o;
       }
+      if (weight != 0.f) weighted = static_cast<double>(weight) * loss;
+      weight_sum = weight;
+    }
+    if (R.partial) {
+      for (int o = 1; o < width; o <<= 1) {
+        weighted += __shfl_xor_sync(0xffffffffu, weighted, o);
+        weight_sum += __shfl_xor_sync(0xffffffffu, weight_sum, o);
+      }
+      if (lane == 0) R.partial[R.row0 / width + blockIdx.x] = make_double2(weighted, weight_sum);
     }
   }
-  if (R.alpha && blockIdx.x == 0) {
-    double norm = 0.0;
-    bool bad = false;
-    if (R.mean) {
-      for (int64_t i = threadIdx.x; i < R.n; i += blockDim.x) norm += weight_of(R.targets, R.weights, i, &bad);
-      norm = block_sum(norm, red);
-    }
-    if (threadIdx.x == 0) *R.alpha = !R.mean ? R.scale : norm != 0.0 ? static_cast<float>(R.scale / norm) : 0.f;
+  if (!R.total && !R.alpha) return;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(R.ticket, 1u) == static_cast<uint32_t>(row_blocks) - 1u;
   }
-  if (!R.total) return;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(R.ticket, 1u) == static_cast<uint32_t>(row_blocks) - 1u;
   __syncthreads();
   if (!last) return;
   __threadfence();
+  const bool all = R.row0 + R.rows >= R.n;  // the partials of every row are there
   double sum = 0.0, norm = 0.0;
-  bool bad = false;
-  for (int64_t i = threadIdx.x; i < R.n; i += blockDim.x) {
-    const float w = weight_of(R.targets, R.weights, i, &bad);
-    if (w != 0.f) sum += static_cast<double>(w) * __ldcg(R.loss + i);
-    norm += w;
+  if (all) {
+    const int64_t parts = (R.n + width - 1) / width;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < parts; i += blockDim.x) {
+      const double2 q = __ldcg(R.partial + i);
+      sum += q.x;
+      norm += q.y;
+    }
+    sum = block_sum(sum, red);
+  } else if (R.mean) {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < R.n; i += blockDim.x) norm += weight_of(R.targets, R.weights, i, &bad);
   }
-  sum = block_sum(sum, red);
-  norm = block_sum(norm, red);
+  if (R.mean) norm = block_sum(norm, red);
   if (threadIdx.x == 0) {
-    *R.total = static_cast<float>(!R.mean ? sum : norm != 0.0 ? sum / norm : 0.0);
+    if (R.total) *R.total = static_cast<float>(!R.mean ? sum : norm != 0.0 ? sum / norm : 0.0);
+    if (R.alpha) *R.alpha = !R.mean ? R.scale : norm != 0.0 ? static_cast<float>(R.scale / norm) : 0.f;
     *R.ticket = 0u;
   }
 }
@@ -235,6 +271,8 @@ template <bool LO>
 __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block, int64_t ld, int vocab, int stats_shift,
                                                                 const float2* stats, int64_t stats_ld,
                                                                 const CeRow* row_info, int64_t lo_rows) {
+  pdl_launch();
+  pdl_wait();
   const int64_t row = blockIdx.y;
   const CeRow R = row_info[row];
   uint16_t* p = block + row * ld;
@@ -285,6 +323,8 @@ template <int VEC>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64_t ld_part, int64_t part_stride, int parts,
                                                         int64_t fold, void* out, int64_t ld_out, int out_bf16,
                                                         int accumulate, const float* alpha, int64_t rows, int cols) {
+  pdl_launch();
+  pdl_wait();
   const int64_t per_row = cols / VEC;
   const float f = alpha ? __ldg(alpha) : 1.f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * per_row;
@@ -335,28 +375,18 @@ cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, i
   const bool vec = cols % 8 == 0 && ld_src % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
   const int64_t blocks = (rows + 7) / 8;
   const int grid = static_cast<int>(blocks < 152 * 16 ? blocks : 152 * 16);
-  if (vec)
-    ce_copy_kernel<true><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols);
-  else
-    ce_copy_kernel<false><<<grid, 256, 0, st>>>(src, ld_src, dst, ld_dst, rows, cols);
-  return cudaGetLastError();
+  return launch_after(vec ? ce_copy_kernel<true> : ce_copy_kernel<false>, dim3(grid), dim3(256), 0, st, src, ld_src, dst,
+                      ld_dst, rows, static_cast<int>(cols));
 }
 
+int ce_rows_width(int64_t n) { return n >= 512 ? 4 : 1; }
+
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st) {
-  // About 256 blocks before a block takes a full warp's width of rows: the way
-  // through a row's blocks is latency (24 rows: 44 us with one block, 9 with 24).
-  int width = 1;
-  while (width < 32 && width * 512 <= R.rows) width <<= 1;
-  const int64_t row_blocks = (R.rows + width - 1) / width;
-  int64_t copy_blocks = 0;
-  if (R.x_copy) copy_blocks = (R.rows + kRowWarps - 1) / kRowWarps;
+  const int64_t row_blocks = (R.rows + R.width - 1) / R.width;
+  const int64_t copy_blocks = R.x_copy ? (R.rows + kRowWarps - 1) / kRowWarps : 0;
   const bool vec = R.dim % 8 == 0 && R.ld_x % 8 == 0 && (reinterpret_cast<uintptr_t>(R.x) & 15u) == 0;
-  const unsigned grid = static_cast<unsigned>(row_blocks + copy_blocks);
-  if (vec)
-    ce_rows_kernel<true><<<grid, kRowWarps * 32, 0, st>>>(R, static_cast<int>(row_blocks), width);
-  else
-    ce_rows_kernel<false><<<grid, kRowWarps * 32, 0, st>>>(R, static_cast<int>(row_blocks), width);
-  return cudaGetLastError();
+  return launch_after(vec ? ce_rows_kernel<true> : ce_rows_kernel<false>, dim3(static_cast<unsigned>(row_blocks + copy_blocks)),
+                      dim3(kRowWarps * 32), 0, st, R, static_cast<int>(row_blocks));
 }
 
 cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_block,
@@ -368,12 +398,12 @@ cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t
   for (int64_t r = 0; r < rows; r += per_launch) {
     const int64_t n = rows - r < per_launch ? rows - r : per_launch;
     const dim3 grid(static_cast<unsigned>((vocab + kDlCols - 1) / kDlCols), static_cast<unsigned>(n));
-    if (lo_rows > 0)
-      ce_dlogits_kernel<true><<<grid, kDlThreads, 0, st>>>(block + r * ld, ld, vocab, shift, stats + r, stats_ld, row_info + r, lo_rows);
-    else
-      ce_dlogits_kernel<false><<<grid, kDlThreads, 0, st>>>(block + r * ld, ld, vocab, shift, stats + r, stats_ld, row_info + r, 0);
+    const cudaError_t e =
+        launch_after(lo_rows > 0 ? ce_dlogits_kernel<true> : ce_dlogits_kernel<false>, grid, dim3(kDlThreads), 0, st,
+                     block + r * ld, ld, static_cast<int>(vocab), shift, stats + r, stats_ld, row_info + r, lo_rows);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, int64_t fold,
@@ -383,11 +413,8 @@ cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_st
   const bool vec = cols % 4 == 0 && ld_out % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
   const int64_t blocks = (rows * (vec ? cols / 4 : cols) + 255) / 256;
   const int grid = static_cast<int>(blocks < 152 * 32 ? blocks : 152 * 32);
-  if (vec)
-    ce_finish_kernel<4><<<grid, 256, 0, st>>>(part, ld_part, part_stride, parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, cols);
-  else
-    ce_finish_kernel<1><<<grid, 256, 0, st>>>(part, ld_part, part_stride, parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, cols);
-  return cudaGetLastError();
+  return launch_after(vec ? ce_finish_kernel<4> : ce_finish_kernel<1>, dim3(grid), dim3(256), 0, st, part, ld_part, part_stride,
+                      parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, static_cast<int>(cols));
 }
 
 }  // namespace dmuon

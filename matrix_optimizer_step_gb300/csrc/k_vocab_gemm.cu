@@ -21,6 +21,16 @@
 // 2^-9.  The logs turn into d logits once the row's sum is known
 // (k_vocab_ce.cu), so the gradient needs no second logits product.
 //
+// Long tiles are handed out by a counter in global memory: the SMs do not run
+// at one pace (with equal shares the first pair was done 5 % before the last),
+// and the two gradient products' tiles differ in length.  One thread of CTA 0
+// draws a number and puts it into a two-deep mailbox of both CTAs, and draws
+// the next but one once every role of both has read it.  Which pair computes
+// a tile does not change its result.  At 8192 x 128256 x 4096 that takes a
+// gradient call from 17.1 to 16.6 ms.  A drawn number costs half a
+// microsecond, so short tiles (vocab.cu says which) have fixed shares: drawn,
+// 24 x 128256 x 4096 took 671 us for 620.
+//
 // Every wait is bounded; after a timeout the CTA records the error, stops
 // issuing, and both CTAs meet at the final cluster barrier before the pair
 // frees its TMEM.
@@ -39,13 +49,17 @@ constexpr int TILE = 256;
 constexpr int BK = 64;
 constexpr int STAGES = 4;
 constexpr int EPI = 8;  // epilogue warps: two per TMEM lane quarter, 128 columns each
-constexpr int kThreads = (3 + EPI) * 32;
+constexpr int kSchedWarp = 3 + EPI;
+constexpr int kThreads = (4 + EPI) * 32;
 constexpr uint32_t HALF_BYTES = 128 * BK * 2;
 constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
 constexpr uint32_t MN_BOX_BYTES = 64 * 64 * 2;
 constexpr uint32_t kStaging = 2 * 4096;  // two boxes of 32 rows x 128 bytes per epilogue warp
-constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1;
-constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + EPI * kStaging + kNumBars * 8 + 16;
+constexpr int kMail = 2;  // tile numbers on their way to the roles
+constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1 + 2 * kMail;
+// Threads that read a tile number: both producers and the epilogue warps of two CTAs, and the MMA issuer.
+constexpr uint32_t kReaders = 2 * (2 + EPI) + 1;
+constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + EPI * kStaging + kNumBars * 8 + 8 + 4 * kMail;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 // Every CTA takes all of its SM's TMEM, so no second one may share the SM.
@@ -75,12 +89,10 @@ __device__ __forceinline__ void place(Tile& T, int r, int tiles_m, int tiles_n, 
   T.n0 = n * TILE;
 }
 
-// The i-th tile of CTA pair `pair` of `pairs`.
-__device__ __forceinline__ Tile tile_at(const VocabLogits& G, int pair, int pairs, int i) {
+// Tile number t (-1: no more).
+__device__ __forceinline__ Tile tile_at(const VocabLogits& G, int t) {
   Tile T;
-  const int t = pair + i * pairs;
-  T.product = t < G.tiles_m * G.tiles_n ? 0 : -1;
-  if (T.product < 0) return T;
+  T.product = t < 0 ? -1 : 0;
   place(T, t, G.tiles_m, G.tiles_n, G.group_m);
   T.split = 0;
   T.kb0 = 0;
@@ -88,27 +100,11 @@ __device__ __forceinline__ Tile tile_at(const VocabLogits& G, int pair, int pair
   return T;
 }
 
-__device__ __forceinline__ Tile tile_at(const VocabGrad& G, int pair, int pairs, int i) {
+__device__ __forceinline__ Tile tile_at(const VocabGrad& G, int t) {
   Tile T;
-  int t = pair + i * pairs;
-  T.product = 0;
-  if (t >= G.n_units[0]) {
-    T.product = 1;
-    // Pairs from `heavy` on have one tile of the first product fewer.
-    const int heavy = G.n_units[0] % pairs;
-    const int light = pairs - heavy;
-    const int extras = min(light * G.extra, G.n_units[1]);
-    i -= G.n_units[0] / pairs + (pair < heavy ? 1 : 0);
-    const int mine = pair >= heavy && pair - heavy < extras ? (extras - (pair - heavy) + light - 1) / light : 0;
-    if (i < mine)
-      t = pair - heavy + i * light;
-    else
-      t = extras + pair + (i - mine) * pairs;
-    if (t >= G.n_units[1]) {
-      T.product = -1;
-      return T;
-    }
-  }
+  T.product = t < 0 ? -1 : t >= G.n_units[0] ? 1 : 0;
+  if (t < 0) return T;
+  if (T.product) t -= G.n_units[0];
   const VgProduct& P = G.p[T.product];
   const int per_split = P.tiles_m * P.tiles_n;
   T.split = t / per_split;
@@ -116,6 +112,30 @@ __device__ __forceinline__ Tile tile_at(const VocabGrad& G, int pair, int pairs,
   T.kb0 = static_cast<int>(static_cast<int64_t>(P.kb_total) * T.split / P.splits);
   T.kb1 = static_cast<int>(static_cast<int64_t>(P.kb_total) * (T.split + 1) / P.splits);
   return T;
+}
+
+__device__ __forceinline__ int tiles_in(const VocabLogits& G) { return G.tiles_m * G.tiles_n; }
+__device__ __forceinline__ int tiles_in(const VocabGrad& G) { return G.n_units[0] + G.n_units[1]; }
+
+// Shares fixed in advance: the number of pair `pair`'s i-th tile.
+__device__ __forceinline__ int fixed_tile(const VocabLogits& G, int pair, int pairs, int i) {
+  const int t = pair + i * pairs;
+  return t < tiles_in(G) ? t : -1;
+}
+// The first product's tiles in turn, then the second's; pairs with one of the
+// first's fewer take `extra` of the second's before the others begin on those.
+__device__ __forceinline__ int fixed_tile(const VocabGrad& G, int pair, int pairs, int i) {
+  const int n0 = G.n_units[0], heavy = n0 % pairs, light = pairs - heavy;
+  if (pair + i * pairs < n0) return pair + i * pairs;
+  i -= n0 / pairs + (pair < heavy ? 1 : 0);
+  const int extras = min(light * G.extra, G.n_units[1]);
+  const int mine = pair >= heavy && pair - heavy < extras ? (extras - (pair - heavy) + light - 1) / light : 0;
+  const int t = i < mine ? pair - heavy + i * light : extras + pair + (i - mine) * pairs;
+  return t < G.n_units[1] ? n0 + t : -1;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -340,17 +360,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + EPI * kStaging);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_mem + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* mailbox = reinterpret_cast<volatile int*>(tmem_slot + 2);  // kMail tile numbers
   const uint32_t bar0 = smem_u32(bar_mem);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
   auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t drain = bar0 + 8u * (2 * STAGES + 4);
+  auto mail_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + i); };
+  auto mail_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + kMail + i); };  // the leader's is used
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 1;
-  const int n_pairs = gridDim.x >> 1;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -364,6 +385,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(tempty(a), 2 * EPI);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < kMail; ++i) {
+      mbar_init(mail_full(i), 1);
+      mbar_init(mail_empty(i), kReaders);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -375,7 +400,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
+  pdl_launch();
+  pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
+
+  const bool drawn = G.drawn != 0;
+  // The i-th tile of this pair, as every role reads it.
+  auto next_tile = [&](int i, bool whole_warp) {
+    if (!drawn) return tile_at(G, fixed_tile(G, blockIdx.x >> 1, gridDim.x >> 1, i));
+    const int at = i % kMail;
+    int t = -1;
+    if (mbar_wait_bounded_cluster(mail_full(at), static_cast<uint32_t>(i / kMail) & 1u, abort_flag, G.err, kErrTimeoutMailbox))
+      t = mailbox[at];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) {
+      if (leader)
+        mbar_arrive(mail_empty(at));
+      else
+        mbar_arrive_cluster(mapa_shared(mail_empty(at), 0));
+    }
+    return tile_at(G, t);
+  };
 
   if ((warp == 0 || warp == kProducerBWarp) && lane == 0) {
     // ------------------------------------ producers (A: warp 0, B: the last)
@@ -385,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      const Tile T = tile_at(G, pair, n_pairs, i);
+      const Tile T = next_tile(i, false);
       if (T.product < 0) break;
       const CUtensorMap* map = operand_map(G, T.product, is_b);
       const bool mn = is_b ? B_MN : a_is_mn(G, T.product);
@@ -428,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int use = 0;
       for (; ok; ++use) {
-        const Tile T = tile_at(G, pair, n_pairs, use);
+        const Tile T = next_tile(use, false);
         if (T.product < 0) break;
         const bool a_mn = a_is_mn(G, T.product);
         const uint32_t idesc = idesc_bf16_f32(TILE, TILE, a_mn, B_MN);
@@ -474,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float alpha = 1.f;
     if constexpr (!LOGITS) alpha = G.alpha ? __ldg(G.alpha) : 1.f;
     for (;; ++use) {
-      const Tile T = tile_at(G, pair, n_pairs, use);
+      const Tile T = next_tile(use, true);
       if (T.product < 0) break;
       const int acc = use & 1;
       const int warp_row0 = T.m0 + 128 * static_cast<int>(rank) + 32 * quarter;
@@ -527,6 +572,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 
+  if (drawn && warp == kSchedWarp && leader && lane == 0) {
+    // ------------------------------------------------------ tile numbers
+    const int total = tiles_in(G);
+    for (int i = 0;; ++i) {
+      const int at = i % kMail;
+      if (!mbar_wait_bounded_cluster(mail_empty(at), (static_cast<uint32_t>(i / kMail) & 1u) ^ 1u, abort_flag, G.err,
+                                     kErrTimeoutMailbox))
+        break;
+      int t = static_cast<int>(atomicAdd(G.counter, 1u));
+      if (t >= total) t = -1;
+      mailbox[at] = t;
+      st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(mailbox)) + 4u * at, 1), static_cast<uint32_t>(t));
+      mbar_arrive(mail_full(at));
+      mbar_arrive_cluster(mapa_shared(mail_full(at), 1));
+      if (t < 0) break;
+    }
+  }
+
   tc_fence_before();
   cluster_sync_all();  // all MMAs drained, no more cross-CTA traffic
   tc_fence_after();
@@ -547,8 +610,7 @@ cudaError_t launch(const Args& G, int64_t tiles, int n_pairs, cudaStream_t st) {
   }
   if (tiles <= 0 || n_pairs <= 0) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < n_pairs ? tiles : n_pairs);
-  vocab_gemm_kernel<Args, B_MN><<<2 * pairs, kThreads, kSmem, st>>>(G);
-  return cudaGetLastError();
+  return launch_after(vocab_gemm_kernel<Args, B_MN>, dim3(2 * pairs), dim3(kThreads), kSmem, st, G);
 }
 
 }  // namespace

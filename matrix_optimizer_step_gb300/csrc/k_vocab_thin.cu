@@ -11,6 +11,9 @@
 // A drained column is a token and a lane a row of W, so a token's statistics
 // go across lanes: 16 columns at a time are reduced together, each exchange
 // halving the columns a lane still works on (16 shuffles for 16 maxima).
+// A long K is cut into up to four accumulators that the epilogue adds: the
+// MMA's running sum truncates, and with one token nothing averages that out
+// (the loss at width 4096 came out 4e-6 off, relatively, from one accumulator).
 // Every wait is bounded, as in k_vocab_gemm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -139,7 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   const uint32_t stage_bytes = A_BYTES + static_cast<uint32_t>(G.np) * (BK * 2);
   const int stages = min(kMaxStages, static_cast<int>(kRingBytes / stage_bytes));
   uint32_t tmem_cols = 32;
-  while (tmem_cols < 2u * static_cast<uint32_t>(G.np)) tmem_cols <<= 1;
+  const uint32_t acc_cols = static_cast<uint32_t>(G.np * G.groups);
+  while (tmem_cols < 2u * acc_cols) tmem_cols <<= 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -162,6 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_launch();
+  pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
   const int n_tiles = G.tiles_m * G.splits;
   auto k_range = [&](int split, int& kb0, int& kb1) {
@@ -225,7 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
         if (!mbar_wait_bounded(tempty(use & 1), (static_cast<uint32_t>(use >> 1) & 1u) ^ 1u, abort_flag, G.err, kErrTimeoutMma))
           break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((use & 1) * G.np);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(use & 1) * acc_cols;
+        const int per_group = (kb1 - kb0 + G.groups - 1) / G.groups;
+        int group = 0, left = per_group;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_bounded(full(stage), phase, abort_flag, G.err, kErrTimeoutMma)) {
             ok = false;
@@ -235,7 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
           const uint32_t sa = ring + stage * stage_bytes, sb = sa + A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            umma_bf16(d_tmem, A_MN ? desc_mn(sa, kk) : desc_k(sa, kk), desc_k(sb, kk), idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+            umma_bf16(d_tmem + static_cast<uint32_t>(group * G.np), A_MN ? desc_mn(sa, kk) : desc_k(sa, kk), desc_k(sb, kk),
+                      idesc, (left != per_group || kk != 0) ? 1u : 0u);
+          if (--left == 0) {
+            ++group;
+            left = per_group;
+          }
           umma_commit(empty(stage));
           if (++stage == stages) {
             stage = 0;
@@ -257,12 +270,19 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
       const int acc = use & 1;
       if (!mbar_wait_bounded(tfull(acc), static_cast<uint32_t>(use >> 1) & 1u, abort_flag, G.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
-      const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * G.np);
+      const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc) * acc_cols;
       if (row0 < G.M) {  // warp-uniform
         for (int c0 = 0; c0 < G.tokens; c0 += 16) {
           uint32_t r[16];
           tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), r);
           tmem_wait_x16(r);
+          for (int g = 1; g < G.groups; ++g) {
+            uint32_t more[16];
+            tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(g * G.np + c0), more);
+            tmem_wait_x16(more);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+          }
           if (LOGITS) {
             thin_logits(G, r, row0, c0, lane);
           } else if (row0 + lane < G.M) {
@@ -296,14 +316,15 @@ cudaError_t launch_variant(const VocabThin& G, int n_ctas, cudaStream_t st) {
     attr_note_current_device(&attr_mask);
   }
   const int64_t tiles = static_cast<int64_t>(G.tiles_m) * G.splits;
-  vocab_thin_kernel<LOGITS><<<static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas), kThreads, kSmem, st>>>(G);
-  return cudaGetLastError();
+  return launch_after(vocab_thin_kernel<LOGITS>, dim3(static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas)), dim3(kThreads),
+                      kSmem, st, G);
 }
 
 }  // namespace
 
 cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaStream_t st) {
-  if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > 128 || G.np % 16 != 0 || n_ctas <= 0)
+  if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > 128 || G.np % 16 != 0 || G.groups < 1 ||
+      2 * G.np * G.groups > 512 || n_ctas <= 0)
     return cudaErrorInvalidValue;
   return logits ? launch_variant<true>(G, n_ctas, st) : launch_variant<false>(G, n_ctas, st);
 }

@@ -153,6 +153,10 @@ bool tma_rows(const void* p, int64_t ld, int elem) { return aligned16(p) && ld *
 
 constexpr int kVgTile = 256;
 
+// Tiles of at least this many k-blocks are drawn (k_vocab_gemm.cu): half a
+// microsecond a tile against 9 us and more of work.
+constexpr int kDrawnBlocks = 32;
+
 int64_t tiles_of(int64_t n) { return (n + kVgTile - 1) / kVgTile; }
 
 // Costs in k-blocks of one 256 x 256 tile (about 0.27 us on a pair): what a
@@ -270,9 +274,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const bool thin = n <= kThinRows / 2;
   const int stats_block = thin ? kCeThinBlock : kCeBlock;
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
-  int64_t stats_ld = round_up(rows, 32);
-  if (rows < 32)
-    for (stats_ld = 1; stats_ld < rows;) stats_ld *= 2;
+  const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
 
   // Operand copies: TMA needs rows on 16 bytes, and rows that are not counted
   // must read as zeros in dW's product whatever they hold.
@@ -283,7 +285,8 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const size_t off_w = copy_w ? L.take(static_cast<size_t>(v * ld8) * 2) : 0;
   const size_t off_stats = L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float2));
   const size_t off_z = L.take(static_cast<size_t>(rows) * 4);
-  const size_t off_loss = C.loss ? 0 : L.take(static_cast<size_t>(n) * 4);
+  const int width = ce_rows_width(n);
+  const size_t off_partial = grads || C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
   size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
   Target dx, dw;
   if (grads) {
@@ -351,11 +354,11 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   }
   float2* stats = reinterpret_cast<float2*>(ws + off_stats);
   float* target_z = reinterpret_cast<float*>(ws + off_z);
-  float* loss = C.loss ? C.loss : reinterpret_cast<float*>(ws + off_loss);
   uint16_t* block = reinterpret_cast<uint16_t*>(ws + off_block);
   CeRow* row_info = reinterpret_cast<CeRow*>(ws + off_rows);
   float* alpha = reinterpret_cast<float*>(ws + off_alpha);
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
+  uint32_t* counters = static_cast<uint32_t*>(ctx->vocab_ticket.p);  // two tile counters, one ticket
   const float scale_log2 = C.logit_scale * 1.4426950408889634f;
 
   for (int64_t r0 = 0; r0 < n; r0 += rows) {
@@ -372,6 +375,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.tiles_m = static_cast<int32_t>((v + 127) / 128);
       G.splits = 1;
       G.kb_total = static_cast<int32_t>((d + 63) / 64);
+      G.groups = std::max(1, std::min(4, G.kb_total / 16));
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
@@ -401,6 +405,8 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.stats_ld = stats_ld;
       G.target_z = target_z;
       G.targets = here;
+      G.counter = counters;
+      G.drawn = G.kb_total >= kDrawnBlocks;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_logits(G, pairs, s); }));
     }
 
@@ -421,16 +427,19 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     R.dim = static_cast<int32_t>(d);
     R.logit_scale_log2 = scale_log2;
     R.out = grads ? row_info : nullptr;
-    R.loss = loss;
+    R.loss = C.loss;
     R.lse = C.lse;
     R.x_copy = C.dw ? masked : nullptr;
     R.ld_copy = ld8;
     R.copies = halves ? 2 : 1;
+    R.width = width;
+    R.partial = grads || C.total ? reinterpret_cast<double2*>(ws + off_partial) : nullptr;
     R.alpha = grads && first ? alpha : nullptr;
     R.scale = C.grad_scale * C.logit_scale;
     R.total = last ? C.total : nullptr;
     R.mean = mean;
-    R.ticket = static_cast<uint32_t*>(ctx->vocab_ticket.p);
+    R.ticket = counters + 2;
+    R.counters = counters;
     R.err = err;
     DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_rows(R, s); }));
     if (!grads) continue;
@@ -441,6 +450,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     }));
     if (C.dx) dx.out = static_cast<char*>(C.dx) + r0 * C.ld_dx * (dx_bf16 ? 2 : 4);
     VocabGrad G = {};
+    G.counter = counters + 1;
     G.alpha = alpha;
     G.err = err;
     if (C.dx && thin) {
@@ -451,6 +461,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       T.tiles_m = static_cast<int32_t>((d + 127) / 128);
       T.splits = dx.splits;
       T.kb_total = static_cast<int32_t>((v + 63) / 64);
+      T.groups = 1;
       T.err = err;
       DM_TRY(encode_2d(enc, &T.map_a, w, d, v, ld_w, 64, 64));
       DM_TRY(encode_2d(enc, &T.map_b, block, v, k_rows, ld_block, 64, static_cast<uint32_t>(T.np)));
@@ -469,10 +480,13 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked, ld8, dw, splits, 8, first));
       G.n_units[1] = G.p[1].tiles_m * G.p[1].tiles_n * G.p[1].splits;
     }
-    if (G.n_units[0] > 0 && G.n_units[0] % pairs != 0 && G.n_units[1] > 0) {
-      const double u0 = static_cast<double>(G.p[0].kb_total) / G.p[0].splits + kTileCost;
-      const double u1 = static_cast<double>(G.p[1].kb_total) / G.p[1].splits + kTileCost;
-      G.extra = static_cast<int32_t>(u0 / u1 + 0.5);
+    if (G.n_units[1] > 0) {
+      const double u1 = static_cast<double>(G.p[1].kb_total) / G.p[1].splits;
+      G.drawn = u1 >= kDrawnBlocks;
+      if (G.n_units[0] % pairs != 0)
+        G.extra = static_cast<int32_t>((static_cast<double>(G.p[0].kb_total) / G.p[0].splits + kTileCost) / (u1 + kTileCost) + 0.5);
+    } else {
+      G.drawn = 1;
     }
     if (G.n_units[0] + G.n_units[1] > 0)
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_grad(G, pairs, s); }));
@@ -542,7 +556,10 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
   DeviceGuard guard(ctx->device);
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, nr));
-  return cross_entropy_impl(ctx, C, static_cast<cudaStream_t>(stream));
+  const int st = cross_entropy_impl(ctx, C, static_cast<cudaStream_t>(stream));
+  // A sequence that broke off may have left its counters up.
+  if (st != DMUON_OK && ctx->vocab_ticket.p) cudaMemsetAsync(ctx->vocab_ticket.p, 0, 256, static_cast<cudaStream_t>(stream));
+  return st;
 }
 
 int dmuon_embed_forward(dmuon_context* ctx, const dmuon_embed* args, void* stream) {

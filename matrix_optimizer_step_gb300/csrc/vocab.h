@@ -9,6 +9,29 @@
 
 namespace dmuon {
 
+// Launch that may begin while the kernel before it on the stream ends: every
+// kernel of the vocabulary operators calls pdl_wait before it touches memory,
+// so only its set-up (barriers, TMEM, launch latency) runs early.
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// All earlier work on the stream is done and visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel's blocks may take free room from here on.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Token ids and targets: 32- or 64-bit, as the caller has them.
 struct IdList {
   const void* p;
@@ -39,6 +62,8 @@ struct VocabLogits {
   int64_t stats_ld;
   float* target_z;                    // [row]: the target's z
   IdList targets;                     // of row 0 of this product
+  uint32_t* counter;                  // zero before
+  int32_t drawn;                      // tiles drawn from the counter, else fixed shares
 };
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st);
 
@@ -55,13 +80,13 @@ struct VgProduct {
   int32_t add;                        // fp32: add to what `out` holds
 };
 
-// One launch for up to two products.  Tiles go to the pairs in turn, the
-// first product's first; the pairs that get one tile fewer of those take
-// `extra` more of the second's.
+// One launch for up to two products, the first's tiles first.
 struct VocabGrad {
   VgProduct p[2];
-  int32_t n_units[2];
-  int32_t extra;
+  int32_t n_units[2];                 // tiles times splits
+  uint32_t* counter;                  // zero before
+  int32_t drawn;                      // tiles drawn from the counter, else fixed shares
+  int32_t extra;                      // fixed shares: see fixed_tile
   const float* alpha;
   int* err;
 };
@@ -75,6 +100,7 @@ struct VocabThin {
   int32_t M;                          // vocabulary (logits) or width (dX)
   int32_t tokens, np;                 // token rows, and those rounded up to 16
   int32_t tiles_m, splits, kb_total;
+  int32_t groups;                     // accumulators that K is cut into
   int* err;
   // logits
   float logit_scale_log2;
@@ -119,13 +145,15 @@ struct CeRows {
   int32_t dim;
   float logit_scale_log2;
   CeRow* out;              // of row row0, or null
-  float* loss;             // of row 0, never null
+  float* loss;             // of row 0, or null
   float* lse;              // of row 0, or null
   // dW's operand: this pass's rows of x, zeros where the row is not counted; twice
   // (copies rows apart) for a gradient in two halves.  Null: not wanted.
   uint16_t* x_copy;
   int64_t ld_copy;
   int32_t copies;
+  int32_t width;           // rows of a block: ce_rows_width(n)
+  double2* partial;        // [row / width]: sums of weight * loss and weight; null without total and alpha
   // Factor of both gradients, written by the first pass: scale [/ sum(weight)].  Null: not wanted.
   float* alpha;
   float scale;
@@ -133,8 +161,10 @@ struct CeRows {
   float* total;            // null: not in this pass
   int32_t mean;
   uint32_t* ticket;        // zero before and after
+  uint32_t* counters;      // the products' two tile counters, set to zero
   int* err;
 };
+int ce_rows_width(int64_t n);
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st);
 
 // Fixed-point logs -> bf16 d logits (before the factor alpha), in place.  With
