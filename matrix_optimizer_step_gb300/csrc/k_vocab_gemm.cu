@@ -77,65 +77,78 @@ struct Tile {
   int m0, n0, kb0, kb1, split;
 };
 
-// Tiles of one split in groups of group_m row tiles, the row tile fastest: the
-// tiles that run at the same time share the group's A rows and a few B blocks.
-__device__ __forceinline__ void place(Tile& T, int r, int tiles_m, int tiles_n, int group_m) {
-  const int per_group = group_m * tiles_n;
-  const int g = r / per_group;
-  r -= g * per_group;
-  const int gm = min(group_m, tiles_m - g * group_m);
-  const int n = r / gm;
-  T.m0 = (g * group_m + (r - n * gm)) * TILE;
+// Tile number t >= 0 of a product.
+__device__ __forceinline__ Tile place(const TileGrid& R, int t) {
+  Tile T;
+  T.product = 0;
+  T.split = R.per_split.div(t);
+  t -= T.split * static_cast<int>(R.per_split.d);
+  const int g = R.per_group.div(t);
+  t -= g * static_cast<int>(R.per_group.d);
+  const bool full = (g + 1) * R.group_m <= R.tiles_m;
+  const int n = full ? R.group.div(t) : R.last.div(t);
+  T.m0 = (g * R.group_m + t - n * (full ? R.group_m : R.last_m)) * TILE;
   T.n0 = n * TILE;
+  T.kb0 = T.split * R.kb_step;
+  T.kb1 = min(R.kb_total, T.kb0 + R.kb_step);
+  return T;
 }
 
-// Tile number t (-1: no more).
+// Tile number t of the launch (-1: no more).
 __device__ __forceinline__ Tile tile_at(const VocabLogits& G, int t) {
   Tile T;
-  T.product = t < 0 ? -1 : 0;
-  place(T, t, G.tiles_m, G.tiles_n, G.group_m);
-  T.split = 0;
-  T.kb0 = 0;
-  T.kb1 = G.kb_total;
-  return T;
+  T.product = -1;
+  return t < 0 ? T : place(G.grid, t);
 }
-
 __device__ __forceinline__ Tile tile_at(const VocabGrad& G, int t) {
   Tile T;
-  T.product = t < 0 ? -1 : t >= G.n_units[0] ? 1 : 0;
+  T.product = -1;
   if (t < 0) return T;
-  if (T.product) t -= G.n_units[0];
-  const VgProduct& P = G.p[T.product];
-  const int per_split = P.tiles_m * P.tiles_n;
-  T.split = t / per_split;
-  place(T, t - T.split * per_split, P.tiles_m, P.tiles_n, P.group_m);
-  T.kb0 = static_cast<int>(static_cast<int64_t>(P.kb_total) * T.split / P.splits);
-  T.kb1 = static_cast<int>(static_cast<int64_t>(P.kb_total) * (T.split + 1) / P.splits);
+  const int p = t >= G.n_units[0] ? 1 : 0;
+  T = place(G.p[p].grid, p ? t - G.n_units[0] : t);
+  T.product = p;
   return T;
 }
 
-__device__ __forceinline__ int tiles_in(const VocabLogits& G) { return G.tiles_m * G.tiles_n; }
+__device__ __forceinline__ int tiles_in(const VocabLogits& G) { return G.grid.count(); }
 __device__ __forceinline__ int tiles_in(const VocabGrad& G) { return G.n_units[0] + G.n_units[1]; }
 
-// Shares fixed in advance: the number of pair `pair`'s i-th tile.
-__device__ __forceinline__ int fixed_tile(const VocabLogits& G, int pair, int pairs, int i) {
-  const int t = pair + i * pairs;
-  return t < tiles_in(G) ? t : -1;
-}
-// The first product's tiles in turn, then the second's; pairs with one of the
-// first's fewer take `extra` of the second's before the others begin on those.
-__device__ __forceinline__ int fixed_tile(const VocabGrad& G, int pair, int pairs, int i) {
-  const int n0 = G.n_units[0], heavy = n0 % pairs, light = pairs - heavy;
-  if (pair + i * pairs < n0) return pair + i * pairs;
-  i -= n0 / pairs + (pair < heavy ? 1 : 0);
-  const int extras = min(light * G.extra, G.n_units[1]);
-  const int mine = pair >= heavy && pair - heavy < extras ? (extras - (pair - heavy) + light - 1) / light : 0;
-  const int t = i < mine ? pair - heavy + i * light : extras + pair + (i - mine) * pairs;
-  return t < G.n_units[1] ? n0 + t : -1;
+// Shares fixed in advance: the numbers of one pair's tiles.  The first
+// product's tiles go to the pairs in turn, then the second's; pairs with one
+// of the first's fewer take `extra` of the second's before the others begin
+// on those.
+struct FixedShares {
+  int pair, pairs, n0, n1, own0, mine, light, heavy, extras;
+  __device__ __forceinline__ FixedShares(int n0_, int n1_, int extra) : n0(n0_), n1(n1_) {
+    pair = blockIdx.x >> 1;
+    pairs = gridDim.x >> 1;
+    heavy = n0 % pairs;
+    light = pairs - heavy;
+    own0 = n0 / pairs + (pair < heavy ? 1 : 0);
+    extras = min(light * extra, n1);
+    mine = pair >= heavy && pair - heavy < extras ? (extras - (pair - heavy) + light - 1) / light : 0;
+  }
+  __device__ __forceinline__ int at(int i) const {
+    if (i < own0) return pair + i * pairs;
+    i -= own0;
+    const int t = i < mine ? pair - heavy + i * light : extras + pair + (i - mine) * pairs;
+    return t < n1 ? n0 + t : -1;
+  }
+};
+__device__ __forceinline__ FixedShares fixed_shares(const VocabLogits& G) { return FixedShares(tiles_in(G), 0, 0); }
+__device__ __forceinline__ FixedShares fixed_shares(const VocabGrad& G) {
+  return FixedShares(G.n_units[0], G.n_units[1], G.extra);
 }
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Arrival on the other CTA's barrier that hands on no ordinary memory: the
+// tensor-core fence before it orders the TMEM reads.  (With release semantics
+// the arrival waits for all of the thread's earlier stores.)
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -405,9 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   const bool drawn = G.drawn != 0;
+  const FixedShares shares = fixed_shares(G);
   // The i-th tile of this pair, as every role reads it.
   auto next_tile = [&](int i, bool whole_warp) {
-    if (!drawn) return tile_at(G, fixed_tile(G, blockIdx.x >> 1, gridDim.x >> 1, i));
+    if (!drawn) return tile_at(G, shares.at(i));
     const int at = i % kMail;
     int t = -1;
     if (mbar_wait_bounded_cluster(mail_full(at), static_cast<uint32_t>(i / kMail) & 1u, abort_flag, G.err, kErrTimeoutMailbox))
@@ -548,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (leader)
             mbar_arrive(tempty(acc));
           else
-            mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+            arrive_relaxed(mapa_shared(tempty(acc), 0));
         }
       };
       if (warp_row0 >= rows || col0 >= cols) {  // warp-uniform
@@ -616,7 +630,7 @@ cudaError_t launch(const Args& G, int64_t tiles, int n_pairs, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st) {
-  return launch<VocabLogits, false>(G, static_cast<int64_t>(G.tiles_m) * G.tiles_n, n_pairs, st);
+  return launch<VocabLogits, false>(G, G.grid.count(), n_pairs, st);
 }
 
 cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st) {

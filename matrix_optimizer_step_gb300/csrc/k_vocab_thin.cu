@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   const uint32_t tmem_base = *tmem_slot;
   const int n_tiles = G.tiles_m * G.splits;
   auto k_range = [&](int split, int& kb0, int& kb1) {
-    kb0 = static_cast<int>(static_cast<int64_t>(G.kb_total) * split / G.splits);
-    kb1 = static_cast<int>(static_cast<int64_t>(G.kb_total) * (split + 1) / G.splits);
+    kb0 = split * G.kb_step;
+    kb1 = min(G.kb_total, kb0 + G.kb_step);
   };
 
   if (warp == 0) {

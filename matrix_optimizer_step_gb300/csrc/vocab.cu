@@ -164,6 +164,12 @@ int64_t tiles_of(int64_t n) { return (n + kVgTile - 1) / kVgTile; }
 // bytes through memory (written, read).
 constexpr double kTileCost = 6.0, kLaunchCost = 12.0, kPartialBytesPerUnit = 1.8e6;
 
+// Parts of equal length (the last may be shorter) that K is cut into when about `parts` are wanted: none is empty.
+int whole_parts(int64_t k, int64_t parts) {
+  const int64_t kb = (k + 63) / 64, step = (kb + parts - 1) / parts;
+  return static_cast<int>((kb + step - 1) / step);
+}
+
 // Parts that the K axis of an M x N product is cut into.  Few output tiles
 // leave pairs idle, and `other` k-blocks of further tiles share the launch;
 // every part costs a pass of its fp32 partial through memory.
@@ -184,7 +190,7 @@ int choose_splits(int64_t m, int64_t n, int64_t k, double other, int pairs, bool
       parts = s;
     }
   }
-  return parts;
+  return whole_parts(k, parts);
 }
 
 int encode_2d(EncodeTiledFn enc, CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t ld, uint32_t box_inner,
@@ -213,11 +219,7 @@ int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_
                    const void* b, int64_t ld_b, const Target& T, int splits, int group_m, bool first) {
   P->M = static_cast<int32_t>(m);
   P->N = static_cast<int32_t>(n);
-  P->tiles_m = static_cast<int32_t>(tiles_of(m));
-  P->tiles_n = static_cast<int32_t>(tiles_of(n));
-  P->splits = splits;
-  P->kb_total = static_cast<int32_t>((k + 63) / 64);
-  P->group_m = group_m;
+  P->grid.set(m, n, k, splits, group_m);
   P->a_mn = a_mn;
   if (a_mn)
     DM_TRY(encode_2d(enc, &P->map_a, a, m, k, ld_a, 64, 64));
@@ -226,7 +228,7 @@ int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_
   DM_TRY(encode_2d(enc, &P->map_b, b, n, k, ld_b, 64, 64));
   if (T.part) {
     P->add = !first;
-    return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.part, n, m, splits, T.ld_part, m * T.ld_part, 32, 32);
+    return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.part, n, m, P->grid.splits, T.ld_part, m * T.ld_part, 32, 32);
   }
   if (T.bf16) {
     P->out_bf16 = 1;
@@ -316,7 +318,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
         int64_t parts = (2 * ctx->num_sms + tiles - 1) / tiles;
         // Whole waves of CTAs, but at least 8 k-blocks in a part.
         if (parts * tiles > ctx->num_sms) parts = std::max<int64_t>(1, (2 * ctx->num_sms) / tiles);
-        dx.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(parts, kb / 8)));
+        dx.splits = whole_parts(v, std::max<int64_t>(1, std::min<int64_t>(parts, kb / 8)));
       } else {
         const double other = C.dw ? static_cast<double>(tiles_of(v) * tiles_of(d) * dw.splits) *
                                         (static_cast<double>((token_rows + 63) / 64) / dw.splits + kTileCost)
@@ -374,7 +376,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.np = static_cast<int32_t>(round_up(nr, 16));
       G.tiles_m = static_cast<int32_t>((v + 127) / 128);
       G.splits = 1;
-      G.kb_total = static_cast<int32_t>((d + 63) / 64);
+      G.kb_total = G.kb_step = static_cast<int32_t>((d + 63) / 64);
       G.groups = std::max(1, std::min(4, G.kb_total / 16));
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
@@ -391,10 +393,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       VocabLogits G = {};
       G.M = static_cast<int32_t>(nr);
       G.N = static_cast<int32_t>(v);
-      G.tiles_m = static_cast<int32_t>(tiles_of(nr));
-      G.tiles_n = static_cast<int32_t>(tiles_of(v));
-      G.kb_total = static_cast<int32_t>((d + 63) / 64);
-      G.group_m = 8;
+      G.grid.set(nr, v, d, 1, 8);
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
@@ -406,7 +405,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.target_z = target_z;
       G.targets = here;
       G.counter = counters;
-      G.drawn = G.kb_total >= kDrawnBlocks;
+      G.drawn = G.grid.kb_total >= kDrawnBlocks;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_logits(G, pairs, s); }));
     }
 
@@ -459,8 +458,9 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       T.tokens = static_cast<int32_t>(k_rows);
       T.np = static_cast<int32_t>(round_up(k_rows, 16));
       T.tiles_m = static_cast<int32_t>((d + 127) / 128);
-      T.splits = dx.splits;
       T.kb_total = static_cast<int32_t>((v + 63) / 64);
+      T.kb_step = (T.kb_total + dx.splits - 1) / dx.splits;
+      T.splits = dx.splits;
       T.groups = 1;
       T.err = err;
       DM_TRY(encode_2d(enc, &T.map_a, w, d, v, ld_w, 64, 64));
@@ -470,7 +470,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(false, T, ctx->num_sms, s); }));
     } else if (C.dx) {
       DM_TRY(encode_product(enc, &G.p[0], k_rows, d, v, false, block, ld_block, w, ld_w, dx, dx.splits, 8, true));
-      G.n_units[0] = G.p[0].tiles_m * G.p[0].tiles_n * G.p[0].splits;
+      G.n_units[0] = G.p[0].grid.count();
     }
     if (C.dw) {
       // The last pass may be shorter: every part needs a k-block of its own,
@@ -478,13 +478,13 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       const int splits = static_cast<int>(std::min<int64_t>(dw.splits, (k_rows + 63) / 64));
       // Short main loops are bound by the stores: whole rows of tiles then go out together.
       DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked, ld8, dw, splits, 8, first));
-      G.n_units[1] = G.p[1].tiles_m * G.p[1].tiles_n * G.p[1].splits;
+      G.n_units[1] = G.p[1].grid.count();
     }
     if (G.n_units[1] > 0) {
-      const double u1 = static_cast<double>(G.p[1].kb_total) / G.p[1].splits;
+      const int u1 = G.p[1].grid.kb_step;
       G.drawn = u1 >= kDrawnBlocks;
       if (G.n_units[0] % pairs != 0)
-        G.extra = static_cast<int32_t>((static_cast<double>(G.p[0].kb_total) / G.p[0].splits + kTileCost) / (u1 + kTileCost) + 0.5);
+        G.extra = static_cast<int32_t>((G.p[0].grid.kb_step + kTileCost) / (u1 + kTileCost) + 0.5);
     } else {
       G.drawn = 1;
     }

@@ -48,13 +48,52 @@ constexpr int kCeThinBlock = 32;  // few tokens (k_vocab_thin.cu)
 // maximum in units of 2^-10 octaves, cut off at 64 octaves.
 constexpr float kCeLogUnits = 1024.f;
 
-// Z = X W^T on 256 x 256 tiles of CTA pairs: statistics, optionally logs.
+// Division by a constant of the launch: n / d for 0 <= n < 2^31 (multiply by the
+// rounded-up reciprocal of 2^32 + mul, shifted).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  __host__ void set(int32_t divisor) {
+    d = static_cast<uint32_t>(divisor);
+    shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
+// The tiles of one product on 256 x 256 tiles of CTA pairs, in the order of
+// their numbers: by parts of K; within a part by groups of group_m row tiles;
+// within a group column by column, the row tile fastest.  Tiles that run at
+// the same time then share the group's A rows and a few B blocks in L2.
+struct TileGrid {
+  int32_t tiles_m, tiles_n, splits;
+  int32_t kb_total, kb_step;  // 64-deep k-blocks, and those of one part
+  int32_t group_m, last_m;    // row tiles of a group, and of the last one
+  FastDiv per_split, per_group, group, last;
+  // m x n x k, K in `parts` or fewer non-empty parts.
+  __host__ void set(int64_t m, int64_t n, int64_t k, int parts, int group_rows) {
+    tiles_m = static_cast<int32_t>((m + 255) / 256);
+    tiles_n = static_cast<int32_t>((n + 255) / 256);
+    kb_total = static_cast<int32_t>((k + 63) / 64);
+    kb_step = (kb_total + parts - 1) / parts;
+    splits = (kb_total + kb_step - 1) / kb_step;
+    group_m = group_rows < tiles_m ? group_rows : tiles_m;
+    last_m = tiles_m % group_m ? tiles_m % group_m : group_m;
+    per_split.set(tiles_m * tiles_n);
+    per_group.set(group_m * tiles_n);
+    group.set(group_m);
+    last.set(last_m);
+  }
+  __host__ __device__ int32_t count() const { return tiles_m * tiles_n * splits; }
+};
+
+// Z = X W^T: statistics, optionally logs.
 struct VocabLogits {
   CUtensorMap map_a, map_b, map_out;  // X, W, logs
   int32_t M, N;                       // tokens, vocabulary
-  int32_t tiles_m, tiles_n;
-  int32_t kb_total;                   // 64-deep k-blocks
-  int32_t group_m;                    // row tiles that are walked together (operand reuse in L2)
+  TileGrid grid;
   int* err;
   float logit_scale_log2;             // logit scale times log2(e)
   int32_t store_logs;
@@ -72,9 +111,7 @@ cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t 
 struct VgProduct {
   CUtensorMap map_a, map_b, map_out;
   int32_t M, N;
-  int32_t tiles_m, tiles_n, splits;   // splits > 1: fp32 partials, one per part of K
-  int32_t kb_total;
-  int32_t group_m;
+  TileGrid grid;                      // grid.splits > 1: fp32 partials, one per part of K
   int32_t a_mn;
   int32_t out_bf16;                   // else fp32
   int32_t add;                        // fp32: add to what `out` holds
@@ -83,7 +120,7 @@ struct VgProduct {
 // One launch for up to two products, the first's tiles first.
 struct VocabGrad {
   VgProduct p[2];
-  int32_t n_units[2];                 // tiles times splits
+  int32_t n_units[2];                 // tiles times parts
   uint32_t* counter;                  // zero before
   int32_t drawn;                      // tiles drawn from the counter, else fixed shares
   int32_t extra;                      // fixed shares: see fixed_tile
@@ -99,7 +136,7 @@ struct VocabThin {
   CUtensorMap map_a, map_b;           // W; X or dZ
   int32_t M;                          // vocabulary (logits) or width (dX)
   int32_t tokens, np;                 // token rows, and those rounded up to 16
-  int32_t tiles_m, splits, kb_total;
+  int32_t tiles_m, splits, kb_total, kb_step;
   int32_t groups;                     // accumulators that K is cut into
   int* err;
   // logits
