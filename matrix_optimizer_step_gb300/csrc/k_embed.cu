@@ -6,9 +6,10 @@
 // Both move bytes and compute next to nothing.  The gradient adds the rows of
 // equal ids in the order of their positions, in fp32, and rounds once, so that
 // it is the same for every run: the (id, position) pairs are sorted with a
-// stable radix sort, the sorted list is cut into runs of kEmbedRun positions,
-// one block sums each run, and ids that cross a cut are joined from the runs'
-// partial sums in order.  Work is even over blocks however often an id comes.
+// stable radix sort, the sorted list is cut into runs, one block sums each run,
+// and ids that cross a cut are joined from the runs' partial sums in order.
+// Work is even over blocks however often an id comes.  Blocks of the same
+// launch write the zeros of the rows that no id names.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -93,6 +94,8 @@ constexpr int kFwdCols = 1024;
 
 template <bool TB, bool OB, bool VEC>
 __global__ void __launch_bounds__(256) embed_forward_kernel(const EmbedForward E) {
+  pdl_launch();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int segs = (E.dim + kFwdCols - 1) / kFwdCols;
   const int64_t tasks = E.n * segs, warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -128,11 +131,14 @@ __global__ void __launch_bounds__(256) embed_forward_kernel(const EmbedForward E
 
 // ----------------------------------------------------------------------- sort
 // Stable radix sort of (id, position), least significant digit first, at most
-// 9 bits a pass.  A block takes 4096 pairs; warp w holds 128 consecutive ones
-// (four rounds of one per lane).  Entries that are not counted get the key
-// `vocab`, which sorts last.
-constexpr int kSortThreads = 1024, kSortItems = 4, kSortTile = kSortThreads * kSortItems;
+// 9 bits a pass.  A block takes kSortThreads * ITEMS pairs; warp w holds
+// 32 * ITEMS consecutive ones (ITEMS rounds of one per lane).  Entries that
+// are not counted get the key `vocab`, which sorts last.
+constexpr int kSortThreads = 1024;
+constexpr int kSortTile = 4096;  // pairs of a block in the sort over several launches
 constexpr int kBins = 512;
+constexpr int kClusterMost = 8, kClusterItems = 8;
+constexpr int kOneLaunch = kSortThreads * kClusterMost * kClusterItems;
 
 __device__ __forceinline__ uint32_t first_key(const EmbedBackward& E, int64_t i) {
   bool bad = false;
@@ -143,14 +149,17 @@ __device__ __forceinline__ uint32_t first_key(const EmbedBackward& E, int64_t i)
 
 // Ranks of this block's pairs among its pairs of the same digit: rank[k] within the
 // warp, and cnt[w][d] the number in the warps before w.  Called by all threads;
-// total (thread d): the block's number of digit d.
-__device__ __forceinline__ uint32_t block_ranks(const uint32_t (&digit)[kSortItems], const bool (&has)[kSortItems],
-                                                uint16_t (*cnt)[kBins], uint32_t (&rank)[kSortItems]) {
+// returns (thread d) the block's number of digit d.
+template <int ITEMS>
+__device__ __forceinline__ uint32_t block_ranks(const uint32_t (&digit)[ITEMS], const bool (&has)[ITEMS],
+                                                uint16_t (*cnt)[kBins], uint32_t (&rank)[ITEMS]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int d = lane; d < kBins; d += 32) cnt[warp][d] = 0;
+  uint32_t* mine = reinterpret_cast<uint32_t*>(cnt[warp]);
+#pragma unroll
+  for (int d = 0; d < kBins / 64; ++d) mine[d * 32 + lane] = 0;
   __syncwarp();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     const uint32_t key = has[k] ? digit[k] : kBins + 1;
     const uint32_t mask = __match_any_sync(0xffffffffu, key);
     const uint32_t before = has[k] ? cnt[warp][digit[k]] : 0u;
@@ -161,18 +170,22 @@ __device__ __forceinline__ uint32_t block_ranks(const uint32_t (&digit)[kSortIte
   }
   __syncthreads();
   uint32_t total = 0;
-  if (threadIdx.x < kBins)
+  if (threadIdx.x < kBins) {
+    uint32_t c[kSortThreads / 32];
+#pragma unroll
+    for (int w = 0; w < kSortThreads / 32; ++w) c[w] = cnt[w][threadIdx.x];
+#pragma unroll
     for (int w = 0; w < kSortThreads / 32; ++w) {
-      const uint32_t c = cnt[w][threadIdx.x];
       cnt[w][threadIdx.x] = static_cast<uint16_t>(total);
-      total += c;
+      total += c[w];
     }
+  }
   __syncthreads();
   return total;
 }
 
-// Exclusive scan of the first kBins threads' values (others pass 0).
-__device__ __forceinline__ uint32_t scan_bins(uint32_t v, uint32_t* tmp) {
+// Exclusive scan over the block's threads.
+__device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* tmp) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t s = v;
 #pragma unroll
@@ -197,62 +210,102 @@ __device__ __forceinline__ uint32_t scan_bins(uint32_t v, uint32_t* tmp) {
   return out;
 }
 
-struct SmallSort {
+// Bit v of the map: some entry names row v.  Set where a key differs from the
+// one before it in the sorted list, so once for each row.
+__device__ __forceinline__ void mark_row(const EmbedBackward& E, uint32_t key, uint32_t before, bool first) {
+  if (key < static_cast<uint32_t>(E.ids.vocab) && (first || before != key))
+    atomicOr(E.present + (key >> 5), 1u << (key & 31));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Up to kOneLaunch entries: the whole sort in one launch of one cluster.  The
+// CTAs read one another's digit counts through distributed shared memory, and
+// the cluster barriers order the pairs that move through global memory.  With
+// 8192 ids of a 128256-row table that is 8 us, where a histogram, a scan and a
+// scatter for each pass took 28.
+struct ClusterSort {
   uint16_t cnt[kSortThreads / 32][kBins];
-  uint32_t key[kSortTile], pos[kSortTile];
+  uint32_t hist[2][kBins];
   uint32_t base[kBins];
   uint32_t tmp[32];
 };
 
-// Up to kSortTile entries: the whole sort in one block.
-__global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(const EmbedBackward E, int passes, int bits) {
-  extern __shared__ uint8_t smem_raw[];
-  SmallSort& S = *reinterpret_cast<SmallSort*>(smem_raw);
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(const EmbedBackward E, int passes, int bits) {
+  __shared__ ClusterSort S;
   const int n = static_cast<int>(E.n);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t key[kSortItems], pos[kSortItems], digit[kSortItems], rank[kSortItems];
-  bool has[kSortItems];
+  const int rank_in_cluster = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(gridDim.x);
+  const int first = (rank_in_cluster * kSortThreads + warp * 32) * ITEMS + lane;
+  uint32_t key[ITEMS], pos[ITEMS], digit[ITEMS], rank[ITEMS];
+  bool has[ITEMS];
+  pdl_launch();
+  pdl_wait();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = warp * 32 * kSortItems + 32 * k + lane;
+  for (int k = 0; k < ITEMS; ++k) {
+    const int i = first + 32 * k;
     has[k] = i < n;
     pos[k] = static_cast<uint32_t>(i);
     key[k] = has[k] ? first_key(E, i) : 0u;
   }
+  if (E.present) {
+    const int words = (E.ids.vocab + 31) / 32;
+    for (int i = rank_in_cluster * kSortThreads + static_cast<int>(threadIdx.x); i < words; i += ctas * kSortThreads) E.present[i] = 0u;
+  }
   for (int p = 0; p < passes; ++p) {
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) digit[k] = (key[k] >> (p * bits)) & ((1u << bits) - 1u);
-    const uint32_t total = block_ranks(digit, has, S.cnt, rank);
-    const uint32_t b = scan_bins(threadIdx.x < kBins ? total : 0u, S.tmp);
-    if (threadIdx.x < kBins) S.base[threadIdx.x] = b;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kSortItems; ++k)
-      if (has[k]) {
-        const uint32_t to = S.base[digit[k]] + S.cnt[warp][digit[k]] + rank[k];
-        S.key[to] = key[k];
-        S.pos[to] = pos[k];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-      const int i = warp * 32 * kSortItems + 32 * k + lane;
-      if (has[k]) {
-        key[k] = S.key[i];
-        pos[k] = S.pos[i];
+    for (int k = 0; k < ITEMS; ++k) digit[k] = (key[k] >> (p * bits)) & ((1u << bits) - 1u);
+    const uint32_t mine = block_ranks<ITEMS>(digit, has, S.cnt, rank);
+    uint32_t* hist = S.hist[p & 1];
+    if (threadIdx.x < kBins) hist[threadIdx.x] = mine;
+    cluster_sync_all();
+    uint32_t before = 0, total = 0;
+    if (threadIdx.x < kBins) {
+      const uint32_t at = smem_u32(hist + threadIdx.x);
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t c = ld_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(r)));
+        before += r < rank_in_cluster ? c : 0u;
+        total += c;
       }
     }
+    const uint32_t b = scan_threads(total, S.tmp);
+    if (threadIdx.x < kBins) S.base[threadIdx.x] = b + before;
     __syncthreads();
-  }
+    const int to_buf = p & 1;
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = warp * 32 * kSortItems + 32 * k + lane;
-    if (has[k]) {
-      E.key[0][i] = key[k];
-      E.pos[0][i] = pos[k];
+    for (int k = 0; k < ITEMS; ++k)
+      if (has[k]) {
+        const uint32_t to = S.base[digit[k]] + S.cnt[warp][digit[k]] + rank[k];
+        __stcg(E.key[to_buf] + to, key[k]);
+        __stcg(E.pos[to_buf] + to, pos[k]);
+      }
+    __syncwarp();
+    cluster_sync_all();  // every CTA's pairs are in place; every read of hist[p & 1] is done
+    if (p + 1 < passes) {
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k)
+        if (has[k]) {
+          key[k] = __ldcg(E.key[to_buf] + first + 32 * k);
+          pos[k] = __ldcg(E.pos[to_buf] + first + 32 * k);
+        }
+    }
+  }
+  if (E.present) {
+    const uint32_t* sorted = E.key[(passes - 1) & 1];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int i = first + 32 * k;
+      if (i < n) mark_row(E, __ldcg(sorted + i), i > 0 ? __ldcg(sorted + i - 1) : 0u, i == 0);
     }
   }
 }
+
+constexpr int kSortItems = kSortTile / kSortThreads;
 
 // Longer lists: per pass a histogram of each block, a scan over the blocks of
 // each digit, and the scatter.  hist[digit][block]; hist[kBins * blocks + digit]: totals.
@@ -260,6 +313,13 @@ __global__ void __launch_bounds__(kSortThreads) embed_hist_kernel(const EmbedBac
   __shared__ uint32_t h[kBins];
   for (int d = threadIdx.x; d < kBins; d += kSortThreads) h[d] = 0;
   __syncthreads();
+  pdl_launch();
+  pdl_wait();
+  if (pass == 0 && E.present) {
+    const int64_t words = (E.ids.vocab + 31) / 32;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+      E.present[i] = 0u;
+  }
   for (int k = 0; k < kSortItems; ++k) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kSortTile + k * kSortThreads + threadIdx.x;
     if (i < E.n) {
@@ -274,12 +334,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_hist_kernel(const EmbedBac
 __global__ void __launch_bounds__(kSortThreads) embed_scan_kernel(uint32_t* hist, int blocks) {
   __shared__ uint32_t tmp[32];
   __shared__ uint32_t chunk;
+  pdl_launch();
+  pdl_wait();
   uint32_t* h = hist + static_cast<int64_t>(blockIdx.x) * blocks;
   uint32_t base = 0;
   for (int b0 = 0; b0 < blocks; b0 += kSortThreads) {
     const int b = b0 + threadIdx.x;
     const uint32_t v = b < blocks ? h[b] : 0u;
-    const uint32_t s = scan_bins(v, tmp);
+    const uint32_t s = scan_threads(v, tmp);
     if (b < blocks) h[b] = base + s;
     if (threadIdx.x == kSortThreads - 1) chunk = s + v;
     __syncthreads();
@@ -297,6 +359,8 @@ struct Scatter {
 
 __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const EmbedBackward E, int pass, int bits, int from) {
   __shared__ Scatter S;
+  pdl_launch();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + warp * 32 * kSortItems + lane;
   uint32_t key[kSortItems], pos[kSortItems], digit[kSortItems], rank[kSortItems];
@@ -313,9 +377,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const Embed
     digit[k] = (key[k] >> (pass * bits)) & ((1u << bits) - 1u);
   }
   const uint32_t total = threadIdx.x < kBins ? E.hist[static_cast<int64_t>(kBins) * gridDim.x + threadIdx.x] : 0u;
-  const uint32_t b = scan_bins(total, S.tmp);
+  const uint32_t b = scan_threads(total, S.tmp);
   if (threadIdx.x < kBins) S.base[threadIdx.x] = b + E.hist[static_cast<int64_t>(threadIdx.x) * gridDim.x + blockIdx.x];
-  block_ranks(digit, has, S.cnt, rank);
+  block_ranks<kSortItems>(digit, has, S.cnt, rank);
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k)
     if (has[k]) {
@@ -325,15 +389,24 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const Embed
     }
 }
 
+__global__ void __launch_bounds__(kSortThreads) embed_mark_kernel(const EmbedBackward E, int from) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x;
+  if (i < E.n) mark_row(E, E.key[from][i], i > 0 ? E.key[from][i - 1] : 0u, i == 0);
+}
+
 // ----------------------------------------------------------------------- sums
 struct Runs {
   const uint32_t* key;
   const uint32_t* pos;
+  int32_t run;        // sorted positions of a run, a multiple of 4
   int64_t n_runs;
+  int32_t col_blocks;
   int64_t ld_part;
 };
 
-// VEC columns a thread; blockIdx.x is the run, blockIdx.y the column block.
+// Adds to, or writes, VEC columns of a row.
 template <bool DB, bool GB, int VEC>
 __device__ __forceinline__ void put_row(const EmbedBackward& E, uint32_t id, int c, const float (&acc)[VEC]) {
   void* dst = at<GB>(E.dtable, static_cast<int64_t>(id) * E.ld_dtable + c);
@@ -353,25 +426,60 @@ __device__ __forceinline__ void put_row(const EmbedBackward& E, uint32_t id, int
   }
 }
 
+// Zeros into the rows [r0, r0 + kZeroRows) that no entry names, by one warp.
+constexpr int kZeroRows = 8;
+
+template <bool GB, bool VEC>
+__device__ __forceinline__ void zero_rows(const EmbedBackward& E, int64_t r0, int lane) {
+  if (r0 >= E.ids.vocab) return;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), E.ids.vocab - r0));
+  uint32_t left = (~__ldcg(E.present + (r0 >> 5)) >> (r0 & 31)) & ((1u << rows) - 1u);
+  while (left) {
+    const int k = __ffs(left) - 1;
+    left &= left - 1;
+    void* dst = at<GB>(E.dtable, (r0 + k) * E.ld_dtable);
+    if (VEC) {
+      const int n16 = E.dim / (GB ? 8 : 4);
+#pragma unroll 4
+      for (int c = lane; c < n16; c += 32) static_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = lane; c < E.dim; c += 32) store1<GB>(at<GB>(dst, c), 0.f);
+    }
+  }
+}
+
+// VEC columns a thread.  n_runs * col_blocks blocks take a run and a column
+// block each, four rows in flight; the others, spread evenly among them so
+// that reads and writes share the memory all along, write zeros.
 template <bool DB, bool GB, int VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBackward E, const Runs R) {
   __shared__ uint32_t keys[kEmbedRun + 2], pos[kEmbedRun];
-  const int64_t run = blockIdx.x;
-  const int64_t p0 = run * kEmbedRun;
+  pdl_launch();
+  pdl_wait();
+  const uint64_t sums = static_cast<uint64_t>(R.n_runs) * R.col_blocks, all = gridDim.x;
+  const uint64_t task = blockIdx.x * sums / all;  // sums in the blocks before this one
+  if ((blockIdx.x + 1) * sums / all == task) {
+    const int64_t zero = static_cast<int64_t>(blockIdx.x - task);
+    zero_rows<GB, VEC == 8>(E, (zero * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kZeroRows, threadIdx.x & 31);
+    return;
+  }
+  const int64_t run = static_cast<int64_t>(task) / R.col_blocks;
+  const int col_block = static_cast<int>(static_cast<int64_t>(task) - run * R.col_blocks);
+  const int64_t p0 = run * R.run;
   const uint32_t none = 0xffffffffu, dropped = static_cast<uint32_t>(E.ids.vocab);
-  for (int k = threadIdx.x; k < kEmbedRun + 2; k += blockDim.x) {
+  for (int k = threadIdx.x; k < R.run + 2; k += blockDim.x) {
     const int64_t p = p0 + k - 1;
-    keys[k] = p >= 0 && p < E.n ? R.key[p] : none;
-    if (k >= 1 && k <= kEmbedRun && p < E.n) pos[k - 1] = R.pos[p];
+    keys[k] = p >= 0 && p < E.n ? __ldcg(R.key + p) : none;
+    if (k >= 1 && k <= R.run && p < E.n) pos[k - 1] = __ldcg(R.pos + p);
   }
   __syncthreads();
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  const int c = (col_block * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * VEC;
   if (c >= E.dim) return;
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
   int seg0 = 0;
-  for (int k0 = 0; k0 < kEmbedRun; k0 += 4) {
+  for (int k0 = 0; k0 < R.run; k0 += 4) {
     float v[4][VEC];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -391,7 +499,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBackward E, c
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[j] += v[u][j];
       const bool ends = keys[k + 2] != id;
-      if (!ends && k + 1 < kEmbedRun) continue;
+      if (!ends && k + 1 < R.run) continue;
       const bool from_before = seg0 == 0 && keys[0] == id;
       if (ends && !from_before) {
         put_row<DB, GB, VEC>(E, id, c, acc);
@@ -410,96 +518,95 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedBackward E, c
 // Joins an id that crosses cuts: run's tail, then the heads of the runs after it.
 template <bool DB, bool GB, int VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBackward E, const Runs R) {
-  const int64_t run = blockIdx.x;
-  const int64_t next = (run + 1) * kEmbedRun;
+  pdl_launch();
+  pdl_wait();
+  const int64_t run = blockIdx.x / R.col_blocks;
+  const int64_t p0 = run * R.run, next = p0 + R.run;
   if (next >= E.n) return;
-  const uint32_t id = R.key[next];
-  if (id >= static_cast<uint32_t>(E.ids.vocab) || R.key[next - 1] != id) return;
-  const int64_t p0 = run * kEmbedRun;
-  if (R.key[p0] == id && p0 > 0 && R.key[p0 - 1] == id) return;  // began in an earlier run
+  const uint32_t id = R.key[next], last = R.key[next - 1], head_key = R.key[p0], before = p0 > 0 ? R.key[p0 - 1] : 0xffffffffu;
+  if (id >= static_cast<uint32_t>(E.ids.vocab) || last != id) return;
+  if (head_key == id && before == id) return;  // began in an earlier run
   int64_t heads = 0;
   for (;;) {
-    const int64_t p = next + (heads + threadIdx.x) * kEmbedRun;
+    const int64_t p = next + (heads + threadIdx.x) * R.run;
     const int more = __syncthreads_count(p < E.n && R.key[p] == id);
     heads += more;
     if (more < static_cast<int>(blockDim.x)) break;
   }
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  const int c = (static_cast<int>(blockIdx.x - run * R.col_blocks) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * VEC;
   if (c >= E.dim) return;
   float acc[VEC];
   const float* tail = E.partial + (2 * run + 1) * R.ld_part + c;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = tail[j];
   const float* head = E.partial + 2 * (run + 1) * R.ld_part + c;
-#pragma unroll 4
-  for (int64_t h = 0; h < heads; ++h)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] += head[2 * h * R.ld_part + j];
-  put_row<DB, GB, VEC>(E, id, c, acc);
-}
-
-// Rows that no entry names become zeros.  A warp takes 32 rows: each lane looks
-// its row up in the sorted list, then the warp writes the absent ones.
-template <bool GB, bool VEC>
-__global__ void __launch_bounds__(256) embed_zero_kernel(const EmbedBackward E, const Runs R) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * 32;
-  if (r0 >= E.ids.vocab) return;
-  const int64_t row = r0 + lane;
-  int64_t lo = 0, hi = E.n;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(R.key[mid]) < row)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  const bool absent = row < E.ids.vocab && !(lo < E.n && static_cast<int64_t>(R.key[lo]) == row);
-  uint32_t left = __ballot_sync(0xffffffffu, absent);
-  while (left) {
-    const int k = __ffs(left) - 1;
-    left &= left - 1;
-    void* dst = at<GB>(E.dtable, (r0 + k) * E.ld_dtable);
-    if (VEC) {
-      const int n16 = E.dim / (GB ? 8 : 4);
-      for (int c = lane; c < n16; c += 32) static_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
+  for (int64_t h = 0; h < heads; ++h) {
+    if (VEC == 8) {
+      const float4 a = *reinterpret_cast<const float4*>(head + 2 * h * R.ld_part);
+      const float4 b = *reinterpret_cast<const float4*>(head + 2 * h * R.ld_part + 4);
+      acc[0] += a.x; acc[1 % VEC] += a.y; acc[2 % VEC] += a.z; acc[3 % VEC] += a.w;
+      acc[4 % VEC] += b.x; acc[5 % VEC] += b.y; acc[6 % VEC] += b.z; acc[7 % VEC] += b.w;
     } else {
-      for (int c = lane; c < E.dim; c += 32) store1<GB>(at<GB>(dst, c), 0.f);
+      acc[0] += head[2 * h * R.ld_part];
     }
   }
+  put_row<DB, GB, VEC>(E, id, c, acc);
 }
 
 inline bool aligned16_rows(const void* p, int64_t ld, int bf16, int dim) {
   return dim % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * (bf16 ? 2 : 4) % 16 == 0;
 }
 
+// Positions of a run: short lists in short runs, so that about two blocks per SM
+// share the memory latency; 64 at most, which bounds the partials at a 32nd of
+// the rows read.
+int run_length(int64_t n, int col_blocks) {
+  int run = 4;
+  while (run < kEmbedRun && n * col_blocks > static_cast<int64_t>(304) * 2 * run) run *= 2;
+  return run;
+}
+
+int sum_threads(int64_t width) { return static_cast<int>(width >= 256 ? 256 : (width + 31) / 32 * 32); }
+
 template <bool DB, bool GB>
-cudaError_t launch_sums(const EmbedBackward& E, const Runs& R, int* launches, cudaStream_t st) {
+cudaError_t launch_sums(const EmbedBackward& E, Runs R, int* launches, cudaStream_t st) {
   const bool vec = aligned16_rows(E.dout, E.ld_dout, DB, E.dim) && aligned16_rows(E.dtable, E.ld_dtable, GB, E.dim);
-  const int width = (E.dim + (vec ? 7 : 0)) / (vec ? 8 : 1);
-  const int threads = width >= 256 ? 256 : (width + 31) / 32 * 32;
-  const dim3 grid(static_cast<unsigned>(R.n_runs), static_cast<unsigned>((width + threads - 1) / threads));
-  if (!E.accumulate) {
-    const unsigned blocks = static_cast<unsigned>((E.ids.vocab + 255) / 256);
-    if (vec)
-      embed_zero_kernel<GB, true><<<blocks, 256, 0, st>>>(E, R);
-    else
-      embed_zero_kernel<GB, false><<<blocks, 256, 0, st>>>(E, R);
-    ++*launches;
-  }
-  if (vec)
-    embed_sum_kernel<DB, GB, 8><<<grid, threads, 0, st>>>(E, R);
-  else
-    embed_sum_kernel<DB, GB, 1><<<grid, threads, 0, st>>>(E, R);
+  const int width = vec ? E.dim / 8 : E.dim;
+  const int threads = sum_threads(width);
+  R.col_blocks = (width + threads - 1) / threads;
+  R.run = run_length(E.n, R.col_blocks);
+  R.n_runs = (E.n + R.run - 1) / R.run;
+  const int64_t sums = R.n_runs * R.col_blocks;
+  const int64_t rows_per_block = threads / 32 * kZeroRows;
+  const int64_t zeros = E.present ? (E.ids.vocab + rows_per_block - 1) / rows_per_block : 0;
+  cudaError_t e = launch_after(vec ? embed_sum_kernel<DB, GB, 8> : embed_sum_kernel<DB, GB, 1>,
+                               dim3(static_cast<unsigned>(sums + zeros)), dim3(threads), 0, st, E, R);
   ++*launches;
-  if (R.n_runs > 1) {
-    if (vec)
-      embed_join_kernel<DB, GB, 8><<<grid, threads, 0, st>>>(E, R);
-    else
-      embed_join_kernel<DB, GB, 1><<<grid, threads, 0, st>>>(E, R);
+  if (e == cudaSuccess && R.n_runs > 1) {
+    e = launch_after(vec ? embed_join_kernel<DB, GB, 8> : embed_join_kernel<DB, GB, 1>, dim3(static_cast<unsigned>(sums)),
+                     dim3(threads), 0, st, E, R);
     ++*launches;
   }
-  return cudaGetLastError();
+  return e;
+}
+
+// One launch of a cluster of `ctas` blocks.
+cudaError_t launch_cluster_sort(void (*kernel)(EmbedBackward, int, int), int ctas, cudaStream_t st, const EmbedBackward& E,
+                                int passes, int bits) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, E, passes, bits);
 }
 
 template <bool TB, bool OB>
@@ -508,11 +615,8 @@ cudaError_t launch_forward(const EmbedForward& E, cudaStream_t st) {
   const int64_t tasks = E.n * ((E.dim + kFwdCols - 1) / kFwdCols);
   const int64_t blocks = (tasks + 7) / 8;
   const unsigned grid = static_cast<unsigned>(blocks < 152 * 64 ? blocks : 152 * 64);
-  if (vec)
-    embed_forward_kernel<TB, OB, true><<<grid, 256, 0, st>>>(E);
-  else
-    embed_forward_kernel<TB, OB, false><<<grid, 256, 0, st>>>(E);
-  return cudaGetLastError();
+  return launch_after(vec ? embed_forward_kernel<TB, OB, true> : embed_forward_kernel<TB, OB, false>, dim3(grid), dim3(256), 0,
+                      st, E);
 }
 
 }  // namespace
@@ -522,7 +626,7 @@ cudaError_t launch_embed_forward(const EmbedForward& E, cudaStream_t st) {
   return E.out_bf16 ? launch_forward<false, true>(E, st) : launch_forward<false, false>(E, st);
 }
 
-EmbedWs embed_backward_ws(int64_t n, int32_t dim) {
+EmbedWs embed_backward_ws(int64_t n, int64_t vocab, int32_t dim) {
   EmbedWs W{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -530,12 +634,21 @@ EmbedWs embed_backward_ws(int64_t n, int32_t dim) {
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  const int64_t blocks = (n + kSortTile - 1) / kSortTile, runs = (n + kEmbedRun - 1) / kEmbedRun;
+  const int64_t blocks = n <= kOneLaunch ? 0 : (n + kSortTile - 1) / kSortTile;
+  // Runs as launch_sums cuts them, for whichever vector width it takes.
+  int64_t runs = 0;
+  for (const int64_t width : {static_cast<int64_t>(dim), static_cast<int64_t>(dim) / 8}) {
+    if (width < 1) continue;
+    const int threads = sum_threads(width);
+    const int run = run_length(n, static_cast<int>((width + threads - 1) / threads));
+    if ((n + run - 1) / run > runs) runs = (n + run - 1) / run;
+  }
   for (int k = 0; k < 2; ++k) {
     W.key[k] = take(static_cast<size_t>(n) * 4);
     W.pos[k] = take(static_cast<size_t>(n) * 4);
   }
   W.hist = take(static_cast<size_t>(kBins) * static_cast<size_t>(blocks + 1) * 4);
+  W.present = take(static_cast<size_t>((vocab + 31) / 32) * 4);
   W.partial = take(static_cast<size_t>(runs) * 2 * static_cast<size_t>((dim + 7) / 8 * 8) * 4);
   W.bytes = off;
   return W;
@@ -546,33 +659,39 @@ cudaError_t launch_embed_backward(const EmbedBackward& E, int* launches, cudaStr
   int key_bits = 1;
   while ((int64_t(1) << key_bits) <= E.ids.vocab) ++key_bits;  // keys 0 .. vocab
   const int passes = (key_bits + 8) / 9, bits = (key_bits + passes - 1) / passes;
-  int from = 0;
-  if (E.n <= kSortTile) {
-    static unsigned long long attr_mask = 0;
-    if (attr_needed_on_current_device(&attr_mask)) {
-      cudaError_t e = cudaFuncSetAttribute(embed_sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(sizeof(SmallSort)));
-      if (e != cudaSuccess) return e;
-      attr_note_current_device(&attr_mask);
-    }
-    embed_sort_small_kernel<<<1, kSortThreads, sizeof(SmallSort), st>>>(E, passes, bits);
+  int sorted = (passes - 1) & 1;
+  cudaError_t e = cudaSuccess;
+  if (E.n <= kOneLaunch) {
+    // One entry a thread while the cluster has room for more blocks.
+    int ctas = 1, items = 1;
+    while (ctas < kClusterMost && ctas * kSortThreads < E.n) ctas *= 2;
+    while (ctas * kSortThreads * items < E.n) items *= 2;
+    e = launch_cluster_sort(items == 1   ? embed_sort_cluster_kernel<1>
+                            : items == 2 ? embed_sort_cluster_kernel<2>
+                            : items == 4 ? embed_sort_cluster_kernel<4>
+                                         : embed_sort_cluster_kernel<8>,
+                            ctas, st, E, passes, bits);
     ++*launches;
   } else {
-    const int blocks = static_cast<int>((E.n + kSortTile - 1) / kSortTile);
-    for (int p = 0; p < passes; ++p) {
-      embed_hist_kernel<<<blocks, kSortThreads, 0, st>>>(E, p, bits, from);
-      embed_scan_kernel<<<kBins, kSortThreads, 0, st>>>(E.hist, blocks);
-      embed_scatter_kernel<<<blocks, kSortThreads, 0, st>>>(E, p, bits, from);
+    const dim3 blocks(static_cast<unsigned>((E.n + kSortTile - 1) / kSortTile)), threads(kSortThreads);
+    int from = 1;
+    for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+      e = launch_after(embed_hist_kernel, blocks, threads, 0, st, E, p, bits, from);
+      if (e == cudaSuccess) e = launch_after(embed_scan_kernel, dim3(kBins), threads, 0, st, E.hist, static_cast<int>(blocks.x));
+      if (e == cudaSuccess) e = launch_after(embed_scatter_kernel, blocks, threads, 0, st, E, p, bits, from);
       from ^= 1;
       *launches += 3;
     }
+    sorted = from;
+    if (E.present && e == cudaSuccess) {
+      e = launch_after(embed_mark_kernel, dim3(static_cast<unsigned>((E.n + kSortThreads - 1) / kSortThreads)), threads, 0, st, E, from);
+      ++*launches;
+    }
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  Runs R;
-  R.key = E.key[from];
-  R.pos = E.pos[from];
-  R.n_runs = (E.n + kEmbedRun - 1) / kEmbedRun;
+  Runs R = {};
+  R.key = E.key[sorted];
+  R.pos = E.pos[sorted];
   R.ld_part = (E.dim + 7) / 8 * 8;
   if (E.dout_bf16)
     return E.dtable_bf16 ? launch_sums<true, true>(E, R, launches, st) : launch_sums<true, false>(E, R, launches, st);

@@ -636,7 +636,7 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
                                 static_cast<size_t>(A.dim * table_elem), static_cast<size_t>(A.vocab), s));
     return DMUON_OK;
   }
-  const EmbedWs W = embed_backward_ws(A.n_tokens, static_cast<int32_t>(A.dim));
+  const EmbedWs W = embed_backward_ws(A.n_tokens, A.vocab, static_cast<int32_t>(A.dim));
   DM_TRY(vocab_workspace(ctx, W.bytes, s));
   char* ws = static_cast<char*>(ctx->vocab_ws.p);
   EmbedBackward E = {};
@@ -657,6 +657,7 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
     E.pos[k] = reinterpret_cast<uint32_t*>(ws + W.pos[k]);
   }
   E.hist = reinterpret_cast<uint32_t*>(ws + W.hist);
+  E.present = add ? nullptr : reinterpret_cast<uint32_t*>(ws + W.present);
   E.partial = reinterpret_cast<float*>(ws + W.partial);
   int launches = 0;
   DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_embed_backward(E, &launches, s); }));

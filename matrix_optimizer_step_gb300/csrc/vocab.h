@@ -249,14 +249,15 @@ struct EmbedBackward {
   uint32_t* key[2];
   uint32_t* pos[2];
   uint32_t* hist;
+  uint32_t* present;  // one bit per table row: named by an entry; null when adding
   float* partial;
 };
-// Sorted positions that one block of the summing kernel takes.
+// Sorted positions that one block of the summing kernel takes at most.
 constexpr int kEmbedRun = 64;
 struct EmbedWs {
-  size_t key[2], pos[2], hist, partial, bytes;
+  size_t key[2], pos[2], hist, present, partial, bytes;
 };
-EmbedWs embed_backward_ws(int64_t n, int32_t dim);
+EmbedWs embed_backward_ws(int64_t n, int64_t vocab, int32_t dim);
 // Enqueues the launches; *launches counts them.
 cudaError_t launch_embed_backward(const EmbedBackward& E, int* launches, cudaStream_t st);
 

@@ -421,3 +421,21 @@ def test_wrapper_checks(ops):
         ops.embed(t, x, torch.zeros(3, 16, device=DEV))
     with pytest.raises(ValueError):
         ops.embed(t, torch.zeros(1, 16, device=DEV, dtype=torch.bfloat16).expand(4, 16))
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 65536, 65537, 140000])
+@pytest.mark.parametrize("v", [300, 70001])
+def test_embed_backward_long_lists(ops, n, v):
+    # Both sorts (one launch up to 65536 entries), one and two digits; whole numbers, so sums are exact.
+    ids = ids_of("padded", n, v, seed=n).to(DEV)
+    dout = torch.randint(-8, 9, (n, 8), device=DEV).float()
+    table = torch.full((v, 8), 7.0, device=DEV)
+    ops.embed_grad(ids, dout, table)
+    ops.sync()
+    want = torch.zeros(v, 8, device=DEV, dtype=torch.float64)
+    keep = ids >= 0
+    want.index_add_(0, ids[keep], dout[keep].double())
+    assert torch.equal(table.double(), want)
+    ops.embed_grad(ids, dout, table, accumulate=True)
+    ops.sync()
+    assert torch.equal(table.double(), 2 * want)
