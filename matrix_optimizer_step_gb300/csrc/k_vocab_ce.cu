@@ -15,14 +15,9 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-__device__ __forceinline__ float weight_of(const IdList& T, const float* weights, int64_t i, bool* bad) {
-  return load_id(T, i, bad) < 0 ? 0.f : weights ? __ldg(weights + i) : 1.f;
-}
-
 // Sum over the block's threads in a fixed order; the result is in thread 0.
 __device__ __forceinline__ double block_sum(double v, double* smem) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
+  v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -30,6 +25,14 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
   if (threadIdx.x == 0)
     for (unsigned w = 0; w < blockDim.x / 32; ++w) s += smem[w];
   return s;
+}
+
+__global__ void __launch_bounds__(1024) ce_norm_kernel(const CeNorm N) {
+  __shared__ double red[32];
+  pdl_launch();
+  pdl_wait();
+  const double sum = block_sum(norm_share(N, threadIdx.x, blockDim.x), red);
+  if (threadIdx.x == 0) put_alpha(N, sum);
 }
 
 // --------------------------------------------------------------- operand copy
@@ -40,7 +43,14 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int col
     for (int c = lane * 8; c < cols; c += 256)
       *reinterpret_cast<uint4*>(d + c) = keep ? __ldg(reinterpret_cast<const uint4*>(s + c)) : make_uint4(0, 0, 0, 0);
   } else {
-    for (int c = lane; c < ld_dst; c += 32) d[c] = keep && c < cols ? s[c] : uint16_t(0);
+    for (int c0 = lane; c0 < ld_dst; c0 += 256) {
+      uint16_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = keep && c0 + 32 * k < cols ? s[c0 + 32 * k] : uint16_t(0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c0 + 32 * k < ld_dst) d[c0 + 32 * k] = v[k];
+    }
   }
 }
 
@@ -52,6 +62,78 @@ __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps)
     copy_row<VEC>(src + row * ld_src, dst + row * ld_dst, cols, static_cast<int>(ld_dst), true, threadIdx.x & 31);
+}
+
+// ------------------------------------------------------------------- d logits
+//   dz = weight (2^(m_b - lse - q / 1024) - [v = target])
+// with the weight folded into the exponent; the factor common to all rows stays
+// out, so that without weights a target's dz is rounded next to 1, not next to
+// 1 / (number of tokens).  Eight entries (16 bytes) a thread, four at a time:
+// 7.0 TB/s read and written at 4096 x 50257.
+// LO: also the rest of the rounding, for the rows below.
+constexpr int kDlThreads = 256;
+constexpr int kDlCols = kDlThreads * 8 * 4;
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Entries [chunk * kDlCols, + kDlCols) of one row; p: its logs; stats: its pairs.
+template <bool LO>
+__device__ __forceinline__ void dlogits_chunk(uint16_t* p, int64_t lo_offset, int vocab, int stats_shift, const float2* stats,
+                                              int64_t stats_ld, const CeRow& R, int chunk) {
+  const int c0 = chunk * kDlCols + threadIdx.x * 8;
+  const bool counted = R.weight != 0.f;  // else zeros, whatever the row's logits are
+  const float lift = log2f(fabsf(R.weight)) - R.lse2;
+  const uint32_t sign = __float_as_uint(R.weight) & 0x80000000u;
+  uint4 q[4];
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = c0 + k * kDlThreads * 8;
+    if (c < vocab) {
+      q[k] = *reinterpret_cast<const uint4*>(p + c);
+      m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = c0 + k * kDlThreads * 8;
+    if (c >= vocab) continue;
+    const float top = m[k] + lift;
+    const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = static_cast<float>(w[j] & 0xffffu);
+      v[2 * j + 1] = static_cast<float>(w[j] >> 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = __uint_as_float(__float_as_uint(ex2_approx(fmaf(v[j], -1.f / kCeLogUnits, top))) ^ sign);
+      if (c + j == R.target) v[j] = R.target_dz;
+      if (!counted) v[j] = 0.f;
+    }
+    *reinterpret_cast<uint4*>(p + c) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    if (LO)
+      *reinterpret_cast<uint4*>(p + lo_offset + c) =
+          make_uint4(pack_bf16x2_remainder(v[0], v[1]), pack_bf16x2_remainder(v[2], v[3]),
+                     pack_bf16x2_remainder(v[4], v[5]), pack_bf16x2_remainder(v[6], v[7]));
+  }
+}
+
+template <bool LO>
+__global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block, int64_t ld, int vocab, int stats_shift,
+                                                                const float2* stats, int64_t stats_ld,
+                                                                const CeRow* row_info, int64_t lo_rows) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t row = blockIdx.y;
+  const CeRow R = row_info[row];
+  dlogits_chunk<LO>(block + row * ld, lo_rows * ld, vocab, stats_shift, stats + row, stats_ld, R, blockIdx.x);
 }
 
 // ------------------------------------------------------------------- row sums
@@ -68,8 +150,11 @@ __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64
 // of pairs) and its 8 warps share their vocabulary blocks and their dot
 // products; what is left is a chain of memory latencies, so each is taken by
 // as many threads as there are.  All joins run in a fixed order.  The blocks
-// after those copy dW's operand.  The last of the row blocks joins the blocks'
-// sums of losses and weights.
+// after those copy dW's operand.
+//
+// DL, for few rows: `chunks` blocks take a row each, all of them find its sum
+// (a few KB from L2 again) and turn their part of its logs into d logits; the
+// first also does the rest.  That saves a launch and its latency.
 constexpr int kRowWarps = 8;
 
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
@@ -116,17 +201,19 @@ __device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, 
   return s;
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks) {
+template <bool VEC, bool DL>
+__global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks, int chunks) {
   __shared__ float sm[kRowWarps][4], ss[kRowWarps][4], dots[kRowWarps];
   __shared__ double red[32];
   __shared__ uint32_t last;
+  __shared__ CeRow info;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = R.width;
   pdl_launch();
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= row_blocks) {
-    const int64_t warps = static_cast<int64_t>(gridDim.x - row_blocks) * kRowWarps;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x - row_blocks) * kRowWarps + warp; r < R.rows; r += warps) {
+  const int copy0 = DL ? row_blocks * chunks : row_blocks;
+  if (static_cast<int>(blockIdx.x) >= copy0) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x - copy0) * kRowWarps;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x - copy0) * kRowWarps + warp; r < R.rows; r += warps) {
       bool bad = false;
       const bool keep = load_id(R.targets, R.row0 + r, &bad) >= 0;
       for (int k = 0; k < R.copies; ++k)
@@ -135,7 +222,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
     return;
   }
   if (blockIdx.x == 0 && threadIdx.x < 2) R.counters[threadIdx.x] = 0u;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * width;
+  const int row_block = DL ? static_cast<int>(blockIdx.x) / chunks : static_cast<int>(blockIdx.x);
+  const int chunk = DL ? static_cast<int>(blockIdx.x) - row_block * chunks : 0;
+  const int64_t base = static_cast<int64_t>(row_block) * width;
   const int shares = kRowWarps / width;
   const int64_t dot_row = base + warp / shares;
   bool bad = false;
@@ -186,7 +275,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
       for (int w = 1; w < kRowWarps; ++w) join(m, s, sm[w][lane], ss[w][lane]);
       const int64_t i = R.row0 + r;
       const int t = load_id(R.targets, i, &bad);
-      if (bad) atomicCAS(R.err, 0, kErrBadIndex);
+      if (bad && chunk == 0) atomicCAS(R.err, 0, kErrBadIndex);
       const float weight = t < 0 ? 0.f : R.weights ? __ldg(R.weights + i) : 1.f;
       float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
       if (t >= 0) {
@@ -200,28 +289,37 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
         lse2 = m + l2;
         share = rest / sum;
       }
-      if (R.loss) R.loss[i] = loss;
-      if (R.lse) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;
-      if (R.out) {
-        CeRow o;
-        o.lse2 = lse2;
-        o.weight = weight;
-        o.target_dz = -weight * share;
-        o.target = t;
+      if (R.loss && chunk == 0) R.loss[i] = loss;
+      if (R.lse && chunk == 0) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;
+      CeRow o;
+      o.lse2 = lse2;
+      o.weight = weight;
+      o.target_dz = -weight * share;
+      o.target = t;
+      if (DL)
+        info = o;
+      else if (R.out)
         R.out[r] = o;
-      }
       if (weight != 0.f) weighted = static_cast<double>(weight) * loss;
       weight_sum = weight;
     }
-    if (R.partial) {
+    if (R.partial && chunk == 0) {
       for (int o = 1; o < width; o <<= 1) {
         weighted += __shfl_xor_sync(0xffffffffu, weighted, o);
         weight_sum += __shfl_xor_sync(0xffffffffu, weight_sum, o);
       }
-      if (lane == 0) R.partial[R.row0 / width + blockIdx.x] = make_double2(weighted, weight_sum);
+      if (lane == 0) R.partial[R.row0 / width + row_block] = make_double2(weighted, weight_sum);
     }
   }
-  if (!R.total && !R.alpha) return;
+  if (DL) {
+    __syncthreads();
+    const CeRow o = info;
+    if (R.lo_rows > 0)
+      dlogits_chunk<true>(R.block + base * R.ld_block, R.lo_rows * R.ld_block, R.vocab, R.stats_shift, R.stats + base, R.stats_ld, o, chunk);
+    else
+      dlogits_chunk<false>(R.block + base * R.ld_block, 0, R.vocab, R.stats_shift, R.stats + base, R.stats_ld, o, chunk);
+  }
+  if (!R.total.total || chunk != 0) return;
   if (threadIdx.x == 0) {
     __threadfence();
     last = atomicAdd(R.ticket, 1u) == static_cast<uint32_t>(row_blocks) - 1u;
@@ -229,91 +327,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
   __syncthreads();
   if (!last) return;
   __threadfence();
-  const bool all = R.row0 + R.rows >= R.n;  // the partials of every row are there
-  double sum = 0.0, norm = 0.0;
-  if (all) {
-    const int64_t parts = (R.n + width - 1) / width;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < parts; i += blockDim.x) {
-      const double2 q = __ldcg(R.partial + i);
-      sum += q.x;
-      norm += q.y;
-    }
-    sum = block_sum(sum, red);
-  } else if (R.mean) {
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < R.n; i += blockDim.x) norm += weight_of(R.targets, R.weights, i, &bad);
-  }
-  if (R.mean) norm = block_sum(norm, red);
+  double2 sums = total_share(R.total, threadIdx.x, blockDim.x);
+  sums.x = block_sum(sums.x, red);
+  sums.y = block_sum(sums.y, red);
   if (threadIdx.x == 0) {
-    if (R.total) *R.total = static_cast<float>(!R.mean ? sum : norm != 0.0 ? sum / norm : 0.0);
-    if (R.alpha) *R.alpha = !R.mean ? R.scale : norm != 0.0 ? static_cast<float>(R.scale / norm) : 0.f;
+    put_total(R.total, sums);
     *R.ticket = 0u;
-  }
-}
-
-// ------------------------------------------------------------------- d logits
-//   dz = weight (2^(m_b - lse - q / 1024) - [v = target])
-// with the weight folded into the exponent; the factor common to all rows stays
-// out, so that without weights a target's dz is rounded next to 1, not next to
-// 1 / (number of tokens).  Eight entries (16 bytes) a thread, four at a time.
-// LO: also the rest of the rounding, for the rows below.
-constexpr int kDlThreads = 256;
-constexpr int kDlCols = kDlThreads * 8 * 4;
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <bool LO>
-__global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block, int64_t ld, int vocab, int stats_shift,
-                                                                const float2* stats, int64_t stats_ld,
-                                                                const CeRow* row_info, int64_t lo_rows) {
-  pdl_launch();
-  pdl_wait();
-  const int64_t row = blockIdx.y;
-  const CeRow R = row_info[row];
-  uint16_t* p = block + row * ld;
-  const int c0 = blockIdx.x * kDlCols + threadIdx.x * 8;
-  const bool counted = R.weight != 0.f;  // else zeros, whatever the row's logits are
-  const float lift = log2f(fabsf(R.weight)) - R.lse2;
-  const uint32_t sign = __float_as_uint(R.weight) & 0x80000000u;
-  uint4 q[4];
-  float m[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + k * kDlThreads * 8;
-    if (c < vocab) {
-      q[k] = *reinterpret_cast<const uint4*>(p + c);
-      m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld + row].x);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + k * kDlThreads * 8;
-    if (c >= vocab) continue;
-    const float top = m[k] + lift;
-    const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = static_cast<float>(w[j] & 0xffffu);
-      v[2 * j + 1] = static_cast<float>(w[j] >> 16);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = __uint_as_float(__float_as_uint(ex2_approx(fmaf(v[j], -1.f / kCeLogUnits, top))) ^ sign);
-      if (c + j == R.target) v[j] = R.target_dz;
-      if (!counted) v[j] = 0.f;
-    }
-    *reinterpret_cast<uint4*>(p + c) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    if (LO)
-      *reinterpret_cast<uint4*>(p + lo_rows * ld + c) =
-          make_uint4(pack_bf16x2_remainder(v[0], v[1]), pack_bf16x2_remainder(v[2], v[3]),
-                     pack_bf16x2_remainder(v[4], v[5]), pack_bf16x2_remainder(v[6], v[7]));
   }
 }
 
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64
       }
     };
     const float* p = part + r * ld_part + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < parts; ++k) {
       add(p + k * part_stride);
       if (fold > 0) add(p + k * part_stride + fold * ld_part);
@@ -380,27 +399,34 @@ cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, i
 }
 
 int ce_rows_width(int64_t n) { return n >= 512 ? 4 : 1; }
+bool ce_rows_make_dlogits(int64_t n) { return n <= 256; }
+
+cudaError_t launch_ce_norm(const CeNorm& N, cudaStream_t st) {
+  return launch_after(ce_norm_kernel, dim3(1), dim3(1024), 0, st, N);
+}
 
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st) {
   const int64_t row_blocks = (R.rows + R.width - 1) / R.width;
   const int64_t copy_blocks = R.x_copy ? (R.rows + kRowWarps - 1) / kRowWarps : 0;
   const bool vec = R.dim % 8 == 0 && R.ld_x % 8 == 0 && (reinterpret_cast<uintptr_t>(R.x) & 15u) == 0;
-  return launch_after(vec ? ce_rows_kernel<true> : ce_rows_kernel<false>, dim3(static_cast<unsigned>(row_blocks + copy_blocks)),
-                      dim3(kRowWarps * 32), 0, st, R, static_cast<int>(row_blocks));
+  const int chunks = R.block ? (R.vocab + kDlCols - 1) / kDlCols : 1;
+  static_assert(kDlThreads == kRowWarps * 32, "one block size");
+  auto kernel = R.block ? (vec ? ce_rows_kernel<true, true> : ce_rows_kernel<false, true>)
+                        : (vec ? ce_rows_kernel<true, false> : ce_rows_kernel<false, false>);
+  return launch_after(kernel, dim3(static_cast<unsigned>(row_blocks * chunks + copy_blocks)), dim3(kRowWarps * 32), 0, st, R,
+                      static_cast<int>(row_blocks), chunks);
 }
 
-cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_block,
+cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_shift,
                               const float2* stats, int64_t stats_ld, const CeRow* row_info, int64_t lo_rows,
                               cudaStream_t st) {
-  const int shift = stats_block == kCeThinBlock ? 5 : 7;
-  static_assert(kCeThinBlock == 32 && kCeBlock == 128, "block shifts");
   const int64_t per_launch = 65535;  // the grid's second dimension
   for (int64_t r = 0; r < rows; r += per_launch) {
     const int64_t n = rows - r < per_launch ? rows - r : per_launch;
     const dim3 grid(static_cast<unsigned>((vocab + kDlCols - 1) / kDlCols), static_cast<unsigned>(n));
     const cudaError_t e =
         launch_after(lo_rows > 0 ? ce_dlogits_kernel<true> : ce_dlogits_kernel<false>, grid, dim3(kDlThreads), 0, st,
-                     block + r * ld, ld, static_cast<int>(vocab), shift, stats + r, stats_ld, row_info + r, lo_rows);
+                     block + r * ld, ld, static_cast<int>(vocab), static_cast<int>(stats_shift), stats + r, stats_ld, row_info + r, lo_rows);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

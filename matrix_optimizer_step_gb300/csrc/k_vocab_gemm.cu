@@ -350,6 +350,55 @@ __device__ __forceinline__ void f32_epilogue(const VgProduct& P, uint32_t (&r)[4
   }
 }
 
+// Without TMA: the warp turns each 32 x 32 block around in shared memory, so
+// that a store instruction writes 32 neighbouring columns of one row.
+__device__ __forceinline__ void direct_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0, int warp_row0,
+                                                uint32_t staging, int lane) {
+  if (lane == 0) bulk_wait_group_read<0>();  // stores of the other product
+  const int rows = min(32, P.M - warp_row0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (col0 + 32 * i >= P.N) break;
+    const uint32_t buf = staging + 4096u * (i & 1);
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) st_shared_16(piece(buf, lane, p), r[i][4 * p], r[i][4 * p + 1], r[i][4 * p + 2], r[i][4 * p + 3]);
+    __syncwarp();
+    const int col = col0 + 32 * i + lane;
+    const int64_t at = static_cast<int64_t>(warp_row0) * P.ld_out + col;
+    uint16_t* h = static_cast<uint16_t*>(P.out) + at;
+    float* f = static_cast<float*>(P.out) + at;
+    if (col < P.N) {
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(piece(buf, r0 + k, lane >> 2) + 4u * (lane & 3)));
+          v[k] = alpha * __uint_as_float(w);
+        }
+        if (P.add) {
+          float old[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            old[k] = r0 + k >= rows ? 0.f : P.out_bf16 ? bf16_bits_to_f32(h[(r0 + k) * P.ld_out]) : f[(r0 + k) * P.ld_out];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += old[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (r0 + k >= rows) break;
+          if (P.out_bf16)
+            h[(r0 + k) * P.ld_out] = to_bf16_bits(v[k]);
+          else
+            f[(r0 + k) * P.ld_out] = v[k];
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // The parts of a tile's product that differ between the two kernels.
 __device__ __forceinline__ const CUtensorMap* operand_map(const VocabLogits& G, int, bool b) { return b ? &G.map_b : &G.map_a; }
 __device__ __forceinline__ const CUtensorMap* operand_map(const VocabGrad& G, int p, bool b) {
@@ -576,7 +625,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t r[4][32];
         load_columns(t_lane, r);
         release();
-        if (P.out_bf16)
+        if (P.direct)
+          direct_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);
+        else if (P.out_bf16)
           bf16_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);
         else
           f32_epilogue(P, r, alpha, col0, warp_row0, T.split, my_staging, lane);
@@ -586,6 +637,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 
+  if (warp == kSchedWarp && !leader && blockIdx.x == 1) {
+    // The other CTA's scheduling warp is free for the sums on the side.
+    if constexpr (LOGITS) {
+      if (G.norm.alpha) write_alpha(G.norm, lane);
+    } else {
+      if (G.total.total) write_total(G.total, lane);
+    }
+    __syncwarp();
+  }
   if (drawn && warp == kSchedWarp && leader && lane == 0) {
     // ------------------------------------------------------ tile numbers
     const int total = tiles_in(G);

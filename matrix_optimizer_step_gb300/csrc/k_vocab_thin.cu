@@ -6,7 +6,10 @@
 // ring holds almost nothing but W, 8 to 11 stages of it in flight per SM,
 // where the 256 x 256 tiles of k_vocab_gemm.cu would fill half of it with
 // rows past the last token.  One CTA per tile (tcgen05, cta_group::1),
-// persistent; warp 0 loads, warp 1 issues the MMAs, warps 2 to 5 drain.
+// persistent; warp 0 loads, warp 1 issues the MMAs, warps 2 to 5 drain, warp 6
+// sums the gradients' common factor on the side.
+// Memory sets the pace, not the SMs' shares: cutting the last round of tiles
+// evenly over the SMs, or halving the ring, changes nothing.
 //
 // A drained column is a token and a lane a row of W, so a token's statistics
 // go across lanes: 16 columns at a time are reduced together, each exchange
@@ -27,7 +30,7 @@ namespace dmuon {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 7 * 32;
 constexpr uint32_t A_BYTES = BM * BK * 2;
 constexpr uint32_t MN_BOX_BYTES = 64 * 64 * 2;
 constexpr int kMaxStages = 12;
@@ -169,10 +172,20 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   pdl_launch();
   pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
-  const int n_tiles = G.tiles_m * G.splits;
-  auto k_range = [&](int split, int& kb0, int& kb1) {
-    kb0 = split * G.kb_step;
-    kb1 = min(G.kb_total, kb0 + G.kb_step);
+  // Tile t of this CTA: rows [m0, m0 + 128) of D^T, k-blocks [kb0, kb1).
+  struct Tile {
+    int m0, split, kb0, kb1;
+  };
+  const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const int n_tiles = (G.tiles_m * G.splits - cta + ctas - 1) / ctas;
+  auto tile_at = [&](int t) {
+    const int u = cta + t * ctas;
+    Tile T;
+    T.split = LOGITS ? 0 : u / G.tiles_m;
+    T.m0 = (u - T.split * G.tiles_m) * BM;
+    T.kb0 = T.split * G.kb_step;
+    T.kb1 = min(G.kb_total, T.kb0 + G.kb_step);
+    return T;
   };
 
   if (warp == 0) {
@@ -183,11 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
       int stage = 0, filled = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-        const int split = t / G.tiles_m, m0 = (t - split * G.tiles_m) * BM;
-        int kb0, kb1;
-        k_range(split, kb0, kb1);
-        for (int kb = kb0; kb < kb1; ++kb) {
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        const Tile T = tile_at(t);
+        for (int kb = T.kb0; kb < T.kb1; ++kb) {
           if (!mbar_wait_bounded(empty(stage), phase ^ 1u, abort_flag, G.err, kErrTimeoutProducer)) {
             ok = false;
             break;
@@ -196,10 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
           mbar_expect_tx(full(stage), stage_bytes);
           ++filled;
           if (A_MN) {
-            tma_load(dst, &G.map_a, full(stage), m0, kb * BK);
-            tma_load(dst + MN_BOX_BYTES, &G.map_a, full(stage), m0 + 64, kb * BK);
+            tma_load(dst, &G.map_a, full(stage), T.m0, kb * BK);
+            tma_load(dst + MN_BOX_BYTES, &G.map_a, full(stage), T.m0 + 64, kb * BK);
           } else {
-            tma_load(dst, &G.map_a, full(stage), kb * BK, m0);
+            tma_load(dst, &G.map_a, full(stage), kb * BK, T.m0);
           }
           tma_load(dst + A_BYTES, &G.map_b, full(stage), kb * BK, 0);
           if (++stage == stages) {
@@ -218,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
         }
       }
     }
+  } else if (warp == 6) {
+    if (LOGITS && blockIdx.x == 0 && G.norm.alpha) write_alpha(G.norm, lane);
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------------------------------------------------- MMA issuer
@@ -225,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
       int stage = 0, use = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++use) {
-        int kb0, kb1;
-        k_range(t / G.tiles_m, kb0, kb1);
+      for (; use < n_tiles && ok; ++use) {
+        const Tile T = tile_at(use);
+        const int kb0 = T.kb0, kb1 = T.kb1;
         if (!mbar_wait_bounded(tempty(use & 1), (static_cast<uint32_t>(use >> 1) & 1u) ^ 1u, abort_flag, G.err, kErrTimeoutMma))
           break;
         tc_fence_after();
@@ -265,8 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;
     int use = 0;
-    for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++use) {
-      const int split = t / G.tiles_m, row0 = (t - split * G.tiles_m) * BM + 32 * quarter;
+    for (; use < n_tiles; ++use) {
+      const Tile T = tile_at(use);
+      const int split = T.split, row0 = T.m0 + 32 * quarter;
       const int acc = use & 1;
       if (!mbar_wait_bounded(tfull(acc), static_cast<uint32_t>(use >> 1) & 1u, abort_flag, G.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();

@@ -199,8 +199,8 @@ int encode_2d(EncodeTiledFn enc, CUtensorMap* map, const void* p, int64_t inner,
 }
 
 // A gradient's way out: written by its product, or as fp32 partials that a
-// further kernel joins (several parts of K, rows that TMA cannot write, two
-// halves to fold, or a bf16 sum over passes or onto what is there).
+// further kernel joins (several parts of K, two halves to fold, or a bf16 sum
+// over passes).
 struct Target {
   void* out = nullptr;
   int64_t ld = 0;
@@ -209,10 +209,6 @@ struct Target {
   float* part = nullptr;
   int64_t ld_part = 0;
 };
-
-bool writes_out(const void* out, int64_t ld, bool bf16, bool keep, bool one_pass) {
-  return tma_rows(out, ld, bf16 ? 2 : 4) && (!bf16 || (one_pass && !keep));
-}
 
 // Product D (m x n) = A B into T; `first`: first pass over the rows.
 int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_t k, bool a_mn, const void* a, int64_t ld_a,
@@ -230,11 +226,13 @@ int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_
     P->add = !first;
     return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.part, n, m, P->grid.splits, T.ld_part, m * T.ld_part, 32, 32);
   }
-  if (T.bf16) {
-    P->out_bf16 = 1;
-    return encode_2d(enc, &P->map_out, T.out, n, m, T.ld, 64, 32);
-  }
+  P->out_bf16 = T.bf16;
   P->add = T.keep || !first;
+  P->direct = !tma_rows(T.out, T.ld, T.bf16 ? 2 : 4) || (T.bf16 && P->add);
+  P->out = T.out;
+  P->ld_out = T.ld;
+  if (P->direct) return DMUON_OK;
+  if (T.bf16) return encode_2d(enc, &P->map_out, T.out, n, m, T.ld, 64, 32);
   return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.out, n, m, 1, T.ld, m * T.ld, 32, 32);
 }
 
@@ -274,7 +272,8 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const bool halves = grads && n <= kThinRows;
   const int64_t token_rows = halves ? 2 * n : rows;
   const bool thin = n <= kThinRows / 2;
-  const int stats_block = thin ? kCeThinBlock : kCeBlock;
+  const int stats_shift = thin ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
+  const bool rows_make_dlogits = grads && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
   const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
 
@@ -288,7 +287,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const size_t off_stats = L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float2));
   const size_t off_z = L.take(static_cast<size_t>(rows) * 4);
   const int width = ce_rows_width(n);
-  const size_t off_partial = grads || C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
+  const size_t off_partial = C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
   size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
   Target dx, dw;
   if (grads) {
@@ -302,7 +301,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       dw.ld = C.ld_dw;
       dw.bf16 = dw_bf16;
       dw.keep = add_dw;
-      dw_part = !writes_out(C.dw, C.ld_dw, dw_bf16, add_dw, one_pass);
+      dw_part = dw_bf16 && !one_pass;
       dw.splits = choose_splits(v, d, token_rows, 0.0, pairs, dw_part);
       dw_part = dw_part || dw.splits > 1;
       dw.ld_part = ld4;
@@ -311,7 +310,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     if (C.dx) {
       dx.bf16 = dx_bf16;
       dx.ld = C.ld_dx;
-      dx_part = halves || !writes_out(C.dx, C.ld_dx, dx_bf16, false, true);
+      dx_part = halves;
       if (thin) {
         // Tiles of 128 columns; parts of the vocabulary for a few tiles per SM.
         const int64_t tiles = (d + 127) / 128, kb = (v + 63) / 64;
@@ -362,6 +361,21 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
   uint32_t* counters = static_cast<uint32_t*>(ctx->vocab_ticket.p);  // two tile counters, one ticket
   const float scale_log2 = C.logit_scale * 1.4426950408889634f;
+  CeNorm norm = {};
+  norm.alpha = grads ? alpha : nullptr;
+  norm.targets = ids;
+  norm.weights = C.weights;
+  norm.n = n;
+  norm.mean = mean;
+  norm.scale = C.grad_scale * C.logit_scale;
+  double2* partial = C.total ? reinterpret_cast<double2*>(ws + off_partial) : nullptr;
+  const CeTotal total = {C.total, partial, (n + width - 1) / width, mean};
+  const bool side_sums = n <= kSideSums;
+  if (grads && !side_sums) {
+    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_norm(norm, s); }));
+    norm.alpha = nullptr;
+  }
+  const bool total_later = side_sums && (C.dw || (C.dx && !thin));  // the gradients' kernel writes it
 
   for (int64_t r0 = 0; r0 < n; r0 += rows) {
     const int64_t nr = std::min(rows, n - r0);
@@ -388,6 +402,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.stats_ld = stats_ld;
       G.target_z = target_z;
       G.targets = here;
+      if (first) G.norm = norm;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
     } else {
       VocabLogits G = {};
@@ -405,6 +420,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.target_z = target_z;
       G.targets = here;
       G.counter = counters;
+      if (first) G.norm = norm;
       G.drawn = G.grid.kb_total >= kDrawnBlocks;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_logits(G, pairs, s); }));
     }
@@ -426,31 +442,37 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     R.dim = static_cast<int32_t>(d);
     R.logit_scale_log2 = scale_log2;
     R.out = grads ? row_info : nullptr;
+    if (rows_make_dlogits) {
+      R.block = block;
+      R.ld_block = ld_block;
+      R.lo_rows = halves ? nr : 0;
+      R.vocab = static_cast<int32_t>(v);
+      R.stats_shift = stats_shift;
+    }
     R.loss = C.loss;
     R.lse = C.lse;
     R.x_copy = C.dw ? masked : nullptr;
     R.ld_copy = ld8;
     R.copies = halves ? 2 : 1;
     R.width = width;
-    R.partial = grads || C.total ? reinterpret_cast<double2*>(ws + off_partial) : nullptr;
-    R.alpha = grads && first ? alpha : nullptr;
-    R.scale = C.grad_scale * C.logit_scale;
-    R.total = last ? C.total : nullptr;
-    R.mean = mean;
+    R.partial = partial;
+    if (last && !total_later) R.total = total;
     R.ticket = counters + 2;
     R.counters = counters;
     R.err = err;
     DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_rows(R, s); }));
     if (!grads) continue;
 
-    DM_TRY(timed_launch(ctx, -1, s, [&] {
-      return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_block, stats, stats_ld, row_info,
-                               halves ? nr : 0, s);
-    }));
+    if (!rows_make_dlogits)
+      DM_TRY(timed_launch(ctx, -1, s, [&] {
+        return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_shift, stats, stats_ld, row_info,
+                                 halves ? nr : 0, s);
+      }));
     if (C.dx) dx.out = static_cast<char*>(C.dx) + r0 * C.ld_dx * (dx_bf16 ? 2 : 4);
     VocabGrad G = {};
     G.counter = counters + 1;
     G.alpha = alpha;
+    if (last && total_later) G.total = total;
     G.err = err;
     if (C.dx && thin) {
       VocabThin T = {};

@@ -39,10 +39,25 @@ struct IdList {
   int32_t vocab;
 };
 
+// id of entry i, or -1 where there is none (negative: not counted; past the
+// vocabulary: *bad is set).
+__device__ __forceinline__ int32_t load_id(const IdList& L, int64_t i, bool* bad) {
+  const int64_t v = L.is64 ? __ldg(static_cast<const long long*>(L.p) + i)
+                           : static_cast<int64_t>(__ldg(static_cast<const int*>(L.p) + i));
+  if (v < 0) return -1;
+  if (v >= L.vocab) {
+    *bad = true;
+    return -1;
+  }
+  return static_cast<int32_t>(v);
+}
+
 // Softmax statistics of a row come as one (maximum, sum) pair for each block
 // of this many vocabulary entries: what one epilogue warp reduces.
 constexpr int kCeBlock = 128;     // 256 x 256 tiles (k_vocab_gemm.cu)
 constexpr int kCeThinBlock = 32;  // few tokens (k_vocab_thin.cu)
+constexpr int kCeShift = 7, kCeThinShift = 5;
+static_assert(kCeBlock == 1 << kCeShift && kCeThinBlock == 1 << kCeThinShift, "block shifts");
 
 // Fixed-point logs: a logit is kept as the 16-bit distance to its block's
 // maximum in units of 2^-10 octaves, cut off at 64 octaves.
@@ -89,6 +104,75 @@ struct TileGrid {
   __host__ __device__ int32_t count() const { return tiles_m * tiles_n * splits; }
 };
 
+// Factor of both gradients, scale [/ sum of the counted weights], which depends
+// on no logit: a warp that the logits' kernel has to spare writes it.
+struct CeNorm {
+  float* alpha;                       // null: not wanted
+  IdList targets;
+  const float* weights;
+  int64_t n;
+  int32_t mean;
+  float scale;
+};
+
+// L = sum(weight * loss) [/ sum(weight)] from the row blocks' sums: a warp that
+// the gradients' kernel has to spare writes it.
+struct CeTotal {
+  float* total;                       // null: not wanted
+  const double2* partial;
+  int64_t parts;
+  int32_t mean;
+};
+
+// Longer lists are summed by a whole block: one warp would outlast the product.
+constexpr int64_t kSideSums = 16384;
+
+// This thread's share of the sums, every `step`-th entry from `first` on, and
+// what is written from the whole.
+__device__ __forceinline__ double norm_share(const CeNorm& N, int first, int step) {
+  double sum = 0.0;
+  if (!N.mean) return sum;
+#pragma unroll 8
+  for (int64_t i = first; i < N.n; i += step) {
+    bool bad = false;
+    const int t = load_id(N.targets, i, &bad);
+    sum += t < 0 ? 0.f : N.weights ? __ldg(N.weights + i) : 1.f;
+  }
+  return sum;
+}
+__device__ __forceinline__ void put_alpha(const CeNorm& N, double sum) {
+  *N.alpha = !N.mean ? N.scale : sum != 0.0 ? static_cast<float>(N.scale / sum) : 0.f;
+}
+__device__ __forceinline__ double2 total_share(const CeTotal& T, int first, int step) {
+  double2 s = make_double2(0.0, 0.0);
+#pragma unroll 8
+  for (int64_t i = first; i < T.parts; i += step) {
+    const double2 q = __ldcg(T.partial + i);
+    s.x += q.x;
+    s.y += q.y;
+  }
+  return s;
+}
+__device__ __forceinline__ void put_total(const CeTotal& T, double2 s) {
+  *T.total = static_cast<float>(!T.mean ? s.x : s.y != 0.0 ? s.x / s.y : 0.0);
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void write_alpha(const CeNorm& N, int lane) {
+  const double sum = warp_sum(norm_share(N, lane, 32));
+  if (lane == 0) put_alpha(N, sum);
+}
+__device__ __forceinline__ void write_total(const CeTotal& T, int lane) {
+  double2 s = total_share(T, lane, 32);
+  s.x = warp_sum(s.x);
+  s.y = warp_sum(s.y);
+  if (lane == 0) put_total(T, s);
+}
+
 // Z = X W^T: statistics, optionally logs.
 struct VocabLogits {
   CUtensorMap map_a, map_b, map_out;  // X, W, logs
@@ -103,6 +187,7 @@ struct VocabLogits {
   IdList targets;                     // of row 0 of this product
   uint32_t* counter;                  // zero before
   int32_t drawn;                      // tiles drawn from the counter, else fixed shares
+  CeNorm norm;
 };
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st);
 
@@ -114,7 +199,11 @@ struct VgProduct {
   TileGrid grid;                      // grid.splits > 1: fp32 partials, one per part of K
   int32_t a_mn;
   int32_t out_bf16;                   // else fp32
-  int32_t add;                        // fp32: add to what `out` holds
+  int32_t add;                        // add to what the output holds (bf16: `direct` only)
+  // Rows that TMA cannot write, or a bf16 sum: stored from registers instead of through map_out.
+  int32_t direct;
+  void* out;
+  int64_t ld_out;
 };
 
 // One launch for up to two products, the first's tiles first.
@@ -125,6 +214,7 @@ struct VocabGrad {
   int32_t drawn;                      // tiles drawn from the counter, else fixed shares
   int32_t extra;                      // fixed shares: see fixed_tile
   const float* alpha;
+  CeTotal total;
   int* err;
 };
 cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st);
@@ -147,6 +237,7 @@ struct VocabThin {
   int64_t stats_ld;
   float* target_z;
   IdList targets;
+  CeNorm norm;
   // dX: fp32 partials [split][token][ld_part]
   float* part;
   int64_t ld_part;
@@ -158,6 +249,9 @@ cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaS
 // the columns up to ld_dst become zeros).
 cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
                            int32_t cols, cudaStream_t st);
+
+// The factor alone, for long lists.
+cudaError_t launch_ce_norm(const CeNorm& N, cudaStream_t st);
 
 // Per-row outcome of the statistics, as the gradient pass reads it.
 struct CeRow {
@@ -182,6 +276,10 @@ struct CeRows {
   int32_t dim;
   float logit_scale_log2;
   CeRow* out;              // of row row0, or null
+  // Few rows: the same launch turns the logs into d logits (launch_ce_dlogits says how). Null: not wanted.
+  uint16_t* block;
+  int64_t ld_block, lo_rows;
+  int32_t vocab, stats_shift;
   float* loss;             // of row 0, or null
   float* lse;              // of row 0, or null
   // dW's operand: this pass's rows of x, zeros where the row is not counted; twice
@@ -190,23 +288,20 @@ struct CeRows {
   int64_t ld_copy;
   int32_t copies;
   int32_t width;           // rows of a block: ce_rows_width(n)
-  double2* partial;        // [row / width]: sums of weight * loss and weight; null without total and alpha
-  // Factor of both gradients, written by the first pass: scale [/ sum(weight)].  Null: not wanted.
-  float* alpha;
-  float scale;
-  // The last pass sums the losses: total = sum(weight * loss) [/ sum(weight)].
-  float* total;            // null: not in this pass
-  int32_t mean;
+  double2* partial;        // [row / width]: sums of weight * loss and weight; null without total
+  CeTotal total;           // written by the last block
   uint32_t* ticket;        // zero before and after
   uint32_t* counters;      // the products' two tile counters, set to zero
   int* err;
 };
 int ce_rows_width(int64_t n);
+// Whether launch_ce_rows makes the d logits too.
+bool ce_rows_make_dlogits(int64_t n);
 cudaError_t launch_ce_rows(const CeRows& R, cudaStream_t st);
 
 // Fixed-point logs -> bf16 d logits (before the factor alpha), in place.  With
 // lo_rows > 0 the rounding's rest goes, as bf16, to the row lo_rows below.
-cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_block,
+cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_shift,
                               const float2* stats, int64_t stats_ld, const CeRow* row_info, int64_t lo_rows,
                               cudaStream_t st);
 
@@ -260,18 +355,5 @@ struct EmbedWs {
 EmbedWs embed_backward_ws(int64_t n, int64_t vocab, int32_t dim);
 // Enqueues the launches; *launches counts them.
 cudaError_t launch_embed_backward(const EmbedBackward& E, int* launches, cudaStream_t st);
-
-// id of entry i, or -1 where there is none (negative: not counted; past the
-// vocabulary: *bad is set).
-__device__ __forceinline__ int32_t load_id(const IdList& L, int64_t i, bool* bad) {
-  const int64_t v = L.is64 ? __ldg(static_cast<const long long*>(L.p) + i)
-                           : static_cast<int64_t>(__ldg(static_cast<const int*>(L.p) + i));
-  if (v < 0) return -1;
-  if (v >= L.vocab) {
-    *bad = true;
-    return -1;
-  }
-  return static_cast<int32_t>(v);
-}
 
 }  // namespace dmuon
