@@ -56,12 +56,15 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int col
 
 template <bool VEC>
 __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
-                                                      int64_t rows, int cols) {
+                                                      int64_t rows, int cols, IdList targets) {
   pdl_launch();
   pdl_wait();
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps)
-    copy_row<VEC>(src + row * ld_src, dst + row * ld_dst, cols, static_cast<int>(ld_dst), true, threadIdx.x & 31);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); row < rows; row += warps) {
+    bool bad = false;
+    const bool keep = !targets.p || load_id(targets, row, &bad) >= 0;
+    copy_row<VEC>(src + row * ld_src, dst + row * ld_dst, cols, static_cast<int>(ld_dst), keep, threadIdx.x & 31);
+  }
 }
 
 // ------------------------------------------------------------------- d logits
@@ -146,8 +149,9 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
 //   loss = ln((rest + 2^(z_t - M)) / 2^(z_t - M)),
 // as log1p where the target holds more than half of the sum.
 //
-// A block takes `width` rows (1, or 4: then a warp reads whole 32-byte sectors
-// of pairs) and its 8 warps share their vocabulary blocks and their dot
+// A block takes `width` rows (1; from 512 on 4, so that a warp reads whole
+// 32-byte sectors of pairs; from 2048 on 8, so that the blocks stay one wave:
+// 4096 x 50257 in 14 us, 21 with 4) and its 8 warps share their vocabulary blocks and their dot
 // products; what is left is a chain of memory latencies, so each is taken by
 // as many threads as there are.  All joins run in a fixed order.  The blocks
 // after those copy dW's operand.
@@ -203,7 +207,7 @@ __device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, 
 
 template <bool VEC, bool DL>
 __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks, int chunks) {
-  __shared__ float sm[kRowWarps][4], ss[kRowWarps][4], dots[kRowWarps];
+  __shared__ float sm[kRowWarps][8], ss[kRowWarps][8], dots[kRowWarps];
   __shared__ double red[32];
   __shared__ uint32_t last;
   __shared__ CeRow info;
@@ -337,38 +341,59 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
 }
 
 // ------------------------------------------------------------- partial sums
-// One thread per four columns (VEC) or one.
-template <int VEC>
+// VEC columns a thread.  LANES threads share an output's partials (thread i takes
+// every LANES-th) and add theirs in a fixed order: a few tokens' gradient is a
+// few thousand outputs of dozens of partials each, and the time is latency
+// (one token of width 2080: 11 us with one thread each, 4 with eight).
+template <int VEC, int LANES>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64_t ld_part, int64_t part_stride, int parts,
                                                         int64_t fold, void* out, int64_t ld_out, int out_bf16,
                                                         int accumulate, const float* alpha, int64_t rows, int cols) {
   pdl_launch();
   pdl_wait();
-  const int64_t per_row = cols / VEC;
+  constexpr int kOutputs = 32 / LANES;  // of a warp, neighbours in neighbouring lanes
+  const int lane = threadIdx.x & 31, sub = lane / kOutputs;
+  const int64_t per_row = cols / VEC, total = rows * per_row;
   const float f = alpha ? __ldg(alpha) : 1.f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * per_row;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / per_row, c = (i - r * per_row) * VEC;
+  const int n = fold > 0 ? 2 * parts : parts;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kOutputs; i0 < total;
+       i0 += warps * kOutputs) {
+    const int64_t i = i0 + lane % kOutputs;
+    const bool live = i < total;
+    const int64_t r = live ? i / per_row : 0, c = live ? (i - r * per_row) * VEC : 0;
     float s[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[j] = 0.f;
-    auto add = [&](const float* p) {
-      if (VEC == 4) {
-        const float4 q = *reinterpret_cast<const float4*>(p);
-        s[0] += q.x;
-        s[1 % VEC] += q.y;
-        s[2 % VEC] += q.z;
-        s[3 % VEC] += q.w;
-      } else {
-        s[0] += p[0];
-      }
-    };
     const float* p = part + r * ld_part + c;
-#pragma unroll 8
-    for (int k = 0; k < parts; ++k) {
-      add(p + k * part_stride);
-      if (fold > 0) add(p + k * part_stride + fold * ld_part);
+    for (int k0 = sub; k0 < n; k0 += 4 * LANES) {
+      float4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u * LANES;
+        q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= n || !live) continue;
+        const float* at = p + (fold > 0 ? (k >> 1) * part_stride + (k & 1) * fold * ld_part : k * part_stride);
+        if (VEC == 4)
+          q[u] = *reinterpret_cast<const float4*>(at);
+        else
+          q[u].x = *at;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        s[0] += q[u].x;
+        if (VEC == 4) {
+          s[1 % VEC] += q[u].y;
+          s[2 % VEC] += q[u].z;
+          s[3 % VEC] += q[u].w;
+        }
+      }
     }
+#pragma unroll
+    for (int o = kOutputs; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    if (sub != 0 || !live) continue;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[j] *= f;
     if (out_bf16) {
@@ -390,16 +415,17 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64
 }  // namespace
 
 cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
-                           int32_t cols, cudaStream_t st) {
+                           int32_t cols, const IdList& targets, cudaStream_t st) {
   const bool vec = cols % 8 == 0 && ld_src % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
   const int64_t blocks = (rows + 7) / 8;
   const int grid = static_cast<int>(blocks < 152 * 16 ? blocks : 152 * 16);
   return launch_after(vec ? ce_copy_kernel<true> : ce_copy_kernel<false>, dim3(grid), dim3(256), 0, st, src, ld_src, dst,
-                      ld_dst, rows, static_cast<int>(cols));
+                      ld_dst, rows, static_cast<int>(cols), targets);
 }
 
-int ce_rows_width(int64_t n) { return n >= 512 ? 4 : 1; }
-bool ce_rows_make_dlogits(int64_t n) { return n <= 256; }
+int ce_rows_width(int64_t n) { return n >= 2048 ? 8 : n >= 512 ? 4 : 1; }
+// Up to 128 rows it is even or saves a microsecond; at 214 x 60556 it cost seven.
+bool ce_rows_make_dlogits(int64_t n) { return n <= 128; }
 
 cudaError_t launch_ce_norm(const CeNorm& N, cudaStream_t st) {
   return launch_after(ce_norm_kernel, dim3(1), dim3(1024), 0, st, N);
@@ -437,10 +463,13 @@ cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_st
                              int64_t rows, int32_t cols, cudaStream_t st) {
   // Partials have pitches of four; the output's rows must start on four bf16.
   const bool vec = cols % 4 == 0 && ld_out % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
-  const int64_t blocks = (rows * (vec ? cols / 4 : cols) + 255) / 256;
+  const bool shared = (fold > 0 ? 2 * parts : parts) >= 8;
+  const int64_t blocks = (rows * (vec ? cols / 4 : cols) * (shared ? 8 : 1) + 255) / 256;
   const int grid = static_cast<int>(blocks < 152 * 32 ? blocks : 152 * 32);
-  return launch_after(vec ? ce_finish_kernel<4> : ce_finish_kernel<1>, dim3(grid), dim3(256), 0, st, part, ld_part, part_stride,
-                      parts, fold, out, ld_out, out_bf16, accumulate, alpha, rows, static_cast<int>(cols));
+  auto kernel = vec ? (shared ? ce_finish_kernel<4, 8> : ce_finish_kernel<4, 1>)
+                    : (shared ? ce_finish_kernel<1, 8> : ce_finish_kernel<1, 1>);
+  return launch_after(kernel, dim3(grid), dim3(256), 0, st, part, ld_part, part_stride, parts, fold, out, ld_out, out_bf16,
+                      accumulate, alpha, rows, static_cast<int>(cols));
 }
 
 }  // namespace dmuon

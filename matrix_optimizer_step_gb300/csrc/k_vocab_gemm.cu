@@ -5,7 +5,7 @@
 //   dW       dW = dZ^T X    (vocabulary x width,  K = tokens)
 // bf16 operands, fp32 accumulation in TMEM.  Each output tile is 256 x 256
 // and belongs to a cluster of two CTAs: CTA r loads rows [128r, 128r + 128)
-// of the tile's A operand and of its B operand into a 4-stage ring, one
+// of the tile's A operand and of its B operand into a 5-stage ring, one
 // thread of CTA 0 issues M = 256, N = 256, K = 16 MMAs that read both CTAs'
 // shared memory, and each CTA's TMEM receives 128 rows of the accumulator.
 // The accumulator is double-buffered (2 x 256 of the 512 TMEM columns), so
@@ -47,7 +47,7 @@ namespace {
 
 constexpr int TILE = 256;
 constexpr int BK = 64;
-constexpr int STAGES = 4;
+constexpr int STAGES = 5;  // with 4: 16.4 ms for 15.6 at 8192 x 128256 x 4096, 762 us for 719 at 4096 x 50257 x 768
 constexpr int EPI = 8;  // epilogue warps: two per TMEM lane quarter, 128 columns each
 constexpr int kSchedWarp = 3 + EPI;
 constexpr int kThreads = (4 + EPI) * 32;
@@ -182,6 +182,13 @@ __device__ __forceinline__ uint32_t piece(uint32_t buf, int lane, int j) {
   return buf + static_cast<uint32_t>(lane) * 128u + (static_cast<uint32_t>(j ^ (lane & 7)) << 4);
 }
 
+// A whole 32-byte sector by one thread (aligned).
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Columns past the vocabulary in a 32-column chunk starting at `col` do not count.
 __device__ __forceinline__ void mask_columns(uint32_t (&r)[32], int col, int n) {
   if (col + 32 <= n) return;
@@ -209,7 +216,7 @@ __device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
 // column has left the TMEM.
 template <class Release>
 __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t_lane, int row, int target, int col0,
-                                                int warp_row0, uint32_t staging, int lane, Release release) {
+                                                Release release) {
   const float c = G.logit_scale_log2;
   const float minus_inf = __int_as_float(0xff800000);
   const int n = G.N;
@@ -232,11 +239,8 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   if (m == minus_inf) m = 0.f;  // only NaN and -inf: the sum below is then NaN or 0
   const bool row_ok = row < G.M;
   const int at = target - col0;
-  const bool store = G.store_logs != 0;
-  if (store) {
-    if (lane == 0) bulk_wait_group_read<0>();
-    __syncwarp();
-  }
+  uint16_t* logs = G.logs && row_ok ? G.logs + static_cast<int64_t>(row) * G.ld_logs + col0 : nullptr;
+  const int stored = static_cast<int>(min(static_cast<int64_t>(kCeBlock), G.ld_logs - col0));  // a multiple of 64
   // A distance is rounded to the nearest unit by adding 2^23, whose low
   // mantissa bits then are the integer; past 64 octaves it stays at the largest.
   const float magic = 8388608.f, most = magic + 65535.f;
@@ -251,18 +255,18 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
     }
     mask_columns(q, col0 + 32 * i, n);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint32_t w[4];
+    for (int p = 0; p < 2; ++p) {
+      uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float lo = fmaf(__uint_as_float(q[8 * p + 2 * k]), c, -m);
-        const float hi = fmaf(__uint_as_float(q[8 * p + 2 * k + 1]), c, -m);
-        s[k] += ex2(lo);
-        s[k] += ex2(hi);
+      for (int k = 0; k < 8; ++k) {
+        const float lo = fmaf(__uint_as_float(q[16 * p + 2 * k]), c, -m);
+        const float hi = fmaf(__uint_as_float(q[16 * p + 2 * k + 1]), c, -m);
+        s[k & 3] += ex2(lo);
+        s[k & 3] += ex2(hi);
         w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),
                            __float_as_uint(fminf(fmaf(hi, -kCeLogUnits, magic), most)), 0x5410);
       }
-      if (store) st_shared_16(piece(staging + 4096u * (i >> 1), lane, 4 * (i & 1) + p), w[0], w[1], w[2], w[3]);
+      if (logs && 32 * i < stored) st_global_32(logs + 32 * i + 16 * p, w);
     }
   };
   // The next chunk's load is in flight while one is worked on.
@@ -281,14 +285,6 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   chunk(rb, 3);
   if (row_ok)
     G.stats[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
-  if (!store) return;
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(&G.map_out, staging, col0, warp_row0, 0);
-    if (col0 + 64 < n) tma_store_3d(&G.map_out, staging + 4096u, col0 + 64, warp_row0, 0);
-    bulk_commit_group();
-  }
 }
 
 __device__ __forceinline__ void bf16_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0,
@@ -348,6 +344,56 @@ __device__ __forceinline__ void f32_epilogue(const VgProduct& P, uint32_t (&r)[4
       bulk_commit_group();
     }
   }
+}
+
+// bf16 rows that start anywhere: the warp packs its 32 x 128 block in shared
+// memory and writes each row in whole 16-byte pieces with single values at
+// the two ends.  (Two-byte stores of 32 columns at a time leave most 32-byte
+// sectors written in two parts, which took twice the time.)
+__device__ __forceinline__ void unaligned_bf16_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0,
+                                                        int warp_row0, uint32_t staging, int lane) {
+  if (lane == 0) bulk_wait_group_read<0>();  // stores of the other product
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = 8 * p + 2 * k;
+      w[k] = pack_bf16x2(alpha * __uint_as_float(r[j >> 5][j & 31]), alpha * __uint_as_float(r[(j + 1) >> 5][(j + 1) & 31]));
+    }
+    st_shared_16(piece(staging + 4096u * (p >> 3), lane, p & 7), w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  const int rows = min(32, P.M - warp_row0), cols = min(128, P.N - col0);
+  const int part = lane & 15;
+#pragma unroll 4
+  for (int it = 0; it < 16; ++it) {
+    const int row = 2 * it + (lane >> 4);
+    if (row >= rows) continue;
+    uint16_t* out = static_cast<uint16_t*>(P.out) + static_cast<int64_t>(warp_row0 + row) * P.ld_out + col0;
+    // Columns 2 i and 2 i + 1 of the row.
+    auto word = [&](int i) {
+      uint32_t v;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(piece(staging + 4096u * (i >> 5), row, (i >> 2) & 7) + 4u * (i & 3)));
+      return v;
+    };
+    auto value = [&](int c) { return static_cast<uint16_t>(word(c >> 1) >> (16 * (c & 1))); };
+    const int head = min(cols, static_cast<int>((8u - ((reinterpret_cast<uintptr_t>(out) >> 1) & 7u)) & 7u));
+    const int pieces = (cols - head) >> 3, tail = head + 8 * pieces;
+    if (part < pieces) {
+      // Eight columns from head + 8 part on: four words, or five where that is odd.
+      const int i = (head + 8 * part) >> 1;
+      const uint32_t odd = head & 1, shift = 16 * odd;
+      const uint32_t w0 = word(i), w1 = word(i + 1), w2 = word(i + 2), w3 = word(i + 3), w4 = odd ? word(i + 4) : 0u;
+      *reinterpret_cast<uint4*>(out + head + 8 * part) =
+          make_uint4(__funnelshift_r(w0, w1, shift), __funnelshift_r(w1, w2, shift), __funnelshift_r(w2, w3, shift),
+                     __funnelshift_r(w3, w4, shift));
+    }
+    if (part < head) out[part] = value(part);
+    if (tail + part < cols) out[tail + part] = value(tail + part);
+  }
+  __syncwarp();
 }
 
 // Without TMA: the warp turns each 32 x 32 block around in shared memory, so
@@ -619,13 +665,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         continue;
       }
       if constexpr (LOGITS) {
-        logits_epilogue(G, t_lane, warp_row0 + lane, target, col0, warp_row0, my_staging, lane, release);
+        logits_epilogue(G, t_lane, warp_row0 + lane, target, col0, release);
       } else {
         const VgProduct& P = G.p[T.product];
         uint32_t r[4][32];
         load_columns(t_lane, r);
         release();
-        if (P.direct)
+        if (P.direct && P.out_bf16 && !P.add)
+          unaligned_bf16_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);
+        else if (P.direct)
           direct_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);
         else if (P.out_bf16)
           bf16_epilogue(P, r, alpha, col0, warp_row0, my_staging, lane);

@@ -278,9 +278,16 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
 
   // Operand copies: TMA needs rows on 16 bytes, and rows that are not counted
-  // must read as zeros in dW's product whatever they hold.
-  const bool copy_x = !tma_rows(C.x, C.ld_x, 2), copy_w = !tma_rows(C.w, C.ld_w, 2);
-  const int64_t ld8 = round_up(d, 8), ld4 = round_up(d, 4);
+  // must read as zeros in dW's product whatever they hold (the row pass makes
+  // that copy where none is needed before it).  Rows off 128 bytes cost the
+  // products on 256 x 256 tiles twice the L2 lines: with x at a pitch of 1000
+  // elements the logits of 4000 x 32003 took 237 us, at 1024 they take 186.
+  // x is small next to what it is multiplied by; a copy of w would cost as
+  // much as it gains (20 of 186 us there).
+  const bool off_lines = n >= 256 && d >= 128 && ((reinterpret_cast<uintptr_t>(C.x) | static_cast<uintptr_t>(C.ld_x * 2)) & 127u) != 0;
+  const bool copy_x = off_lines || !tma_rows(C.x, C.ld_x, 2), copy_w = !tma_rows(C.w, C.ld_w, 2);
+  const bool masked_first = copy_x && C.dw && !halves;  // that copy serves dW's product too
+  const int64_t ld8 = round_up(d, n >= 256 ? 64 : 8), ld4 = round_up(d, 4);
   Layout L;
   const size_t off_x = copy_x ? L.take(static_cast<size_t>(n * ld8) * 2) : 0;
   const size_t off_w = copy_w ? L.take(static_cast<size_t>(v * ld8) * 2) : 0;
@@ -296,7 +303,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     off_alpha = L.take(4);
     bool dx_part = false, dw_part = false;
     if (C.dw) {
-      off_masked = L.take(static_cast<size_t>(token_rows * ld8) * 2);
+      if (!masked_first) off_masked = L.take(static_cast<size_t>(token_rows * ld8) * 2);
       dw.out = C.dw;
       dw.ld = C.ld_dw;
       dw.bf16 = dw_bf16;
@@ -343,13 +350,13 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   int64_t ld_x = C.ld_x, ld_w = C.ld_w;
   if (copy_x) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + off_x);
-    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.x, C.ld_x, to, ld8, n, static_cast<int32_t>(d), s); }));
+    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.x, C.ld_x, to, ld8, n, static_cast<int32_t>(d), masked_first ? ids : IdList{}, s); }));
     x = to;
     ld_x = ld8;
   }
   if (copy_w) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + off_w);
-    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.w, C.ld_w, to, ld8, v, static_cast<int32_t>(d), s); }));
+    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_copy(C.w, C.ld_w, to, ld8, v, static_cast<int32_t>(d), IdList{}, s); }));
     w = to;
     ld_w = ld8;
   }
@@ -412,9 +419,9 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
-      if (grads) DM_TRY(encode_2d(enc, &G.map_out, block, v, nr, ld_block, 64, 32));
       G.logit_scale_log2 = scale_log2;
-      G.store_logs = grads;
+      G.logs = grads ? block : nullptr;
+      G.ld_logs = ld_block;
       G.stats = stats;
       G.stats_ld = stats_ld;
       G.target_z = target_z;
@@ -451,7 +458,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     }
     R.loss = C.loss;
     R.lse = C.lse;
-    R.x_copy = C.dw ? masked : nullptr;
+    R.x_copy = C.dw && !masked_first ? masked : nullptr;
     R.ld_copy = ld8;
     R.copies = halves ? 2 : 1;
     R.width = width;
@@ -499,7 +506,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       // and the parts it leaves out hold the earlier passes' sums.
       const int splits = static_cast<int>(std::min<int64_t>(dw.splits, (k_rows + 63) / 64));
       // Short main loops are bound by the stores: whole rows of tiles then go out together.
-      DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked, ld8, dw, splits, 8, first));
+      DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked_first ? x + r0 * ld_x : masked, ld8, dw, splits, 8, first));
       G.n_units[1] = G.p[1].grid.count();
     }
     if (G.n_units[1] > 0) {

@@ -175,12 +175,13 @@ __device__ __forceinline__ void write_total(const CeTotal& T, int lane) {
 
 // Z = X W^T: statistics, optionally logs.
 struct VocabLogits {
-  CUtensorMap map_a, map_b, map_out;  // X, W, logs
+  CUtensorMap map_a, map_b;           // X, W
   int32_t M, N;                       // tokens, vocabulary
   TileGrid grid;
   int* err;
   float logit_scale_log2;             // logit scale times log2(e)
-  int32_t store_logs;
+  uint16_t* logs;                     // [row][ld_logs], ld_logs a multiple of 64; or null
+  int64_t ld_logs;
   float2* stats;                      // [block][row]: maximum and sum of 2^(z - maximum), z in octaves
   int64_t stats_ld;
   float* target_z;                    // [row]: the target's z
@@ -245,10 +246,10 @@ struct VocabThin {
 cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaStream_t st);
 
 // ---- k_vocab_ce.cu
-// Copy of rows x cols bf16 values into rows of pitch ld_dst (a multiple of 8;
-// the columns up to ld_dst become zeros).
+// Copy of rows x cols bf16 values into rows of pitch ld_dst (a multiple of 8).
+// With targets, rows that are not counted become zeros.
 cudaError_t launch_ce_copy(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int64_t rows,
-                           int32_t cols, cudaStream_t st);
+                           int32_t cols, const IdList& targets, cudaStream_t st);
 
 // The factor alone, for long lists.
 cudaError_t launch_ce_norm(const CeNorm& N, cudaStream_t st);
