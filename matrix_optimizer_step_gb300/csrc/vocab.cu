@@ -666,7 +666,7 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
     return DMUON_OK;
   }
   const EmbedWs W = embed_backward_ws(A.n_tokens, A.vocab, static_cast<int32_t>(A.dim));
-  DM_TRY(vocab_workspace(ctx, W.bytes, s));
+  if (W.bytes > 0) DM_TRY(vocab_workspace(ctx, W.bytes, s));
   char* ws = static_cast<char*>(ctx->vocab_ws.p);
   EmbedBackward E = {};
   E.ids = IdList{A.ids, A.id_dtype == DMUON_INDEX_I64, static_cast<int32_t>(A.vocab)};
@@ -691,7 +691,7 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
   int launches = 0;
   DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_embed_backward(E, &launches, s); }));
   ctx->launches += launches - 1;  // timed_launch counted one
-  return vocab_used(ctx, s);
+  return W.bytes > 0 ? vocab_used(ctx, s) : DMUON_OK;
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@ import torch
 from . import capi
 
 _FLOATS = {torch.bfloat16: capi.DMUON_DTYPE_BF16, torch.float32: capi.DMUON_DTYPE_F32}
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _INDEX = {torch.int32: capi.DMUON_INDEX_I32, torch.int64: capi.DMUON_INDEX_I64}
 
 
@@ -106,34 +107,33 @@ class VocabOps:
         in ``dx`` (like x) and ``dw`` (like w; added to with
         ``accumulate_dw``), bf16 or fp32.  With none given, ``loss`` is
         allocated.  Returns ``loss``."""
-        a = capi.DmuonCe()
-        bf16 = (torch.bfloat16,)
-        a.x, a.ld_x = self._matrix(x, "x", bf16)
-        a.n_tokens, a.dim = x.shape
-        a.w, a.ld_w = self._matrix(w, "w", bf16, cols=a.dim)
-        a.vocab = w.shape[0]
-        n, f32 = a.n_tokens, (torch.float32,)
-        a.targets = self._list(targets, "targets", _INDEX, n)
+        x_p, ld_x = self._matrix(x, "x", _BF16)
+        n, dim = x.shape
+        w_p, ld_w = self._matrix(w, "w", _BF16, cols=dim)
+        vocab = w.shape[0]
+        targets_p = self._list(targets, "targets", _INDEX, n)
+        weights_p = loss_p = lse_p = total_p = dx_p = dw_p = None
+        ld_dx = ld_dw = dx_type = dw_type = 0
         if loss is None and lse is None and total is None and dx is None and dw is None:
             loss = torch.empty(n, device=x.device, dtype=torch.float32)
         if weights is not None:
-            a.weights = self._list(weights, "weights", f32, n)
+            weights_p = self._list(weights, "weights", _F32, n)
         if loss is not None:
-            a.loss = self._list(loss, "loss", f32, n)
+            loss_p = self._list(loss, "loss", _F32, n)
         if lse is not None:
-            a.lse = self._list(lse, "lse", f32, n)
+            lse_p = self._list(lse, "lse", _F32, n)
         if total is not None:
-            a.total = self._list(total, "total", f32, 1)
+            total_p = self._list(total, "total", _F32, 1)
         if dx is not None:
-            a.dx, a.ld_dx = self._matrix(dx, "dx", _FLOATS, n, a.dim)
-            a.dx_dtype = _FLOATS[dx.dtype]
+            dx_p, ld_dx = self._matrix(dx, "dx", _FLOATS, n, dim)
+            dx_type = _FLOATS[dx.dtype]
         if dw is not None:
-            a.dw, a.ld_dw = self._matrix(dw, "dw", _FLOATS, a.vocab, a.dim)
-            a.dw_dtype = _FLOATS[dw.dtype]
-        a.x_dtype = a.w_dtype = capi.DMUON_DTYPE_BF16
-        a.target_dtype = _INDEX[targets.dtype]
-        a.logit_scale, a.grad_scale = logit_scale, grad_scale
-        a.flags = (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0)
+            dw_p, ld_dw = self._matrix(dw, "dw", _FLOATS, vocab, dim)
+            dw_type = _FLOATS[dw.dtype]
+        a = capi.DmuonCe(n, vocab, dim, x_p, w_p, ld_x, ld_w, targets_p, weights_p, loss_p, lse_p, total_p, dx_p, dw_p,
+                         ld_dx, ld_dw, capi.DMUON_DTYPE_BF16, capi.DMUON_DTYPE_BF16, _INDEX[targets.dtype], dx_type,
+                         dw_type, logit_scale, grad_scale,
+                         (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0))
         self._call(self._lib.dmuon_cross_entropy, a, stream)
         return loss
 

@@ -304,7 +304,8 @@ def ids_of(kind, n, v, seed):
 EMBED_SHAPES = [(1, 5, 8, "zipf"), (1, 1, 1, "one"), (17, 300, 768, "padded"), (63, 40, 33, "zipf"), (64, 1, 16, "one"),
                 (65, 70000, 24, "distinct"), (300, 50, 2056, "padded"), (4096, 1000, 40, "zipf"), (4097, 600, 64, "padded"),
                 (9001, 513, 72, "zipf"), (5000, 7, 16, "one"), (130, 20, 8, "padding"), (20000, 130000, 8, "distinct"),
-                (8200, 511, 5, "zipf")]
+                (8200, 511, 5, "zipf"), (128, 1, 40, "one"), (128, 33, 776, "padded"), (129, 33, 776, "padded"),
+                (100, 90000, 264, "distinct"), (97, 64, 2056, "zipf"), (33, 7, 100, "padding")]
 TYPES = [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.float32, torch.bfloat16),
          (torch.bfloat16, torch.float32)]
 
