@@ -385,12 +385,16 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  *
  * The logits are never stored: their maxima, sums and, for the gradients, one
  * 16-bit fixed-point log per entry leave the product's epilogue, for as many
- * tokens at a time as tuning key 14 allows.
- * Rounding: products of bf16 operands with fp32 sums; softmax statistics, the
- * loss and L in fp32 (L's sum in fp64); d logits are rounded to bf16 once,
- * before the gradient products; dx and dw once on output (fp32 outputs thus
- * carry the d logits' bf16 rounding too).  dW of several passes, and
- * DMUON_CE_ADD_DW, add in fp32 before the one rounding.
+ * tokens at a time as tuning key 14 allows (without gradients only the
+ * maxima and sums of 128 or 32 entries at a time).
+ * Rounding: products of bf16 operands with fp32 sums, the target's logit in
+ * fp32 throughout; softmax statistics, the loss and the factor of the
+ * gradients in fp32 (sums over tokens in fp64); a probability's log is kept
+ * in steps of 2^-10 octaves (3.4e-4 of the probability at most); d logits,
+ * before that factor, are rounded to bf16 once, up to 128 tokens to two bf16
+ * halves; dx and dw once on output (fp32 outputs thus carry the d logits'
+ * rounding too).  dW of several passes, and DMUON_CE_ADD_DW, add in fp32
+ * before the one rounding.
  *
  *   x        bf16, n_tokens x dim, rows ld_x elements apart
  *   w        bf16, vocab x dim, rows ld_w elements apart
@@ -401,11 +405,13 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  *   loss, lse  fp32 per token (written); total  one fp32: L (written)
  *   dx, dw   bf16 or fp32, row pitches ld_dx and ld_dw (written; dw is added to
  *            with DMUON_CE_ADD_DW)
- * Each of loss, lse, total, dx and dw may be NULL (not all of them).  Rows on
- * 16-byte boundaries (pointer and pitch) are read and written in place by TMA;
- * other x and w are copied first, and other dx and dw go through a partial
- * buffer, as does a bf16 dw that is added to.  n_tokens = 0: total is 0, and
- * dw is zeroed unless it is added to.
+ * Each of loss, lse, total, dx and dw may be NULL (not all of them), and every
+ * row pitch >= dim is taken.  Fast where rows start on 16-byte boundaries
+ * (pointer and pitch; TMA): other x and w are copied first, and other dx and
+ * dw stored without TMA.  Scratch: with gradients 2 bytes per token of a pass
+ * and vocabulary entry and a copy of x; the copies above; 4 bytes per entry of
+ * w for a bf16 dw of several passes.  n_tokens = 0: total is 0, and dw is
+ * zeroed unless it is added to.
  * Errors: DMUON_ERR_INVALID_ARG (null or overlapping memory, no output, bad
  * scale or flags), DMUON_ERR_SHAPE (n_tokens >= 2^31, vocab outside
  * [1, 2^24], dim outside [1, 2^20], a pitch below dim), DMUON_ERR_DTYPE,

@@ -445,3 +445,42 @@ def test_embed_backward_long_lists(ops, n, v):
     ops.sync()
     want.zero_().index_add_(0, ids[: n // 4][keep[: n // 4]], dout[: n // 4][keep[: n // 4]].double())
     assert torch.equal(table.double(), want)
+
+
+# ------------------------------------------------------------------- example
+
+def _example():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "tied_lm.py")
+    spec = importlib.util.spec_from_file_location("tied_lm", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_gradients_against_autograd(cuda_lib):
+    # The example's whole backward pass against torch's in fp32 on the same bf16 parameters.  Each bf16 tensor on
+    # the way (h, x, dx, da, dh) adds one rounding of u = 2^-8: five of them, in norm, stay below 3 u.
+    m = _example()
+    model = m.TiedLM(vocab=700, dim=64, hidden=96, tokens=500, seed=3)
+    g = torch.Generator().manual_seed(4)
+    ids, targets = (torch.randint(0, 700, (500,), generator=g).to(DEV) for _ in range(2))
+    loss = model.gradients(ids, targets)
+    model.sync()
+    p = {k: v.float().requires_grad_() for k, v in model.param.items()}
+    h = p["table"][ids]
+    x = h + torch.relu(h @ p["A"]) @ p["B"]
+    want = torch.nn.functional.cross_entropy(x @ p["table"].T, targets)
+    want.backward()
+    want = float(want.detach())
+    assert abs(float(loss) - want) < 1e-2 * want
+    for k in p:
+        err = float((model.grad[k].double() - p[k].grad.double()).norm() / p[k].grad.double().norm())
+        assert err < 3 * U, (k, err)
+
+
+def test_example_learns(cuda_lib):
+    losses = _example().main(steps=60)
+    assert losses[0] > 8.0 and losses[-1] < 0.75 * losses[0], losses
