@@ -337,7 +337,7 @@ cudaError_t launch_variant(const VocabThin& G, int n_ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaStream_t st) {
-  if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > 128 || G.np % 16 != 0 || G.groups < 1 ||
+  if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > kThinRows || G.np % 16 != 0 || G.groups < 1 ||
       2 * G.np * G.groups > 512 || n_ctas <= 0)
     return cudaErrorInvalidValue;
   return logits ? launch_variant<true>(G, n_ctas, st) : launch_variant<false>(G, n_ctas, st);

@@ -153,6 +153,23 @@ bool tma_rows(const void* p, int64_t ld, int elem) { return aligned16(p) && ld *
 
 constexpr int kVgTile = 256;
 
+// Tokens up to which d logits come in two halves.
+constexpr int kHalvesTokens = 128;
+
+// The products that read W run on k_vocab_thin.cu where that is faster.
+//  Logits, microseconds there / on 256 x 256 tiles: 9.5 / 12.4 with 8 tokens and
+//  11.4 / 12.5 with 30 at 11000 x 1000, 178 / 302 with one and 183 / 188 with 24 at
+//  128256 x 4096, 62 / 59 with 30 and 67 / 61 with 64 at 60000 x 2048.
+constexpr int64_t kThinLogitsTokens = 24;
+//  dX (with dW beside it in the 256 x 256 tiles' launch): 18.6 / 13.3 with 8 tokens
+//  at 11000 x 1000, 88 / 107 with 30 at 60000 x 2048, 334 / 432 with one at
+//  128256 x 4096; with 129 to 256 rows of d logits 48 / 44 at 50000 x 768,
+//  125 / 122 at 30000 x 4096, 450 / 504 at 128256 x 4096.
+bool thin_dx(int64_t rows, int64_t vocab, int64_t dim) {
+  const int64_t entries = vocab * dim;
+  return rows <= kThinRows / 2 ? entries > 36000000 : rows <= kThinRows && entries > 250000000;
+}
+
 // Tiles of at least this many k-blocks are drawn (k_vocab_gemm.cu): half a
 // microsecond a tile against 9 us and more of work.
 constexpr int kDrawnBlocks = 32;
@@ -267,12 +284,11 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
 
   // Few tokens: a 256-row tile has room for d logits in two bf16 halves (value
   // and the rounding's rest), so they come at no cost, and with as few terms in
-  // the gradients' sums one rounding would not average out.  Up to half of
-  // that, the products that read W have it as the long operand.
-  const bool halves = grads && n <= kThinRows;
+  // the gradients' sums one rounding would not average out.
+  const bool halves = grads && n <= kHalvesTokens;
   const int64_t token_rows = halves ? 2 * n : rows;
-  const bool thin = n <= kThinRows / 2;
-  const int stats_shift = thin ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
+  const bool thin_logits = n <= kThinLogitsTokens, thin_x = C.dx && thin_dx(token_rows, v, d);
+  const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
   const bool rows_make_dlogits = grads && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
   const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
@@ -317,8 +333,8 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     if (C.dx) {
       dx.bf16 = dx_bf16;
       dx.ld = C.ld_dx;
-      dx_part = halves;
-      if (thin) {
+      dx_part = halves || thin_x;
+      if (thin_x) {
         // Tiles of 128 columns; parts of the vocabulary for a few tiles per SM.
         const int64_t tiles = (d + 127) / 128, kb = (v + 63) / 64;
         int64_t parts = (2 * ctx->num_sms + tiles - 1) / tiles;
@@ -382,7 +398,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_norm(norm, s); }));
     norm.alpha = nullptr;
   }
-  const bool total_later = side_sums && (C.dw || (C.dx && !thin));  // the gradients' kernel writes it
+  const bool total_later = side_sums && (C.dw || (C.dx && !thin_x));  // the gradients' kernel writes it
 
   for (int64_t r0 = 0; r0 < n; r0 += rows) {
     const int64_t nr = std::min(rows, n - r0);
@@ -390,7 +406,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     const int64_t k_rows = halves ? 2 * nr : nr;  // rows of d logits
     IdList here = ids;
     here.p = static_cast<const char*>(ids.p) + r0 * (ids.is64 ? 8 : 4);
-    if (thin) {
+    if (thin_logits) {
       VocabThin G = {};
       G.M = static_cast<int32_t>(v);
       G.tokens = static_cast<int32_t>(nr);
@@ -398,7 +414,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.tiles_m = static_cast<int32_t>((v + 127) / 128);
       G.splits = 1;
       G.kb_total = G.kb_step = static_cast<int32_t>((d + 63) / 64);
-      G.groups = std::max(1, std::min(4, G.kb_total / 16));
+      G.groups = std::max(1, std::min({4, G.kb_total / 16, 256 / G.np}));
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
@@ -481,7 +497,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     G.alpha = alpha;
     if (last && total_later) G.total = total;
     G.err = err;
-    if (C.dx && thin) {
+    if (thin_x) {
       VocabThin T = {};
       T.M = static_cast<int32_t>(d);
       T.tokens = static_cast<int32_t>(k_rows);
@@ -523,7 +539,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       DM_TRY(timed_launch(ctx, -1, s, [&] {
         // The tile kernel has applied alpha already.
         return launch_ce_finish(dx.part, dx.ld_part, k_rows * dx.ld_part, dx.splits, halves ? nr : 0, dx.out, dx.ld, dx.bf16, 0,
-                                thin ? alpha : nullptr, nr, static_cast<int32_t>(d), s);
+                                thin_x ? alpha : nullptr, nr, static_cast<int32_t>(d), s);
       }));
     if (dw.part && last)
       DM_TRY(timed_launch(ctx, -1, s, [&] {

@@ -222,7 +222,7 @@ cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st);
 int vocab_gemm_max_pairs();
 
 // The products that read W, for few tokens (k_vocab_thin.cu).
-constexpr int kThinRows = 128;        // token rows at most
+constexpr int kThinRows = 256;        // token rows at most
 struct VocabThin {
   CUtensorMap map_a, map_b;           // W; X or dZ
   int32_t M;                          // vocabulary (logits) or width (dX)

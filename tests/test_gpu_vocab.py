@@ -106,7 +106,8 @@ def run_ce(ops, x, w, t, grads=True, dtype=torch.bfloat16, **kw):
 
 CE_SHAPES = [(1, 1, 8), (1, 2, 1), (1, 300, 64), (2, 128, 16), (5, 129, 33), (31, 1000, 72), (64, 257, 256), (130, 1000, 96),
              (257, 513, 1000), (300, 5003, 136), (513, 130, 40), (70, 777, 1001), (129, 40000, 64), (1100, 600, 264),
-             (3000, 65, 24)]
+             (3000, 65, 24), (24, 400, 80), (25, 400, 80), (128, 1030, 200), (257, 1030, 200),
+             (2049, 300, 136)]
 
 
 @pytest.mark.parametrize("n, v, d", CE_SHAPES)
@@ -116,6 +117,61 @@ def test_cross_entropy_sizes(ops, n, v, d):
     check_ce(x, w, t, run_ce(ops, x, w, t, weights=a, mean=False, grad_scale=0.25, logit_scale=0.7),
              weights=a, mean=False, grad_scale=0.25, logit_scale=0.7)
     check_ce(x, w, t, run_ce(ops, x, w, t, grads=False))
+
+
+def large_reference(x, w, t, a):
+    """The oracle's formulas and this file's bounds in float64 on the GPU, for heads too large for the host's."""
+    n, d = x.shape
+    v = w.shape[0]
+    counted = t >= 0
+    X, W = x.double() * counted[:, None], w.double()
+    z = X @ W.T
+    ez = (d / 16 + 8) * 4 * F * float((X.abs() @ W.T.abs()).max())
+    lse = torch.logsumexp(z, dim=1)
+    rows, at = counted.nonzero().squeeze(1), t[counted]
+    loss = torch.zeros_like(lse)
+    loss[rows] = lse[rows] - z[rows, at]
+    coef = (a.double() if a is not None else torch.ones_like(lse)) * counted
+    coef = coef / coef.sum()
+    p = torch.softmax(z, dim=1) * coef[:, None]
+    del z
+    dz = p.clone()
+    dz[rows, at] -= coef[rows]
+    ep = 2 * ez + np.log(2) / 2048 + 32 * F
+    edz = dz.abs() * U * (1 + ep) + p * ep + coef[:, None] * 2.0 ** -60
+    edz[rows, at] += 8 * F * coef[rows]
+    out = {"loss": (loss, (2 * ez + 64 * F + 16 * F * lse.abs()) * counted)}
+    for name, k, A, B in (("dx", v, dz, W), ("dw", n, dz.T, X)):
+        E = edz if name == "dx" else edz.T
+        want = A @ B
+        e = E @ B.abs() + (k / 16 + 8) * 4 * F * (A.abs() @ B.abs())
+        out[name] = (want, e + U * (want.abs() + e) + 1e-38)
+    return out
+
+
+def test_large_reference_is_the_oracle():
+    x, w, t, a = (q.to(DEV) for q in inputs(40, 300, 64, seed=13))
+    got = large_reference(x, w, t, a)
+    want = ovocab.cross_entropy(f64(x), f64(w), t.cpu().numpy(), f64(a))
+    for k in ("loss", "dx", "dw"):
+        assert np.allclose(f64(got[k][0]), want[k], rtol=1e-10, atol=1e-14), k
+
+
+# Heads from 36 and from 250 million entries on take dX with w as the long operand, up to 128 and 256 rows of d logits.
+@pytest.mark.parametrize("n, v, d", [(1, 40000, 1000), (24, 36864, 1000), (25, 40009, 1001), (64, 9000, 4096), (65, 40000, 1000),
+                                     (120, 62500, 4008), (129, 62500, 4008), (255, 65000, 4000)])
+def test_cross_entropy_large_heads(ops, n, v, d):
+    g = torch.Generator(device=DEV).manual_seed(n)
+    w = (torch.randn(v, d, generator=g, device=DEV) * (1.3 / d ** 0.5)).to(torch.bfloat16)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    x = (torch.randn(n, d, generator=g, device=DEV) + torch.rand(n, 1, generator=g, device=DEV) * 7 * w[t].float()).to(torch.bfloat16)
+    if n > 2:
+        t[1::5] = -1
+    a = torch.rand(n, generator=g, device=DEV) + 0.5
+    got = run_ce(ops, x, w, t, weights=a)
+    for k, (want, tol) in large_reference(x, w, t, a).items():
+        bad = ~((got[k].double() - want).abs() <= tol)
+        assert not bool(bad.any()), (k, int(bad.sum()), bad.nonzero()[:3].tolist())
 
 
 @pytest.mark.parametrize("n, v, d", [(5, 129, 33), (130, 1000, 96), (300, 5003, 136)])
