@@ -19,6 +19,16 @@ _FLOATS = {torch.bfloat16: capi.DMUON_DTYPE_BF16, torch.float32: capi.DMUON_DTYP
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _INDEX = {torch.int32: capi.DMUON_INDEX_I32, torch.int64: capi.DMUON_INDEX_I64}
 
+_Tensor = torch.Tensor
+
+
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The handle alone where torch offers it (the stream object costs a microsecond).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
 
 class VocabOps:
     """Embedding and cross entropy on one GPU.
@@ -33,11 +43,12 @@ class VocabOps:
         self.ctx = capi.dmuon_context_create(self.device)
         self._lib = capi.load_library()
 
-    # These run on every call: the checks are ordered so that a good tensor
-    # takes few attribute reads (a small lookup is bound by this code).
+    # These run on every call: a good tensor takes few attribute reads and no
+    # further calls (a small lookup is bound by this code).
     def _matrix(self, t, name, dtypes, rows=None, cols=None):
         """(pointer, row pitch) of a checked matrix."""
-        self._on_device(t, name, dtypes)
+        if not isinstance(t, _Tensor) or t.get_device() != self.device or t.dtype not in dtypes:
+            self._refuse(t, name, dtypes)
         shape = t.shape
         if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
             raise ValueError(f"{name} has shape {tuple(shape)}, expected ({'*' if rows is None else rows}, "
@@ -52,21 +63,23 @@ class VocabOps:
         return t.data_ptr(), pitch
 
     def _list(self, t, name, dtypes, n):
-        self._on_device(t, name, dtypes)
+        if not isinstance(t, _Tensor) or t.get_device() != self.device or t.dtype not in dtypes:
+            self._refuse(t, name, dtypes)
         if t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name}: expected {n} contiguous elements")
         return t.data_ptr()
 
-    def _on_device(self, t, name, dtypes):
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.device or not t.is_cuda:
+    def _refuse(self, t, name, dtypes):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
             raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
 
     def _call(self, fn, args, stream):
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        status = fn(self.ctx, ctypes.byref(args), getattr(stream, "cuda_stream", stream))
+            stream = _raw_stream(self.device)
+        else:
+            stream = getattr(stream, "cuda_stream", stream)
+        status = fn(self.ctx, ctypes.byref(args), stream)
         if status:
             capi._check(status)
 
