@@ -412,8 +412,8 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  * and vocabulary entry and a copy of x; the copies above; 4 bytes per entry of
  * w for a bf16 dw of several passes.  n_tokens = 0: total is 0, and dw is
  * zeroed unless it is added to.
- * Errors: DMUON_ERR_INVALID_ARG (null or overlapping memory, no output, bad
- * scale or flags), DMUON_ERR_SHAPE (n_tokens >= 2^31, vocab outside
+ * Errors: DMUON_ERR_INVALID_ARG (null, misaligned or overlapping memory, no
+ * output, bad scale or flags), DMUON_ERR_SHAPE (n_tokens >= 2^31, vocab outside
  * [1, 2^24], dim outside [1, 2^20], a pitch below dim), DMUON_ERR_DTYPE,
  * DMUON_ERR_NOMEM, DMUON_ERR_CUDA, DMUON_ERR_UNSUPPORTED.
  */
@@ -460,9 +460,11 @@ DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void
  *
  * The vocabulary operators share scratch of the context, apart from the Muon
  * step's: a call on another stream than the last one's waits for that one.
- * A call whose scratch has its size already (any earlier call of the sizes) can
- * be captured into a CUDA graph; captured calls and their replays must not
- * overlap other calls of these entries on the context.
+ * A context's calls are made by one host thread at a time.  A call whose
+ * scratch has its size already (any earlier call of the sizes) can be captured
+ * into a CUDA graph, and scratch that a capture has seen is kept until the
+ * context is destroyed; captured calls and their replays must not overlap
+ * other calls of these entries on the context.
  */
 enum { DMUON_EMBED_ADD = 1u };
 
@@ -538,9 +540,9 @@ DMUON_API int dmuon_selftest_wait_timeout(dmuon_context* ctx, int32_t timeout_us
  *          tiles average at least `value` 64-deep k-blocks runs 256 x 512
  *          tiles wherever two adjacent column blocks exist (0..1e6, default
  *          128; 0 = never).  Results do not depend on the setting.
- *   key 14: dmuon_cross_entropy with gradients: the block of 16-bit logs that
- *          is held at a time is at most `value` MiB (1..65536, default 2048;
- *          at least 256 tokens' worth).  A call whose tokens do not fit runs
+ *   key 14: dmuon_cross_entropy: the block of 16-bit logs (without gradients:
+ *          of statistics) that is held at a time is at most `value` MiB
+ *          (1..65536, default 2048; at least 256 tokens' worth).  A call whose tokens do not fit runs
  *          in passes; their number only moves the rounding of dW's fp32 sums.
  * Results never depend on keys 3, 4, 6, 8, 9, 10, 11 and 12 (bit for bit);
  * key 2 changes the kernel and key 7 the rounding points, both within the

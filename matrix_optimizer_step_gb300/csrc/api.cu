@@ -416,6 +416,8 @@ int dmuon_context_destroy(dmuon_context* ctx) {
     if (ctx->vocab_done) cudaEventDestroy(ctx->vocab_done);
     ctx->vocab_done = nullptr;
     ctx->vocab_ws.release();
+    for (auto& b : ctx->vocab_retired) b.release();
+    ctx->vocab_retired.clear();
     ctx->vocab_ticket.release();
     ctx->ws.release();
     ctx->err.release();

@@ -349,6 +349,9 @@ struct dmuon_context {
   cudaEvent_t vocab_done = nullptr;
   cudaStream_t vocab_stream = nullptr;
   bool vocab_used = false;
+  // Scratch that a captured graph may use is kept when it is outgrown.
+  bool vocab_captured = false;
+  std::vector<dmuon::DevBuf> vocab_retired;
   int vocab_pairs = 0;
   // AdamW descriptor array whose pointers last passed the reachability check.
   std::vector<uint8_t> checked_vecs;

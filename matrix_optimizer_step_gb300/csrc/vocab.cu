@@ -33,6 +33,7 @@ namespace {
 struct Range {
   const void* p;
   int64_t bytes;
+  int elem;  // element size, and the alignment that kernels rely on
   bool written;
   const char* what;
 };
@@ -42,8 +43,14 @@ int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
   return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * elem;
 }
 
-int check_ranges(const dmuon_context* ctx, const char* op, const Range* r, int n) {
+// Alignment of each, and no written range shared with another.
+int check_ranges(const char* op, const Range* r, int n) {
   char buf[200];
+  for (int i = 0; i < n; ++i)
+    if (reinterpret_cast<uintptr_t>(r[i].p) % static_cast<uintptr_t>(r[i].elem) != 0) {
+      snprintf(buf, sizeof buf, "%s: %s is not aligned to its %d-byte elements", op, r[i].what, r[i].elem);
+      return set_error(DMUON_ERR_INVALID_ARG, buf);
+    }
   for (int i = 0; i < n; ++i)
     for (int j = i + 1; j < n; ++j) {
       if (!r[i].p || !r[j].p || (!r[i].written && !r[j].written)) continue;
@@ -114,6 +121,16 @@ int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
   if (cap == cudaStreamCaptureStatusNone && ctx->vocab_used && ctx->vocab_stream != s)
     DM_CUDA(cudaStreamWaitEvent(s, ctx->vocab_done, 0));
   if (bytes > ctx->vocab_ws.bytes) {
+    if (ctx->vocab_captured) {
+      // Captured graphs point into the old scratch: it lives as long as the context.
+      try {
+        ctx->vocab_retired.push_back(ctx->vocab_ws);
+      } catch (...) {
+        return set_error(DMUON_ERR_NOMEM, "host allocation failed");
+      }
+      ctx->vocab_ws = DevBuf();
+      ctx->vocab_captured = false;
+    }
     ctx->vocab_ws.release();
     const int st = dev_alloc(ctx->vocab_ws, bytes);
     if (st != DMUON_OK) return st;
@@ -123,6 +140,7 @@ int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
     if (st != DMUON_OK) return st;
     DM_CUDA(cudaMemset(ctx->vocab_ticket.p, 0, 256));
   }
+  if (cap != cudaStreamCaptureStatusNone) ctx->vocab_captured = true;
   return DMUON_OK;
 }
 
@@ -271,14 +289,16 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const int pairs = ctx->vocab_pairs;
   if (pairs < 1) return set_error(DMUON_ERR_UNSUPPORTED, "cross_entropy: no CTA pair of the product kernel fits the device");
 
-  // Rows of one pass: the block of fixed-point logs stays within its limit.
-  // Without gradients there is no block and one pass takes all rows.
+  // Rows of one pass: what is held for each (its logs, or without gradients its
+  // statistics) stays within the limit, and tiles are numbered in 32 bits.
   const int64_t ld_block = round_up(v, 64);
+  const int64_t row_bytes = grads ? 2 * ld_block : 8 * ((v + kCeBlock - 1) / kCeBlock);
+  const int64_t most = std::max<int64_t>(kVgTile, std::min(ctx->tune.ce_block_bytes / row_bytes,
+                                                           (int64_t(1) << 30) / tiles_of(v) * kVgTile) / kVgTile * kVgTile);
   int64_t rows = n;
-  if (grads) {
-    const int64_t most = std::max<int64_t>(kVgTile, ctx->tune.ce_block_bytes / (2 * ld_block) / kVgTile * kVgTile);
+  if (n > most) {
     const int64_t passes = (n + most - 1) / most;
-    rows = passes == 1 ? n : round_up((n + passes - 1) / passes, kVgTile);
+    rows = round_up((n + passes - 1) / passes, kVgTile);
   }
   const bool one_pass = rows >= n;
 
@@ -585,19 +605,21 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
     DM_TRY(check_type(op, "dw", C.dw_dtype, true));
     DM_TRY(check_ld(op, "dw", C.ld_dw, C.dim));
   }
+  const int id_size = C.target_dtype == DMUON_INDEX_I64 ? 8 : 4;
+  const int dx_size = C.dx_dtype == DMUON_DTYPE_BF16 ? 2 : 4, dw_size = C.dw_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {C.x, span_bytes(C.n_tokens, C.dim, C.ld_x, 2), false, "x"},
-      {C.w, span_bytes(C.vocab, C.dim, C.ld_w, 2), false, "w"},
-      {C.targets, C.n_tokens * (C.target_dtype == DMUON_INDEX_I64 ? 8 : 4), false, "targets"},
-      {C.weights, C.n_tokens * 4, false, "weights"},
-      {C.loss, C.n_tokens * 4, true, "loss"},
-      {C.lse, C.n_tokens * 4, true, "lse"},
-      {C.total, 4, true, "total"},
-      {C.dx, span_bytes(C.n_tokens, C.dim, C.ld_dx, C.dx_dtype == DMUON_DTYPE_BF16 ? 2 : 4), true, "dx"},
-      {C.dw, span_bytes(C.vocab, C.dim, C.ld_dw, C.dw_dtype == DMUON_DTYPE_BF16 ? 2 : 4), true, "dw"},
+      {C.x, span_bytes(C.n_tokens, C.dim, C.ld_x, 2), 2, false, "x"},
+      {C.w, span_bytes(C.vocab, C.dim, C.ld_w, 2), 2, false, "w"},
+      {C.targets, C.n_tokens * id_size, id_size, false, "targets"},
+      {C.weights, C.n_tokens * 4, 4, false, "weights"},
+      {C.loss, C.n_tokens * 4, 4, true, "loss"},
+      {C.lse, C.n_tokens * 4, 4, true, "lse"},
+      {C.total, 4, 4, true, "total"},
+      {C.dx, span_bytes(C.n_tokens, C.dim, C.ld_dx, dx_size), dx_size, true, "dx"},
+      {C.dw, span_bytes(C.vocab, C.dim, C.ld_dw, dw_size), dw_size, true, "dw"},
   };
   const int nr = static_cast<int>(sizeof r / sizeof r[0]);
-  DM_TRY(check_ranges(ctx, op, r, nr));
+  DM_TRY(check_ranges(op, r, nr));
   DeviceGuard guard(ctx->device);
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, nr));
@@ -622,12 +644,14 @@ int dmuon_embed_forward(dmuon_context* ctx, const dmuon_embed* args, void* strea
   DM_TRY(check_type(op, "rows", A.row_dtype, true));
   DM_TRY(check_ld(op, "table", A.ld_table, A.dim));
   DM_TRY(check_ld(op, "rows", A.ld_rows, A.dim));
+  const int id_size = A.id_dtype == DMUON_INDEX_I64 ? 8 : 4;
+  const int table_elem = A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4, row_elem = A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {A.ids, A.n_tokens * (A.id_dtype == DMUON_INDEX_I64 ? 8 : 4), false, "ids"},
-      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4), false, "table"},
-      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4), true, "rows"},
+      {A.ids, A.n_tokens * id_size, id_size, false, "ids"},
+      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, table_elem), table_elem, false, "table"},
+      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, row_elem), row_elem, true, "rows"},
   };
-  DM_TRY(check_ranges(ctx, op, r, 3));
+  DM_TRY(check_ranges(op, r, 3));
   DeviceGuard guard(ctx->device);
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, 3));
@@ -663,13 +687,14 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
   DM_TRY(check_type(op, "rows", A.row_dtype, true));
   DM_TRY(check_ld(op, "table", A.ld_table, A.dim));
   DM_TRY(check_ld(op, "rows", A.ld_rows, A.dim));
-  const int table_elem = A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
+  const int id_size = A.id_dtype == DMUON_INDEX_I64 ? 8 : 4;
+  const int table_elem = A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4, row_elem = A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {A.ids, A.n_tokens * (A.id_dtype == DMUON_INDEX_I64 ? 8 : 4), false, "ids"},
-      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, table_elem), true, "table"},
-      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4), false, "rows"},
+      {A.ids, A.n_tokens * id_size, id_size, false, "ids"},
+      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, table_elem), table_elem, true, "table"},
+      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, row_elem), row_elem, false, "rows"},
   };
-  DM_TRY(check_ranges(ctx, op, r, 3));
+  DM_TRY(check_ranges(op, r, 3));
   DeviceGuard guard(ctx->device);
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, 3));

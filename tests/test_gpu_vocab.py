@@ -261,6 +261,81 @@ def test_cross_entropy_far_and_equal_logits(ops, spread):
     check_ce(x, w, t, run_ce(ops, x, w, t))
 
 
+def test_cross_entropy_weights_of_either_sign(ops):
+    # Advantages as weights: negative, zero; and weights that cancel (the mean is over a zero sum: nothing comes out).
+    x, w, t, a = (q.to(DEV) for q in inputs(90, 700, 64, seed=14))
+    a = a - 1.0
+    a[::4] = 0.0
+    check_ce(x, w, t, run_ce(ops, x, w, t, weights=a, mean=False), weights=a, mean=False)
+    t = t.clamp(min=0)
+    a[1::2] = -a[::2]
+    out = run_ce(ops, x, w, t, weights=a)
+    assert float(out["total"]) == 0 and not bool(out["dx"].any()) and not bool(out["dw"].any())
+
+
+@pytest.mark.parametrize("n", [20, 300])
+def test_cross_entropy_memory_off_16_bytes(ops, n):
+    # Every array one element past a boundary.
+    x, w, t, a = (q.to(DEV) for q in inputs(n, 700, 72, seed=15))
+    def off(q):
+        b = torch.zeros(q.numel() + 1, device=DEV, dtype=q.dtype)
+        b[1:] = q.reshape(-1)
+        return b[1:].view(q.shape)
+    for dtype in (torch.bfloat16, torch.float32):
+        out = {"loss": off(torch.zeros(n, device=DEV)), "dx": off(torch.zeros(n, 72, device=DEV, dtype=dtype)),
+               "dw": off(torch.zeros(700, 72, device=DEV, dtype=dtype)), "total": off(torch.zeros(1, device=DEV))}
+        ops.cross_entropy(off(x), off(w), off(t), weights=off(a), **out)
+        ops.sync()
+        check_ce(x, w, t, out, weights=a, bf16=dtype == torch.bfloat16)
+    ids, table = off(t), off(w)
+    rows = ops.embed(ids, table, off(x))
+    assert torch.equal(rows, torch.where((t >= 0).unsqueeze(1), w[t.clamp(min=0)], torch.zeros_like(x)))
+    grad = off(torch.zeros(700, 72, device=DEV))
+    ops.embed_grad(ids, rows, grad)
+    ops.sync()
+    want, absolute = (ovocab.embed_grad(t.cpu().numpy(), q, 700) for q in (f64(rows), np.abs(f64(rows))))
+    within(grad, want, n * F * absolute, "grad")
+
+
+def test_cross_entropy_scores_in_passes(cuda_lib):
+    # 7000 tokens x 40 blocks x 8 bytes in at most 1 MiB: three passes, the total over all of them.
+    one = cuda_lib.VocabOps(0)
+    one.set_tuning(14, 1)
+    x, w, t, a = (q.to(DEV) for q in inputs(7000, 5003, 16, seed=16))
+    out = {"loss": torch.empty(7000, device=DEV), "lse": torch.empty(7000, device=DEV), "total": torch.empty(1, device=DEV)}
+    one.cross_entropy(x, w, t, weights=a, **out)
+    one.sync()
+    check_ce(x, w, t, out, weights=a)
+    one.close()
+
+
+def test_cross_entropy_past_32_bit_offsets(ops):
+    # A head of 600000 x 4096 values, zero but for its last 1000 rows.
+    n, v, d, last = 3, 600_000, 4096, 1000
+    g = torch.Generator(device=DEV).manual_seed(17)
+    w = torch.zeros(v, d, device=DEV, dtype=torch.bfloat16)
+    w[-last:] = torch.randn(last, d, generator=g, device=DEV) * (1.3 / d ** 0.5)
+    x = torch.randn(n, d, generator=g, device=DEV).to(torch.bfloat16) * 4
+    t = torch.tensor([v - 1, v - last, 0], device=DEV)
+    out = {"loss": torch.empty(n, device=DEV), "dx": torch.empty_like(x), "dw": torch.empty_like(w)}
+    ops.cross_entropy(x, w, t, **out)
+    ops.sync()
+    z = x.double() @ w[-last:].double().T
+    lse = torch.log(torch.exp(z).sum(1) + (v - last))
+    zt = torch.stack([z[0, -1], z[1, 0], torch.zeros((), device=DEV, dtype=torch.float64)])
+    assert float((out["loss"].double() - (lse - zt)).abs().max()) < 1e-3
+    dz = torch.exp(z - lse[:, None])
+    dz[0, -1] -= 1
+    dz[1, 0] -= 1
+    want = dz @ w[-last:].double() / n
+    assert float((out["dx"].double() - want).norm() / want.norm()) < 3 * U
+    rest = torch.exp(-lse)[:, None].repeat(1, 2)  # rows 0 and v / 2, where w is zero
+    rest[2, 0] -= 1
+    for rows, part in ((slice(v - last, v), dz), ([0, v // 2], rest)):
+        want = part.T @ x.double() / n
+        assert float((out["dw"][rows].double() - want).norm() / want.norm()) < 3 * U
+
+
 def test_cross_entropy_targets_past_the_vocabulary(ops, cuda_lib):
     x, w, t, _ = (q.to(DEV) for q in inputs(60, 300, 64, seed=7))
     bad = t.clone()
@@ -319,7 +394,8 @@ def test_cross_entropy_same_bits_again_and_on_other_streams(ops):
             assert all(torch.equal(want[k], out[k]) for k in want)
 
 
-def test_vocab_calls_in_a_graph(ops):
+def test_vocab_calls_in_a_graph(cuda_lib):
+    ops = cuda_lib.VocabOps(0)
     x, w, t, _ = (q.to(DEV) for q in inputs(200, 1500, 64, seed=12))
     want = run_ce(ops, x, w, t)
     rows = torch.empty(200, 64, device=DEV, dtype=torch.bfloat16)
@@ -337,6 +413,15 @@ def test_vocab_calls_in_a_graph(ops):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(want[k], out[k]) for k in want) and torch.equal(table, want_table)
+    # A larger call outgrows the scratch; the graph's stays.
+    big = inputs(1000, 9000, 64, seed=18)
+    run_ce(ops, *(q.to(DEV) for q in big[:3]))
+    for q in out.values():
+        q.zero_()
+    table.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[k], out[k]) for k in want) and torch.equal(table, want_table)
     ops.sync()
 
 

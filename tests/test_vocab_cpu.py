@@ -101,6 +101,10 @@ CE_BAD = [
     ("ERR_INVALID_ARG", dict(dx=BASE)), ("ERR_INVALID_ARG", dict(dw=BASE + 0x1000 + 100)),
     ("ERR_INVALID_ARG", dict(loss=BASE + 0x21000)), ("ERR_INVALID_ARG", dict(total=BASE + 0x30000 + 126)),
     ("ERR_INVALID_ARG", dict(lse=BASE + 0x10000 + 16)),
+    # not on their elements' boundaries
+    ("ERR_INVALID_ARG", dict(x=BASE + 1)), ("ERR_INVALID_ARG", dict(targets=BASE + 0x10004)),
+    ("ERR_INVALID_ARG", dict(loss=BASE + 0x20002)), ("ERR_INVALID_ARG", dict(dw=BASE + 0x40002, dw_dtype=0)),
+    ("ERR_INVALID_ARG", dict(weights=BASE + 0x50001)),
 ]
 
 
@@ -137,6 +141,8 @@ EMBED_BAD = [
     ("ERR_INVALID_ARG", dict(scale=float("inf"))), ("ERR_INVALID_ARG", dict(flags=2)),
     ("ERR_DTYPE", dict(id_dtype=2)), ("ERR_DTYPE", dict(table_dtype=2)), ("ERR_DTYPE", dict(row_dtype=3)),
     ("ERR_INVALID_ARG", dict(rows=BASE + 0x1000 + 64)),
+    ("ERR_INVALID_ARG", dict(ids=BASE + 2)), ("ERR_INVALID_ARG", dict(table=BASE + 0x1002)),
+    ("ERR_INVALID_ARG", dict(rows=BASE + 0x10001)),
 ]
 
 
