@@ -83,30 +83,39 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Entries [chunk * kDlCols, + kDlCols) of one row; p: its logs; stats: its pairs.
-template <bool LO>
-__device__ __forceinline__ void dlogits_chunk(uint16_t* p, int64_t lo_offset, int vocab, int stats_shift, const float2* stats,
-                                              int64_t stats_ld, const CeRow& R, int chunk) {
-  const int c0 = chunk * kDlCols + threadIdx.x * 8;
-  const bool counted = R.weight != 0.f;  // else zeros, whatever the row's logits are
-  const float lift = log2f(fabsf(R.weight)) - R.lse2;
-  const uint32_t sign = __float_as_uint(R.weight) & 0x80000000u;
+// A thread's part of the entries [chunk * kDlCols, + kDlCols) of one row: the
+// logs (from p) and their blocks' maxima (from the row's pairs) ...
+struct Logs {
   uint4 q[4];
   float m[4];
+};
+__device__ __forceinline__ Logs load_logs(const uint16_t* p, int vocab, int stats_shift, const float2* stats, int64_t stats_ld,
+                                          int chunk) {
+  Logs L;
+  const int c0 = chunk * kDlCols + threadIdx.x * 8;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int c = c0 + k * kDlThreads * 8;
     if (c < vocab) {
-      q[k] = *reinterpret_cast<const uint4*>(p + c);
-      m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x);
+      L.q[k] = *reinterpret_cast<const uint4*>(p + c);
+      L.m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x);
     }
   }
+  return L;
+}
+// ... and their d logits, in place.
+template <bool LO>
+__device__ __forceinline__ void put_dlogits(const Logs& L, uint16_t* p, int64_t lo_offset, int vocab, const CeRow& R, int chunk) {
+  const int c0 = chunk * kDlCols + threadIdx.x * 8;
+  const bool counted = R.weight != 0.f;  // else zeros, whatever the row's logits are
+  const float lift = log2f(fabsf(R.weight)) - R.lse2;
+  const uint32_t sign = __float_as_uint(R.weight) & 0x80000000u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int c = c0 + k * kDlThreads * 8;
     if (c >= vocab) continue;
-    const float top = m[k] + lift;
-    const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+    const float top = L.m[k] + lift;
+    const uint32_t w[4] = {L.q[k].x, L.q[k].y, L.q[k].z, L.q[k].w};
     float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -135,8 +144,10 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
   pdl_launch();
   pdl_wait();
   const int64_t row = blockIdx.y;
+  uint16_t* p = block + row * ld;
   const CeRow R = row_info[row];
-  dlogits_chunk<LO>(block + row * ld, lo_rows * ld, vocab, stats_shift, stats + row, stats_ld, R, blockIdx.x);
+  const Logs L = load_logs(p, vocab, stats_shift, stats + row, stats_ld, blockIdx.x);
+  put_dlogits<LO>(L, p, lo_rows * ld, vocab, R, blockIdx.x);
 }
 
 // ------------------------------------------------------------------- row sums
@@ -233,6 +244,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
   const int64_t dot_row = base + warp / shares;
   bool bad = false;
   const int dot_target = dot_row < R.rows ? load_id(R.targets, R.row0 + dot_row, &bad) : -1;
+  Logs logs;  // on their way while the row's sum is found
+  if (DL) logs = load_logs(R.block + base * R.ld_block, R.vocab, R.stats_shift, R.stats + base, R.stats_ld, chunk);
   {
     const int64_t r = base + (lane & (width - 1));
     const int per_warp = 32 / width, stride = kRowWarps * per_warp;
@@ -240,23 +253,19 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
     if (r < R.rows) {
       const float2* p = R.stats + r;
       int b = warp * per_warp + lane / width;
-      for (; b + 7 * stride < R.n_blocks; b += 8 * stride) {
+      for (; b < R.n_blocks; b += 8 * stride) {
         float2 q[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld);
+        for (int k = 0; k < 8; ++k)
+          q[k] = b + k * stride < R.n_blocks ? __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld)
+                                             : make_float2(__int_as_float(0xff800000), 0.f);
         float top = m;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, q[k].x);
-        if (top != __int_as_float(0xff800000)) {
-          s *= exp2f(m - top);
+        s *= exp2f(m - top);  // a pair's maximum is never -inf: neither is top
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s += q[k].y * exp2f(q[k].x - top);
-          m = top;
-        }
-      }
-      for (; b < R.n_blocks; b += stride) {
-        const float2 q = __ldg(p + static_cast<int64_t>(b) * R.stats_ld);
-        join(m, s, q.x, q.y);
+        for (int k = 0; k < 8; ++k) s += q[k].y * exp2f(q[k].x - top);
+        m = top;
       }
     }
     join_lanes(m, s, width);
@@ -318,10 +327,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
   if (DL) {
     __syncthreads();
     const CeRow o = info;
+    uint16_t* p = R.block + base * R.ld_block;
     if (R.lo_rows > 0)
-      dlogits_chunk<true>(R.block + base * R.ld_block, R.lo_rows * R.ld_block, R.vocab, R.stats_shift, R.stats + base, R.stats_ld, o, chunk);
+      put_dlogits<true>(logs, p, R.lo_rows * R.ld_block, R.vocab, o, chunk);
     else
-      dlogits_chunk<false>(R.block + base * R.ld_block, 0, R.vocab, R.stats_shift, R.stats + base, R.stats_ld, o, chunk);
+      put_dlogits<false>(logs, p, 0, R.vocab, o, chunk);
   }
   if (!R.total.total || chunk != 0) return;
   if (threadIdx.x == 0) {
