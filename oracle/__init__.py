@@ -21,6 +21,8 @@ What the oracle computes, and the passages it follows:
   the dtype paragraph).
 * ``lpt``    -- the longest-processing-time greedy assignment and Graham's
   bound (DMuon docs, "架构设计" §3.1 "分区（全局 LPT）").
+* ``vocab``  -- softmax cross entropy over an output head and embedding lookup,
+  with their gradients (no counterpart on the pages).
 
 Everything is float64 numpy (host BLAS for the matrix products) or pure
 Python; there is no blocking, fusion or reordering beyond the definitions.
@@ -36,6 +38,9 @@ Parity status per function (what pins it is in ``tests/test_oracle.py``):
   the composition of the parts has no printed worked example on the pages.
 * ``adamw.adamw_step``        pinned (torch.optim.AdamW float64 on CPU,
   constant-gradient closed form).
+* ``vocab``                   pinned (closed form at equal logits, gradients
+  against differences, lookup and gradient as each other's transposes;
+  ``tests/test_vocab_cpu.py``).
 * ``lpt.lpt_assign``          pinned (brute-force optimum + Graham bound,
   equal-size balance, the pages' 7-items/8-slots idle example).
 * ``muon.bf16_round``         pinned (torch bfloat16 cast on CPU).
