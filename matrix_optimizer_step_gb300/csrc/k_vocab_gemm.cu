@@ -535,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------ producers (A: warp 0, B: the last)
     const bool is_b = warp != 0;
     const uint32_t dst_off = is_b ? HALF_BYTES : 0u;
+    const uint32_t leader_full0 = mapa_shared(full(0), 0);
     int stage = 0, filled = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -549,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t leader_full = mapa_shared(full(stage), 0);
+        const uint32_t leader_full = leader_full0 + 8u * stage;
         if (leader) mbar_expect_tx(full(stage), 2 * HALF_BYTES);
         ++filled;
         const uint32_t dst = ring + stage * STAGE_BYTES + dst_off;
@@ -586,6 +587,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (T.product < 0) break;
         const bool a_mn = a_is_mn(G, T.product);
         const uint32_t idesc = idesc_bf16_f32(TILE, TILE, a_mn, B_MN);
+        // Descriptors of stage 0; a stage or a 16-deep step on is an addition to
+        // the address field (units of 16 bytes).
+        const uint64_t a0 = a_mn ? desc_mn(ring, 0) : desc_k(ring, 0);
+        const uint64_t b0 = B_MN ? desc_mn(ring + HALF_BYTES, 0) : desc_k(ring + HALF_BYTES, 0);
+        const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4;
+        constexpr uint32_t b_step = B_MN ? 2048u >> 4 : 32u >> 4;
         if (!mbar_wait_bounded_cluster(tempty(use & 1), (static_cast<uint32_t>(use >> 1) & 1u) ^ 1u, abort_flag, G.err,
                                        kErrTimeoutMma))
           break;
@@ -597,14 +604,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = ring + stage * STAGE_BYTES;
-          const uint32_t sb = sa + HALF_BYTES;
+          const uint64_t ad = a0 + static_cast<uint32_t>(stage) * (STAGE_BYTES >> 4);
+          const uint64_t bd = b0 + static_cast<uint32_t>(stage) * (STAGE_BYTES >> 4);
+          umma_bf16_pair(d_tmem, ad, bd, idesc, kb != T.kb0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = a_mn ? desc_mn(sa, kk) : desc_k(sa, kk);
-            const uint64_t bd = B_MN ? desc_mn(sb, kk) : desc_k(sb, kk);
-            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != T.kb0 || kk != 0) ? 1u : 0u);
-          }
+          for (int kk = 1; kk < BK / 16; ++kk) umma_bf16_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, 1u);
           umma_commit_pair_multicast(empty(stage), 0x3);
           if (++stage == STAGES) {
             stage = 0;
