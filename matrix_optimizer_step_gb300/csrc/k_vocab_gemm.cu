@@ -531,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return tile_at(G, t);
   };
 
-  if ((warp == 0 || warp == kProducerBWarp) && lane == 0) {
+  if ((warp == 0 || warp == kProducerBWarp) && elect_one()) {
     // ------------------------------------ producers (A: warp 0, B: the last)
     const bool is_b = warp != 0;
     const uint32_t dst_off = is_b ? HALF_BYTES : 0u;
@@ -577,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (leader only)
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ producer
       tma_prefetch_map(&G.map_a);
       tma_prefetch_map(&G.map_b);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   } else if (warp == 6) {
     if (LOGITS && blockIdx.x == 0 && G.norm.alpha) write_alpha(G.norm, lane);
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t idesc = idesc_bf16_f32(BM, G.np, A_MN, false);
       int stage = 0, use = 0;
