@@ -175,17 +175,21 @@ constexpr int kVgTile = 256;
 constexpr int kHalvesTokens = 128;
 
 // The products that read W run on k_vocab_thin.cu where that is faster.
-//  Logits, microseconds there / on 256 x 256 tiles: 9.5 / 12.4 with 8 tokens and
-//  11.4 / 12.5 with 30 at 11000 x 1000, 178 / 302 with one and 183 / 188 with 24 at
-//  128256 x 4096, 62 / 59 with 30 and 67 / 61 with 64 at 60000 x 2048.
-constexpr int64_t kThinLogitsTokens = 24;
-//  dX (with dW beside it in the 256 x 256 tiles' launch): 18.6 / 13.3 with 8 tokens
-//  at 11000 x 1000, 88 / 107 with 30 at 60000 x 2048, 334 / 432 with one at
-//  128256 x 4096; with 129 to 256 rows of d logits 48 / 44 at 50000 x 768,
-//  125 / 122 at 30000 x 4096, 450 / 504 at 128256 x 4096.
+//  Logits, microseconds there / on 256 x 256 tiles, scores: 7.6 / 12.3 with 8 tokens
+//  and 12.3 / 13.9 with 64 at 11000 x 1000, 157 / 241 with 8 and 158 / 171 with 64 at
+//  128256 x 4096, 48 / 52 with 64 and 52 / 52 with 96 at 60000 x 2048, 26 / 16 with 96
+//  at 50257 x 768.  With logs to write: 55 / 57 with 32 and 63 / 59 with 64 at
+//  60000 x 2048, 32 / 32 with 32 and 44 / 31 with 64 at 60000 x 1024.
+bool thin_logits_pay(int64_t tokens, bool logs) { return tokens <= (logs ? 32 : 64); }
+//  dX (with dW and the sum of the partials), by rows of d logits (two a token up to
+//  128 tokens): 37 / 37 with 16 rows at 50257 x 768 but 4 us more before it, 53 / 58
+//  with 16 and 62 / 64 with 128 at 32000 x 2048, 62 / 63 with 128 at 60000 x 1024,
+//  330 / 427 with 48 at 128256 x 4096.  With 200 rows 78 / 73 at 32000 x 2048,
+//  128 / 127 at 32000 x 4096, 191 / 210 at 100000 x 2048; with 250 rows 134 / 124 at
+//  30000 x 4096, 231 / 237 at 60000 x 4096, 452 / 490 at 128256 x 4096.
 bool thin_dx(int64_t rows, int64_t vocab, int64_t dim) {
   const int64_t entries = vocab * dim;
-  return rows <= kThinRows / 2 ? entries > 36000000 : rows <= kThinRows && entries > 250000000;
+  return rows <= kThinRows / 2 ? entries > 55000000 : rows <= kThinRows && entries > 180000000;
 }
 
 // Tiles of at least this many k-blocks are drawn (k_vocab_gemm.cu): half a
@@ -307,7 +311,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   // the gradients' sums one rounding would not average out.
   const bool halves = grads && n <= kHalvesTokens;
   const int64_t token_rows = halves ? 2 * n : rows;
-  const bool thin_logits = n <= kThinLogitsTokens, thin_x = C.dx && thin_dx(token_rows, v, d);
+  const bool thin_logits = thin_logits_pay(n, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
   const bool rows_make_dlogits = grads && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);

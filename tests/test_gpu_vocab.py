@@ -107,7 +107,7 @@ def run_ce(ops, x, w, t, grads=True, dtype=torch.bfloat16, **kw):
 CE_SHAPES = [(1, 1, 8), (1, 2, 1), (1, 300, 64), (2, 128, 16), (5, 129, 33), (31, 1000, 72), (64, 257, 256), (130, 1000, 96),
              (257, 513, 1000), (300, 5003, 136), (513, 130, 40), (70, 777, 1001), (129, 40000, 64), (1100, 600, 264),
              (3000, 65, 24), (24, 400, 80), (25, 400, 80), (128, 1030, 200), (257, 1030, 200),
-             (2049, 300, 136)]
+             (2049, 300, 136), (32, 400, 80), (33, 700, 72), (48, 1030, 1000), (63, 5003, 136), (65, 777, 2056)]
 
 
 @pytest.mark.parametrize("n, v, d", CE_SHAPES)
@@ -157,9 +157,10 @@ def test_large_reference_is_the_oracle():
         assert np.allclose(f64(got[k][0]), want[k], rtol=1e-10, atol=1e-14), k
 
 
-# Heads from 36 and from 250 million entries on take dX with w as the long operand, up to 128 and 256 rows of d logits.
+# Heads from 55 and from 180 million entries on take dX with w as the long operand, up to 128 and 256 rows of d logits.
 @pytest.mark.parametrize("n, v, d", [(1, 40000, 1000), (24, 36864, 1000), (25, 40009, 1001), (64, 9000, 4096), (65, 40000, 1000),
-                                     (120, 62500, 4008), (129, 62500, 4008), (255, 65000, 4000)])
+                                     (120, 62500, 4008), (129, 62500, 4008), (255, 65000, 4000),
+                                     (1, 60000, 1000), (24, 14000, 4096), (32, 55100, 1001), (33, 60000, 1000), (64, 27600, 2000), (65, 46000, 4000)])
 def test_cross_entropy_large_heads(ops, n, v, d):
     g = torch.Generator(device=DEV).manual_seed(n)
     w = (torch.randn(v, d, generator=g, device=DEV) * (1.3 / d ** 0.5)).to(torch.bfloat16)
