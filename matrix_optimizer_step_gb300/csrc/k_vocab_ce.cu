@@ -153,12 +153,14 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
 // ------------------------------------------------------------------- row sums
 // Joins a row's (maximum, sum) pairs of all vocabulary blocks:
 //   M = max m_b,  S = sum_b s_b 2^(m_b - M),
-// and from them the row's loss.  The product's fp32 sums may truncate, which
-// shows where one logit is large: the target's.  So the target's logit is
-// summed again here (one dot product a row) and takes the place of the
-// product's in S: with rest = S - 2^(z_t - M) and the new z_t,
-//   loss = ln((rest + 2^(z_t - M)) / 2^(z_t - M)),
-// as log1p where the target holds more than half of the sum.
+// and from them the row's loss.  S leaves the target out: its logit is summed
+// here (one dot product a row; the product's fp32 sums truncate, which shows
+// where one logit is large), and with o = 2^(z_t - M)
+//   loss = ln((S + o) / o),
+// as log1p(S / o) where the target holds more than half of the sum, so that
+// the loss of a token that is all but certain keeps its digits: nothing is
+// subtracted from a sum, and z_t - M is taken in 64 bits, an octave count's
+// rounding to 32 being up to 2e-6 of the loss.
 //
 // A block takes `width` rows (1; from 512 on 4, so that a warp reads whole
 // 32-byte sectors of pairs; from 2048 on 8, so that the blocks stay one wave:
@@ -190,9 +192,9 @@ __device__ __forceinline__ void join_lanes(float& m, float& s, int step) {
   }
 }
 
-// This warp's share (of `shares`) of the dot product of two bf16 rows, in fp32;
-// the same in every lane.
-__device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane) {
+// This warp's share (of `shares`) of the dot product of two bf16 rows: a lane's
+// part in fp32, their sum in 64 bits, the same in every lane.
+__device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const int start = share * 32 + lane, step = shares * 32;
   int done = 0;
@@ -210,15 +212,13 @@ __device__ __forceinline__ float warp_dot(const uint16_t* a, const uint16_t* b, 
     }
   }
   for (int c = done + start; c < n; c += step) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
-  float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  return warp_sum(static_cast<double>((acc[0] + acc[1]) + (acc[2] + acc[3])));
 }
 
 template <bool VEC, bool DL>
 __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R, int row_blocks, int chunks) {
-  __shared__ float sm[kRowWarps][8], ss[kRowWarps][8], dots[kRowWarps];
+  __shared__ float sm[kRowWarps][8], ss[kRowWarps][8];
+  __shared__ double dots[kRowWarps];
   __shared__ double red[32];
   __shared__ uint32_t last;
   __shared__ CeRow info;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
     }
   }
   if (dot_target >= 0) {
-    const float d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
+    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
     if (lane == 0) dots[warp] = d;
   }
   __syncthreads();
@@ -292,15 +292,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
       const float weight = t < 0 ? 0.f : R.weights ? __ldg(R.weights + i) : 1.f;
       float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
       if (t >= 0) {
-        float z = 0.f;
+        double z = 0.0;
         for (int k = 0; k < shares; ++k) z += dots[lane * shares + k];
-        z *= R.logit_scale_log2;
-        float rest = s - exp2f(R.target_z[r] - m);
-        if (rest < 0.f) rest = 0.f;  // (a NaN stays)
-        const float own = exp2f(z - m), sum = rest + own, l2 = log2f(sum);
-        loss = own > rest ? log1pf(rest / own) : kLn2 * ((m - z) + l2);
+        const float dz = static_cast<float>(z * R.logit_scale_log2 - m);
+        const float own = exp2f(dz), sum = s + own, l2 = log2f(sum);
+        loss = own > s ? log1pf(s / own) : kLn2 * (l2 - dz);
         lse2 = m + l2;
-        share = rest / sum;
+        share = s / sum;
       }
       if (R.loss && chunk == 0) R.loss[i] = loss;
       if (R.lse && chunk == 0) R.lse[i] = t >= 0 ? kLn2 * lse2 : 0.f;

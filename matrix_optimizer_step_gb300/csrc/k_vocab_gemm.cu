@@ -12,8 +12,8 @@
 // the epilogue of a tile runs under the main loop of the next.
 //
 // The logits' epilogue never stores a logit.  Each thread owns one row and
-// 128 columns: it takes their maximum m and the sum of 2^(z - m), with
-// z = logit * log2(e), and writes that pair.  For the gradient it also leaves
+// 128 columns: it takes their maximum m and the sum of 2^(z - m) over all but
+// the target, with z = logit * log2(e), and writes that pair.  For the gradient it also leaves
 // round((m - z) * 1024) as 16 bits: the exponential's argument in fixed point
 // is within 2^-11 octaves, i.e. a relative error of at most 3.4e-4 in the
 // probability, a quarter of the rounding to bf16 that d logits get anyway,
@@ -238,7 +238,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   m += fabsf(m) * 2.4e-7f;
   if (m == minus_inf) m = 0.f;  // only NaN and -inf: the sum below is then NaN or 0
   const bool row_ok = row < G.M;
-  const int at = target - col0;
+  const int at = target >= 0 ? target - col0 : -1;
   uint16_t* logs = G.logs && row_ok ? G.logs + static_cast<int64_t>(row) * G.ld_logs + col0 : nullptr;
   const int stored = static_cast<int>(min(static_cast<int64_t>(kCeBlock), G.ld_logs - col0));  // a multiple of 64
   // A distance is rounded to the nearest unit by adding 2^23, whose low
@@ -246,12 +246,11 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   const float magic = 8388608.f, most = magic + 65535.f;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   auto chunk = [&](uint32_t (&q)[32], int i) {
-    if (__any_sync(0xffffffffu, target >= 0 && (at >> 5) == i)) {
-      float z = 0.f;
+    // The target's share of the sum is added by the row pass.
+    if (__any_sync(0xffffffffu, (at >> 5) == i)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (at == 32 * i + j) z = __uint_as_float(q[j]);
-      if (target >= 0 && (at >> 5) == i) G.target_z[row] = z * c;
+        if (at == 32 * i + j) q[j] = 0xff800000u;  // -inf
     }
     mask_columns(q, col0 + 32 * i, n);
 #pragma unroll

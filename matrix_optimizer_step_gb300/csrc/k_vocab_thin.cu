@@ -114,8 +114,8 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
     const float mj = __shfl_sync(0xffffffffu, m, j);
     const int tj = __shfl_sync(0xffffffffu, target, j);
     const float z = __uint_as_float(r[j]);
-    if (tj == v) G.target_z[token0 + j] = z * c;
-    const float d = v < G.M ? fmaf(z, c, -mj) : minus_inf;
+    // The target's share of the sum is added by the row pass.
+    const float d = v < G.M && v != tj ? fmaf(z, c, -mj) : minus_inf;
     t[j] = ex2(d);
     if (G.logs && token0 + j < G.tokens && v < G.M)
       G.logs[static_cast<int64_t>(token0 + j) * G.ld_logs + v] =

@@ -201,7 +201,7 @@ bool thin_dx(int64_t rows, int64_t vocab, int64_t dim) {
 // 7e-8 instead of 3e-6.  A logit with few terms that are not zero loses nothing,
 // and is then 4e-6 of itself too large at a width of 4096.
 constexpr double kTruncated = 0.99e-9;
-float untruncated(float scale, int64_t terms) { return static_cast<float>(scale * (1.0 + kTruncated * static_cast<double>(terms))); }
+float untruncated(double scale, int64_t terms) { return static_cast<float>(scale * (1.0 + kTruncated * static_cast<double>(terms))); }
 
 // Tiles of at least this many k-blocks are drawn (k_vocab_gemm.cu): half a
 // microsecond a tile against 9 us and more of work.
@@ -343,7 +343,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const size_t off_x = copy_x ? L.take(static_cast<size_t>(n * ld8) * 2) : 0;
   const size_t off_w = copy_w ? L.take(static_cast<size_t>(v * ld8) * 2) : 0;
   const size_t off_stats = L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float2));
-  const size_t off_z = L.take(static_cast<size_t>(rows) * 4);
   const int width = ce_rows_width(n);
   const size_t off_partial = C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
   size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
@@ -412,13 +411,12 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     ld_w = ld8;
   }
   float2* stats = reinterpret_cast<float2*>(ws + off_stats);
-  float* target_z = reinterpret_cast<float*>(ws + off_z);
   uint16_t* block = reinterpret_cast<uint16_t*>(ws + off_block);
   CeRow* row_info = reinterpret_cast<CeRow*>(ws + off_rows);
   float* alpha = reinterpret_cast<float*>(ws + off_alpha);
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
   uint32_t* counters = static_cast<uint32_t*>(ctx->vocab_ticket.p);  // two tile counters, one ticket
-  const float scale_log2 = C.logit_scale * 1.4426950408889634f;
+  const double scale_log2 = C.logit_scale * 1.4426950408889634;
   CeNorm norm = {};
   norm.alpha = grads ? alpha : nullptr;
   norm.targets = ids;
@@ -458,7 +456,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.ld_logs = ld_block;
       G.stats = stats;
       G.stats_ld = stats_ld;
-      G.target_z = target_z;
       G.targets = here;
       if (first) G.norm = norm;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
@@ -475,7 +472,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.ld_logs = ld_block;
       G.stats = stats;
       G.stats_ld = stats_ld;
-      G.target_z = target_z;
       G.targets = here;
       G.counter = counters;
       if (first) G.norm = norm;
@@ -490,7 +486,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     R.row0 = r0;
     R.rows = nr;
     R.n = n;
-    R.target_z = target_z;
     R.targets = ids;
     R.weights = C.weights;
     R.x = x + r0 * ld_x;

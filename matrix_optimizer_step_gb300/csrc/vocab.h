@@ -200,9 +200,8 @@ struct VocabLogits {
   float logit_scale_log2;             // logit scale times log2(e)
   uint16_t* logs;                     // [row][ld_logs], ld_logs a multiple of 64; or null
   int64_t ld_logs;
-  float2* stats;                      // [block][row]: maximum and sum of 2^(z - maximum), z in octaves
+  float2* stats;                      // [block][row]: maximum, and sum of 2^(z - maximum) without the target's; z in octaves
   int64_t stats_ld;
-  float* target_z;                    // [row]: the target's z
   IdList targets;                     // of row 0 of this product
   uint32_t* counter;                  // zero before
   int32_t drawn;                      // tiles drawn from the counter, else fixed shares
@@ -254,7 +253,6 @@ struct VocabThin {
   int64_t ld_logs;
   float2* stats;
   int64_t stats_ld;
-  float* target_z;
   IdList targets;
   CeNorm norm;
   // dX: fp32 partials [split][token][ld_part]
@@ -286,14 +284,13 @@ struct CeRows {
   int32_t n_blocks;        // vocabulary blocks
   int64_t row0, rows;      // rows of this pass, as part of n
   int64_t n;
-  const float* target_z;   // of row row0: the target's z as the product summed it
   IdList targets;          // of row 0
   const float* weights;    // of row 0, or null
   const uint16_t* x;       // of row row0
   const uint16_t* w;
   int64_t ld_x, ld_w;
   int32_t dim;
-  float logit_scale_log2;
+  double logit_scale_log2;
   CeRow* out;              // of row row0, or null
   // Few rows: the same launch turns the logs into d logits (launch_ce_dlogits says how). Null: not wanted.
   uint16_t* block;

@@ -242,6 +242,37 @@ def test_cross_entropy_rows_that_are_not_counted(ops):
         check_ce(x, w, t, out, weights=a)
 
 
+@pytest.mark.parametrize("n", [3, 40, 70, 300])
+def test_cross_entropy_certain_tokens_keep_their_digits(ops, n):
+    # Logits that are sums of one product, exact in fp32: w's column k, whose id 10 k stands out by 6 + 3 k (a loss
+    # down to 1e-8).  What is left, relative to the loss: the rounding of the scale and of z - m, 45 octaves at most
+    # (45 ln 2 F each), of the exponentials (8 F), of the few hundred additions in four chains (64 F in the worst
+    # case) and of the last steps (8 F); d logits are then rounded to bf16.
+    v, d = 500, 8
+    g = torch.Generator(device=DEV).manual_seed(n)
+    w = (torch.rand(v, d, generator=g, device=DEV) * 4 - 2).to(torch.bfloat16)
+    k = torch.arange(d, device=DEV)
+    w[10 * k, k] = (6 + 3 * k).to(torch.bfloat16)
+    which = torch.arange(n, device=DEV) % d
+    x = torch.nn.functional.one_hot(which, d).to(torch.bfloat16)
+    t = 10 * which
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    dw = torch.empty(v, d, device=DEV)
+    ops.cross_entropy(x, w, t, loss=loss, lse=lse, dw=dw, mean=False)
+    scores = torch.empty(n, device=DEV)
+    ops.cross_entropy(x, w, t, loss=scores)
+    ops.sync()
+    z = w.double().T[which]
+    top = z.gather(1, t[:, None])
+    rest = (torch.exp(z - top).scatter(1, t[:, None], 0.0)).sum(1)
+    want = torch.log1p(rest)
+    tol = (2 * 45 * np.log(2) + 80) * F
+    for got in (loss, scores):
+        within(f64(got), f64(want), tol * f64(want), "loss")
+    share = torch.zeros(d, dtype=torch.float64, device=DEV).index_add_(0, which, rest / (1 + rest))
+    within(f64(dw[10 * k, k]), -f64(share), (tol + U + n * F) * f64(share), "dw")
+
+
 def test_cross_entropy_nothing_counted(ops):
     x, w, t, _ = (q.to(DEV) for q in inputs(40, 300, 64, seed=5))
     out = run_ce(ops, x, w, torch.full_like(t, -1))
