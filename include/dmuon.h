@@ -453,7 +453,7 @@ DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void
  * Backward's `table` is the gradient (written) and its `rows` the gradient of
  * the lookup's output (read).  ids below zero are padding: zero rows forward,
  * no gradient backward; ids at or above vocab likewise, and dmuon_sync reports
- * DMUON_ERR_INVALID_ARG.  Rows of equal ids are added in the order of their
+ * DMUON_ERR_INVALID_ARG.  Rows of equal ids are added in an order fixed by their
  * positions, in fp32, and the result is rounded once.  Both arrays are bf16 or
  * fp32 each, at any row pitch >= dim; rows on 16-byte boundaries with
  * dim % 8 = 0 move as 16-byte vectors.  Errors as dmuon_cross_entropy.
