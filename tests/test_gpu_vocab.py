@@ -597,10 +597,11 @@ def test_wrapper_checks(ops):
         ops.embed(t, torch.zeros(1, 16, device=DEV, dtype=torch.bfloat16).expand(4, 16))
 
 
-@pytest.mark.parametrize("n", [1024, 1025, 8192, 8193, 65536, 65537, 140000])
-@pytest.mark.parametrize("v", [300, 70001])
+@pytest.mark.parametrize("n", [129, 1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 8192, 8193, 65536, 65537, 140000])
+@pytest.mark.parametrize("v", [300, 70001, 2000032])
 def test_embed_backward_long_lists(ops, n, v):
-    # Both sorts (one launch up to 65536 entries), one and two digits; whole numbers, so sums are exact.
+    # Counted places (up to 2048 entries, or 4096 added), both sorts (one launch up to 65536 entries), one to three
+    # digits; whole numbers, so sums are exact.
     ids = ids_of("padded", n, v, seed=n).to(DEV)
     dout = torch.randint(-8, 9, (n, 8), device=DEV).float()
     table = torch.full((v, 8), 7.0, device=DEV)
