@@ -505,6 +505,7 @@ struct Runs {
   int64_t n_runs;
   int32_t col_blocks;
   int32_t join_lanes, join_blocks;  // threads side by side in the join, and its column blocks
+  int32_t zero_rows;                // rows of a warp that writes zeros
   int64_t ld_part;
 };
 
@@ -528,8 +529,12 @@ __device__ __forceinline__ void put_row(const EmbedBackward& E, uint32_t id, int
   }
 }
 
-// Zeros into the rows [r0, r0 + kZeroRows) that no entry names, by one warp.
-constexpr int kZeroRows = 8;
+// Zeros into rows that no entry names: a warp takes kZeroRows of them, or
+// kZeroShortRows of at most kZeroShort bytes (5000 entries of 128256 x 256 in bf16:
+// 27.6 us a call for 32; with rows of 2 KB 32 a warp are too few warps, 22 us for 14
+// at 100 entries of 32000).
+constexpr int kZeroRows = 8, kZeroShortRows = 32, kZeroShort = 512;
+int zero_rows_of(int64_t row_bytes) { return row_bytes <= kZeroShort ? kZeroShortRows : kZeroRows; }
 
 // Row r0 + k for each bit k of `left`.
 template <bool GB, bool VEC>
@@ -549,10 +554,10 @@ __device__ __forceinline__ void zero_marked(const EmbedBackward& E, int64_t r0, 
 }
 
 template <bool GB, bool VEC>
-__device__ __forceinline__ void zero_rows(const EmbedBackward& E, int64_t r0, int lane) {
+__device__ __forceinline__ void zero_rows(const EmbedBackward& E, int64_t r0, int most, int lane) {
   if (r0 >= E.ids.vocab) return;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), E.ids.vocab - r0));
-  zero_marked<GB, VEC>(E, r0, (~__ldcg(E.present + (r0 >> 5)) >> (r0 & 31)) & ((1u << rows) - 1u), lane);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(most), E.ids.vocab - r0));
+  zero_marked<GB, VEC>(E, r0, (~__ldcg(E.present + (r0 >> 5)) >> (r0 & 31)) & (0xffffffffu >> (32 - rows)), lane);
 }
 
 // VEC columns a thread.  n_runs * col_blocks blocks take a run and a column
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const EmbedBackward E
   const uint64_t task = blockIdx.x * sums / all;  // sums in the blocks before this one
   if ((blockIdx.x + 1) * sums / all == task) {
     const int64_t zero = static_cast<int64_t>(blockIdx.x - task);
-    zero_rows<GB, VEC == 8>(E, (zero * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kZeroRows, threadIdx.x & 31);
+    zero_rows<GB, VEC == 8>(E, (zero * (blockDim.x >> 5) + (threadIdx.x >> 5)) * R.zero_rows, R.zero_rows, threadIdx.x & 31);
     return;
   }
   const int64_t run = static_cast<int64_t>(task) / R.col_blocks;
@@ -696,7 +701,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const EmbedBac
 constexpr int kFew = 128;
 
 template <bool DB, bool GB, int VEC>
-__global__ void __launch_bounds__(256) embed_few_kernel(const EmbedBackward E, int col_blocks) {
+__global__ void __launch_bounds__(256) embed_few_kernel(const EmbedBackward E, int col_blocks, int zero_rows) {
   __shared__ uint32_t raw[kFew], keys[kFew + 1], pos[kFew];
   __shared__ uint32_t starts[kFew / 32];
   const int n = static_cast<int>(E.n), t = threadIdx.x, lane = t & 31;
@@ -722,13 +727,13 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedBackward E, i
   __syncthreads();
   const int sums = n * col_blocks;
   if (static_cast<int>(blockIdx.x) >= sums) {
-    // Zeros: a warp takes kZeroRows rows and looks them up.
-    const int64_t r0 = (static_cast<int64_t>(blockIdx.x - sums) * (blockDim.x >> 5) + (t >> 5)) * kZeroRows;
+    // Zeros: a warp takes its rows and looks them up.
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x - sums) * (blockDim.x >> 5) + (t >> 5)) * zero_rows;
     if (r0 >= E.ids.vocab) return;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), E.ids.vocab - r0));
+    const int rows = static_cast<int>(min(static_cast<int64_t>(zero_rows), E.ids.vocab - r0));
     bool named = false;
     for (int j = lane; j < n; j += 32) named = named || (keys[j] >= r0 && keys[j] < r0 + rows);
-    uint32_t left = (1u << rows) - 1u;
+    uint32_t left = 0xffffffffu >> (32 - rows);
     if (__any_sync(0xffffffffu, named)) {
       for (int j = 0; j < n; ++j)
         if (keys[j] >= r0 && keys[j] < r0 + rows) left &= ~(1u << (keys[j] - r0));
@@ -808,7 +813,8 @@ cudaError_t launch_sums(const EmbedBackward& E, Runs R, int* launches, cudaStrea
   const int64_t sums = R.n_runs * R.col_blocks;
   R.join_lanes = std::min(kJoinLanes, (width + 31) / 32 * 32);
   R.join_blocks = (width + R.join_lanes - 1) / R.join_lanes;
-  const int64_t rows_per_block = threads / 32 * kZeroRows;
+  R.zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4));
+  const int64_t rows_per_block = threads / 32 * R.zero_rows;
   const int64_t zeros = E.present ? (E.ids.vocab + rows_per_block - 1) / rows_per_block : 0;
   cudaError_t e = launch_after(vec ? embed_sum_kernel<DB, GB, 8> : embed_sum_kernel<DB, GB, 1>,
                                dim3(static_cast<unsigned>(sums + zeros)), dim3(threads), 0, st, E, R);
@@ -826,11 +832,12 @@ cudaError_t launch_few(const EmbedBackward& E, int* launches, cudaStream_t st) {
   const bool vec = aligned16_rows(E.dout, E.ld_dout, DB, E.dim) && aligned16_rows(E.dtable, E.ld_dtable, GB, E.dim);
   const int width = vec ? E.dim / 8 : E.dim;
   const int threads = sum_threads(width), col_blocks = (width + threads - 1) / threads;
-  const int64_t rows_per_block = threads / 32 * kZeroRows;
+  const int zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4));
+  const int64_t rows_per_block = threads / 32 * zero_rows;
   const int64_t zeros = E.accumulate ? 0 : (E.ids.vocab + rows_per_block - 1) / rows_per_block;
   ++*launches;
   return launch_after(vec ? embed_few_kernel<DB, GB, 8> : embed_few_kernel<DB, GB, 1>,
-                      dim3(static_cast<unsigned>(E.n * col_blocks + zeros)), dim3(threads), 0, st, E, col_blocks);
+                      dim3(static_cast<unsigned>(E.n * col_blocks + zeros)), dim3(threads), 0, st, E, col_blocks, zero_rows);
 }
 
 // One launch of a cluster of `ctas` blocks.
