@@ -529,12 +529,13 @@ __device__ __forceinline__ void put_row(const EmbedBackward& E, uint32_t id, int
   }
 }
 
-// Zeros into rows that no entry names: a warp takes kZeroRows of them, or
-// kZeroShortRows of at most kZeroShort bytes (5000 entries of 128256 x 256 in bf16:
-// 27.6 us a call for 32; with rows of 2 KB 32 a warp are too few warps, 22 us for 14
-// at 100 entries of 32000).
-constexpr int kZeroRows = 8, kZeroShortRows = 32, kZeroShort = 512;
-int zero_rows_of(int64_t row_bytes) { return row_bytes <= kZeroShort ? kZeroShortRows : kZeroRows; }
+// Zeros into rows that no entry names, by a warp each: four rows beside the sums (5001
+// entries of 1031 x 1000 in fp32: 20.4 us a call, 22 with eight), eight where every
+// block sorts the list first (100 entries of 50257 x 768: 19 us, 26 with four), 32 of
+// at most kZeroShort bytes (5000 entries of 128256 x 256 in bf16: 27.6 us for 32;
+// with rows of 2 KB they are too few warps, 22 us for 14 at 100 entries of 32000).
+constexpr int kZeroShort = 512;
+int zero_rows_of(int64_t row_bytes, int usual) { return row_bytes <= kZeroShort ? 32 : usual; }
 
 // Row r0 + k for each bit k of `left`.
 template <bool GB, bool VEC>
@@ -813,7 +814,7 @@ cudaError_t launch_sums(const EmbedBackward& E, Runs R, int* launches, cudaStrea
   const int64_t sums = R.n_runs * R.col_blocks;
   R.join_lanes = std::min(kJoinLanes, (width + 31) / 32 * 32);
   R.join_blocks = (width + R.join_lanes - 1) / R.join_lanes;
-  R.zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4));
+  R.zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4), 4);
   const int64_t rows_per_block = threads / 32 * R.zero_rows;
   const int64_t zeros = E.present ? (E.ids.vocab + rows_per_block - 1) / rows_per_block : 0;
   cudaError_t e = launch_after(vec ? embed_sum_kernel<DB, GB, 8> : embed_sum_kernel<DB, GB, 1>,
@@ -832,7 +833,7 @@ cudaError_t launch_few(const EmbedBackward& E, int* launches, cudaStream_t st) {
   const bool vec = aligned16_rows(E.dout, E.ld_dout, DB, E.dim) && aligned16_rows(E.dtable, E.ld_dtable, GB, E.dim);
   const int width = vec ? E.dim / 8 : E.dim;
   const int threads = sum_threads(width), col_blocks = (width + threads - 1) / threads;
-  const int zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4));
+  const int zero_rows = zero_rows_of(static_cast<int64_t>(E.dim) * (GB ? 2 : 4), 8);
   const int64_t rows_per_block = threads / 32 * zero_rows;
   const int64_t zeros = E.accumulate ? 0 : (E.ids.vocab + rows_per_block - 1) / rows_per_block;
   ++*launches;
