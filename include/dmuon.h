@@ -391,9 +391,11 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  * fp32 throughout; softmax statistics, the loss and the factor of the
  * gradients in fp32 (sums over tokens in fp64); a probability's log is kept
  * in steps of 2^-10 octaves (3.4e-4 of the probability at most); d logits,
- * before that factor, are rounded to bf16 once, up to 128 tokens to two bf16
- * halves; dx and dw once on output (fp32 outputs thus carry the d logits'
- * rounding too).  dW of several passes, and DMUON_CE_ADD_DW, add in fp32
+ * before that factor, are rounded to bf16 once, up to 128 tokens, and with
+ * DMUON_CE_FINE_GRADS always, to two bf16 halves; dx and dw once on output (fp32
+ * outputs thus carry the d logits' rounding too: with one half 2^-9 of a d logit
+ * at most, with two the step of its log).  DMUON_CE_FINE_GRADS doubles the work
+ * of both gradient products above 128 tokens, and the scratch per token.  dW of several passes, and DMUON_CE_ADD_DW, add in fp32
  * before the one rounding.
  *
  *   x        bf16, n_tokens x dim, rows ld_x elements apart
@@ -419,7 +421,8 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  */
 enum {
   DMUON_CE_MEAN = 1u,   /* divide by the counted weights' sum */
-  DMUON_CE_ADD_DW = 2u  /* dw += ... instead of dw = ...      */
+  DMUON_CE_ADD_DW = 2u, /* dw += ... instead of dw = ...      */
+  DMUON_CE_FINE_GRADS = 8u /* d logits in two bf16 halves for any number of tokens */
 };
 
 typedef struct dmuon_ce {

@@ -16,6 +16,7 @@ raises if it has not been built.
 
 from .capi import (  # noqa: F401
     DMUON_CE_ADD_DW,
+    DMUON_CE_FINE_GRADS,
     DMUON_CE_MEAN,
     DMUON_DTYPE_BF16,
     DMUON_DTYPE_F32,

@@ -38,6 +38,7 @@ DMUON_INDEX_I64 = 1
 
 DMUON_CE_MEAN = 1
 DMUON_CE_ADD_DW = 2
+DMUON_CE_FINE_GRADS = 8
 DMUON_EMBED_ADD = 1
 
 EXPORTED = (

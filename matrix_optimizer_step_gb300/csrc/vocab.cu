@@ -171,7 +171,7 @@ bool tma_rows(const void* p, int64_t ld, int elem) { return aligned16(p) && ld *
 
 constexpr int kVgTile = 256;
 
-// Tokens up to which d logits come in two halves.
+// Tokens up to which d logits always come in two halves.
 constexpr int kHalvesTokens = 128;
 
 // The products that read W run on k_vocab_thin.cu where that is faster.
@@ -311,10 +311,17 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const int pairs = ctx->vocab_pairs;
   if (pairs < 1) return set_error(DMUON_ERR_UNSUPPORTED, "cross_entropy: no CTA pair of the product kernel fits the device");
 
+  // Few tokens: a 256-row tile has room for d logits in two bf16 halves (value
+  // and the rounding's rest), so they come at no cost, and with as few terms in
+  // the gradients' sums one rounding would not average out.  More tokens take
+  // them where the caller asks for it: both gradient products are then twice as
+  // long, and what is left of a d logit's error is that of its 16-bit log.
+  const bool halves = grads && (n <= kHalvesTokens || (C.flags & DMUON_CE_FINE_GRADS) != 0);
+
   // Rows of one pass: what is held for each (its logs, or without gradients its
   // statistics) stays within the limit, and tiles are numbered in 32 bits.
   const int64_t ld_block = round_up(v, 64);
-  const int64_t row_bytes = grads ? 2 * ld_block : 8 * ((v + kCeBlock - 1) / kCeBlock);
+  const int64_t row_bytes = grads ? (halves ? 4 : 2) * ld_block : 8 * ((v + kCeBlock - 1) / kCeBlock);
   const int64_t most = std::max<int64_t>(kVgTile, std::min(ctx->tune.ce_block_bytes / row_bytes,
                                                            (int64_t(1) << 30) / tiles_of(v) * kVgTile) / kVgTile * kVgTile);
   int64_t rows = n;
@@ -323,12 +330,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     rows = round_up((n + passes - 1) / passes, kVgTile);
   }
   const bool one_pass = rows >= n;
-
-  // Few tokens: a 256-row tile has room for d logits in two bf16 halves (value
-  // and the rounding's rest), so they come at no cost, and with as few terms in
-  // the gradients' sums one rounding would not average out.
-  const bool halves = grads && n <= kHalvesTokens;
-  const int64_t token_rows = halves ? 2 * n : rows;
+  const int64_t token_rows = halves ? 2 * rows : rows;
   const bool thin_logits = thin_logits_pay(n, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
   const bool rows_make_dlogits = grads && ce_rows_make_dlogits(n);
@@ -607,7 +609,7 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
     return set_error(DMUON_ERR_INVALID_ARG, "cross_entropy: no output asked for");
   if (!finite(C.logit_scale) || C.logit_scale <= 0.f || !finite(C.grad_scale))
     return set_error(DMUON_ERR_INVALID_ARG, "cross_entropy: logit_scale must be positive, grad_scale finite");
-  if (C.flags & ~uint32_t(DMUON_CE_MEAN | DMUON_CE_ADD_DW))
+  if (C.flags & ~uint32_t(DMUON_CE_MEAN | DMUON_CE_ADD_DW | DMUON_CE_FINE_GRADS))
     return set_error(DMUON_ERR_INVALID_ARG, "cross_entropy: unknown flag bits");
   DM_TRY(check_type(op, "x", C.x_dtype, false));
   DM_TRY(check_type(op, "w", C.w_dtype, false));

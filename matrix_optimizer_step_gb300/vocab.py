@@ -110,7 +110,8 @@ class VocabOps:
 
     # ------------------------------------------------------- cross entropy
     def cross_entropy(self, x, w, targets, weights=None, mean=True, logit_scale=1.0, grad_scale=1.0,
-                      loss=None, lse=None, total=None, dx=None, dw=None, accumulate_dw=False, stream=None):
+                      loss=None, lse=None, total=None, dx=None, dw=None, accumulate_dw=False, stream=None,
+                      fine_grads=False):
         """Softmax cross entropy of logits ``logit_scale * x @ w.T`` against
         ``targets`` (below zero: not counted), without storing the logits.
 
@@ -119,7 +120,11 @@ class VocabOps:
         of weights with ``mean``), and the gradients of ``grad_scale * total``
         in ``dx`` (like x) and ``dw`` (like w; added to with
         ``accumulate_dw``), bf16 or fp32.  With none given, ``loss`` is
-        allocated.  Returns ``loss``."""
+        allocated.  Returns ``loss``.
+
+        The gradients are products of d logits in bf16; up to 128 tokens, and
+        with ``fine_grads`` always, a second bf16 holds what the first rounds
+        away (twice the work of both products above 128 tokens)."""
         x_p, ld_x = self._matrix(x, "x", _BF16)
         n, dim = x.shape
         w_p, ld_w = self._matrix(w, "w", _BF16, cols=dim)
@@ -146,7 +151,8 @@ class VocabOps:
         a = capi.DmuonCe(n, vocab, dim, x_p, w_p, ld_x, ld_w, targets_p, weights_p, loss_p, lse_p, total_p, dx_p, dw_p,
                          ld_dx, ld_dw, capi.DMUON_DTYPE_BF16, capi.DMUON_DTYPE_BF16, _INDEX[targets.dtype], dx_type,
                          dw_type, logit_scale, grad_scale,
-                         (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0))
+                         (capi.DMUON_CE_MEAN if mean else 0) | (capi.DMUON_CE_ADD_DW if accumulate_dw else 0)
+                         | (capi.DMUON_CE_FINE_GRADS if fine_grads else 0))
         self._call(self._lib.dmuon_cross_entropy, a, stream)
         return loss
 

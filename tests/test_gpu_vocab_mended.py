@@ -1,0 +1,90 @@
+"""Vocabulary operators on the GPU, cases that an earlier form of them answered wrongly.
+
+Bounds are those of test_gpu_vocab.py (U = 2^-8 and F = 2^-24, the unit roundoffs of bf16 and fp32), each
+with what the case adds to them.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import vocab as ovocab
+from test_gpu_vocab import DEV, F, U, f64, inputs, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops(cuda_lib):
+    o = cuda_lib.VocabOps(0)
+    yield o
+    o.close()
+
+
+# -------------------------------------------------- d logits in two halves
+
+def fine_bounds(x, w, t, a, grad_scale):
+    """dx, dw in float64, and how far off they may be with fp32 outputs and d logits in two bf16 halves: of a
+    d logit (dz) the remainder's rounding U^2 |dz|, of a probability its log's step and the logit's error, as in
+    check_ce; then the product's fp32 sums (twice as long: hi and lo) and one rounding."""
+    n, d = x.shape
+    v = w.shape[0]
+    X, W, T = f64(x), f64(w), t.cpu().numpy()
+    A = f64(a)
+    r = ovocab.cross_entropy(X, W, T, A, grad_scale=grad_scale)
+    counted = T >= 0
+    X = np.where(counted[:, None], X, 0.0)
+    ez = (d / 16 + 8) * 4 * F * float((np.abs(X) @ np.abs(W).T).max())
+    coef = np.where(counted, A, 0.0)
+    coef = grad_scale * coef / coef.sum()
+    adz = np.abs(r["dz"])
+    p = adz.copy()
+    rows = np.arange(n)[counted]
+    p[rows, T[counted]] = coef[counted] - p[rows, T[counted]]
+    ep = 2 * ez + np.log(2) / 2048 + 32 * F
+    edz = adz * U * U + p * ep + coef[:, None] * 2.0 ** -60
+    edz[rows, T[counted]] += 8 * F * coef[counted]
+    out = {}
+    for name, k, E, A_, B in (("dx", 2 * v, edz, adz, np.abs(W)), ("dw", 2 * n, edz.T, adz.T, np.abs(X))):
+        e = E @ B + (k / 16 + 8) * 4 * F * (A_ @ B)
+        out[name] = (r[name], e + F * (np.abs(r[name]) + e) + 1e-38)
+    return out
+
+
+@pytest.mark.parametrize("n, v, d, block_mib", [(129, 513, 72, 0), (300, 5003, 136, 0), (257, 1030, 200, 0), (700, 777, 1001, 0),
+                                                (700, 5003, 136, 1), (1100, 600, 264, 0), (2100, 130, 40, 0)])
+@pytest.mark.parametrize("add", [False, True])
+def test_fine_gradients(cuda_lib, n, v, d, block_mib, add):
+    ops = cuda_lib.VocabOps(0)
+    if block_mib:
+        ops.set_tuning(14, block_mib)  # several passes
+    x, w, t, a = (q.to(DEV) for q in inputs(n, v, d, seed=n + v))
+    base = torch.randn(v, d, device=DEV) * 1e-3
+    want = fine_bounds(x, w, t, a, 0.5)
+    err = {}
+    for fine in (True, False):
+        dx, dw = torch.full((n, d), 7.0, device=DEV), base.clone()
+        ops.cross_entropy(x, w, t, weights=a, grad_scale=0.5, dx=dx, dw=dw, accumulate_dw=add, fine_grads=fine)
+        ops.sync()
+        for name, got in (("dx", dx), ("dw", dw)):
+            ref, tol = want[name]
+            if name == "dw" and add:
+                ref, tol = ref + f64(base), tol + 4 * F * (np.abs(ref) + np.abs(f64(base)))
+            if fine:
+                within(got, ref, tol, name)
+            err[name, fine] = np.linalg.norm(f64(got) - ref)
+    # What the option is for: dw's error is that of its targets' d logits, which one half rounds to U / 2.
+    assert err["dw", True] < 0.5 * err["dw", False], err
+    ops.close()
+
+
+def test_fine_gradients_of_few_tokens_are_the_same(ops):
+    # Up to 128 tokens come in two halves anyway.
+    x, w, t, a = (q.to(DEV) for q in inputs(128, 900, 64, seed=3))
+    got = []
+    for fine in (False, True):
+        dx, dw = torch.empty(128, 64, device=DEV), torch.empty(900, 64, device=DEV)
+        ops.cross_entropy(x, w, t, weights=a, dx=dx, dw=dw, fine_grads=fine)
+        got.append((dx, dw))
+    ops.sync()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

@@ -174,6 +174,17 @@ def test_refusals_of_null_context_and_forward_flags(mos):
         mos.dmuon_context_destroy(ctx)
 
 
+@pytest.mark.parametrize("flags", [16, 1 | 2 | 8 | 32, 1 << 31])
+def test_cross_entropy_refuses_flags_it_does_not_know(mos, flags):
+    ctx = mos.dmuon_context_create(0)
+    try:
+        with pytest.raises(mos.DmuonError) as e:
+            mos.dmuon_cross_entropy(ctx, ce_args(mos.capi, flags=flags), 0)
+        assert e.value.status == mos.capi.DMUON_ERR_INVALID_ARG and "flag" in str(e.value)
+    finally:
+        mos.dmuon_context_destroy(ctx)
+
+
 def test_block_limit_key(mos):
     capi = mos.capi
     ctx = mos.dmuon_context_create(0)
