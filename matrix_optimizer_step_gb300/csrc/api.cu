@@ -116,6 +116,26 @@ int dev_alloc(DevBuf& b, size_t bytes) {
   return DMUON_OK;
 }
 
+// cudaMalloc and a clear that is over when this returns.  cudaMemset goes to the
+// default stream and returns at once, and streams that do not wait for the default
+// one (torch's side streams) could run a kernel on the memory before its clear.
+int dev_alloc_zeroed(DevBuf& b, size_t bytes) {
+  cudaStream_t own = nullptr;
+  DM_CUDA(cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking));
+  int st = dev_alloc(b, bytes);
+  if (st == DMUON_OK) {
+    cudaError_t e = cudaMemsetAsync(b.p, 0, bytes, own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      b.release();
+      st = set_error(DMUON_ERR_CUDA, cudaGetErrorString(e));
+    }
+  }
+  cudaStreamDestroy(own);
+  return st;
+}
+
 int ensure_device(dmuon_context* ctx) {
   if (ctx->dev_ready) return DMUON_OK;
   int count = 0;
@@ -130,9 +150,8 @@ int ensure_device(dmuon_context* ctx) {
     return set_error(DMUON_ERR_UNSUPPORTED,
                      "device is not of the sm_100 family (this library is built for sm_103a)");
   ctx->num_sms = prop.multiProcessorCount;
-  int st = dev_alloc(ctx->err, 16);
+  int st = dev_alloc_zeroed(ctx->err, 16);
   if (st != DMUON_OK) return st;
-  DM_CUDA(cudaMemset(ctx->err.p, 0, 16));
   ctx->dev_ready = true;
   return DMUON_OK;
 }
@@ -476,7 +495,9 @@ int dmuon_sync(dmuon_context* ctx, void* stream) {
   int word = 0;
   DM_CUDA(cudaMemcpy(&word, ctx->err.p, sizeof(int), cudaMemcpyDeviceToHost));
   if (word != kErrNone) {
-    DM_CUDA(cudaMemset(ctx->err.p, 0, sizeof(int)));
+    // Over when this returns, as in dev_alloc_zeroed: the next call may be on any stream.
+    DM_CUDA(cudaMemsetAsync(ctx->err.p, 0, sizeof(int), static_cast<cudaStream_t>(stream)));
+    DM_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
     if (word == kErrBadIndex)
       return set_error(DMUON_ERR_INVALID_ARG, "a token id or target past the vocabulary (the entry was not counted)");
     char buf[96];

@@ -106,6 +106,8 @@ struct DevBuf {
 };
 
 int dev_alloc(DevBuf& b, size_t bytes);
+// Memory of zeros, for kernels on any stream.
+int dev_alloc_zeroed(DevBuf& b, size_t bytes);
 
 template <class T>
 inline int upload(DevBuf& b, const std::vector<T>& v) {

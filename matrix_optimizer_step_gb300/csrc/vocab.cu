@@ -136,9 +136,8 @@ int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
     if (st != DMUON_OK) return st;
   }
   if (!ctx->vocab_ticket.p) {
-    const int st = dev_alloc(ctx->vocab_ticket, 256);
+    const int st = dev_alloc_zeroed(ctx->vocab_ticket, 256);
     if (st != DMUON_OK) return st;
-    DM_CUDA(cudaMemset(ctx->vocab_ticket.p, 0, 256));
   }
   if (cap != cudaStreamCaptureStatusNone) ctx->vocab_captured = true;
   return DMUON_OK;

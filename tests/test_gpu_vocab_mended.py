@@ -88,3 +88,46 @@ def test_fine_gradients_of_few_tokens_are_the_same(ops):
         got.append((dx, dw))
     ops.sync()
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ------------------------------------------------------------------- streams
+
+def busy(stream, ms=60):
+    """About `ms` of work on `stream` (a kernel of torch's that counts clock cycles)."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 2.0e6))
+
+
+@pytest.mark.parametrize("busy_default", [True, False])
+def test_first_call_of_a_handle_on_a_side_stream(cuda_lib, busy_default):
+    # The handle's counters and error word are cleared by its first call.  That call's kernels, on a stream that does
+    # not wait for the default one, must not run before the clearing, whatever the default stream has to do.
+    # More than 76 pairs' worth of tiles of 32 k-blocks: they are drawn from the counters.
+    n, v, d = 300, 22000, 2056
+    x, w, t, a = (q.to(DEV) for q in inputs(n, v, d, seed=21))
+    bad = t.clone()
+    bad[5] = v
+    s = torch.cuda.Stream()
+    keys = ("loss", "lse", "total", "dx", "dw")
+
+    def outputs():
+        return dict(loss=torch.full((n,), 7.0, device=DEV), lse=torch.full((n,), 7.0, device=DEV),
+                    total=torch.full((1,), 7.0, device=DEV), dx=torch.full_like(x, 7.0), dw=torch.full_like(w, 7.0))
+
+    for targets in (t, bad):
+        ops = cuda_lib.VocabOps(0)
+        first, second = outputs(), outputs()
+        torch.cuda.synchronize()
+        if busy_default:
+            busy(torch.cuda.default_stream())
+        ops.cross_entropy(x, w, targets, weights=a, stream=s, **first)
+        if targets is bad:  # the report is not cleared away either
+            with pytest.raises(cuda_lib.DmuonError):
+                ops.sync(s)
+        else:
+            ops.sync(s)
+        torch.cuda.synchronize()
+        ops.cross_entropy(x, w, targets, weights=a, **second)
+        torch.cuda.synchronize()
+        assert all(torch.equal(first[k], second[k]) for k in keys)
+        ops.close()
