@@ -26,24 +26,6 @@ namespace {
 template <bool BF16>
 __device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
   if (BF16) {
-    const uint4 q = __ldg(static_cast<const uint4*>(p));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-}
-
-// The same for memory that the kernel also writes.
-template <bool BF16>
-__device__ __forceinline__ void load8_rw(const void* p, float (&v)[8]) {
-  if (BF16) {
     const uint4 q = *static_cast<const uint4*>(p);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -391,8 +373,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(const 
 #pragma unroll
       for (int k = 0; k < ITEMS; ++k)
         if (has[k]) {
-          key[k] = __ldcg(E.key[to_buf] + first + 32 * k);
-          pos[k] = __ldcg(E.pos[to_buf] + first + 32 * k);
+          key[k] = load_l2(E.key[to_buf] + first + 32 * k);
+          pos[k] = load_l2(E.pos[to_buf] + first + 32 * k);
         }
     }
   }
@@ -401,7 +383,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(const 
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int i = first + 32 * k;
-      if (i < n) mark_row(E, __ldcg(sorted + i), i > 0 ? __ldcg(sorted + i - 1) : 0u, i == 0);
+      if (i < n) mark_row(E, load_l2(sorted + i), i > 0 ? load_l2(sorted + i - 1) : 0u, i == 0);
     }
   }
 }
@@ -516,7 +498,7 @@ __device__ __forceinline__ void put_row(const EmbedBackward& E, uint32_t id, int
   if (VEC == 8) {
     float v[8];
     if (E.accumulate) {
-      load8_rw<GB>(dst, v);
+      load8<GB>(dst, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = fmaf(E.scale, acc[j % VEC], v[j]);
     } else {
@@ -558,7 +540,7 @@ template <bool GB, bool VEC>
 __device__ __forceinline__ void zero_rows(const EmbedBackward& E, int64_t r0, int most, int lane) {
   if (r0 >= E.ids.vocab) return;
   const int rows = static_cast<int>(min(static_cast<int64_t>(most), E.ids.vocab - r0));
-  zero_marked<GB, VEC>(E, r0, (~__ldcg(E.present + (r0 >> 5)) >> (r0 & 31)) & (0xffffffffu >> (32 - rows)), lane);
+  zero_marked<GB, VEC>(E, r0, (~load_l2(E.present + (r0 >> 5)) >> (r0 & 31)) & (0xffffffffu >> (32 - rows)), lane);
 }
 
 // VEC columns a thread.  n_runs * col_blocks blocks take a run and a column
@@ -584,8 +566,8 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const EmbedBackward E
   const uint32_t none = 0xffffffffu, dropped = static_cast<uint32_t>(E.ids.vocab);
   for (int k = threadIdx.x; k < R.run + 2; k += blockDim.x) {
     const int64_t p = p0 + k - 1;
-    keys[k] = p >= 0 && p < E.n ? __ldcg(R.key + p) : none;
-    if (k >= 1 && k <= R.run && p < E.n) pos[k - 1] = __ldcg(R.pos + p);
+    keys[k] = p >= 0 && p < E.n ? load_l2(R.key + p) : none;
+    if (k >= 1 && k <= R.run && p < E.n) pos[k - 1] = load_l2(R.pos + p);
   }
   __syncthreads();
   const int c = (col_block * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * VEC;

@@ -40,8 +40,15 @@ __global__ void __launch_bounds__(1024) ce_norm_kernel(const CeNorm N) {
 template <bool VEC>
 __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int cols, int ld_dst, bool keep, int lane) {
   if (VEC) {
-    for (int c = lane * 8; c < cols; c += 256)
-      *reinterpret_cast<uint4*>(d + c) = keep ? __ldg(reinterpret_cast<const uint4*>(s + c)) : make_uint4(0, 0, 0, 0);
+    for (int c0 = lane * 8; c0 < cols; c0 += 1024) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = keep && c0 + 256 * k < cols ? *reinterpret_cast<const uint4*>(s + c0 + 256 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + 256 * k < cols) *reinterpret_cast<uint4*>(d + c0 + 256 * k) = v[k];
+    }
   } else {
     for (int c0 = lane; c0 < ld_dst; c0 += 256) {
       uint16_t v[8];
@@ -98,7 +105,7 @@ __device__ __forceinline__ Logs load_logs(const uint16_t* p, int vocab, int stat
     const int c = c0 + k * kDlThreads * 8;
     if (c < vocab) {
       L.q[k] = *reinterpret_cast<const uint4*>(p + c);
-      L.m[k] = __ldg(&stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x);
+      L.m[k] = stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x;
     }
   }
   return L;
@@ -202,7 +209,7 @@ __device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b,
     done = n & ~7;
 #pragma unroll 4
     for (int c = start; c < n >> 3; c += step) {
-      const uint4 p = __ldg(reinterpret_cast<const uint4*>(a) + c), q = __ldg(reinterpret_cast<const uint4*>(b) + c);
+      const uint4 p = reinterpret_cast<const uint4*>(a)[c], q = reinterpret_cast<const uint4*>(b)[c];
       const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
         float2 q[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          q[k] = b + k * stride < R.n_blocks ? __ldg(p + static_cast<int64_t>(b + k * stride) * R.stats_ld)
+          q[k] = b + k * stride < R.n_blocks ? p[static_cast<int64_t>(b + k * stride) * R.stats_ld]
                                              : make_float2(__int_as_float(0xff800000), 0.f);
         float top = m;
 #pragma unroll
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
       const int64_t i = R.row0 + r;
       const int t = load_id(R.targets, i, &bad);
       if (bad && chunk == 0) atomicCAS(R.err, 0, kErrBadIndex);
-      const float weight = t < 0 ? 0.f : R.weights ? __ldg(R.weights + i) : 1.f;
+      const float weight = t < 0 ? 0.f : R.weights ? R.weights[i] : 1.f;
       float loss = 0.f, lse2 = m + log2f(s), share = 0.f;  // share: 1 - p_target
       if (t >= 0) {
         double z = 0.0;
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int64
   constexpr int kOutputs = 32 / LANES;  // of a warp, neighbours in neighbouring lanes
   const int lane = threadIdx.x & 31, sub = lane / kOutputs;
   const int64_t per_row = cols / VEC, total = rows * per_row;
-  const float f = alpha ? __ldg(alpha) : 1.f;
+  const float f = alpha ? *alpha : 1.f;
   const int n = fold > 0 ? 2 * parts : parts;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kOutputs; i0 < total;

@@ -629,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t my_staging = staging + static_cast<uint32_t>(warp - 2) * kStaging;
     int use = 0;
     float alpha = 1.f;
-    if constexpr (!LOGITS) alpha = G.alpha ? __ldg(G.alpha) : 1.f;
+    if constexpr (!LOGITS) alpha = G.alpha ? *G.alpha : 1.f;
     for (;; ++use) {
       const Tile T = next_tile(use, true);
       if (T.product < 0) break;

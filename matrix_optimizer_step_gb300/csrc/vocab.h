@@ -45,8 +45,23 @@ __device__ __forceinline__ bool elect_one() {
   return elected != 0;
 }
 
-// All earlier work on the stream is done and visible.
+// All earlier work on the stream is done and visible.  What is read after it may
+// have been written while this block was already resident (by the kernel before,
+// ours or the caller's), so the kernels read with ordinary loads, which are
+// ordered after the wait: the read-only path (ld.global.nc, __ldg) is for memory
+// that nothing writes during a kernel's life, and its lines may be old ones.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From L2, and not before the barrier or fence that it follows: what other blocks wrote.
+__device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ double2 load_l2(const double2* p) {
+  double2 v;
+  asm volatile("ld.global.cg.v2.f64 {%0, %1}, [%2];" : "=d"(v.x), "=d"(v.y) : "l"(p) : "memory");
+  return v;
+}
 // The next kernel's blocks may take free room from here on.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -60,8 +75,7 @@ struct IdList {
 // id of entry i, or -1 where there is none (negative: not counted; past the
 // vocabulary: *bad is set).
 __device__ __forceinline__ int32_t load_id(const IdList& L, int64_t i, bool* bad) {
-  const int64_t v = L.is64 ? __ldg(static_cast<const long long*>(L.p) + i)
-                           : static_cast<int64_t>(__ldg(static_cast<const int*>(L.p) + i));
+  const int64_t v = L.is64 ? static_cast<const long long*>(L.p)[i] : static_cast<int64_t>(static_cast<const int*>(L.p)[i]);
   if (v < 0) return -1;
   if (v >= L.vocab) {
     *bad = true;
@@ -154,7 +168,7 @@ __device__ __forceinline__ double norm_share(const CeNorm& N, int first, int ste
   for (int64_t i = first; i < N.n; i += step) {
     bool bad = false;
     const int t = load_id(N.targets, i, &bad);
-    sum += t < 0 ? 0.f : N.weights ? __ldg(N.weights + i) : 1.f;
+    sum += t < 0 ? 0.f : N.weights ? N.weights[i] : 1.f;
   }
   return sum;
 }
@@ -165,7 +179,7 @@ __device__ __forceinline__ double2 total_share(const CeTotal& T, int first, int 
   double2 s = make_double2(0.0, 0.0);
 #pragma unroll 8
   for (int64_t i = first; i < T.parts; i += step) {
-    const double2 q = __ldcg(T.partial + i);
+    const double2 q = load_l2(T.partial + i);
     s.x += q.x;
     s.y += q.y;
   }

@@ -131,3 +131,31 @@ def test_first_call_of_a_handle_on_a_side_stream(cuda_lib, busy_default):
         torch.cuda.synchronize()
         assert all(torch.equal(first[k], second[k]) for k in keys)
         ops.close()
+
+
+@pytest.mark.parametrize("n, v, d", [(64, 900, 64), (300, 3000, 264), (2100, 1500, 72), (5000, 700, 40)])
+def test_calls_that_feed_one_another(ops, n, v, d):
+    # A call's kernels may be resident while the one before still writes what they read: ids, rows and gradients go
+    # from call to call, other ones each time and in the same memory, against the same calls one at a time.
+    steps = [tuple(q.to(DEV) for q in inputs(n, v, d, seed=30 + k)) for k in range(4)]
+    w = steps[0][1]
+    ids, targets = torch.empty(n, dtype=torch.int64, device=DEV), torch.empty(n, dtype=torch.int64, device=DEV)
+    weights, x, dx = torch.empty(n, device=DEV), torch.empty(n, d, device=DEV, dtype=torch.bfloat16), torch.empty(n, d, device=DEV)
+    out = {}
+    for wait in (True, False):
+        out[wait] = []
+        dw = torch.empty(v, d, device=DEV)
+        for k, (_, _, t, a) in enumerate(steps * 3):
+            ids.copy_(t.roll(1))
+            targets.copy_(t)
+            weights.copy_(a)
+            for call in (lambda: ops.embed(ids, w, x, scale=3.0),
+                         lambda: ops.cross_entropy(x, w, targets, weights=weights, dx=dx, dw=dw),
+                         lambda: ops.embed_grad(ids, dx, dw, accumulate=True),
+                         lambda: out[wait].append((dx.clone(), dw.clone()))):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+    ops.sync()
+    for a, b in zip(out[True], out[False]):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

@@ -209,3 +209,16 @@ def test_python_wrapper_checks(mos):
     with pytest.raises(TypeError):
         ops.embed(torch.zeros(4, dtype=torch.int64), cpu, cpu)
     ops.close()
+
+
+def test_overlapped_kernels_read_with_ordered_loads():
+    # These kernels' blocks are resident while the kernel before them still writes; the read-only path is for memory
+    # that nothing writes during a kernel's life.
+    import os
+    import re
+
+    here = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "matrix_optimizer_step_gb300", "csrc")
+    for name in ("vocab.h", "vocab.cu", "k_embed.cu", "k_vocab_ce.cu", "k_vocab_gemm.cu", "k_vocab_thin.cu"):
+        with open(os.path.join(here, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__ldcg\s*\(", code), name
