@@ -349,7 +349,7 @@ struct dmuon_context {
   // of CTA pairs their products run on.
   dmuon::DevBuf vocab_ws, vocab_ticket;
   cudaEvent_t vocab_done = nullptr;
-  cudaStream_t vocab_stream = nullptr;
+  unsigned long long vocab_stream = 0;  // its id
   bool vocab_used = false;
   // Scratch that a captured graph may use is kept when it is outgrown.
   bool vocab_captured = false;

@@ -114,12 +114,17 @@ int check_index(const char* op, int32_t t) {
 
 // ------------------------------------------------------------------ workspace
 // The vocabulary operators' own scratch: grown on demand, shared by all calls
-// on the context.  A call on another stream than the last one waits for it.
+// on the context.  A call on another stream than the last one waits for it;
+// streams are told apart by their ids, since a handle may stand for another stream
+// than before (cudaStreamPerThread in each thread; a handle freed and given out again).
 int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   DM_CUDA(cudaStreamIsCapturing(s, &cap));
-  if (cap == cudaStreamCaptureStatusNone && ctx->vocab_used && ctx->vocab_stream != s)
-    DM_CUDA(cudaStreamWaitEvent(s, ctx->vocab_done, 0));
+  if (cap == cudaStreamCaptureStatusNone && ctx->vocab_used) {
+    unsigned long long id = 0;
+    DM_CUDA(cudaStreamGetId(s, &id));
+    if (id != ctx->vocab_stream) DM_CUDA(cudaStreamWaitEvent(s, ctx->vocab_done, 0));
+  }
   if (bytes > ctx->vocab_ws.bytes) {
     if (ctx->vocab_captured) {
       // Captured graphs point into the old scratch: it lives as long as the context.
@@ -143,16 +148,21 @@ int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
   return DMUON_OK;
 }
 
-// After the last launch that uses the workspace.
-int vocab_used(dmuon_context* ctx, cudaStream_t s) {
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  DM_CUDA(cudaStreamIsCapturing(s, &cap));
-  if (cap != cudaStreamCaptureStatusNone) return DMUON_OK;
-  if (!ctx->vocab_done) DM_CUDA(cudaEventCreateWithFlags(&ctx->vocab_done, cudaEventDisableTiming));
-  DM_CUDA(cudaEventRecord(ctx->vocab_done, s));
-  ctx->vocab_stream = s;
-  ctx->vocab_used = true;
-  return DMUON_OK;
+// After the last launch that uses the workspace, also of a call that broke off
+// with `st`; returns the call's status.
+int end_use(dmuon_context* ctx, cudaStream_t s, int st) {
+  const auto note = [&] {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess || cap != cudaStreamCaptureStatusNone) return e;
+    if (!ctx->vocab_done) e = cudaEventCreateWithFlags(&ctx->vocab_done, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaEventRecord(ctx->vocab_done, s);
+    if (e == cudaSuccess) e = cudaStreamGetId(s, &ctx->vocab_stream);
+    ctx->vocab_used = ctx->vocab_used || e == cudaSuccess;
+    return e;
+  };
+  const cudaError_t e = note();
+  return st != DMUON_OK || e == cudaSuccess ? st : cuda_fail(e, "end of a vocabulary operator");
 }
 
 struct Layout {
@@ -585,7 +595,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
                                 static_cast<int32_t>(d), s);
       }));
   }
-  return vocab_used(ctx, s);
+  return DMUON_OK;
 }
 
 }  // namespace
@@ -641,10 +651,12 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
   DeviceGuard guard(ctx->device);
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, nr));
-  const int st = cross_entropy_impl(ctx, C, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int st = cross_entropy_impl(ctx, C, s);
+  if (C.n_tokens == 0) return st;  // no scratch
   // A sequence that broke off may have left its counters up.
-  if (st != DMUON_OK && ctx->vocab_ticket.p) cudaMemsetAsync(ctx->vocab_ticket.p, 0, 256, static_cast<cudaStream_t>(stream));
-  return st;
+  if (st != DMUON_OK && ctx->vocab_ticket.p) cudaMemsetAsync(ctx->vocab_ticket.p, 0, 256, s);
+  return end_use(ctx, s, st);
 }
 
 int dmuon_embed_forward(dmuon_context* ctx, const dmuon_embed* args, void* stream) {
@@ -748,9 +760,9 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
   E.present = add ? nullptr : reinterpret_cast<uint32_t*>(ws + W.present);
   E.partial = reinterpret_cast<float*>(ws + W.partial);
   int launches = 0;
-  DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_embed_backward(E, &launches, s); }));
-  ctx->launches += launches - 1;  // timed_launch counted one
-  return W.bytes > 0 ? vocab_used(ctx, s) : DMUON_OK;
+  const int st = timed_launch(ctx, -1, s, [&] { return launch_embed_backward(E, &launches, s); });
+  if (st == DMUON_OK) ctx->launches += launches - 1;  // timed_launch counted one
+  return W.bytes > 0 ? end_use(ctx, s, st) : st;
 }
 
 }  // extern "C"

@@ -159,3 +159,44 @@ def test_calls_that_feed_one_another(ops, n, v, d):
     ops.sync()
     for a, b in zip(out[True], out[False]):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_one_stream_handle_in_two_threads(cuda_lib):
+    # cudaStreamPerThread (handle 2) is another stream in each thread; calls on the two share the context's scratch
+    # and have to wait for one another.
+    import threading
+
+    per_thread = 2
+    ops = cuda_lib.VocabOps(0)
+    sets = [tuple(q.to(DEV) for q in inputs(n, v, d, seed=n)) for n, v, d in ((500, 3000, 200), (300, 5000, 264))]
+    want, got = [], []
+    for x, w, t, a in sets:
+        for to in (want, got):
+            to.append(dict(loss=torch.empty(x.shape[0], device=DEV), dx=torch.empty_like(x), dw=torch.empty_like(w)))
+        ops.cross_entropy(x, w, t, weights=a, **want[-1])
+    ops.sync()
+    torch.cuda.synchronize()
+
+    def call(k, first, then):
+        if first:
+            busy(torch.cuda.ExternalStream(per_thread, device=0), 30)
+        x, w, t, a = sets[k]
+        ops.cross_entropy(x, w, t, weights=a, stream=per_thread, **got[k])
+        if then is not None:
+            then()
+        torch.cuda.ExternalStream(per_thread, device=0).synchronize()
+
+    def other():
+        # While the first thread's call still waits behind its stream's work.
+        th = threading.Thread(target=call, args=(1, False, None))
+        th.start()
+        th.join()
+
+    first = threading.Thread(target=call, args=(0, True, other))
+    first.start()
+    first.join()
+    torch.cuda.synchronize()
+    ops.sync()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[k], b[k]) for k in a)
+    ops.close()
