@@ -74,6 +74,15 @@ class VocabOps:
             raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
 
+    def _empty(self, stream, *shape, dtype):
+        """Memory for a result that ``stream`` writes: torch's allocator gives a block out again in the order of the
+        stream it was taken on, so it is taken on that one."""
+        if stream is None:
+            return torch.empty(shape, device=torch.device("cuda", self.device), dtype=dtype)
+        handle = getattr(stream, "cuda_stream", stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)):
+            return torch.empty(shape, device=torch.device("cuda", self.device), dtype=dtype)
+
     def _call(self, fn, args, stream):
         if stream is None:
             stream = _raw_stream(self.device)
@@ -95,9 +104,12 @@ class VocabOps:
 
     def embed(self, ids, table, out=None, scale=1.0, stream=None):
         """out[i] = scale * table[ids[i]] (zeros for ids below zero); returns
-        ``out`` (allocated in the table's dtype if None)."""
+        ``out`` (allocated on ``stream``, in the table's dtype, if None)."""
         if out is None:
-            out = torch.empty(ids.numel(), table.shape[1], device=table.device, dtype=table.dtype)
+            self._matrix(table, "table", _FLOATS)
+            if not isinstance(ids, _Tensor):
+                self._refuse(ids, "ids", _INDEX)
+            out = self._empty(stream, ids.numel(), table.shape[1], dtype=table.dtype)
         self._embed(self._lib.dmuon_embed_forward, ids, table, out, scale, 0, stream)
         return out
 
@@ -120,7 +132,7 @@ class VocabOps:
         of weights with ``mean``), and the gradients of ``grad_scale * total``
         in ``dx`` (like x) and ``dw`` (like w; added to with
         ``accumulate_dw``), bf16 or fp32.  With none given, ``loss`` is
-        allocated.  Returns ``loss``.
+        allocated, on ``stream``.  Returns ``loss``.
 
         The gradients are products of d logits in bf16; up to 128 tokens, and
         with ``fine_grads`` always, a second bf16 holds what the first rounds
@@ -133,7 +145,7 @@ class VocabOps:
         weights_p = loss_p = lse_p = total_p = dx_p = dw_p = None
         ld_dx = ld_dw = dx_type = dw_type = 0
         if loss is None and lse is None and total is None and dx is None and dw is None:
-            loss = torch.empty(n, device=x.device, dtype=torch.float32)
+            loss = self._empty(stream, n, dtype=torch.float32)
         if weights is not None:
             weights_p = self._list(weights, "weights", _F32, n)
         if loss is not None:

@@ -200,3 +200,53 @@ def test_one_stream_handle_in_two_threads(cuda_lib):
     for a, b in zip(want, got):
         assert all(torch.equal(a[k], b[k]) for k in a)
     ops.close()
+
+
+@pytest.mark.parametrize("what", ["embed", "loss"])
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_results_that_the_wrapper_allocates_belong_to_the_stream(ops, what, as_handle):
+    # Memory that the current stream has freed but is still to write must not become the result of a call on another.
+    n, v, d = 60000, 500, 8
+    x, w, t, _ = (q.to(DEV) for q in inputs(n, v, d, seed=5))
+
+    def call(stream=None):
+        if what == "embed":
+            return ops.embed(t, w, stream=stream)
+        return ops.cross_entropy(x, w, t, stream=stream)
+
+    want = call().clone()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        old = torch.empty_like(want)
+        busy(torch.cuda.current_stream(), 20)
+        old.fill_(3.0)
+        del old
+        got = call(s.cuda_stream if as_handle else s)
+        with torch.cuda.stream(s):
+            same = torch.equal(got, want)
+        torch.cuda.synchronize()
+        assert same and torch.equal(got, want)
+    ops.sync()
+
+
+def test_lookup_on_the_default_streams_handle(ops):
+    # Handle 0 is the default stream, whichever is current.
+    w = torch.randn(50, 16, device=DEV)
+    t = torch.arange(40, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = ops.embed(t, w, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, w[:40])
+
+
+@pytest.mark.parametrize("ids, table", [([1, 2], None), (None, torch.zeros(4)), (None, [[1.0]])])
+def test_lookup_without_an_output_refuses_before_it_allocates(ops, ids, table):
+    good = torch.zeros(4, 16, device=DEV)
+    index = torch.zeros(2, dtype=torch.int64, device=DEV)
+    if isinstance(table, torch.Tensor):
+        table = table.to(DEV)
+    with pytest.raises((TypeError, ValueError)):
+        ops.embed(index if ids is None else ids, good if table is None else table)
