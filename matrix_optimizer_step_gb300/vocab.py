@@ -170,8 +170,9 @@ class VocabOps:
 
     # ---------------------------------------------------------------- misc
     def sync(self, stream=None):
-        """Wait for ``stream`` and raise DmuonError for device-side errors."""
-        capi.dmuon_sync(self.ctx, stream)
+        """Wait for ``stream`` (None: the handle's device's current one) and raise
+        DmuonError for device-side errors."""
+        capi.dmuon_sync(self.ctx, _raw_stream(self.device) if stream is None else stream)
 
     def set_tuning(self, key, value):
         """One tuning key of this context (dmuon_context_set_tuning)."""

@@ -211,6 +211,19 @@ def test_python_wrapper_checks(mos):
     ops.close()
 
 
+def test_sync_waits_for_its_own_devices_stream(mos, monkeypatch):
+    from matrix_optimizer_step_gb300 import vocab
+
+    ops = mos.VocabOps(1)
+    seen = []
+    monkeypatch.setattr(vocab, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(vocab.capi, "dmuon_sync", lambda ctx, stream=None: seen.append(stream))
+    ops.sync()
+    ops.sync(7)
+    assert seen == [1001, 7]
+    ops.close()
+
+
 def test_overlapped_kernels_read_with_ordered_loads():
     # These kernels' blocks are resident while the kernel before them still writes; the read-only path is for memory
     # that nothing writes during a kernel's life.
