@@ -387,8 +387,10 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  * 16-bit fixed-point log per entry leave the product's epilogue, for as many
  * tokens at a time as tuning key 14 allows (without gradients only the
  * maxima and sums of 128 or 32 entries at a time).
- * Rounding: products of bf16 operands with fp32 sums, the target's logit in
- * fp32 throughout; softmax statistics, the loss and the factor of the
+ * Rounding: products of bf16 operands with fp32 sums, which the matrix
+ * instruction truncates (once for 16 terms: with dense operands a logit comes out
+ * nearer to zero by about 1e-9 * dim of itself); the target's logit in fp32 and
+ * fp64 sums apart from the product; softmax statistics, the loss and the factor of the
  * gradients in fp32 (sums over tokens in fp64); a probability's log is kept
  * in steps of 2^-10 octaves (3.4e-4 of the probability at most); d logits,
  * before that factor, are rounded to bf16 once, up to 128 tokens, and with

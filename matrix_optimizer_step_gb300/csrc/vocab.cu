@@ -201,17 +201,6 @@ bool thin_dx(int64_t rows, int64_t vocab, int64_t dim) {
   return rows <= kThinRows / 2 ? entries > 55000000 : rows <= kThinRows && entries > 180000000;
 }
 
-// The MMA's running fp32 sum truncates, so that a logit comes out nearer to
-// zero: by `terms` times this share of itself on average, where its terms add
-// up steadily or at random (widths 512 to 8192; normal operands, shifted ones
-// and ones with outliers: 0.93e-9 to 1.02e-9).  The logits are scaled in the
-// epilogue anyway, and there the mean is taken back: the log-sums of 512 x 16384 x
-// 4096 are then off by 4e-8 instead of 6e-7 (plain fp32: 2e-7), of shifted ones by
-// 7e-8 instead of 3e-6.  A logit with few terms that are not zero loses nothing,
-// and is then 4e-6 of itself too large at a width of 4096.
-constexpr double kTruncated = 0.99e-9;
-float untruncated(double scale, int64_t terms) { return static_cast<float>(scale * (1.0 + kTruncated * static_cast<double>(terms))); }
-
 // Row tiles that go through the columns together, so that L2 keeps them while the
 // other operand passes once for all.  Logits: 184 us with 16 at 4096 x 50257 x 768,
 // 190 with 8; 32 take 67 MB of X at 8192 x 128256 x 4096 and 5.07 ms for 4.82.  dX:
@@ -469,7 +458,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
-      G.logit_scale_log2 = untruncated(scale_log2, std::min<int64_t>(d, (G.kb_total + G.groups - 1) / G.groups * 64));
+      G.logit_scale_log2 = static_cast<float>(scale_log2);
       G.logs = grads ? block : nullptr;
       G.ld_logs = ld_block;
       G.stats = stats;
@@ -485,7 +474,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
-      G.logit_scale_log2 = untruncated(scale_log2, d);
+      G.logit_scale_log2 = static_cast<float>(scale_log2);
       G.logs = grads ? block : nullptr;
       G.ld_logs = ld_block;
       G.stats = stats;

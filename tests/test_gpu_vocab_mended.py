@@ -250,3 +250,59 @@ def test_lookup_without_an_output_refuses_before_it_allocates(ops, ids, table):
         table = table.to(DEV)
     with pytest.raises((TypeError, ValueError)):
         ops.embed(index if ids is None else ids, good if table is None else table)
+
+
+# ------------------------------------------------------------ logits as summed
+
+@pytest.mark.parametrize("d", [4096, 8192])
+@pytest.mark.parametrize("n", [3, 40, 70, 300])
+def test_sparse_rows_keep_the_digits_of_certain_tokens(ops, n, d):
+    # One-hot hidden states: every logit is one product, exact in fp32, whatever the width.  Column k's target
+    # stands at 40, the next entry at 20 to 30, so the loss is exp(that - 40) and more, relatively off by the
+    # absolute error of the competitor's logit: the rounding of the scale and of z - m at 60 octaves (60 ln 2 F
+    # each), the exponentials, the additions and the last steps (80 F, as for narrow heads).
+    v, used = 500, 8
+    g = torch.Generator(device=DEV).manual_seed(n)
+    at = torch.randperm(d, generator=g, device=DEV)[:used]
+    w = torch.zeros(v, d, device=DEV, dtype=torch.bfloat16)
+    k = torch.arange(used, device=DEV)
+    w[:, at] = (torch.rand(v, used, generator=g, device=DEV) * 4 - 2).to(torch.bfloat16)
+    w[10 * k, at] = 40.0
+    w[10 * k + 1, at] = (20 + 10 * k / 7).to(torch.bfloat16)
+    which = torch.arange(n, device=DEV) % used
+    x = torch.zeros(n, d, device=DEV, dtype=torch.bfloat16)
+    x[torch.arange(n, device=DEV), at[which]] = 1.0
+    t = 10 * which
+    loss, scores, dw = torch.empty(n, device=DEV), torch.empty(n, device=DEV), torch.empty(v, d, device=DEV)
+    ops.cross_entropy(x, w, t, loss=loss, dw=dw)
+    ops.cross_entropy(x, w, t, loss=scores)
+    ops.sync()
+    z = w.double()[:, at].T[which]
+    top = z.gather(1, t[:, None])
+    want = torch.log1p(torch.exp(z - top).scatter(1, t[:, None], 0.0).sum(1))
+    tol = (2 * 60 * np.log(2) + 80) * F
+    for got in (loss, scores):
+        within(f64(got), f64(want), tol * f64(want), "loss")
+
+
+@pytest.mark.parametrize("n", [16, 300])
+@pytest.mark.parametrize("d", [1024, 4096, 8192])
+def test_dense_log_sums_are_not_lifted(ops, n, d):
+    # The matrix instruction's running sum may truncate, towards zero: 2 F of the sum at most for each 16 products.
+    # Rows that lean on a few of w's rows have log-sums that are these logits', whose sums grow steadily: on average
+    # a log-sum may come out lower by that, and higher by no more than the roundings outside of the product.
+    v = 2000
+    g = torch.Generator(device=DEV).manual_seed(n + d)
+    w = (torch.randn(v, d, generator=g, device=DEV) * (1.3 / d ** 0.5)).to(torch.bfloat16)
+    on = torch.randint(0, v, (n,), generator=g, device=DEV)
+    x = (torch.randn(n, d, generator=g, device=DEV) * 0.1 + 12.0 * w[on].float()).to(torch.bfloat16)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    lse = torch.empty(n, device=DEV)
+    ops.cross_entropy(x, w, t, lse=lse)
+    ops.sync()
+    z = x.double() @ w.double().T
+    want = torch.logsumexp(z, 1)
+    off = float((lse.double() - want).mean())
+    top = float(z.max(1).values.mean())
+    assert off <= 8 * F * top, (off, top)
+    assert off >= -(d / 16) * 2 * F * top - 8 * F * top, (off, top)
