@@ -269,9 +269,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
         float top = m;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, q[k].x);
-        s *= exp2f(m - top);  // a pair's maximum is never -inf: neither is top
+        const float ref = top == __int_as_float(0xff800000) ? 0.f : top;  // nothing but -inf yet: all sums are 0 or NaN
+        s *= exp2f(m - ref);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += q[k].y * exp2f(q[k].x - top);
+        for (int k = 0; k < 8; ++k) s += q[k].y * exp2f(q[k].x - ref);
         m = top;
       }
     }

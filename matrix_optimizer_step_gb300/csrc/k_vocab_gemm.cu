@@ -235,8 +235,9 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   m *= c;  // c > 0
   // Above every z by more than the rounding of the products below, so that no
   // distance comes out negative.
-  m += fabsf(m) * 2.4e-7f;
-  if (m == minus_inf) m = 0.f;  // only NaN and -inf: the sum below is then NaN or 0
+  // Only -inf and NaN: the pair is -inf and a sum of 0 or NaN, and takes no part in the row's maximum.
+  if (m != minus_inf) m += fabsf(m) * 2.4e-7f;
+  const float ref = m == minus_inf ? 0.f : m;
   const bool row_ok = row < G.M;
   const int at = target >= 0 ? target - col0 : -1;
   uint16_t* logs = G.logs && row_ok ? G.logs + static_cast<int64_t>(row) * G.ld_logs + col0 : nullptr;
@@ -258,8 +259,8 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
       uint32_t w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float lo = fmaf(__uint_as_float(q[16 * p + 2 * k]), c, -m);
-        const float hi = fmaf(__uint_as_float(q[16 * p + 2 * k + 1]), c, -m);
+        const float lo = fmaf(__uint_as_float(q[16 * p + 2 * k]), c, -ref);
+        const float hi = fmaf(__uint_as_float(q[16 * p + 2 * k + 1]), c, -ref);
         s[k & 3] += ex2(lo);
         s[k & 3] += ex2(hi);
         w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),

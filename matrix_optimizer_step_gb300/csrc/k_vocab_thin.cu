@@ -100,8 +100,8 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
   const float top = reduce16(t, lane, [](float a, float b) { return fmaxf(a, b); });
   // Above every z by more than the rounding of the products below.
   float m = top * c;  // c > 0
-  m += fabsf(m) * 2.4e-7f;
-  if (m == minus_inf) m = 0.f;
+  if (m != minus_inf) m += fabsf(m) * 2.4e-7f;
+  const float ref = m == minus_inf ? 0.f : m;  // only -inf and NaN: as in k_vocab_gemm.cu
   const int token = token0 + (lane & 15);
   int target = -1;
   if (token < G.tokens) {
@@ -111,7 +111,7 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
   const float magic = 8388608.f, most = magic + 65535.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float mj = __shfl_sync(0xffffffffu, m, j);
+    const float mj = __shfl_sync(0xffffffffu, ref, j);
     const int tj = __shfl_sync(0xffffffffu, target, j);
     const float z = __uint_as_float(r[j]);
     // The target's share of the sum is added by the row pass.

@@ -306,3 +306,38 @@ def test_dense_log_sums_are_not_lifted(ops, n, d):
     top = float(z.max(1).values.mean())
     assert off <= 8 * F * top, (off, top)
     assert off >= -(d / 16) * 2 * F * top - 8 * F * top, (off, top)
+
+
+@pytest.mark.parametrize("n", [3, 70, 300])
+@pytest.mark.parametrize("level", [-200.0, -5.0])
+def test_blocks_without_finite_logits(ops, n, level):
+    # 256 entries of every row are -inf (ids ruled out by w), the others far below zero, or not.  Each logit is a sum
+    # of two products, exact in fp32; lse and loss: the scale's and m's roundings and the last steps, 8 F |lse| each
+    # as elsewhere, the exponentials and additions 64 F.  The target of row 0 is itself ruled out.
+    v, d = 1000, 16
+    g = torch.Generator(device=DEV).manual_seed(n)
+    w = torch.zeros(v, d, device=DEV, dtype=torch.bfloat16)
+    w[:, 0] = level
+    w[128:384, 0] = float("-inf")
+    w[:, 1] = torch.randint(-16, 17, (v,), generator=g, device=DEV).to(torch.bfloat16) / 8
+    x = torch.zeros(n, d, device=DEV, dtype=torch.bfloat16)
+    x[:, :2] = 1.0
+    t = torch.randint(384, v, (n,), generator=g, device=DEV)
+    t[0], t[1] = 200, -1
+    for grads in (False, True):
+        loss, lse, dw = torch.empty(n, device=DEV), torch.empty(n, device=DEV), torch.zeros(v, d, device=DEV)
+        ops.cross_entropy(x, w, t, loss=loss, lse=lse, mean=False, **(dict(dw=dw) if grads else {}))
+        ops.sync()
+        z = w[:, 0].double() + w[:, 1].double()
+        want = float(torch.logsumexp(z, 0))
+        tol = (64 + 16 * abs(want)) * F
+        counted = t >= 0
+        assert bool(((lse[counted].double() - want).abs() <= tol).all()), (lse[:4], want)
+        assert float(lse[1]) == 0 and float(loss[1]) == 0 and float(loss[0]) == float("inf")
+        assert bool(((loss[2:].double() - (want - z[t[2:]])).abs() <= tol).all())
+    p = torch.exp(z - want)
+    counts = torch.bincount(t[counted], minlength=v).double()
+    ref = p * float(counted.sum()) - counts
+    # a probability's log is kept in steps of 2^-10 octaves, d logits as one bf16 (two up to 128 tokens), sums in fp32
+    tol = (p * float(counted.sum()) + counts) * (np.log(2) / 2048 + U + (n + 64) * F) + 1e-30
+    assert bool(((dw[:, 0].double() - ref).abs() <= tol).all())
