@@ -416,6 +416,8 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  * and vocabulary entry and a copy of x; the copies above; 4 bytes per entry of
  * w for a bf16 dw of several passes.  n_tokens = 0: total is 0, and dw is
  * zeroed unless it is added to.
+ * Memory that a call writes shares no byte with other arguments; column ranges
+ * of one buffer (rows of one pitch in bytes) may lie between one another.
  * Errors: DMUON_ERR_INVALID_ARG (null, misaligned or overlapping memory, no
  * output, bad scale or flags), DMUON_ERR_SHAPE (n_tokens >= 2^31, vocab outside
  * [1, 2^24], dim outside [1, 2^20], a pitch below dim), DMUON_ERR_DTYPE,

@@ -32,15 +32,41 @@ namespace {
 // ------------------------------------------------------------ argument checks
 struct Range {
   const void* p;
-  int64_t bytes;
+  int64_t rows, row_bytes, pitch;  // in bytes; a list is one row
   int elem;  // element size, and the alignment that kernels rely on
   bool written;
   const char* what;
+  // Bytes from the first to the last element.
+  int64_t bytes() const { return rows <= 0 || row_bytes <= 0 ? 0 : (rows - 1) * pitch + row_bytes; }
 };
 
-// Bytes from the first to the last element of rows x cols at pitch ld.
-int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
-  return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * elem;
+Range matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int elem, bool written, const char* what) {
+  return Range{p, rows, cols * elem, ld * elem, elem, written, what};
+}
+Range list(const void* p, int64_t n, int elem, bool written, const char* what) {
+  return Range{p, 1, n * elem, n * elem, elem, written, what};
+}
+
+// Whether two ranges share a byte.  Matrices of one pitch may be column ranges of
+// one buffer, whose rows lie between one another; of two pitches the spans are compared.
+bool share_bytes(const Range& a, const Range& b) {
+  if (!a.p || !b.p || a.bytes() <= 0 || b.bytes() <= 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (pa >= pb + static_cast<uintptr_t>(b.bytes()) || pb >= pa + static_cast<uintptr_t>(a.bytes())) return false;
+  if (a.rows == 1 || b.rows == 1) {
+    // One row against many of `pitch`: it may lie in a gap.
+    const Range& one = a.rows == 1 ? a : b;
+    const Range& many = a.rows == 1 ? b : a;
+    if (many.rows == 1 || one.p < many.p) return true;
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(one.p) - reinterpret_cast<uintptr_t>(many.p)) % many.pitch;
+    return at < many.row_bytes || at + one.row_bytes > many.pitch;
+  }
+  if (a.pitch != b.pitch) return true;
+  const Range& lo = pa <= pb ? a : b;
+  const Range& hi = pa <= pb ? b : a;
+  // Row starts of `hi` lie `at` bytes past row starts of `lo`, or past where they would be.
+  const int64_t at = static_cast<int64_t>(pa <= pb ? pb - pa : pa - pb) % a.pitch;
+  return at < lo.row_bytes || at + hi.row_bytes > a.pitch;
 }
 
 // Alignment of each, and no written range shared with another.
@@ -53,9 +79,7 @@ int check_ranges(const char* op, const Range* r, int n) {
     }
   for (int i = 0; i < n; ++i)
     for (int j = i + 1; j < n; ++j) {
-      if (!r[i].p || !r[j].p || (!r[i].written && !r[j].written)) continue;
-      const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].p), b = reinterpret_cast<uintptr_t>(r[j].p);
-      if (r[i].bytes > 0 && r[j].bytes > 0 && a < b + r[j].bytes && b < a + r[i].bytes) {
+      if ((r[i].written || r[j].written) && share_bytes(r[i], r[j])) {
         snprintf(buf, sizeof buf, "%s: %s overlaps %s (memory the call writes must not be shared)", op, r[i].what,
                  r[j].what);
         return set_error(DMUON_ERR_INVALID_ARG, buf);
@@ -66,7 +90,7 @@ int check_ranges(const char* op, const Range* r, int n) {
 
 int check_pointers(const dmuon_context* ctx, const Range* r, int n) {
   for (int i = 0; i < n; ++i) {
-    if (!r[i].p || r[i].bytes <= 0) continue;
+    if (!r[i].p || r[i].bytes() <= 0) continue;
     const int st = check_reachable(ctx, r[i].p, r[i].what, 0);
     if (st != DMUON_OK) return st;
   }
@@ -625,15 +649,15 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
   const int id_size = C.target_dtype == DMUON_INDEX_I64 ? 8 : 4;
   const int dx_size = C.dx_dtype == DMUON_DTYPE_BF16 ? 2 : 4, dw_size = C.dw_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {C.x, span_bytes(C.n_tokens, C.dim, C.ld_x, 2), 2, false, "x"},
-      {C.w, span_bytes(C.vocab, C.dim, C.ld_w, 2), 2, false, "w"},
-      {C.targets, C.n_tokens * id_size, id_size, false, "targets"},
-      {C.weights, C.n_tokens * 4, 4, false, "weights"},
-      {C.loss, C.n_tokens * 4, 4, true, "loss"},
-      {C.lse, C.n_tokens * 4, 4, true, "lse"},
-      {C.total, 4, 4, true, "total"},
-      {C.dx, span_bytes(C.n_tokens, C.dim, C.ld_dx, dx_size), dx_size, true, "dx"},
-      {C.dw, span_bytes(C.vocab, C.dim, C.ld_dw, dw_size), dw_size, true, "dw"},
+      matrix(C.x, C.n_tokens, C.dim, C.ld_x, 2, false, "x"),
+      matrix(C.w, C.vocab, C.dim, C.ld_w, 2, false, "w"),
+      list(C.targets, C.n_tokens, id_size, false, "targets"),
+      list(C.weights, C.n_tokens, 4, false, "weights"),
+      list(C.loss, C.n_tokens, 4, true, "loss"),
+      list(C.lse, C.n_tokens, 4, true, "lse"),
+      list(C.total, 1, 4, true, "total"),
+      matrix(C.dx, C.n_tokens, C.dim, C.ld_dx, dx_size, true, "dx"),
+      matrix(C.dw, C.vocab, C.dim, C.ld_dw, dw_size, true, "dw"),
   };
   const int nr = static_cast<int>(sizeof r / sizeof r[0]);
   DM_TRY(check_ranges(op, r, nr));
@@ -666,9 +690,9 @@ int dmuon_embed_forward(dmuon_context* ctx, const dmuon_embed* args, void* strea
   const int id_size = A.id_dtype == DMUON_INDEX_I64 ? 8 : 4;
   const int table_elem = A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4, row_elem = A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {A.ids, A.n_tokens * id_size, id_size, false, "ids"},
-      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, table_elem), table_elem, false, "table"},
-      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, row_elem), row_elem, true, "rows"},
+      list(A.ids, A.n_tokens, id_size, false, "ids"),
+      matrix(A.table, A.vocab, A.dim, A.ld_table, table_elem, false, "table"),
+      matrix(A.rows, A.n_tokens, A.dim, A.ld_rows, row_elem, true, "rows"),
   };
   DM_TRY(check_ranges(op, r, 3));
   DeviceGuard guard(ctx->device);
@@ -709,9 +733,9 @@ int dmuon_embed_backward(dmuon_context* ctx, const dmuon_embed* args, void* stre
   const int id_size = A.id_dtype == DMUON_INDEX_I64 ? 8 : 4;
   const int table_elem = A.table_dtype == DMUON_DTYPE_BF16 ? 2 : 4, row_elem = A.row_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
   const Range r[] = {
-      {A.ids, A.n_tokens * id_size, id_size, false, "ids"},
-      {A.table, span_bytes(A.vocab, A.dim, A.ld_table, table_elem), table_elem, true, "table"},
-      {A.rows, span_bytes(A.n_tokens, A.dim, A.ld_rows, row_elem), row_elem, false, "rows"},
+      list(A.ids, A.n_tokens, id_size, false, "ids"),
+      matrix(A.table, A.vocab, A.dim, A.ld_table, table_elem, true, "table"),
+      matrix(A.rows, A.n_tokens, A.dim, A.ld_rows, row_elem, false, "rows"),
   };
   DM_TRY(check_ranges(op, r, 3));
   DeviceGuard guard(ctx->device);

@@ -341,3 +341,53 @@ def test_blocks_without_finite_logits(ops, n, level):
     # a probability's log is kept in steps of 2^-10 octaves, d logits as one bf16 (two up to 128 tokens), sums in fp32
     tol = (p * float(counted.sum()) + counts) * (np.log(2) / 2048 + U + (n + 64) * F) + 1e-30
     assert bool(((dw[:, 0].double() - ref).abs() <= tol).all())
+
+
+# ------------------------------------------------------ column ranges of one buffer
+
+@pytest.mark.parametrize("n, d, gap", [(300, 64, 0), (40, 40, 0), (300, 33, 3), (130, 72, 8)])
+def test_column_ranges_of_one_buffer(ops, n, d, gap):
+    # x and dx, w and dw, a table and its rows: the same bits as apart, and nothing between them written.
+    v = 700
+    x, w, t, a = (q.to(DEV) for q in inputs(n, v, d, seed=n + d))
+
+    def apart():
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        loss = torch.empty(n, device=DEV)
+        ops.cross_entropy(x, w, t, weights=a, loss=loss, dx=dx, dw=dw)
+        return loss, dx, dw
+
+    def together(left):
+        out = []
+        for q in (x, w):
+            buf = torch.full((q.shape[0], 2 * d + 3 * gap), 3.0, device=DEV, dtype=torch.bfloat16)
+            first, second = buf[:, gap:gap + d], buf[:, d + 2 * gap:2 * d + 2 * gap]
+            first.copy_(q) if left else second.copy_(q)
+            out.append((buf, first if left else second, second if left else first))
+        (bx, xs, dx), (bw, ws, dw) = out
+        loss = torch.empty(n, device=DEV)
+        ops.cross_entropy(xs, ws, t, weights=a, loss=loss, dx=dx, dw=dw)
+        ops.sync()
+        assert torch.equal(xs, x) and torch.equal(ws, w)
+        for buf in (bx, bw):
+            for k in (0, d + gap, 2 * d + 2 * gap):
+                assert bool((buf[:, k:k + gap] == 3).all())
+        return loss, dx, dw
+
+    want = apart()
+    for left in (True, False):
+        for p, q in zip(want, together(left)):
+            # x and w start elsewhere in memory (copied or not), which moves no sum but the target's few lanes
+            assert torch.allclose(p.float(), q.float(), rtol=2 * U, atol=1e-6), float((p.float() - q.float()).abs().max())
+    buf = torch.full((v, 2 * d), 3.0, device=DEV)
+    buf[:, :d] = w
+    rows = buf[:n, d:]
+    ids = t.clamp(min=0)
+    ops.embed(ids, buf[:, :d], rows)
+    ops.embed_grad(ids, rows, buf[:, :d])
+    ops.sync()
+    assert torch.equal(rows, w[ids].float()) and bool((buf[n:, d:] == 3).all())
+    want = torch.zeros(v, d, dtype=torch.float64, device=DEV).index_add_(0, ids, rows.double())
+    assert bool(((buf[:, :d].double() - want).abs() <= n * F * want.abs() + 1e-30).all())
+    with pytest.raises(RuntimeError):
+        ops.embed(ids, buf[:, :d], buf[:n, d - 1:2 * d - 1])

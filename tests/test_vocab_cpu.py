@@ -211,6 +211,31 @@ def test_python_wrapper_checks(mos):
     ops.close()
 
 
+# Column ranges of one buffer at 80 elements (160 bytes) a row: x 16 wide at column 0.
+INTERLEAVED = [
+    (True, dict(ld_x=80, ld_dx=80, dx=BASE + 32)), (True, dict(ld_x=80, ld_dx=80, dx=BASE + 128)),
+    (False, dict(ld_x=80, ld_dx=80, dx=BASE + 30)), (False, dict(ld_x=80, ld_dx=80, dx=BASE + 130)),
+    (False, dict(ld_x=80, ld_dx=80, dx=BASE + 160)), (False, dict(ld_x=80, ld_dx=80, dx=BASE + 160 * 3 + 30)),
+    (True, dict(ld_x=80, ld_dx=80, dx=BASE + 160 * 3 + 32)), (True, dict(ld_x=80, ld_dx=40, dx_dtype=0, dx=BASE + 32)),
+    (False, dict(ld_x=80, ld_dx=40, dx_dtype=0, dx=BASE + 100)),
+    (False, dict(ld_x=80, ld_dx=40, dx=BASE + 32)),  # other pitches: by their spans
+    (True, dict(ld_x=80, loss=BASE + 32)), (True, dict(ld_x=80, loss=BASE + 160 + 144)), (False, dict(ld_x=80, loss=BASE + 148)),
+    (False, dict(ld_x=80, loss=BASE - 12)), (True, dict(ld_x=80, loss=BASE - 16)), (False, dict(ld_x=80, total=BASE + 160 + 28)),
+]
+
+
+@pytest.mark.parametrize("fine, kw", INTERLEAVED, ids=lambda v: str(v)[:60])
+def test_column_ranges_of_one_buffer(mos, fine, kw):
+    # Without a device a call that passes its checks ends at that; a refusal names the overlap.
+    ctx = mos.dmuon_context_create(99)
+    try:
+        with pytest.raises(mos.DmuonError) as e:
+            mos.dmuon_cross_entropy(ctx, ce_args(mos.capi, **kw), 0)
+        assert ("overlaps" not in str(e.value)) == fine, (kw, e.value)
+    finally:
+        mos.dmuon_context_destroy(ctx)
+
+
 def test_sync_waits_for_its_own_devices_stream(mos, monkeypatch):
     from matrix_optimizer_step_gb300 import vocab
 
