@@ -333,11 +333,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) ce_rows_kernel(const CeRows R,
   if (DL) {
     __syncthreads();
     const CeRow o = info;
-    uint16_t* p = R.block + base * R.ld_block;
-    if (R.lo_rows > 0)
-      put_dlogits<true>(logs, p, R.lo_rows * R.ld_block, R.vocab, o, chunk);
-    else
-      put_dlogits<false>(logs, p, 0, R.vocab, o, chunk);
+    put_dlogits<true>(logs, R.block + base * R.ld_block, R.lo_rows * R.ld_block, R.vocab, o, chunk);
   }
   if (!R.total.total || chunk != 0) return;
   if (threadIdx.x == 0) {

@@ -355,7 +355,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const int64_t token_rows = halves ? 2 * rows : rows;
   const bool thin_logits = thin_logits_pay(n, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
-  const bool rows_make_dlogits = grads && ce_rows_make_dlogits(n);
+  const bool rows_make_dlogits = halves && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
   const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
 
@@ -516,7 +516,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     R.n_blocks = n_blocks;
     R.row0 = r0;
     R.rows = nr;
-    R.n = n;
     R.targets = ids;
     R.weights = C.weights;
     R.x = x + r0 * ld_x;
@@ -529,7 +528,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     if (rows_make_dlogits) {
       R.block = block;
       R.ld_block = ld_block;
-      R.lo_rows = halves ? nr : 0;
+      R.lo_rows = nr;
       R.vocab = static_cast<int32_t>(v);
       R.stats_shift = stats_shift;
     }

@@ -296,8 +296,7 @@ struct CeRows {
   const float2* stats;
   int64_t stats_ld;
   int32_t n_blocks;        // vocabulary blocks
-  int64_t row0, rows;      // rows of this pass, as part of n
-  int64_t n;
+  int64_t row0, rows;      // rows of this pass
   IdList targets;          // of row 0
   const float* weights;    // of row 0, or null
   const uint16_t* x;       // of row row0
@@ -306,7 +305,7 @@ struct CeRows {
   int32_t dim;
   double logit_scale_log2;
   CeRow* out;              // of row row0, or null
-  // Few rows: the same launch turns the logs into d logits (launch_ce_dlogits says how). Null: not wanted.
+  // Few rows: the same launch turns the logs into d logits in two halves (launch_ce_dlogits says how). Null: not wanted.
   uint16_t* block;
   int64_t ld_block, lo_rows;
   int32_t vocab, stats_shift;
