@@ -208,12 +208,19 @@ constexpr int kVgTile = 256;
 constexpr int kHalvesTokens = 128;
 
 // The products that read W run on k_vocab_thin.cu where that is faster.
-//  Logits, microseconds there / on 256 x 256 tiles, scores: 7.6 / 12.3 with 8 tokens
-//  and 12.3 / 13.9 with 64 at 11000 x 1000, 157 / 241 with 8 and 158 / 171 with 64 at
-//  128256 x 4096, 48 / 52 with 64 and 52 / 52 with 96 at 60000 x 2048, 26 / 16 with 96
-//  at 50257 x 768.  With logs to write: 55 / 57 with 32 and 63 / 59 with 64 at
-//  60000 x 2048, 32 / 32 with 32 and 44 / 31 with 64 at 60000 x 1024.
-bool thin_logits_pay(int64_t tokens, bool logs) { return tokens <= (logs ? 32 : 64); }
+//  Logits, microseconds of a call there / on 256 x 256 tiles, W from HBM.  Scores: 162 / 248
+//  with 1 token and 169 / 185 with 64 at 128256 x 4096, 39 / 65 and 51 / 55 at 128256 x 768,
+//  8.2 / 11 with 1 and 12 / 11 with 64 at 8000 x 256, 41 / 49 with 48 and 46 / 42 with 64 at
+//  128256 x 512: to 64 tokens, narrow heads to 48.  With logs to write, two bytes at a time
+//  there (gradient calls): 160 / 186 with 1 and 165 / 171 with 32 at 32000 x 4096, 302 / 304
+//  with 24 and 314 / 306 with 32 at 128256 x 2048, 548 / 546 with 32 at 128256 x 4096; of
+//  narrow heads 71 / 78 with 32 at 50257 x 768, 111 / 115 with 8, 116 / 115 with 16 and
+//  135 / 122 with 32 at 128256 x 512, 236 / 245 with 8 and 270 / 251 with 16 at 250000 x 768:
+//  to 32 tokens, and where the main loop is too short to hide the stores to 2.2 million logs.
+bool thin_logits_pay(int64_t tokens, int64_t vocab, int64_t dim, bool logs) {
+  if (!logs) return tokens <= (dim < 768 ? 48 : 64);
+  return tokens <= 32 && (dim >= 2048 || tokens * vocab <= 2200000);
+}
 //  dX (with dW and the sum of the partials), by rows of d logits (two a token up to
 //  128 tokens): 37 / 37 with 16 rows at 50257 x 768 but 4 us more before it, 53 / 58
 //  with 16 and 62 / 64 with 128 at 32000 x 2048, 62 / 63 with 128 at 60000 x 1024,
@@ -353,7 +360,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   }
   const bool one_pass = rows >= n;
   const int64_t token_rows = halves ? 2 * rows : rows;
-  const bool thin_logits = thin_logits_pay(n, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
+  const bool thin_logits = thin_logits_pay(n, v, d, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
   const bool rows_make_dlogits = halves && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);

@@ -85,3 +85,20 @@ def test_large_heads_log_sums_and_total(ops, n, v, d):
         ops.sync()
         assert bool(((out["lse"].double() - want * counted).abs() <= tol * counted).all())
         assert abs(float(out["total"]) - total) <= float(tol.max()) + 8 * F * abs(total)
+
+
+# Few-token logits on both sides of where they leave their own kernel: narrow heads at 48 tokens for scores and at
+# 2.2 million logs for gradients (n x v), wide ones at 32.
+@pytest.mark.parametrize("n, v, d", [(48, 9000, 512), (49, 9000, 512), (48, 9000, 768), (64, 9000, 768), (15, 140000, 72),
+                                     (16, 140000, 72), (32, 68750, 136), (32, 68751, 136), (32, 70000, 2048), (33, 70000, 2048)])
+def test_few_tokens_at_the_kernels_borders(ops, n, v, d):
+    x, w, t, a = batch(n, v, d, n + d)
+    ref = large_reference(x, w, t, a)
+    scores, out = torch.empty(n, device=DEV), dict(loss=torch.empty(n, device=DEV), dx=torch.empty_like(x), dw=torch.empty_like(w))
+    ops.cross_entropy(x, w, t, weights=a, loss=scores)
+    ops.cross_entropy(x, w, t, weights=a, **out)
+    ops.sync()
+    for k, got in (("loss", scores), *out.items()):
+        want, tol = ref[k]
+        bad = ~((got.double() - want).abs() <= tol)
+        assert not bool(bad.any()), (k, int(bad.sum()), bad.nonzero()[:3].tolist())
