@@ -150,19 +150,24 @@ int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
     if (id != ctx->vocab_stream) DM_CUDA(cudaStreamWaitEvent(s, ctx->vocab_done, 0));
   }
   if (bytes > ctx->vocab_ws.bytes) {
-    if (ctx->vocab_captured) {
-      // Captured graphs point into the old scratch: it lives as long as the context.
+    if (ctx->vocab_captured || cap != cudaStreamCaptureStatusNone) {
+      // Captured graphs point into the old scratch, and a capture refuses to free memory:
+      // it lives as long as the context, and stays in use if there is no other to be had.
+      DevBuf next;
+      const int st = dev_alloc(next, bytes);
+      if (st != DMUON_OK) return st;
       try {
         ctx->vocab_retired.push_back(ctx->vocab_ws);
       } catch (...) {
+        next.release();
         return set_error(DMUON_ERR_NOMEM, "host allocation failed");
       }
-      ctx->vocab_ws = DevBuf();
+      ctx->vocab_ws = next;
       ctx->vocab_captured = false;
+    } else {
+      const int st = dev_alloc(ctx->vocab_ws, bytes);  // frees the old first
+      if (st != DMUON_OK) return st;
     }
-    ctx->vocab_ws.release();
-    const int st = dev_alloc(ctx->vocab_ws, bytes);
-    if (st != DMUON_OK) return st;
   }
   if (!ctx->vocab_ticket.p) {
     const int st = dev_alloc_zeroed(ctx->vocab_ticket, 256);

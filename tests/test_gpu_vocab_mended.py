@@ -391,3 +391,44 @@ def test_column_ranges_of_one_buffer(ops, n, d, gap):
     assert bool(((buf[:, :d].double() - want).abs() <= n * F * want.abs() + 1e-30).all())
     with pytest.raises(RuntimeError):
         ops.embed(ids, buf[:, :d], buf[:n, d - 1:2 * d - 1])
+
+
+def test_a_capture_that_cannot_grow_the_scratch_loses_nothing(cuda_lib):
+    # Memory cannot be had or freed while a stream is captured (in the default mode): the call is refused, and the
+    # scratch that was there serves the calls after it.
+    import ctypes
+
+    cuda = ctypes.CDLL("libcuda.so.1")
+    ops = cuda_lib.VocabOps(0)
+    x, w, t, _ = (q.to(DEV) for q in inputs(1000, 60000, 16, seed=2))  # 120 MB of logs
+    bx, bt = x.repeat(3, 1), t.repeat(3)
+    out = dict(loss=torch.empty(1000, device=DEV), dx=torch.empty_like(x))
+    big = dict(loss=torch.empty(3000, device=DEV), dx=torch.empty_like(bx))
+    s = torch.cuda.Stream()
+    ops.cross_entropy(x, w, t, **out)
+    ops.sync()
+    want = {k: q.clone() for k, q in out.items()}
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        assert cuda.cuStreamBeginCapture_v2(ctypes.c_void_p(s.cuda_stream), 0) == 0
+        with pytest.raises(cuda_lib.DmuonError):
+            ops.cross_entropy(bx, w, bt, stream=s, **big)
+        graph = ctypes.c_void_p()
+        cuda.cuStreamEndCapture(ctypes.c_void_p(s.cuda_stream), ctypes.byref(graph))
+        assert not graph.value
+        out["loss"].zero_()
+        ops.cross_entropy(x, w, t, **out)
+        ops.sync()
+        assert all(torch.equal(want[k], out[k]) for k in want)
+    assert torch.cuda.mem_get_info()[0] > free - (64 << 20)
+    # The larger call then gives what it gives on a handle of its own.
+    ops.cross_entropy(bx, w, bt, **big)
+    ops.sync()
+    other = cuda_lib.VocabOps(0)
+    ref = {k: torch.empty_like(q) for k, q in big.items()}
+    other.cross_entropy(bx, w, bt, **ref)
+    other.sync()
+    assert all(torch.equal(ref[k], big[k]) for k in ref)
+    ops.close()
+    other.close()
