@@ -109,11 +109,16 @@ int dev_alloc(DevBuf& b, size_t bytes);
 // Memory of zeros, for kernels on any stream.
 int dev_alloc_zeroed(DevBuf& b, size_t bytes);
 
+// A table for kernels on any stream.  A copy from pageable memory may return with its
+// last part still on its way, on the default stream, which side streams do not wait for.
 template <class T>
 inline int upload(DevBuf& b, const std::vector<T>& v) {
   int st = dev_alloc(b, std::max<size_t>(v.size() * sizeof(T), 16));
   if (st != DMUON_OK) return st;
-  if (!v.empty()) DM_CUDA(cudaMemcpy(b.p, v.data(), v.size() * sizeof(T), cudaMemcpyHostToDevice));
+  if (!v.empty()) {
+    DM_CUDA(cudaMemcpy(b.p, v.data(), v.size() * sizeof(T), cudaMemcpyHostToDevice));
+    DM_CUDA(cudaStreamSynchronize(cudaStreamLegacy));
+  }
   return DMUON_OK;
 }
 
