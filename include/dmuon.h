@@ -414,7 +414,7 @@ DMUON_API int dmuon_step_host(dmuon_context* ctx,
  * (pointer and pitch; TMA): other x and w are copied first, and other dx and
  * dw stored without TMA.  Scratch: with gradients 2 bytes per token of a pass
  * and vocabulary entry and a copy of x; the copies above; 4 bytes per entry of
- * w for a bf16 dw of several passes.  n_tokens = 0: total is 0, and dw is
+ * w for a bf16 dw of several passes; kept until the context is destroyed.  n_tokens = 0: total is 0, and dw is
  * zeroed unless it is added to.
  * Memory that a call writes shares no byte with other arguments; column ranges
  * of one buffer (rows of one pitch in bytes) may lie between one another.

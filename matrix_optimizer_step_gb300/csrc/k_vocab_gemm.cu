@@ -210,7 +210,7 @@ __device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
 
 // The accumulator is read twice, 32 columns at a time: once for the maximum
 // and once for the sums and logs.  Holding all 128 columns in registers
-// spills (168 registers a thread with 11 warps) and measured 2.1 times the
+// spills (168 registers a thread with 12 warps) and measured 2.1 times the
 // time of the whole product at 4096 x 50257 x 768.
 // `target`: of this thread's row, -1 for none.  Calls `release` once the last
 // column has left the TMEM.

@@ -1,11 +1,11 @@
 // The cross entropy's two products that read the head matrix, for few tokens:
 //   logits   Z^T  = W X^T       (vocabulary x tokens, K = width)
 //   dX       dX^T = W^T dZ^T    (width x tokens,      K = vocabulary)
-// With up to 128 token rows the time is W's way through memory, so W is the
-// MMA's 128-row operand and the tokens are its short N side (16 to 128): the
-// ring holds almost nothing but W, 8 to 11 stages of it in flight per SM,
-// where the 256 x 256 tiles of k_vocab_gemm.cu would fill half of it with
-// rows past the last token.  One CTA per tile (tcgen05, cta_group::1),
+// With few token rows the time is W's way through memory, so W is the MMA's
+// 128-row operand and the tokens are its short N side (16 to 256): the ring's 200 KB
+// are 11 stages of W in flight per SM with 16 rows, 6 with 128 and 4 with 256, where
+// the 256 x 256 tiles of k_vocab_gemm.cu would fill half of theirs with rows past
+// the last token.  vocab.cu has the rules of size.  One CTA per tile (tcgen05, cta_group::1),
 // persistent; warp 0 loads, warp 1 issues the MMAs, warps 2 to 5 drain, warp 6
 // sums the gradients' common factor on the side.
 // Memory sets the pace, not the SMs' shares: cutting the last round of tiles

@@ -593,7 +593,6 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       // The last pass may be shorter: every part needs a k-block of its own,
       // and the parts it leaves out hold the earlier passes' sums.
       const int splits = static_cast<int>(std::min<int64_t>(dw.splits, (k_rows + 63) / 64));
-      // Short main loops are bound by the stores: whole rows of tiles then go out together.
       DM_TRY(encode_product(enc, &G.p[1], v, d, k_rows, true, block, ld_block, masked_first ? x + r0 * ld_x : masked, ld8, dw, splits, kDwGroup, first));
       G.n_units[1] = G.p[1].grid.count();
     }

@@ -95,8 +95,9 @@ static_assert(kCeBlock == 1 << kCeShift && kCeThinBlock == 1 << kCeThinShift, "b
 // maximum in units of 2^-10 octaves, cut off at 64 octaves.
 constexpr float kCeLogUnits = 1024.f;
 
-// Division by a constant of the launch: n / d for 0 <= n < 2^31 (multiply by the
-// rounded-up reciprocal of 2^32 + mul, shifted).
+// Division by a constant of the launch: n / d for 0 <= n < 2^31, by the rounded-up
+// reciprocal 2^32 + mul and a shift (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
 struct FastDiv {
   uint32_t mul, shift, d;
   __host__ void set(int32_t divisor) {

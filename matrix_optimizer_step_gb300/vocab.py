@@ -36,7 +36,13 @@ class VocabOps:
     Matrices are (rows, width) tensors with contiguous rows (any row pitch);
     lists are contiguous.  Work is enqueued on ``stream`` (a torch stream or
     handle; None: the current one) and returns without waiting; ``sync``
-    reports device-side errors, an id past the vocabulary among them."""
+    reports device-side errors, an id past the vocabulary among them.
+
+    No autograd graph is recorded, whether tensors require gradients or not: a
+    result is plain data, and gradients are the outputs asked for (``dx`` goes on
+    as ``x.backward(dx)``).  The handle's scratch comes from CUDA, not from
+    torch's allocator, and is kept until ``close``; ``cross_entropy`` says how
+    much it takes."""
 
     def __init__(self, device=0):
         self.device = int(device)
@@ -125,7 +131,11 @@ class VocabOps:
                       loss=None, lse=None, total=None, dx=None, dw=None, accumulate_dw=False, stream=None,
                       fine_grads=False):
         """Softmax cross entropy of logits ``logit_scale * x @ w.T`` against
-        ``targets`` (below zero: not counted), without storing the logits.
+        ``targets`` (below zero: not counted).
+
+        The logits are not stored; with gradients the scratch holds 16 bits of
+        each (32 with two halves, below) between the products, for as many tokens
+        at a time as fit in 2 GiB (tuning key 14, in MiB).
 
         Writes whichever outputs are given: ``loss`` and ``lse`` (fp32 per
         token), ``total`` (one fp32: the weighted sum of losses, over the sum
