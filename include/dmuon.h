@@ -452,6 +452,69 @@ typedef struct dmuon_ce {
 DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream);
 
 /*
+ * dmuon_token_logprobs -- log probabilities of given tokens under a head, the
+ * entropy of each distribution, its most likely entries, and the gradients.
+ *
+ *   z_iv      = logit_scale * (x_i . w_v)       (logit_scale = 1 / temperature)
+ *   lse_i     = log sum_v exp(z_iv),  ln p_iv = z_iv - lse_i
+ *   logprob_i = ln p_{i, t_i};   entropy_i = - sum_v p_iv ln p_iv
+ *   top       = the n_top largest z_iv of a row and their ln p, falling; equal
+ *               ones by ascending id
+ *   L         = sum_i (dlogprobs_i logprob_i + dentropy_i entropy_i)
+ *   dx_i      = grad_scale * dL/dx_i,   dw_v = grad_scale * dL/dw_v
+ *
+ * The products, their rounding, their passes (tuning key 14) and their scratch
+ * are dmuon_cross_entropy's: a policy gradient's loss gives dlogprobs and
+ * dentropy from a first call's outputs, and a second call turns them into
+ * gradients (its logits are multiplied out again).  Both may be one call where
+ * the coefficients are known before.  The alternatives are found among the
+ * entries that the matrix instruction's sums put within 2^-8 octaves and 2^-13
+ * of the row's maximum of the last place, and their order is that of logits
+ * summed to 48 bits or more.
+ *
+ *   x, w        as in dmuon_cross_entropy
+ *   tokens      n_tokens ids of token_dtype; below zero: the row is not scored (its
+ *               outputs 0, its alternatives -1, no gradient, whatever x holds there);
+ *               at or above vocab: likewise, and dmuon_sync reports
+ *               DMUON_ERR_INVALID_ARG.  NULL: every row is scored, with no token given
+ *               (logprobs and dlogprobs must then be NULL)
+ *   logprobs, lse, entropy   fp32 per token (written), each may be NULL
+ *   top_ids, top_logprobs    n_tokens x n_top, ids of top_dtype and fp32 (written);
+ *               both NULL and n_top 0, or n_top in [1, min(32, vocab)];
+ *               top_logprobs may be NULL.  A row with a NaN or infinite
+ *               log-sum has ids -1 and NaN
+ *   dlogprobs, dentropy      fp32 per token (read), NULL: zeros; with dx or dw at
+ *               least one of them, without neither.  A row whose two are 0 has d logits of 0
+ *   dx, dw, flags            as in dmuon_cross_entropy (DMUON_CE_ADD_DW, DMUON_CE_FINE_GRADS)
+ * Errors and n_tokens = 0 as dmuon_cross_entropy.
+ */
+typedef struct dmuon_logprobs {
+  int64_t n_tokens, vocab, dim;
+  const uint16_t* x;
+  const uint16_t* w;
+  int64_t ld_x, ld_w;
+  const void* tokens;
+  float* logprobs;
+  float* lse;
+  float* entropy;
+  void* top_ids;
+  float* top_logprobs;
+  const float* dlogprobs;
+  const float* dentropy;
+  void* dx;
+  void* dw;
+  int64_t ld_dx, ld_dw;
+  int32_t x_dtype, w_dtype;        /* DMUON_DTYPE_BF16 */
+  int32_t token_dtype, top_dtype;  /* DMUON_INDEX_*    */
+  int32_t dx_dtype, dw_dtype;      /* DMUON_DTYPE_*    */
+  int32_t n_top;
+  float logit_scale, grad_scale;
+  uint32_t flags;
+} dmuon_logprobs;
+
+DMUON_API int dmuon_token_logprobs(dmuon_context* ctx, const dmuon_logprobs* args, void* stream);
+
+/*
  * dmuon_embed_forward  -- rows[i] = scale * table[ids[i]]
  * dmuon_embed_backward -- table[v] = scale * sum of rows[i] over ids[i] = v,
  *                         for every v of the vocabulary (rows that no id names

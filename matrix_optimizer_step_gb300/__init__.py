@@ -5,8 +5,9 @@ of ``include/dmuon.h``); this package is its thin Python binding:
 
 * ``capi``       ctypes wrappers named after the C entry points;
 * ``optim``      ``OwnerStep``, a context plus cached descriptor arrays;
-* ``vocab``      ``VocabOps``: embedding lookup and cross entropy over the
-  output head, each with its gradient (the tensors of the AdamW routes);
+* ``vocab``      ``VocabOps``: embedding lookup, cross entropy and log
+  probabilities over the output head, each with its gradient (the tensors of
+  the AdamW routes);
 * ``workloads``  seeded synthetic inputs and work accounting;
 * ``build``      the nvcc build of the library.
 
@@ -44,6 +45,7 @@ from .capi import (  # noqa: F401
     dmuon_status_string,
     dmuon_step_host,
     dmuon_sync,
+    dmuon_token_logprobs,
     load_library,
 )
 from .optim import OwnerStep, adamw_shard_ranges, adamw_shard_views, owner_partition  # noqa: F401

@@ -47,7 +47,7 @@ EXPORTED = (
     "dmuon_selftest_wait_timeout", "dmuon_set_tuning", "dmuon_kernel_launches", "dmuon_profile",
     "dmuon_profile_read", "dmuon_muon_step_noalloc", "dmuon_lpt_assign_layered", "dmuon_step_host",
     "dmuon_muon_step_noalloc_sync", "dmuon_profile_host_timeline", "dmuon_context_set_tuning",
-    "dmuon_cross_entropy", "dmuon_embed_forward", "dmuon_embed_backward",
+    "dmuon_cross_entropy", "dmuon_embed_forward", "dmuon_embed_backward", "dmuon_token_logprobs",
 )
 
 KERNEL_KINDS = ("momentum", "norm", "ns_gram", "ns_poly", "ns_combine", "update", "adamw")
@@ -119,6 +119,23 @@ class DmuonCe(ctypes.Structure):
     ]
 
 
+class DmuonLogprobs(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("w", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p), ("logprobs", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_logprobs", ctypes.c_void_p),
+        ("dlogprobs", ctypes.c_void_p), ("dentropy", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("ld_dw", ctypes.c_int64),
+        ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("token_dtype", ctypes.c_int32),
+        ("top_dtype", ctypes.c_int32), ("dx_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+        ("n_top", ctypes.c_int32), ("logit_scale", ctypes.c_float), ("grad_scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
 class DmuonEmbed(ctypes.Structure):
     _fields_ = [
         ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
@@ -170,6 +187,7 @@ def load_library(path=LIB_PATH):
         "dmuon_cross_entropy": (ctypes.c_int, [vp, ctypes.POINTER(DmuonCe), vp]),
         "dmuon_embed_forward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
         "dmuon_embed_backward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
+        "dmuon_token_logprobs": (ctypes.c_int, [vp, ctypes.POINTER(DmuonLogprobs), vp]),
         "dmuon_step_host": (ctypes.c_int, [vp, ctypes.POINTER(DmuonMatrix), ctypes.POINTER(DmuonHostIO), i32,
                                            ctypes.POINTER(DmuonMuonHparams), ctypes.POINTER(DmuonVector),
                                            ctypes.POINTER(DmuonHostIO), i32, ctypes.POINTER(DmuonAdamwHparams),
@@ -421,3 +439,8 @@ def dmuon_embed_forward(ctx, args, stream=None):
 def dmuon_embed_backward(ctx, args, stream=None):
     """``args``: one DmuonEmbed (``table``: the gradient, ``rows``: the lookup output's)."""
     _check(load_library().dmuon_embed_backward(ctx, ctypes.byref(args), _stream_handle(stream)))
+
+
+def dmuon_token_logprobs(ctx, args, stream=None):
+    """``args``: one DmuonLogprobs."""
+    _check(load_library().dmuon_token_logprobs(ctx, ctypes.byref(args), _stream_handle(stream)))

@@ -9,11 +9,10 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "vocab.h"
+#include "vocab_rows.cuh"
 
 namespace dmuon {
 namespace {
-
-constexpr float kLn2 = 0.69314718055994531f;
 
 // Sum over the block's threads in a fixed order; the result is in thread 0.
 __device__ __forceinline__ double block_sum(double v, double* smem) {
@@ -36,31 +35,6 @@ __global__ void __launch_bounds__(1024) ce_norm_kernel(const CeNorm N) {
 }
 
 // --------------------------------------------------------------- operand copy
-// One warp per row; VEC: source rows start on 16 bytes and cols % 8 == 0.
-template <bool VEC>
-__device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int cols, int ld_dst, bool keep, int lane) {
-  if (VEC) {
-    for (int c0 = lane * 8; c0 < cols; c0 += 1024) {
-      uint4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        v[k] = keep && c0 + 256 * k < cols ? *reinterpret_cast<const uint4*>(s + c0 + 256 * k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c0 + 256 * k < cols) *reinterpret_cast<uint4*>(d + c0 + 256 * k) = v[k];
-    }
-  } else {
-    for (int c0 = lane; c0 < ld_dst; c0 += 256) {
-      uint16_t v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = keep && c0 + 32 * k < cols ? s[c0 + 32 * k] : uint16_t(0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + 32 * k < ld_dst) d[c0 + 32 * k] = v[k];
-    }
-  }
-}
-
 template <bool VEC>
 __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
                                                       int64_t rows, int cols, IdList targets) {
@@ -81,36 +55,8 @@ __global__ void __launch_bounds__(256) ce_copy_kernel(const uint16_t* src, int64
 // 1 / (number of tokens).  Eight entries (16 bytes) a thread, four at a time:
 // 7.0 TB/s read and written at 4096 x 50257.
 // LO: also the rest of the rounding, for the rows below.
-constexpr int kDlThreads = 256;
-constexpr int kDlCols = kDlThreads * 8 * 4;
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// A thread's part of the entries [chunk * kDlCols, + kDlCols) of one row: the
-// logs (from p) and their blocks' maxima (from the row's pairs) ...
-struct Logs {
-  uint4 q[4];
-  float m[4];
-};
-__device__ __forceinline__ Logs load_logs(const uint16_t* p, int vocab, int stats_shift, const float2* stats, int64_t stats_ld,
-                                          int chunk) {
-  Logs L;
-  const int c0 = chunk * kDlCols + threadIdx.x * 8;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + k * kDlThreads * 8;
-    if (c < vocab) {
-      L.q[k] = *reinterpret_cast<const uint4*>(p + c);
-      L.m[k] = stats[static_cast<int64_t>(c >> stats_shift) * stats_ld].x;
-    }
-  }
-  return L;
-}
-// ... and their d logits, in place.
+//
+// A thread's entries (load_logs) to d logits, in place.
 template <bool LO>
 __device__ __forceinline__ void put_dlogits(const Logs& L, uint16_t* p, int64_t lo_offset, int vocab, const CeRow& R, int chunk) {
   const int c0 = chunk * kDlCols + threadIdx.x * 8;
@@ -179,7 +125,6 @@ __global__ void __launch_bounds__(kDlThreads) ce_dlogits_kernel(uint16_t* block,
 // DL, for few rows: `chunks` blocks take a row each, all of them find its sum
 // (a few KB from L2 again) and turn their part of its logs into d logits; the
 // first also does the rest.  That saves a launch and its latency.
-constexpr int kRowWarps = 8;
 
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
@@ -197,29 +142,6 @@ __device__ __forceinline__ void join_lanes(float& m, float& s, int step) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     join(m, s, m2, s2);
   }
-}
-
-// This warp's share (of `shares`) of the dot product of two bf16 rows: a lane's
-// part in fp32, their sum in 64 bits, the same in every lane.
-__device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane) {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const int start = share * 32 + lane, step = shares * 32;
-  int done = 0;
-  if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
-    done = n & ~7;
-#pragma unroll 4
-    for (int c = start; c < n >> 3; c += step) {
-      const uint4 p = reinterpret_cast<const uint4*>(a)[c], q = reinterpret_cast<const uint4*>(b)[c];
-      const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), acc[i]);
-        acc[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc[i]);
-      }
-    }
-  }
-  for (int c = done + start; c < n; c += step) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
-  return warp_sum(static_cast<double>((acc[0] + acc[1]) + (acc[2] + acc[3])));
 }
 
 template <bool VEC, bool DL>

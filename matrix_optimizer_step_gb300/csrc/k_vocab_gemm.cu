@@ -38,6 +38,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "vocab.h"
@@ -214,8 +216,9 @@ __device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
 // time of the whole product at 4096 x 50257 x 768.
 // `target`: of this thread's row, -1 for none.  Calls `release` once the last
 // column has left the TMEM.
-template <class Release>
-__device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t_lane, int row, int target, int col0,
+// ENT: also the sum of 2^(z - m) (z - m), of which the entropy is made; a z of -inf has no part in it.
+template <bool ENT, class Args, class Release>
+__device__ __forceinline__ void logits_epilogue(const Args& G, uint32_t t_lane, int row, int target, int col0,
                                                 Release release) {
   const float c = G.logit_scale_log2;
   const float minus_inf = __int_as_float(0xff800000);
@@ -245,7 +248,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   // A distance is rounded to the nearest unit by adding 2^23, whose low
   // mantissa bits then are the integer; past 64 octaves it stays at the largest.
   const float magic = 8388608.f, most = magic + 65535.f;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
   auto chunk = [&](uint32_t (&q)[32], int i) {
     // The target's share of the sum is added by the row pass.
     if (__any_sync(0xffffffffu, (at >> 5) == i)) {
@@ -261,8 +264,13 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
       for (int k = 0; k < 8; ++k) {
         const float lo = fmaf(__uint_as_float(q[16 * p + 2 * k]), c, -ref);
         const float hi = fmaf(__uint_as_float(q[16 * p + 2 * k + 1]), c, -ref);
-        s[k & 3] += ex2(lo);
-        s[k & 3] += ex2(hi);
+        const float e_lo = ex2(lo), e_hi = ex2(hi);
+        s[k & 3] += e_lo;
+        s[k & 3] += e_hi;
+        if constexpr (ENT) {
+          t[k & 3] = fmaf(e_lo, fmaxf(lo, kNoLogit), t[k & 3]);
+          t[k & 3] = fmaf(e_hi, fmaxf(hi, kNoLogit), t[k & 3]);
+        }
         w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),
                            __float_as_uint(fminf(fmaf(hi, -kCeLogUnits, magic), most)), 0x5410);
       }
@@ -285,6 +293,9 @@ __device__ __forceinline__ void logits_epilogue(const VocabLogits& G, uint32_t t
   chunk(rb, 3);
   if (row_ok)
     G.stats[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+  if constexpr (ENT) {
+    if (row_ok) G.weighted[static_cast<int64_t>(col0 / kCeBlock) * G.stats_ld + row] = (t[0] + t[1]) + (t[2] + t[3]);
+  }
 }
 
 __device__ __forceinline__ void bf16_epilogue(const VgProduct& P, uint32_t (&r)[4][32], float alpha, int col0,
@@ -453,8 +464,8 @@ __device__ __forceinline__ const CUtensorMap* operand_map(const VocabGrad& G, in
 __device__ __forceinline__ bool a_is_mn(const VocabLogits&, int) { return false; }
 __device__ __forceinline__ bool a_is_mn(const VocabGrad& G, int p) { return G.p[p].a_mn != 0; }
 
-// Args: VocabLogits (B is vocabulary x width, K-contiguous) or VocabGrad (B is
-// N-contiguous).
+// Args: VocabLogits or VocabLogProbs (B is vocabulary x width, K-contiguous), or
+// VocabGrad (B is N-contiguous).
 template <class Args, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Args G) {
@@ -642,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         rows = G.M;
         cols = G.N;
         bool bad = false;
-        if (warp_row0 + lane < rows) target = load_id(G.targets, warp_row0 + lane, &bad);
+        if (G.targets.p && warp_row0 + lane < rows) target = load_id(G.targets, warp_row0 + lane, &bad);
       } else {
         rows = G.p[T.product].M;
         cols = G.p[T.product].N;
@@ -669,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         continue;
       }
       if constexpr (LOGITS) {
-        logits_epilogue(G, t_lane, warp_row0 + lane, target, col0, release);
+        logits_epilogue<std::is_same<Args, VocabLogProbs>::value>(G, t_lane, warp_row0 + lane, target, col0, release);
       } else {
         const VgProduct& P = G.p[T.product];
         uint32_t r[4][32];
@@ -743,6 +754,10 @@ cudaError_t launch(const Args& G, int64_t tiles, int n_pairs, cudaStream_t st) {
 
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st) {
   return launch<VocabLogits, false>(G, G.grid.count(), n_pairs, st);
+}
+
+cudaError_t launch_vocab_logits(const VocabLogProbs& G, int n_pairs, cudaStream_t st) {
+  return launch<VocabLogProbs, false>(G, G.grid.count(), n_pairs, st);
 }
 
 cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st) {

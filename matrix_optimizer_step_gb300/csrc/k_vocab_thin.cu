@@ -90,11 +90,12 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
 }
 
 // One warp's 32 vocabulary rows (v0 + lane) of 16 tokens from `token0` on.
+template <bool ENT>
 __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16], int v0, int token0, int lane) {
   const float c = G.logit_scale_log2;
   const float minus_inf = __int_as_float(0xff800000);
   const int v = v0 + lane;
-  float t[16];
+  float t[16], wt[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) t[j] = v < G.M ? __uint_as_float(r[j]) : minus_inf;
   const float top = reduce16(t, lane, [](float a, float b) { return fmaxf(a, b); });
@@ -104,7 +105,7 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
   const float ref = m == minus_inf ? 0.f : m;  // only -inf and NaN: as in k_vocab_gemm.cu
   const int token = token0 + (lane & 15);
   int target = -1;
-  if (token < G.tokens) {
+  if (token < G.tokens && G.targets.p) {
     bool bad = false;
     target = load_id(G.targets, token, &bad);
   }
@@ -117,15 +118,21 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
     // The target's share of the sum is added by the row pass.
     const float d = v < G.M && v != tj ? fmaf(z, c, -mj) : minus_inf;
     t[j] = ex2(d);
+    if (ENT) wt[j] = t[j] * fmaxf(d, kNoLogit);
     if (G.logs && token0 + j < G.tokens && v < G.M)
       G.logs[static_cast<int64_t>(token0 + j) * G.ld_logs + v] =
           static_cast<uint16_t>(__float_as_uint(fminf(fmaf(d, -kCeLogUnits, magic), most)));
   }
   const float s = reduce16(t, lane, [](float a, float b) { return a + b; });
   if (lane < 16 && token < G.tokens) G.stats[static_cast<int64_t>(v0 / kCeThinBlock) * G.stats_ld + token] = make_float2(m, s);
+  if (ENT) {
+    const float w = reduce16(wt, lane, [](float a, float b) { return a + b; });
+    if (lane < 16 && token < G.tokens) G.weighted[static_cast<int64_t>(v0 / kCeThinBlock) * G.stats_ld + token] = w;
+  }
 }
 
-template <bool LOGITS>
+// ENT: with what the entropy takes (VocabLogProbs).
+template <bool LOGITS, bool ENT>
 __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_constant__ VocabThin G) {
   constexpr bool A_MN = !LOGITS;
   extern __shared__ uint8_t smem_raw[];
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
             for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
           }
           if (LOGITS) {
-            thin_logits(G, r, row0, c0, lane);
+            thin_logits<ENT>(G, r, row0, c0, lane);
           } else if (row0 + lane < G.M) {
             float* p = G.part + (static_cast<int64_t>(split) * G.tokens + c0) * G.ld_part + row0 + lane;
 #pragma unroll
@@ -320,17 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   if (warp == 1) tmem_dealloc(tmem_base, tmem_cols);
 }
 
-template <bool LOGITS>
+template <bool LOGITS, bool ENT>
 cudaError_t launch_variant(const VocabThin& G, int n_ctas, cudaStream_t st) {
   static unsigned long long attr_mask = 0;
   if (attr_needed_on_current_device(&attr_mask)) {
-    cudaError_t e = cudaFuncSetAttribute(vocab_thin_kernel<LOGITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(vocab_thin_kernel<LOGITS, ENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
     attr_note_current_device(&attr_mask);
   }
   const int64_t tiles = static_cast<int64_t>(G.tiles_m) * G.splits;
-  return launch_after(vocab_thin_kernel<LOGITS>, dim3(static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas)), dim3(kThreads),
+  return launch_after(vocab_thin_kernel<LOGITS, ENT>, dim3(static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas)), dim3(kThreads),
                       kSmem, st, G);
 }
 
@@ -340,7 +347,8 @@ cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaS
   if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > kThinRows || G.np % 16 != 0 || G.groups < 1 ||
       2 * G.np * G.groups > 512 || n_ctas <= 0)
     return cudaErrorInvalidValue;
-  return logits ? launch_variant<true>(G, n_ctas, st) : launch_variant<false>(G, n_ctas, st);
+  if (!logits) return launch_variant<false, false>(G, n_ctas, st);
+  return G.weighted ? launch_variant<true, true>(G, n_ctas, st) : launch_variant<true, false>(G, n_ctas, st);
 }
 
 }  // namespace dmuon

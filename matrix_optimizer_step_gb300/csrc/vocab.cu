@@ -1,6 +1,6 @@
 // Entry points of the vocabulary operators: argument checks, workspace layout
-// and launch order of the cross entropy and of the embedding lookup (kernels:
-// k_vocab_gemm.cu, k_vocab_ce.cu, k_embed.cu).
+// and launch order of the cross entropy, the log probabilities and the embedding
+// lookup (kernels: k_vocab_gemm.cu, k_vocab_thin.cu, k_vocab_ce.cu, k_logprobs.cu, k_embed.cu).
 #include "vocab.h"
 
 #include "runtime.h"
@@ -327,9 +327,13 @@ int encode_product(EncodeTiledFn enc, VgProduct* P, int64_t m, int64_t n, int64_
   return make_map_typed(enc, &P->map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T.out, n, m, 1, T.ld, m * T.ld, 32, 32);
 }
 
-int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
+// Cross entropy, or with P the log probabilities of the given tokens (C holds the
+// arguments that both have).
+int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cudaStream_t s) {
   const int64_t n = C.n_tokens, v = C.vocab, d = C.dim;
   const bool grads = C.dx || C.dw;
+  const int n_top = P && P->top_ids ? P->n_top : 0;
+  const bool keep_logs = grads || n_top > 0;
   const bool mean = (C.flags & DMUON_CE_MEAN) != 0, add_dw = (C.flags & DMUON_CE_ADD_DW) != 0;
   const bool dx_bf16 = C.dx_dtype == DMUON_DTYPE_BF16, dw_bf16 = C.dw_dtype == DMUON_DTYPE_BF16;
   if (n == 0) {
@@ -352,10 +356,10 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   // long, and what is left of a d logit's error is that of its 16-bit log.
   const bool halves = grads && (n <= kHalvesTokens || (C.flags & DMUON_CE_FINE_GRADS) != 0);
 
-  // Rows of one pass: what is held for each (its logs, or without gradients its
+  // Rows of one pass: what is held for each (its logs, or without gradients and alternatives its
   // statistics) stays within the limit, and tiles are numbered in 32 bits.
   const int64_t ld_block = round_up(v, 64);
-  const int64_t row_bytes = grads ? (halves ? 4 : 2) * ld_block : 8 * ((v + kCeBlock - 1) / kCeBlock);
+  const int64_t row_bytes = keep_logs ? (halves ? 4 : 2) * ld_block : (P ? 12 : 8) * ((v + kCeBlock - 1) / kCeBlock);
   const int64_t most = std::max<int64_t>(kVgTile, std::min(ctx->tune.ce_block_bytes / row_bytes,
                                                            (int64_t(1) << 30) / tiles_of(v) * kVgTile) / kVgTile * kVgTile);
   int64_t rows = n;
@@ -365,9 +369,9 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   }
   const bool one_pass = rows >= n;
   const int64_t token_rows = halves ? 2 * rows : rows;
-  const bool thin_logits = thin_logits_pay(n, v, d, grads), thin_x = C.dx && thin_dx(token_rows, v, d);
+  const bool thin_logits = thin_logits_pay(n, v, d, keep_logs), thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
-  const bool rows_make_dlogits = halves && ce_rows_make_dlogits(n);
+  const bool rows_make_dlogits = !P && halves && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
   const int64_t stats_ld = rows >= 4 ? round_up(rows, 4) : rows;
 
@@ -386,13 +390,14 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   const size_t off_x = copy_x ? L.take(static_cast<size_t>(n * ld8) * 2) : 0;
   const size_t off_w = copy_w ? L.take(static_cast<size_t>(v * ld8) * 2) : 0;
   const size_t off_stats = L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float2));
+  const size_t off_weighted = P ? L.take(static_cast<size_t>(n_blocks * stats_ld) * sizeof(float)) : 0;
   const int width = ce_rows_width(n);
   const size_t off_partial = C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
   size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
   Target dx, dw;
+  if (keep_logs) off_block = L.take(static_cast<size_t>(token_rows * ld_block) * 2);
+  if (grads || P) off_rows = L.take(static_cast<size_t>(rows) * (P ? sizeof(LpRow) : sizeof(CeRow)));
   if (grads) {
-    off_block = L.take(static_cast<size_t>(token_rows * ld_block) * 2);
-    off_rows = L.take(static_cast<size_t>(rows) * sizeof(CeRow));
     off_alpha = L.take(4);
     bool dx_part = false, dw_part = false;
     if (C.dw) {
@@ -455,7 +460,9 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
   }
   float2* stats = reinterpret_cast<float2*>(ws + off_stats);
   uint16_t* block = reinterpret_cast<uint16_t*>(ws + off_block);
+  float* weighted = reinterpret_cast<float*>(ws + off_weighted);
   CeRow* row_info = reinterpret_cast<CeRow*>(ws + off_rows);
+  LpRow* lp_info = reinterpret_cast<LpRow*>(ws + off_rows);
   float* alpha = reinterpret_cast<float*>(ws + off_alpha);
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
   uint32_t* counters = static_cast<uint32_t*>(ctx->vocab_ticket.p);  // two tile counters, one ticket
@@ -481,7 +488,7 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
     const bool first = r0 == 0, last = r0 + rows >= n;
     const int64_t k_rows = halves ? 2 * nr : nr;  // rows of d logits
     IdList here = ids;
-    here.p = static_cast<const char*>(ids.p) + r0 * (ids.is64 ? 8 : 4);
+    if (ids.p) here.p = static_cast<const char*>(ids.p) + r0 * (ids.is64 ? 8 : 4);
     if (thin_logits) {
       VocabThin G = {};
       G.M = static_cast<int32_t>(v);
@@ -495,15 +502,16 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
       G.logit_scale_log2 = static_cast<float>(scale_log2);
-      G.logs = grads ? block : nullptr;
+      G.logs = keep_logs ? block : nullptr;
       G.ld_logs = ld_block;
       G.stats = stats;
       G.stats_ld = stats_ld;
       G.targets = here;
+      if (P) G.weighted = weighted;
       if (first) G.norm = norm;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
     } else {
-      VocabLogits G = {};
+      VocabLogProbs G = {};
       G.M = static_cast<int32_t>(nr);
       G.N = static_cast<int32_t>(v);
       G.grid.set(nr, v, d, 1, kLogitsGroup);
@@ -511,58 +519,119 @@ int cross_entropy_impl(dmuon_context* ctx, const dmuon_ce& C, cudaStream_t s) {
       DM_TRY(encode_2d(enc, &G.map_a, x + r0 * ld_x, d, nr, ld_x, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, w, d, v, ld_w, 64, 128));
       G.logit_scale_log2 = static_cast<float>(scale_log2);
-      G.logs = grads ? block : nullptr;
+      G.logs = keep_logs ? block : nullptr;
       G.ld_logs = ld_block;
       G.stats = stats;
       G.stats_ld = stats_ld;
       G.targets = here;
       G.counter = counters;
       if (first) G.norm = norm;
+      G.weighted = weighted;
       G.drawn = G.grid.kb_total >= kDrawnBlocks;
-      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_logits(G, pairs, s); }));
-    }
-
-    CeRows R = {};
-    R.stats = stats;
-    R.stats_ld = stats_ld;
-    R.n_blocks = n_blocks;
-    R.row0 = r0;
-    R.rows = nr;
-    R.targets = ids;
-    R.weights = C.weights;
-    R.x = x + r0 * ld_x;
-    R.w = w;
-    R.ld_x = ld_x;
-    R.ld_w = ld_w;
-    R.dim = static_cast<int32_t>(d);
-    R.logit_scale_log2 = scale_log2;
-    R.out = grads ? row_info : nullptr;
-    if (rows_make_dlogits) {
-      R.block = block;
-      R.ld_block = ld_block;
-      R.lo_rows = nr;
-      R.vocab = static_cast<int32_t>(v);
-      R.stats_shift = stats_shift;
-    }
-    R.loss = C.loss;
-    R.lse = C.lse;
-    R.x_copy = C.dw && !masked_first ? masked : nullptr;
-    R.ld_copy = ld8;
-    R.copies = halves ? 2 : 1;
-    R.width = width;
-    R.partial = partial;
-    if (last && !total_later) R.total = total;
-    R.ticket = counters + 2;
-    R.counters = counters;
-    R.err = err;
-    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_rows(R, s); }));
-    if (!grads) continue;
-
-    if (!rows_make_dlogits)
       DM_TRY(timed_launch(ctx, -1, s, [&] {
-        return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_shift, stats, stats_ld, row_info,
+        return P ? launch_vocab_logits(G, pairs, s) : launch_vocab_logits(static_cast<const VocabLogits&>(G), pairs, s);
+      }));
+    }
+
+    if (P) {
+      LpRows R = {};
+      R.stats = stats;
+      R.weighted = weighted;
+      R.stats_ld = stats_ld;
+      R.n_blocks = n_blocks;
+      R.row0 = r0;
+      R.rows = nr;
+      R.tokens = ids;
+      R.dlogprobs = grads ? P->dlogprobs : nullptr;
+      R.dentropy = grads ? P->dentropy : nullptr;
+      R.x = x + r0 * ld_x;
+      R.w = w;
+      R.ld_x = ld_x;
+      R.ld_w = ld_w;
+      R.dim = static_cast<int32_t>(d);
+      R.logit_scale_log2 = scale_log2;
+      R.logprobs = P->logprobs;
+      R.lse = P->lse;
+      R.entropy = P->entropy;
+      R.out = lp_info;
+      R.x_copy = C.dw && !masked_first ? masked : nullptr;
+      R.ld_copy = ld8;
+      R.copies = halves ? 2 : 1;
+      R.width = width;
+      R.counters = counters;
+      R.err = err;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_rows(R, s); }));
+      if (n_top > 0) {
+        LpTop T = {};
+        T.block = block;
+        T.ld_block = ld_block;
+        T.stats = stats;
+        T.stats_ld = stats_ld;
+        T.n_blocks = n_blocks;
+        T.stats_shift = stats_shift;
+        T.vocab = static_cast<int32_t>(v);
+        T.rows_in = lp_info;
+        T.rows = nr;
+        T.x = R.x;
+        T.w = w;
+        T.ld_x = ld_x;
+        T.ld_w = ld_w;
+        T.dim = R.dim;
+        T.logit_scale_log2 = scale_log2;
+        T.k = n_top;
+        T.ids64 = P->top_dtype == DMUON_INDEX_I64;
+        T.ids = static_cast<char*>(P->top_ids) + r0 * n_top * (T.ids64 ? 8 : 4);
+        T.logprobs = P->top_logprobs ? P->top_logprobs + r0 * n_top : nullptr;
+        DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_top(T, s); }));
+      }
+      if (!grads) continue;
+      DM_TRY(timed_launch(ctx, -1, s, [&] {
+        return launch_lp_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_shift, stats, stats_ld, lp_info,
                                  halves ? nr : 0, s);
       }));
+    } else {
+      CeRows R = {};
+      R.stats = stats;
+      R.stats_ld = stats_ld;
+      R.n_blocks = n_blocks;
+      R.row0 = r0;
+      R.rows = nr;
+      R.targets = ids;
+      R.weights = C.weights;
+      R.x = x + r0 * ld_x;
+      R.w = w;
+      R.ld_x = ld_x;
+      R.ld_w = ld_w;
+      R.dim = static_cast<int32_t>(d);
+      R.logit_scale_log2 = scale_log2;
+      R.out = grads ? row_info : nullptr;
+      if (rows_make_dlogits) {
+        R.block = block;
+        R.ld_block = ld_block;
+        R.lo_rows = nr;
+        R.vocab = static_cast<int32_t>(v);
+        R.stats_shift = stats_shift;
+      }
+      R.loss = C.loss;
+      R.lse = C.lse;
+      R.x_copy = C.dw && !masked_first ? masked : nullptr;
+      R.ld_copy = ld8;
+      R.copies = halves ? 2 : 1;
+      R.width = width;
+      R.partial = partial;
+      if (last && !total_later) R.total = total;
+      R.ticket = counters + 2;
+      R.counters = counters;
+      R.err = err;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_ce_rows(R, s); }));
+      if (!grads) continue;
+
+      if (!rows_make_dlogits)
+        DM_TRY(timed_launch(ctx, -1, s, [&] {
+          return launch_ce_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_shift, stats, stats_ld, row_info,
+                                   halves ? nr : 0, s);
+        }));
+    }
     if (C.dx) dx.out = static_cast<char*>(C.dx) + r0 * C.ld_dx * (dx_bf16 ? 2 : 4);
     VocabGrad G = {};
     G.counter = counters + 1;
@@ -675,8 +744,96 @@ int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void* stream) 
   DM_TRY(ensure_device(ctx));
   DM_TRY(check_pointers(ctx, r, nr));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int st = cross_entropy_impl(ctx, C, s);
+  const int st = head_impl(ctx, C, nullptr, s);
   if (C.n_tokens == 0) return st;  // no scratch
+  // A sequence that broke off may have left its counters up.
+  if (st != DMUON_OK && ctx->vocab_ticket.p) cudaMemsetAsync(ctx->vocab_ticket.p, 0, 256, s);
+  return end_use(ctx, s, st);
+}
+
+int dmuon_token_logprobs(dmuon_context* ctx, const dmuon_logprobs* args, void* stream) {
+  clear_error();
+  if (!ctx || !args) return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: null context or arguments");
+  const dmuon_logprobs& P = *args;
+  const char* op = "token_logprobs";
+  DM_TRY(check_sizes(op, P.n_tokens, P.vocab, P.dim));
+  const bool grads = P.dx || P.dw;
+  // An empty list may come without memory.
+  const bool some = P.n_tokens > 0;
+  if (!P.w || (some && !P.x)) return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: null x or w");
+  if (some && !P.logprobs && !P.lse && !P.entropy && !P.top_ids && !grads)
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: no output asked for");
+  if (some && !P.tokens && (P.logprobs || P.dlogprobs))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: log probabilities and their gradients need tokens");
+  if (some && grads && !P.dlogprobs && !P.dentropy)
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: dx and dw need dlogprobs or dentropy");
+  if (some && !grads && (P.dlogprobs || P.dentropy))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: dlogprobs and dentropy without dx or dw");
+  if (some && !P.top_ids && (P.n_top != 0 || P.top_logprobs))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: alternatives asked for without top_ids");
+  if (P.top_ids && (P.n_top < 1 || P.n_top > kTopMost || P.n_top > P.vocab))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: n_top outside [1, min(32, vocab)]");
+  if (!finite(P.logit_scale) || P.logit_scale <= 0.f || !finite(P.grad_scale))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: logit_scale must be positive, grad_scale finite");
+  if (P.flags & ~uint32_t(DMUON_CE_ADD_DW | DMUON_CE_FINE_GRADS))
+    return set_error(DMUON_ERR_INVALID_ARG, "token_logprobs: unknown flag bits");
+  DM_TRY(check_type(op, "x", P.x_dtype, false));
+  DM_TRY(check_type(op, "w", P.w_dtype, false));
+  if (P.tokens) DM_TRY(check_index(op, P.token_dtype));
+  if (P.top_ids) DM_TRY(check_index(op, P.top_dtype));
+  DM_TRY(check_ld(op, "x", P.ld_x, P.dim));
+  DM_TRY(check_ld(op, "w", P.ld_w, P.dim));
+  if (P.dx) {
+    DM_TRY(check_type(op, "dx", P.dx_dtype, true));
+    DM_TRY(check_ld(op, "dx", P.ld_dx, P.dim));
+  }
+  if (P.dw) {
+    DM_TRY(check_type(op, "dw", P.dw_dtype, true));
+    DM_TRY(check_ld(op, "dw", P.ld_dw, P.dim));
+  }
+  const int64_t n = P.n_tokens, n_top = P.top_ids ? P.n_top : 0;
+  const int dx_size = P.dx_dtype == DMUON_DTYPE_BF16 ? 2 : 4, dw_size = P.dw_dtype == DMUON_DTYPE_BF16 ? 2 : 4;
+  const Range r[] = {
+      matrix(P.x, n, P.dim, P.ld_x, 2, false, "x"),
+      matrix(P.w, P.vocab, P.dim, P.ld_w, 2, false, "w"),
+      list(P.tokens, n, P.token_dtype == DMUON_INDEX_I64 ? 8 : 4, false, "tokens"),
+      list(P.dlogprobs, n, 4, false, "dlogprobs"),
+      list(P.dentropy, n, 4, false, "dentropy"),
+      list(P.logprobs, n, 4, true, "logprobs"),
+      list(P.lse, n, 4, true, "lse"),
+      list(P.entropy, n, 4, true, "entropy"),
+      list(P.top_ids, n * n_top, P.top_dtype == DMUON_INDEX_I64 ? 8 : 4, true, "top_ids"),
+      list(P.top_logprobs, n * n_top, 4, true, "top_logprobs"),
+      matrix(P.dx, n, P.dim, P.ld_dx, dx_size, true, "dx"),
+      matrix(P.dw, P.vocab, P.dim, P.ld_dw, dw_size, true, "dw"),
+  };
+  const int nr = static_cast<int>(sizeof r / sizeof r[0]);
+  DM_TRY(check_ranges(op, r, nr));
+  dmuon_ce C = {};
+  C.n_tokens = n;
+  C.vocab = P.vocab;
+  C.dim = P.dim;
+  C.x = P.x;
+  C.w = P.w;
+  C.ld_x = P.ld_x;
+  C.ld_w = P.ld_w;
+  C.targets = P.tokens;
+  C.dx = P.dx;
+  C.dw = P.dw;
+  C.ld_dx = P.ld_dx;
+  C.ld_dw = P.ld_dw;
+  C.target_dtype = P.token_dtype;
+  C.dx_dtype = P.dx_dtype;
+  C.dw_dtype = P.dw_dtype;
+  C.logit_scale = P.logit_scale;
+  C.grad_scale = P.grad_scale;
+  C.flags = P.flags;
+  DeviceGuard guard(ctx->device);
+  DM_TRY(ensure_device(ctx));
+  DM_TRY(check_pointers(ctx, r, nr));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int st = head_impl(ctx, C, &P, s);
+  if (n == 0) return st;  // no scratch
   // A sequence that broke off may have left its counters up.
   if (st != DMUON_OK && ctx->vocab_ticket.p) cudaMemsetAsync(ctx->vocab_ticket.p, 0, 256, s);
   return end_use(ctx, s, st);

@@ -1,6 +1,6 @@
 // Private types of the vocabulary operators (vocab.cu, k_vocab_gemm.cu,
-// k_vocab_ce.cu, k_embed.cu): softmax cross entropy over a head matrix and
-// embedding lookup, each with its gradient.
+// k_vocab_ce.cu, k_logprobs.cu, k_embed.cu): softmax cross entropy and log
+// probabilities over a head matrix and embedding lookup, each with its gradient.
 #pragma once
 
 #include <cuda.h>
@@ -94,6 +94,9 @@ static_assert(kCeBlock == 1 << kCeShift && kCeThinBlock == 1 << kCeThinShift, "b
 // Fixed-point logs: a logit is kept as the 16-bit distance to its block's
 // maximum in units of 2^-10 octaves, cut off at 64 octaves.
 constexpr float kCeLogUnits = 1024.f;
+
+// Stands for a distance of -inf where one is multiplied: 2^it is 0.
+constexpr float kNoLogit = -256.f;
 
 // Division by a constant of the launch: n / d for 0 <= n < 2^31, by the rounded-up
 // reciprocal 2^32 + mul and a shift (Granlund and Montgomery, "Division by invariant
@@ -224,6 +227,13 @@ struct VocabLogits {
 };
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st);
 
+// The same with what the entropy takes: a block's sum of 2^(z - maximum) (z - maximum), again
+// without the target's.  `targets.p` may be null.
+struct VocabLogProbs : VocabLogits {
+  float* weighted;                    // [block][row], as stats
+};
+cudaError_t launch_vocab_logits(const VocabLogProbs& G, int n_pairs, cudaStream_t st);
+
 // One gradient product D (M x N) = alpha A B: B is k x n with contiguous
 // columns, A is m x k, or k x m with a_mn.
 struct VgProduct {
@@ -269,6 +279,7 @@ struct VocabThin {
   float2* stats;
   int64_t stats_ld;
   IdList targets;
+  float* weighted;                    // as in VocabLogProbs, or null: not wanted
   CeNorm norm;
   // dX: fp32 partials [split][token][ld_part]
   float* part;
@@ -340,6 +351,71 @@ cudaError_t launch_ce_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t
 cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_stride, int parts, int64_t fold,
                              void* out, int64_t ld_out, int out_bf16, int accumulate, const float* alpha,
                              int64_t rows, int32_t cols, cudaStream_t st);
+
+// ---- k_logprobs.cu
+constexpr int kTopMost = 32;  // alternatives of a row at most
+
+// A row's distribution, as the passes after the sums read it.  Octaves unless said otherwise.
+struct LpRow {
+  float top, log_sum;  // maximum, and log2 of the sum relative to it
+  float logprob;       // of the given token, natural
+  float a, b;          // d logit of entry v: -p_v (a + b log2 p_v); both 0: none for this row
+  float target_dz;     // and of the given token
+  int32_t target;      // -1: none
+  int32_t scored;
+};
+
+struct LpRows {
+  const float2* stats;
+  const float* weighted;
+  int64_t stats_ld;
+  int32_t n_blocks;
+  int64_t row0, rows;      // rows of this pass
+  IdList tokens;           // of row 0; p null: every row is scored, with no given token
+  const float* dlogprobs;  // of row 0, or null
+  const float* dentropy;
+  const uint16_t* x;       // of row row0
+  const uint16_t* w;
+  int64_t ld_x, ld_w;
+  int32_t dim;
+  double logit_scale_log2;
+  float* logprobs;         // of row 0, or null
+  float* lse;
+  float* entropy;
+  LpRow* out;              // of row row0
+  uint16_t* x_copy;        // as in CeRows
+  int64_t ld_copy;
+  int32_t copies;
+  int32_t width;           // rows of a block: ce_rows_width(n)
+  uint32_t* counters;      // the products' two tile counters, set to zero
+  int* err;
+};
+cudaError_t launch_lp_rows(const LpRows& R, cudaStream_t st);
+
+struct LpTop {
+  const uint16_t* block;   // logs of row row0
+  int64_t ld_block;
+  const float2* stats;
+  int64_t stats_ld;
+  int32_t n_blocks, stats_shift, vocab;
+  const LpRow* rows_in;
+  int64_t rows;
+  const uint16_t* x;       // of row row0
+  const uint16_t* w;
+  int64_t ld_x, ld_w;
+  int32_t dim;
+  double logit_scale_log2;
+  int32_t k;               // at most kTopMost and the vocabulary
+  void* ids;               // of row row0, k a row
+  int32_t ids64;
+  float* logprobs;         // of row row0, k a row, or null
+};
+cudaError_t launch_lp_top(const LpTop& T, cudaStream_t st);
+
+// Fixed-point logs -> bf16 d logits in place, as launch_ce_dlogits.
+cudaError_t launch_lp_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_shift,
+                              const float2* stats, int64_t stats_ld, const LpRow* row_info, int64_t lo_rows,
+                              cudaStream_t st);
 
 // ---- k_embed.cu
 struct EmbedForward {

@@ -1,5 +1,5 @@
-"""User-facing wrapper of the vocabulary operators: embedding lookup and softmax
-cross entropy over the output head, each with its gradient.
+"""User-facing wrapper of the vocabulary operators: embedding lookup, softmax
+cross entropy and log probabilities over the output head, each with its gradient.
 
 ``VocabOps`` keeps a library context; its methods check and marshal torch
 tensors, and everything runs in the CUDA library through the C ABI.  The
@@ -30,8 +30,74 @@ def _current_stream(device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
-class VocabOps:
-    """Embedding and cross entropy on one GPU.
+def empty_on(stream, device, *shape, dtype):
+    """Memory for a result that ``stream`` writes: torch's allocator gives a block out again in the order of the
+    stream it was taken on, so it is taken on that one."""
+    if stream is None:
+        return torch.empty(shape, device=torch.device("cuda", device), dtype=dtype)
+    handle = getattr(stream, "cuda_stream", stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)):
+        return torch.empty(shape, device=torch.device("cuda", device), dtype=dtype)
+
+
+class Ops:
+    """A context on one GPU, and what its operators' handles have in common."""
+
+    def __init__(self, device=0):
+        self.device = int(device)
+        self.ctx = capi.dmuon_context_create(self.device)
+        self._lib = capi.load_library()
+
+    def _list(self, t, name, dtypes, n):
+        if not isinstance(t, _Tensor) or t.get_device() != self.device or t.dtype not in dtypes:
+            self._refuse(t, name, dtypes)
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: expected {n} contiguous elements")
+        return t.data_ptr()
+
+    def _refuse(self, t, name, dtypes):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
+            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+
+    def _empty(self, stream, *shape, dtype):
+        return empty_on(stream, self.device, *shape, dtype=dtype)
+
+    def _stream(self, stream):
+        return _raw_stream(self.device) if stream is None else getattr(stream, "cuda_stream", stream)
+
+    def _call(self, fn, args, stream):
+        status = fn(self.ctx, ctypes.byref(args), self._stream(stream))
+        if status:
+            capi._check(status)
+
+    # ---------------------------------------------------------------- misc
+    def sync(self, stream=None):
+        """Wait for ``stream`` (None: the handle's device's current one) and raise
+        DmuonError for device-side errors."""
+        capi.dmuon_sync(self.ctx, _raw_stream(self.device) if stream is None else stream)
+
+    def set_tuning(self, key, value):
+        """One tuning key of this context (dmuon_context_set_tuning)."""
+        capi.dmuon_context_set_tuning(self.ctx, key, value)
+
+    def kernel_launches(self):
+        return capi.dmuon_kernel_launches(self.ctx)
+
+    def close(self):
+        if self.ctx is not None:
+            capi.dmuon_context_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class VocabOps(Ops):
+    """Embedding, cross entropy and log probabilities on one GPU.
 
     Matrices are (rows, width) tensors with contiguous rows (any row pitch);
     lists are contiguous.  Work is enqueued on ``stream`` (a torch stream or
@@ -43,11 +109,6 @@ class VocabOps:
     as ``x.backward(dx)``).  The handle's scratch comes from CUDA, not from
     torch's allocator, and is kept until ``close``; ``cross_entropy`` says how
     much it takes."""
-
-    def __init__(self, device=0):
-        self.device = int(device)
-        self.ctx = capi.dmuon_context_create(self.device)
-        self._lib = capi.load_library()
 
     # These run on every call: a good tensor takes few attribute reads and no
     # further calls (a small lookup is bound by this code).
@@ -67,36 +128,6 @@ class VocabOps:
         elif pitch < shape[1]:
             raise ValueError(f"{name} has overlapping rows (stride {pitch})")
         return t.data_ptr(), pitch
-
-    def _list(self, t, name, dtypes, n):
-        if not isinstance(t, _Tensor) or t.get_device() != self.device or t.dtype not in dtypes:
-            self._refuse(t, name, dtypes)
-        if t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name}: expected {n} contiguous elements")
-        return t.data_ptr()
-
-    def _refuse(self, t, name, dtypes):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
-            raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-
-    def _empty(self, stream, *shape, dtype):
-        """Memory for a result that ``stream`` writes: torch's allocator gives a block out again in the order of the
-        stream it was taken on, so it is taken on that one."""
-        if stream is None:
-            return torch.empty(shape, device=torch.device("cuda", self.device), dtype=dtype)
-        handle = getattr(stream, "cuda_stream", stream)
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)):
-            return torch.empty(shape, device=torch.device("cuda", self.device), dtype=dtype)
-
-    def _call(self, fn, args, stream):
-        if stream is None:
-            stream = _raw_stream(self.device)
-        else:
-            stream = getattr(stream, "cuda_stream", stream)
-        status = fn(self.ctx, ctypes.byref(args), stream)
-        if status:
-            capi._check(status)
 
     # ----------------------------------------------------------- embedding
     def _embed(self, fn, ids, table, rows, scale, flags, stream):
@@ -178,26 +209,69 @@ class VocabOps:
         self._call(self._lib.dmuon_cross_entropy, a, stream)
         return loss
 
-    # ---------------------------------------------------------------- misc
-    def sync(self, stream=None):
-        """Wait for ``stream`` (None: the handle's device's current one) and raise
-        DmuonError for device-side errors."""
-        capi.dmuon_sync(self.ctx, _raw_stream(self.device) if stream is None else stream)
+    # ---------------------------------------------------- log probabilities
+    def token_logprobs(self, x, w, tokens=None, logit_scale=1.0, logprobs=None, lse=None, entropy=None, top_ids=None,
+                       top_logprobs=None, dlogprobs=None, dentropy=None, grad_scale=1.0, dx=None, dw=None,
+                       accumulate_dw=False, stream=None, fine_grads=False):
+        """Log probabilities of ``tokens`` under the logits ``logit_scale * x @ w.T``
+        (``logit_scale``: one over the temperature), the entropies of the
+        distributions, their most likely entries, and the gradients.
 
-    def set_tuning(self, key, value):
-        """One tuning key of this context (dmuon_context_set_tuning)."""
-        capi.dmuon_context_set_tuning(self.ctx, key, value)
+        Writes whichever outputs are given: ``logprobs``, ``lse`` and
+        ``entropy`` (fp32 per token), ``top_ids`` (int32 or int64, tokens x k,
+        k up to 32) with ``top_logprobs`` (fp32, the same shape), in falling
+        order, equal ones by ascending id.  With none given, ``logprobs`` is
+        allocated, on ``stream``.  Returns ``logprobs``.
 
-    def kernel_launches(self):
-        return capi.dmuon_kernel_launches(self.ctx)
+        ``tokens`` below zero: the row is not scored (outputs 0, alternatives -1,
+        no gradient).  None: every row is scored, with no token given.
 
-    def close(self):
-        if self.ctx is not None:
-            capi.dmuon_context_destroy(self.ctx)
-            self.ctx = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+        With ``dlogprobs`` and ``dentropy`` (fp32 per token, the gradients of a
+        loss with respect to both; either may be None) ``dx`` and ``dw`` are
+        the loss's gradients times ``grad_scale``, as in ``cross_entropy``."""
+        x_p, ld_x = self._matrix(x, "x", _BF16)
+        n, dim = x.shape
+        w_p, ld_w = self._matrix(w, "w", _BF16, cols=dim)
+        vocab = w.shape[0]
+        tokens_p = logprobs_p = lse_p = entropy_p = top_p = top_lp_p = dlogprobs_p = dentropy_p = dx_p = dw_p = None
+        ld_dx = ld_dw = dx_type = dw_type = token_type = top_type = n_top = 0
+        if logprobs is None and lse is None and entropy is None and top_ids is None and dx is None and dw is None:
+            logprobs = self._empty(stream, n, dtype=torch.float32)
+        if tokens is not None:
+            tokens_p = self._list(tokens, "tokens", _INDEX, n)
+            token_type = _INDEX[tokens.dtype]
+        if logprobs is not None:
+            logprobs_p = self._list(logprobs, "logprobs", _F32, n)
+        if lse is not None:
+            lse_p = self._list(lse, "lse", _F32, n)
+        if entropy is not None:
+            entropy_p = self._list(entropy, "entropy", _F32, n)
+        if top_ids is not None:
+            n_top = top_ids.shape[1] if isinstance(top_ids, _Tensor) and top_ids.dim() == 2 else 0
+            top_p = self._list(top_ids, "top_ids", _INDEX, n * n_top)
+            if top_ids.dim() != 2 or top_ids.shape[0] != n:
+                raise ValueError(f"top_ids has shape {tuple(top_ids.shape)}, expected ({n}, *)")
+            top_type = _INDEX[top_ids.dtype]
+        if top_logprobs is not None:
+            if top_ids is None:
+                raise ValueError("top_logprobs without top_ids")
+            top_lp_p = self._list(top_logprobs, "top_logprobs", _F32, n * n_top)
+            if top_logprobs.shape != top_ids.shape:
+                raise ValueError(f"top_logprobs has shape {tuple(top_logprobs.shape)}, expected {tuple(top_ids.shape)}")
+        if dlogprobs is not None:
+            dlogprobs_p = self._list(dlogprobs, "dlogprobs", _F32, n)
+        if dentropy is not None:
+            dentropy_p = self._list(dentropy, "dentropy", _F32, n)
+        if dx is not None:
+            dx_p, ld_dx = self._matrix(dx, "dx", _FLOATS, n, dim)
+            dx_type = _FLOATS[dx.dtype]
+        if dw is not None:
+            dw_p, ld_dw = self._matrix(dw, "dw", _FLOATS, vocab, dim)
+            dw_type = _FLOATS[dw.dtype]
+        a = capi.DmuonLogprobs(n, vocab, dim, x_p, w_p, ld_x, ld_w, tokens_p, logprobs_p, lse_p, entropy_p, top_p, top_lp_p,
+                               dlogprobs_p, dentropy_p, dx_p, dw_p, ld_dx, ld_dw, capi.DMUON_DTYPE_BF16,
+                               capi.DMUON_DTYPE_BF16, token_type, top_type, dx_type, dw_type, n_top, logit_scale,
+                               grad_scale, (capi.DMUON_CE_ADD_DW if accumulate_dw else 0)
+                               | (capi.DMUON_CE_FINE_GRADS if fine_grads else 0))
+        self._call(self._lib.dmuon_token_logprobs, a, stream)
+        return logprobs

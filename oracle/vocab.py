@@ -1,6 +1,6 @@
-"""Float64 oracle of the vocabulary operators: softmax cross entropy over an
-output head, embedding lookup, and their gradients, straight from the
-definitions (numpy, whole logits, no blocking)."""
+"""Float64 oracle of the vocabulary operators: softmax cross entropy and log
+probabilities over an output head, embedding lookup, and their gradients,
+straight from the definitions (numpy, whole logits, no blocking)."""
 
 from __future__ import annotations
 
@@ -47,3 +47,36 @@ def embed_grad(ids, dout, vocab, scale=1.0, base=None):
         if t >= 0:
             out[t] += scale * dout[i]
     return out
+
+
+def token_logprobs(x, w, tokens=None, logit_scale=1.0, n_top=0, dlogprobs=None, dentropy=None, grad_scale=1.0):
+    """Log probabilities of ``tokens`` (below zero: not scored; None: every row
+    scored, no token given), lse, entropy, the n_top most likely ids (equal
+    logits by ascending id) with theirs, and the gradients of
+    sum(dlogprobs * logprobs + dentropy * entropy)."""
+    n = len(x)
+    given = np.full(n, tokens is not None)
+    tokens = np.zeros(n, np.int64) if tokens is None else np.asarray(tokens)
+    scored = tokens >= 0
+    given &= scored
+    x = np.where(scored[:, None], np.asarray(x, np.float64), 0.0)
+    w = np.asarray(w, np.float64)
+    z = logit_scale * (x @ w.T)
+    top = z.max(axis=1, keepdims=True)
+    lse = top[:, 0] + np.log(np.exp(z - top).sum(axis=1))
+    logp = z - lse[:, None]
+    p = np.exp(logp)
+    entropy = -(p * logp).sum(axis=1)
+    rows = np.arange(n)
+    at = np.where(given, tokens, 0)
+    order = np.argsort(-z, axis=1, kind="stable")[:, :n_top]
+    zero = np.zeros(n)
+    g = np.where(given, zero if dlogprobs is None else np.asarray(dlogprobs, np.float64), 0.0)
+    h = np.where(scored, zero if dentropy is None else np.asarray(dentropy, np.float64), 0.0)
+    dz = -p * (g[:, None] + h[:, None] * (logp + entropy[:, None]))
+    dz[rows, at] += g
+    dz *= grad_scale * logit_scale
+    return {"logprobs": np.where(given, logp[rows, at], 0.0), "lse": np.where(scored, lse, 0.0),
+            "entropy": np.where(scored, entropy, 0.0), "top_ids": np.where(scored[:, None], order, -1),
+            "top_logprobs": np.where(scored[:, None], np.take_along_axis(logp, order, axis=1), 0.0),
+            "dx": dz @ w, "dw": dz.T @ x, "dz": dz, "logp": logp}
