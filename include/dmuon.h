@@ -298,6 +298,65 @@ DMUON_API int dmuon_adamw_step(dmuon_context* ctx, const dmuon_vector* ts, int32
                      float lr, float beta1, float beta2, float eps, float wd,
                      int64_t step, void* stream);
 
+/*
+ * dmuon_muon_step_scaled, dmuon_adamw_step_scaled -- the two steps on
+ * g <- *grad_scale * g, a factor in device memory that is read when the step
+ * runs (dmuon_grad_norm's coef, the inverse of a loss scale); the gradients stay
+ * as they are.  NULL: dmuon_muon_step and dmuon_adamw_step, which they equal bit
+ * for bit with a factor of 1.  DMUON_ERR_INVALID_ARG for a factor that the
+ * device cannot reach or that lies in memory the step writes; other errors and
+ * conditions as those two.
+ */
+DMUON_API int dmuon_muon_step_scaled(dmuon_context* ctx, const dmuon_matrix* mats, int32_t n,
+                    float lr, float momentum, float wd, int32_t ns_steps,
+                    float a, float b, float c, uint32_t flags, const float* grad_scale, void* stream);
+DMUON_API int dmuon_adamw_step_scaled(dmuon_context* ctx, const dmuon_vector* ts, int32_t n,
+                     float lr, float beta1, float beta2, float eps, float wd,
+                     int64_t step, const float* grad_scale, void* stream);
+
+/*
+ * Norms of many gradients, and clipping to a global norm before the step.
+ *
+ * dmuon_grad_norm   -- norms_i = ||g_i||_2,  norm = sqrt(sum_i norms_i^2),
+ *                      coef = min(1, max_norm / (norm + 1e-6))
+ * dmuon_clip_grads  -- the same, and out_i = coef * g_i
+ * dmuon_scale_grads -- out_i = *coef * g_i for a factor in device memory
+ *
+ *   gs       host array of n descriptors (read during the call only).  numel
+ *            contiguous elements each, at any alignment that their type allows;
+ *            out may be grad itself (in place, same dtype) and is else memory
+ *            of its own; dmuon_grad_norm does not look at it.  grad and out are
+ *            bf16 or fp32 each: fp32 accumulators go to bf16 gradients in the
+ *            same pass, rounded once.
+ *   max_norm positive; infinity asks for a factor of 1.  Read where coef or out
+ *            is written
+ *   norm, coef   one fp32 each in device memory, norms n of them (written);
+ *            each may be NULL (not all three for dmuon_grad_norm)
+ * Squares are summed in fp32, a few hundred of them, and on from there in 64
+ * bits; a chunk whose squares leave the range of fp32 is summed again at
+ * another scale, so that no element is too large or too small.  A norm that is
+ * not finite gives the factor that the formula gives: 0 for an infinite one (0
+ * times the infinite elements is NaN), NaN for NaN.
+ * In place with a factor of exactly 1 nothing is written.
+ * Uses the vocabulary operators' scratch (below): the same holds for streams,
+ * host threads and captured graphs.  Errors: DMUON_ERR_INVALID_ARG (null or
+ * overlapping memory, no output, bad max_norm), DMUON_ERR_SHAPE (numel),
+ * DMUON_ERR_DTYPE, DMUON_ERR_NOMEM, DMUON_ERR_CUDA, DMUON_ERR_UNSUPPORTED.
+ */
+typedef struct dmuon_grad {
+  int64_t numel;
+  const void* grad;
+  void* out;
+  int32_t grad_dtype, out_dtype;  /* DMUON_DTYPE_* */
+} dmuon_grad;
+
+DMUON_API int dmuon_grad_norm(dmuon_context* ctx, const dmuon_grad* gs, int32_t n, float max_norm,
+                              float* norm, float* norms, float* coef, void* stream);
+DMUON_API int dmuon_clip_grads(dmuon_context* ctx, const dmuon_grad* gs, int32_t n, float max_norm,
+                               float* norm, float* norms, float* coef, void* stream);
+DMUON_API int dmuon_scale_grads(dmuon_context* ctx, const dmuon_grad* gs, int32_t n, const float* coef,
+                                void* stream);
+
 /* Host side of one tensor in dmuon_step_host: page-locked host buffers
  * (cudaHostAlloc, or cudaHostRegister'ed) with the tensor's shape.
  *   grad_host   this step's gradient, dtype = the descriptor's grad_dtype;

@@ -8,6 +8,7 @@ of ``include/dmuon.h``); this package is its thin Python binding:
 * ``vocab``      ``VocabOps``: embedding lookup, cross entropy and log
   probabilities over the output head, each with its gradient (the tensors of
   the AdamW routes);
+* ``grads``      ``GradOps``: norms of many gradients, and clipping;
 * ``workloads``  seeded synthetic inputs and work accounting;
 * ``build``      the nvcc build of the library.
 
@@ -26,20 +27,25 @@ from .capi import (  # noqa: F401
     DMUON_FLAG_NESTEROV,
     DmuonError,
     dmuon_adamw_step,
+    dmuon_adamw_step_scaled,
+    dmuon_clip_grads,
     dmuon_context_create,
     dmuon_context_destroy,
     dmuon_context_set_tuning,
     dmuon_cross_entropy,
     dmuon_embed_backward,
     dmuon_embed_forward,
+    dmuon_grad_norm,
     dmuon_kernel_launches,
     dmuon_lpt_assign,
     dmuon_lpt_assign_layered,
     dmuon_muon_step,
     dmuon_muon_step_noalloc,
     dmuon_muon_step_noalloc_sync,
+    dmuon_muon_step_scaled,
     dmuon_profile,
     dmuon_profile_read,
+    dmuon_scale_grads,
     dmuon_selftest_wait_timeout,
     dmuon_set_tuning,
     dmuon_status_string,
@@ -48,5 +54,6 @@ from .capi import (  # noqa: F401
     dmuon_token_logprobs,
     load_library,
 )
+from .grads import GradList, GradOps  # noqa: F401
 from .optim import OwnerStep, adamw_shard_ranges, adamw_shard_views, owner_partition  # noqa: F401
 from .vocab import VocabOps  # noqa: F401

@@ -22,8 +22,9 @@ LIB = os.path.join(PKG, "libdmuon.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 SOURCES = ["api.cu", "plan.cu", "step.cu", "host_io.cu", "lpt.cpp", "k_stream.cu", "k_ns_simt.cu", "k_ns_tc.cu", "k_ns_tc2.cu", "noalloc.cu",
-           "vocab.cu", "k_vocab_gemm.cu", "k_vocab_thin.cu", "k_vocab_ce.cu", "k_logprobs.cu", "k_embed.cu"]
-HEADERS = ["internal.h", "runtime.h", "ptx.cuh", "host_util.h", "ns_epilogue.cuh", "vocab.h", "vocab_rows.cuh"]
+           "vocab.cu", "k_vocab_gemm.cu", "k_vocab_thin.cu", "k_vocab_ce.cu", "k_logprobs.cu", "k_embed.cu",
+           "grads.cu", "k_grads.cu"]
+HEADERS = ["internal.h", "runtime.h", "ptx.cuh", "host_util.h", "ns_epilogue.cuh", "vocab.h", "vocab_rows.cuh", "grads.h"]
 
 
 def _nvcc():

@@ -48,6 +48,7 @@ EXPORTED = (
     "dmuon_profile_read", "dmuon_muon_step_noalloc", "dmuon_lpt_assign_layered", "dmuon_step_host",
     "dmuon_muon_step_noalloc_sync", "dmuon_profile_host_timeline", "dmuon_context_set_tuning",
     "dmuon_cross_entropy", "dmuon_embed_forward", "dmuon_embed_backward", "dmuon_token_logprobs",
+    "dmuon_muon_step_scaled", "dmuon_adamw_step_scaled", "dmuon_grad_norm", "dmuon_clip_grads", "dmuon_scale_grads",
 )
 
 KERNEL_KINDS = ("momentum", "norm", "ns_gram", "ns_poly", "ns_combine", "update", "adamw")
@@ -136,6 +137,13 @@ class DmuonLogprobs(ctypes.Structure):
     ]
 
 
+class DmuonGrad(ctypes.Structure):
+    _fields_ = [
+        ("numel", ctypes.c_int64), ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+    ]
+
+
 class DmuonEmbed(ctypes.Structure):
     _fields_ = [
         ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
@@ -188,6 +196,13 @@ def load_library(path=LIB_PATH):
         "dmuon_embed_forward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
         "dmuon_embed_backward": (ctypes.c_int, [vp, ctypes.POINTER(DmuonEmbed), vp]),
         "dmuon_token_logprobs": (ctypes.c_int, [vp, ctypes.POINTER(DmuonLogprobs), vp]),
+        "dmuon_muon_step_scaled": (ctypes.c_int, [vp, ctypes.POINTER(DmuonMatrix), i32, f32, f32, f32, i32,
+                                                  f32, f32, f32, ctypes.c_uint32, vp, vp]),
+        "dmuon_adamw_step_scaled": (ctypes.c_int, [vp, ctypes.POINTER(DmuonVector), i32, f32, f32, f32, f32,
+                                                   f32, i64, vp, vp]),
+        "dmuon_grad_norm": (ctypes.c_int, [vp, ctypes.POINTER(DmuonGrad), i32, f32, vp, vp, vp, vp]),
+        "dmuon_clip_grads": (ctypes.c_int, [vp, ctypes.POINTER(DmuonGrad), i32, f32, vp, vp, vp, vp]),
+        "dmuon_scale_grads": (ctypes.c_int, [vp, ctypes.POINTER(DmuonGrad), i32, vp, vp]),
         "dmuon_step_host": (ctypes.c_int, [vp, ctypes.POINTER(DmuonMatrix), ctypes.POINTER(DmuonHostIO), i32,
                                            ctypes.POINTER(DmuonMuonHparams), ctypes.POINTER(DmuonVector),
                                            ctypes.POINTER(DmuonHostIO), i32, ctypes.POINTER(DmuonAdamwHparams),
@@ -444,3 +459,34 @@ def dmuon_embed_backward(ctx, args, stream=None):
 def dmuon_token_logprobs(ctx, args, stream=None):
     """``args``: one DmuonLogprobs."""
     _check(load_library().dmuon_token_logprobs(ctx, ctypes.byref(args), _stream_handle(stream)))
+
+
+def dmuon_muon_step_scaled(ctx, mats, lr, momentum, wd, ns_steps, a, b, c, grad_scale, flags=DMUON_FLAG_NESTEROV,
+                           stream=None):
+    """``mats``: a ctypes array of DmuonMatrix; ``grad_scale``: one fp32 on the device, or None."""
+    _check(load_library().dmuon_muon_step_scaled(ctx, mats, len(mats), float(lr), float(momentum), float(wd), int(ns_steps),
+                                                 float(a), float(b), float(c), int(flags), _ptr(grad_scale),
+                                                 _stream_handle(stream)))
+
+
+def dmuon_adamw_step_scaled(ctx, vecs, lr, beta1, beta2, eps, wd, step, grad_scale, stream=None):
+    """``vecs``: a ctypes array of DmuonVector; ``grad_scale``: one fp32 on the device, or None."""
+    _check(load_library().dmuon_adamw_step_scaled(ctx, vecs, len(vecs), float(lr), float(beta1), float(beta2), float(eps),
+                                                  float(wd), int(step), _ptr(grad_scale), _stream_handle(stream)))
+
+
+def dmuon_grad_norm(ctx, grads, n, max_norm, norm, norms, coef, stream=None):
+    """``grads``: a ctypes array of DmuonGrad; results: fp32 tensors on the device, or None."""
+    _check(load_library().dmuon_grad_norm(ctx, grads, int(n), float(max_norm), _ptr(norm), _ptr(norms), _ptr(coef),
+                                          _stream_handle(stream)))
+
+
+def dmuon_clip_grads(ctx, grads, n, max_norm, norm, norms, coef, stream=None):
+    """As dmuon_grad_norm; the descriptors' outs are written."""
+    _check(load_library().dmuon_clip_grads(ctx, grads, int(n), float(max_norm), _ptr(norm), _ptr(norms), _ptr(coef),
+                                           _stream_handle(stream)))
+
+
+def dmuon_scale_grads(ctx, grads, n, coef, stream=None):
+    """``coef``: one fp32 on the device."""
+    _check(load_library().dmuon_scale_grads(ctx, grads, int(n), _ptr(coef), _stream_handle(stream)))

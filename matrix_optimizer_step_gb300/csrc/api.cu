@@ -373,6 +373,27 @@ int validate_adamw_call(const dmuon_vector* ts, int32_t n, float lr, float beta1
   return DMUON_OK;
 }
 
+// A factor of the gradients is aligned and no part of what the step writes.
+static int check_grad_scale(const float* p, const dmuon_matrix* mats, int n, const dmuon_vector* vecs, int nv) {
+  if (!p) return DMUON_OK;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (at % sizeof(float) != 0) return set_error(DMUON_ERR_INVALID_ARG, "grad_scale is not aligned to its element");
+  const auto in = [&](const void* q, int64_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(q);
+    return q && at < lo + static_cast<uintptr_t>(bytes) && lo < at + sizeof(float);
+  };
+  bool shared = false;
+  for (int i = 0; i < n; ++i) {
+    const int64_t k = matrix_elems(mats[i]);
+    shared = shared || in(mats[i].master, 4 * k) || in(mats[i].momentum, 4 * k) || in(mats[i].param_bf16, 2 * k);
+  }
+  for (int i = 0; i < nv; ++i) {
+    const int64_t k = vecs[i].numel;
+    shared = shared || in(vecs[i].master, 4 * k) || in(vecs[i].exp_avg, 4 * k) || in(vecs[i].exp_avg_sq, 4 * k) || in(vecs[i].param_bf16, 2 * k);
+  }
+  return shared ? set_error(DMUON_ERR_INVALID_ARG, "grad_scale overlaps memory that the step writes") : static_cast<int>(DMUON_OK);
+}
+
 }  // namespace dmuon
 
 using namespace dmuon;
@@ -447,17 +468,20 @@ int dmuon_context_destroy(dmuon_context* ctx) {
 
 int64_t dmuon_kernel_launches(const dmuon_context* ctx) { return ctx ? ctx->launches : -1; }
 
-int dmuon_muon_step(dmuon_context* ctx, const dmuon_matrix* mats, int32_t n, float lr,
-                    float momentum, float wd, int32_t ns_steps, float a, float b, float c,
-                    uint32_t flags, void* stream) {
+int dmuon_muon_step_scaled(dmuon_context* ctx, const dmuon_matrix* mats, int32_t n, float lr,
+                           float momentum, float wd, int32_t ns_steps, float a, float b, float c,
+                           uint32_t flags, const float* grad_scale, void* stream) {
   clear_error();
   if (!ctx) return set_error(DMUON_ERR_INVALID_ARG, "muon_step: null context");
   int st = validate_muon_call(mats, n, lr, momentum, wd, ns_steps, a, b, c, flags);
   if (st != DMUON_OK || n == 0) return st;
   st = check_no_overlap_cached(ctx, mats, n, nullptr, 0);
   if (st != DMUON_OK) return st;
+  st = check_grad_scale(grad_scale, mats, n, nullptr, 0);
+  if (st != DMUON_OK) return st;
   DeviceGuard guard(ctx->device);
   st = ensure_device(ctx);
+  if (st == DMUON_OK) st = check_reachable(ctx, grad_scale, "grad_scale", 0);
   if (st != DMUON_OK) return st;
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += matrix_elems(mats[i]);
@@ -465,25 +489,39 @@ int dmuon_muon_step(dmuon_context* ctx, const dmuon_matrix* mats, int32_t n, flo
       static_cast<int>(std::min<int64_t>({int64_t(ctx->tune.mom_groups), int64_t(n), total / ctx->tune.group_min_elems}));
   if (groups > 1)
     return muon_step_overlapped(ctx, mats, n, groups, lr, momentum, wd, ns_steps, a, b, c, flags,
-                                static_cast<cudaStream_t>(stream));
+                                static_cast<cudaStream_t>(stream), grad_scale);
   MuonSlot* S = get_slot(ctx, 0);
   if (!S) return set_error(DMUON_ERR_NOMEM, "muon_step: host allocation failed");
   return muon_step_impl(ctx, *S, mats, n, lr, momentum, wd, ns_steps, a, b, c, flags,
-                        static_cast<cudaStream_t>(stream));
+                        static_cast<cudaStream_t>(stream), true, grad_scale);
 }
 
-int dmuon_adamw_step(dmuon_context* ctx, const dmuon_vector* ts, int32_t n, float lr, float beta1,
-                     float beta2, float eps, float wd, int64_t step, void* stream) {
+int dmuon_muon_step(dmuon_context* ctx, const dmuon_matrix* mats, int32_t n, float lr,
+                    float momentum, float wd, int32_t ns_steps, float a, float b, float c,
+                    uint32_t flags, void* stream) {
+  return dmuon_muon_step_scaled(ctx, mats, n, lr, momentum, wd, ns_steps, a, b, c, flags, nullptr, stream);
+}
+
+int dmuon_adamw_step_scaled(dmuon_context* ctx, const dmuon_vector* ts, int32_t n, float lr, float beta1,
+                            float beta2, float eps, float wd, int64_t step, const float* grad_scale, void* stream) {
   clear_error();
   if (!ctx) return set_error(DMUON_ERR_INVALID_ARG, "adamw_step: null context");
   int st = validate_adamw_call(ts, n, lr, beta1, beta2, eps, wd, step);
   if (st != DMUON_OK || n == 0) return st;
   st = check_no_overlap_cached(ctx, nullptr, 0, ts, n);
   if (st != DMUON_OK) return st;
+  st = check_grad_scale(grad_scale, nullptr, 0, ts, n);
+  if (st != DMUON_OK) return st;
   DeviceGuard guard(ctx->device);
   st = ensure_device(ctx);
+  if (st == DMUON_OK) st = check_reachable(ctx, grad_scale, "grad_scale", 0);
   if (st != DMUON_OK) return st;
-  return adamw_step_impl(ctx, ts, n, lr, beta1, beta2, eps, wd, step, static_cast<cudaStream_t>(stream));
+  return adamw_step_impl(ctx, ts, n, lr, beta1, beta2, eps, wd, step, static_cast<cudaStream_t>(stream), grad_scale);
+}
+
+int dmuon_adamw_step(dmuon_context* ctx, const dmuon_vector* ts, int32_t n, float lr, float beta1,
+                     float beta2, float eps, float wd, int64_t step, void* stream) {
+  return dmuon_adamw_step_scaled(ctx, ts, n, lr, beta1, beta2, eps, wd, step, nullptr, stream);
 }
 
 int dmuon_sync(dmuon_context* ctx, void* stream) {

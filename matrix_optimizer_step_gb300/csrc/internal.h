@@ -166,9 +166,10 @@ struct NsLaunch {
 };
 
 // ---- launch wrappers (each returns the cudaError_t of its launch) ----
+// grad_scale: a factor of every gradient, in device memory, or null (1).
 cudaError_t launch_momentum(const SliceDesc* slices, const Chunk* chunks, int n_chunks,
                             float mu, int nesterov, int x_fp32, float* partials,
-                            cudaStream_t st);
+                            const float* grad_scale, cudaStream_t st);
 cudaError_t launch_norm(const SliceDesc* slices, int n_slices, const float* partials,
                         float* inv_norm, cudaStream_t st);
 cudaError_t launch_update(const SliceDesc* slices, const Chunk* chunks, int n_chunks,
@@ -176,7 +177,7 @@ cudaError_t launch_update(const SliceDesc* slices, const Chunk* chunks, int n_ch
                           cudaStream_t st);
 cudaError_t launch_adamw(const VecDesc* vecs, const Chunk* chunks, int n_chunks,
                          float lr, float beta1, float beta2, float eps, float wd,
-                         float bc1, float bc2_sqrt, cudaStream_t st);
+                         float bc1, float bc2_sqrt, const float* grad_scale, cudaStream_t st);
 cudaError_t launch_selftest_wait(int* err, long long timeout_ns, cudaStream_t st);
 
 cudaError_t launch_ns_tc(const NsLaunch& L, int n_ctas, cudaStream_t st);

@@ -93,13 +93,14 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const SliceDesc* __restrict__ slices,
                                                             const Chunk* __restrict__ chunks,
                                                             float mu, int nesterov, int x_fp32,
-                                                            float* __restrict__ partials) {
+                                                            float* __restrict__ partials, const float* grad_scale) {
   __shared__ float red[kThreads / 32];
   const Chunk ch = chunks[blockIdx.x];
   const SliceDesc S = slices[ch.slice];
   const int64_t end = ch.start + ch.count;
   x_fp32 = x_fp32 || S.x_f32;
   float ss = 0.f;
+  const float gs = grad_scale ? *grad_scale : 1.f;
   if (S.vec_ok) {
     const bool dense = (S.ld == S.n);
     for (int64_t e = ch.start + 8 * static_cast<int64_t>(threadIdx.x); e < end;
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const SliceDesc* __r
       load8_f32_rw(S.momentum + e, buf);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        g[i] *= gs;
         buf[i] = fmaf(mu, buf[i], g[i]);
         u[i] = nesterov ? fmaf(mu, buf[i], g[i]) : buf[i];
         ss = fmaf(u[i], u[i], ss);
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const SliceDesc* __r
     }
   } else {
     for (int64_t e = ch.start + threadIdx.x; e < end; e += kThreads) {
-      const float g = load1(S.grad, e, S.grad_bf16);
+      const float g = gs * load1(S.grad, e, S.grad_bf16);
       const float b = fmaf(mu, S.momentum[e], g);
       const float u = nesterov ? fmaf(mu, b, g) : b;
       S.momentum[e] = b;
@@ -223,12 +225,14 @@ __device__ __forceinline__ float adamw_elem(float g, float& w, float& m, float& 
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const VecDesc* __restrict__ vecs,
                                                          const Chunk* __restrict__ chunks,
                                                          float lr, float b1, float b2, float eps,
-                                                         float wd, float bc1, float bc2_sqrt) {
+                                                         float wd, float bc1, float bc2_sqrt,
+                                                         const float* grad_scale) {
   const Chunk ch = chunks[blockIdx.x];
   const VecDesc V = vecs[ch.slice];
   const int64_t end = ch.start + ch.count;
   const float decay = 1.0f - lr * wd;
   const float step_size = lr / bc1;
+  const float gs = grad_scale ? *grad_scale : 1.f;
   int64_t e0 = ch.start;
   if (V.vec_ok) {
     const int64_t vec_end = ch.start + (static_cast<int64_t>(ch.count) & ~int64_t(7));
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const VecDesc* __restri
       load8_f32_rw(V.exp_avg_sq + e, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        adamw_elem(g[i], w[i], m[i], v[i], b1, b2, eps, decay, step_size, bc2_sqrt);
+        adamw_elem(gs * g[i], w[i], m[i], v[i], b1, b2, eps, decay, step_size, bc2_sqrt);
       store8_f32(V.master + e, w);
       store8_f32(V.exp_avg + e, m);
       store8_f32(V.exp_avg_sq + e, v);
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const VecDesc* __restri
   }
   for (int64_t e = e0 + threadIdx.x; e < end; e += kThreads) {
     float w = V.master[e], m = V.exp_avg[e], v = V.exp_avg_sq[e];
-    adamw_elem(load1(V.grad, e, V.grad_bf16), w, m, v, b1, b2, eps, decay, step_size, bc2_sqrt);
+    adamw_elem(gs * load1(V.grad, e, V.grad_bf16), w, m, v, b1, b2, eps, decay, step_size, bc2_sqrt);
     V.master[e] = w;
     V.exp_avg[e] = m;
     V.exp_avg_sq[e] = v;
@@ -283,9 +287,9 @@ __global__ void selftest_wait_kernel(int* err, unsigned long long limit_ns) {
 }  // namespace
 
 cudaError_t launch_momentum(const SliceDesc* slices, const Chunk* chunks, int n_chunks, float mu,
-                            int nesterov, int x_fp32, float* partials, cudaStream_t st) {
+                            int nesterov, int x_fp32, float* partials, const float* grad_scale, cudaStream_t st) {
   if (n_chunks <= 0) return cudaSuccess;
-  momentum_kernel<<<n_chunks, kThreads, 0, st>>>(slices, chunks, mu, nesterov, x_fp32, partials);
+  momentum_kernel<<<n_chunks, kThreads, 0, st>>>(slices, chunks, mu, nesterov, x_fp32, partials, grad_scale);
   return cudaGetLastError();
 }
 
@@ -307,10 +311,10 @@ cudaError_t launch_update(const SliceDesc* slices, const Chunk* chunks, int n_ch
 
 cudaError_t launch_adamw(const VecDesc* vecs, const Chunk* chunks, int n_chunks, float lr,
                          float beta1, float beta2, float eps, float wd, float bc1, float bc2_sqrt,
-                         cudaStream_t st) {
+                         const float* grad_scale, cudaStream_t st) {
   if (n_chunks <= 0) return cudaSuccess;
   adamw_kernel<<<n_chunks, kThreads, 0, st>>>(vecs, chunks, lr, beta1, beta2, eps, wd, bc1,
-                                              bc2_sqrt);
+                                              bc2_sqrt, grad_scale);
   return cudaGetLastError();
 }
 

@@ -432,7 +432,7 @@ extern "C" int dmuon_muon_step_noalloc(const dmuon_matrix* mat, float lr, float 
   float* partials = reinterpret_cast<float*>(base + o_part);
   float* inv_norm = reinterpret_cast<float*>(base + o_norm);
   const int nesterov = (flags & DMUON_FLAG_NESTEROV) ? 1 : 0;
-  if ((e = launch_momentum(d_slices, d_chunks, static_cast<int>(n_chunks), momentum, nesterov, 0, partials, stm)) !=
+  if ((e = launch_momentum(d_slices, d_chunks, static_cast<int>(n_chunks), momentum, nesterov, 0, partials, nullptr, stm)) !=
       cudaSuccess)
     return fail_cuda(e, "momentum launch");
   if ((e = launch_norm(d_slices, static_cast<int>(S), partials, inv_norm, stm)) != cudaSuccess)

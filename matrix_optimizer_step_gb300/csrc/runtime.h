@@ -362,6 +362,10 @@ struct dmuon_context {
   int vocab_pairs = 0;
   // AdamW descriptor array whose pointers last passed the reachability check.
   std::vector<uint8_t> checked_vecs;
+  // Gradient lists, with the results' places, that last passed their checks (grads.cu).
+  static constexpr int kCheckedGrads = 8;
+  std::vector<uint8_t> checked_grads[kCheckedGrads];
+  int checked_next = 0;
   // Descriptor arrays (Muon, AdamW) that last passed the overlap check.
   std::vector<uint8_t> checked_overlap;
   // Host pipeline: copy streams, events, cached groups and copy lists.
@@ -422,6 +426,12 @@ int validate_muon_call(const dmuon_matrix* mats, int32_t n, float lr, float mome
 int validate_adamw_call(const dmuon_vector* ts, int32_t n, float lr, float beta1, float beta2, float eps,
                         float wd, int64_t step);
 
+// ---- vocab.cu: scratch shared by the vocabulary and the gradient operators
+// (ctx->vocab_ws of at least `bytes`, ctx->vocab_ticket with words that are zero),
+// and the end of a call that used it on stream s and came to status st.
+int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s);
+int end_use(dmuon_context* ctx, cudaStream_t s, int st);
+
 // ---- plan.cu
 std::string plan_key(const dmuon_matrix* mats, int n, bool fp32, int tile_order);
 int layout_plan(MuonPlan& P, const dmuon_matrix* mats, int n, bool fp32, size_t ws_base);
@@ -436,23 +446,23 @@ int prepare_slot(dmuon_context* ctx, MuonSlot& S, const dmuon_matrix* mats, int 
                  size_t ws_base = 0);
 int muon_stage_table(dmuon_context* ctx, MuonSlot& S, const dmuon_matrix* mats, int n, int32_t ns_steps,
                      cudaStream_t s);
-int muon_launch_front(dmuon_context* ctx, MuonSlot& S, float momentum, uint32_t flags, cudaStream_t s);
+int muon_launch_front(dmuon_context* ctx, MuonSlot& S, float momentum, uint32_t flags, const float* grad_scale, cudaStream_t s);
 // call_tma: every tensor of the whole call (all groups of a grouped call)
 // can take the fused update's TMA copies; false keeps every group unfused.
 int muon_launch_ns(dmuon_context* ctx, MuonSlot& S, float lr, float wd, int32_t ns_steps, float a, float b,
                    float c, cudaStream_t s, bool call_tma = true);
 int muon_step_impl(dmuon_context* ctx, MuonSlot& S, const dmuon_matrix* mats, int n, float lr,
                    float momentum, float wd, int32_t ns_steps, float a, float b, float c,
-                   uint32_t flags, cudaStream_t s, bool call_tma = true);
+                   uint32_t flags, cudaStream_t s, bool call_tma = true, const float* grad_scale = nullptr);
 // Whether every bf16-class tensor of plan P (over mats[0..n)) can take the
 // fused update's TMA copies.
 bool plan_tma_copyable(const MuonPlan& P, const dmuon_matrix* mats, int n);
 int64_t matrix_elems(const dmuon_matrix& M);
 int muon_step_overlapped(dmuon_context* ctx, const dmuon_matrix* mats, int n, int groups, float lr,
                          float momentum, float wd, int32_t ns_steps, float a, float b, float c,
-                         uint32_t flags, cudaStream_t s);
+                         uint32_t flags, cudaStream_t s, const float* grad_scale);
 int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr, float beta1, float beta2,
-                    float eps, float wd, int64_t step, cudaStream_t s);
+                    float eps, float wd, int64_t step, cudaStream_t s, const float* grad_scale = nullptr);
 
 // Run one launch, counting it and (when profiling) bracketing it with events.
 template <class F>

@@ -159,7 +159,8 @@ int muon_stage_table(dmuon_context* ctx, MuonSlot& S, const dmuon_matrix* mats, 
 }
 
 // Stage 2: momentum pass and per-slice norms (needs stage 1 on s).
-int muon_launch_front(dmuon_context* ctx, MuonSlot& S, float momentum, uint32_t flags, cudaStream_t s) {
+// grad_scale: a factor of every gradient in device memory, or null.
+int muon_launch_front(dmuon_context* ctx, MuonSlot& S, float momentum, uint32_t flags, const float* grad_scale, cudaStream_t s) {
   MuonPlan& P = S.plan;
   const SliceDesc* d_slices = static_cast<const SliceDesc*>(S.table.dev.p);
   const Chunk* d_chunks = static_cast<const Chunk*>(P.chunks_dev.p);
@@ -168,7 +169,7 @@ int muon_launch_front(dmuon_context* ctx, MuonSlot& S, float momentum, uint32_t 
   const int n_chunks = static_cast<int>(P.chunks.size());
   const int nesterov = (flags & DMUON_FLAG_NESTEROV) ? 1 : 0;
   int st = timed_launch(ctx, DMUON_KERNEL_MOMENTUM, s, [&] {
-    return launch_momentum(d_slices, d_chunks, n_chunks, momentum, nesterov, 0, partials, s);
+    return launch_momentum(d_slices, d_chunks, n_chunks, momentum, nesterov, 0, partials, grad_scale, s);
   });
   if (st != DMUON_OK) return st;
   return timed_launch(ctx, DMUON_KERNEL_NORM, s, [&] {
@@ -274,12 +275,12 @@ int muon_launch_ns(dmuon_context* ctx, MuonSlot& S, float lr, float wd, int32_t 
 // every stage on stream s.
 int muon_step_impl(dmuon_context* ctx, MuonSlot& S, const dmuon_matrix* mats, int n, float lr,
                    float momentum, float wd, int32_t ns_steps, float a, float b, float c,
-                   uint32_t flags, cudaStream_t s, bool call_tma) {
+                   uint32_t flags, cudaStream_t s, bool call_tma, const float* grad_scale) {
   int st = prepare_slot(ctx, S, mats, n, (flags & DMUON_FLAG_FP32_NS) != 0);
   if (st != DMUON_OK) return st;
   st = muon_stage_table(ctx, S, mats, n, ns_steps, s);
   if (st != DMUON_OK) return st;
-  st = muon_launch_front(ctx, S, momentum, flags, s);
+  st = muon_launch_front(ctx, S, momentum, flags, grad_scale, s);
   if (st != DMUON_OK) return st;
   return muon_launch_ns(ctx, S, lr, wd, ns_steps, a, b, c, s, call_tma);
 }
@@ -295,7 +296,7 @@ int64_t matrix_elems(const dmuon_matrix& M) {
 // count, each with its own plan and workspace region).
 int muon_step_overlapped(dmuon_context* ctx, const dmuon_matrix* mats, int n, int groups, float lr,
                          float momentum, float wd, int32_t ns_steps, float a, float b, float c,
-                         uint32_t flags, cudaStream_t s) {
+                         uint32_t flags, cudaStream_t s, const float* grad_scale) {
   const bool fp32 = (flags & DMUON_FLAG_FP32_NS) != 0;
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += matrix_elems(mats[i]);
@@ -347,7 +348,7 @@ int muon_step_overlapped(dmuon_context* ctx, const dmuon_matrix* mats, int n, in
   for (int g = 0; g < G && st == DMUON_OK; ++g) {
     const int b0 = range[static_cast<size_t>(g)].first, cnt = range[static_cast<size_t>(g)].second - b0;
     st = muon_stage_table(ctx, *S[static_cast<size_t>(g)], mats + b0, cnt, ns_steps, ctx->side);
-    if (st == DMUON_OK) st = muon_launch_front(ctx, *S[static_cast<size_t>(g)], momentum, flags, ctx->side);
+    if (st == DMUON_OK) st = muon_launch_front(ctx, *S[static_cast<size_t>(g)], momentum, flags, grad_scale, ctx->side);
     if (st == DMUON_OK && cudaEventRecord(ctx->side_events[2 + static_cast<size_t>(g)], ctx->side) != cudaSuccess)
       st = cuda_fail(cudaGetLastError(), "muon_step: event record");
   }
@@ -371,7 +372,7 @@ int muon_step_overlapped(dmuon_context* ctx, const dmuon_matrix* mats, int n, in
 
 // One AdamW step of a validated, non-empty tensor list on the current device.
 int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr, float beta1, float beta2,
-                    float eps, float wd, int64_t step, cudaStream_t s) {
+                    float eps, float wd, int64_t step, cudaStream_t s, const float* grad_scale) {
   int st = check_vectors_reachable(ctx, ts, n);
   if (st != DMUON_OK) return st;
 
@@ -417,7 +418,7 @@ int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr,
     return launch_adamw(static_cast<const VecDesc*>(ctx->vec_table.dev.p),
                         static_cast<const Chunk*>(A.chunks_dev.p), static_cast<int>(A.chunks.size()),
                         lr, beta1, beta2, eps, wd, static_cast<float>(bc1),
-                        static_cast<float>(std::sqrt(bc2)), s);
+                        static_cast<float>(std::sqrt(bc2)), grad_scale, s);
   });
 }
 

@@ -137,10 +137,12 @@ int check_index(const char* op, int32_t t) {
   } while (0)
 
 // ------------------------------------------------------------------ workspace
-// The vocabulary operators' own scratch: grown on demand, shared by all calls
-// on the context.  A call on another stream than the last one waits for it;
+// The scratch of the vocabulary and the gradient operators: grown on demand, shared by all
+// their calls on the context.  A call on another stream than the last one waits for it;
 // streams are told apart by their ids, since a handle may stand for another stream
 // than before (cudaStreamPerThread in each thread; a handle freed and given out again).
+}  // namespace
+
 int vocab_workspace(dmuon_context* ctx, size_t bytes, cudaStream_t s) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   DM_CUDA(cudaStreamIsCapturing(s, &cap));
@@ -191,8 +193,10 @@ int end_use(dmuon_context* ctx, cudaStream_t s, int st) {
     return e;
   };
   const cudaError_t e = note();
-  return st != DMUON_OK || e == cudaSuccess ? st : cuda_fail(e, "end of a vocabulary operator");
+  return st != DMUON_OK || e == cudaSuccess ? st : cuda_fail(e, "end of a call that uses the shared scratch");
 }
+
+namespace {
 
 struct Layout {
   size_t bytes = 0;

@@ -13,6 +13,7 @@ import ctypes
 import torch
 
 from . import capi
+from .vocab import _raw_stream, empty_on
 
 
 def _check_tensor(t, name, dtypes, like=None):
@@ -37,6 +38,8 @@ class OwnerStep:
         self._vecs = None
         self._n_vecs = 0
         self._keep = []
+        self._grad_lists = {}
+        self._coef = None
 
     # -------------------------------------------------------------- Muon
     def set_muon(self, masters, momenta, grads, params=None):
@@ -56,15 +59,17 @@ class OwnerStep:
         self._mats = capi.descriptor_array(descs, capi.DmuonMatrix)
         self._n_mats = len(descs)
         self._keep = [masters, momenta, grads, params]
+        self._grad_lists = {}
 
     def muon_step(self, lr, momentum, wd, ns_steps=5, a=3.4445, b=-4.7750, c=2.0315,
-                  nesterov=True, fp32_ns=False, stream=None):
+                  nesterov=True, fp32_ns=False, stream=None, grad_scale=None):
+        """``grad_scale``: a factor of every gradient, one fp32 on the device (None: 1)."""
         if self._mats is None:
             raise RuntimeError("set_muon() first")
         flags = (capi.DMUON_FLAG_NESTEROV if nesterov else 0) | (capi.DMUON_FLAG_FP32_NS if fp32_ns else 0)
-        capi._check(capi.load_library().dmuon_muon_step(
+        capi._check(capi.load_library().dmuon_muon_step_scaled(
             self.ctx, self._mats, self._n_mats, float(lr), float(momentum), float(wd), int(ns_steps),
-            float(a), float(b), float(c), flags, capi._stream_handle(stream)))
+            float(a), float(b), float(c), flags, self._one(grad_scale, "grad_scale"), capi._stream_handle(stream)))
 
     # ------------------------------------------------------------- AdamW
     def set_adamw(self, masters, exp_avgs, exp_avg_sqs, grads, params=None):
@@ -81,24 +86,90 @@ class OwnerStep:
         self._vecs = capi.descriptor_array(descs, capi.DmuonVector)
         self._n_vecs = len(descs)
         self._keep_adam = [masters, exp_avgs, exp_avg_sqs, grads, params]
+        self._grad_lists = {}
 
-    def adamw_step(self, lr, beta1, beta2, eps, wd, step, stream=None):
+    def adamw_step(self, lr, beta1, beta2, eps, wd, step, stream=None, grad_scale=None):
+        """``grad_scale``: a factor of every gradient, one fp32 on the device (None: 1)."""
         if self._vecs is None:
             raise RuntimeError("set_adamw() first")
-        capi._check(capi.load_library().dmuon_adamw_step(
+        capi._check(capi.load_library().dmuon_adamw_step_scaled(
             self.ctx, self._vecs, self._n_vecs, float(lr), float(beta1), float(beta2), float(eps),
-            float(wd), int(step), capi._stream_handle(stream)))
+            float(wd), int(step), self._one(grad_scale, "grad_scale"), capi._stream_handle(stream)))
+
+    # ---------------------------------------------------- gradient norm
+    def _one(self, t, name, n=1):
+        """Pointer of an fp32 result or factor on the device."""
+        if t is None:
+            return None
+        _check_tensor(t, name, (torch.float32,))
+        if t.numel() != n or t.get_device() != self.device:
+            raise ValueError(f"{name}: expected {n} elements on cuda:{self.device}")
+        return t.data_ptr()
+
+    def _grad_list(self, muon, adamw):
+        """Descriptors of the registered gradients of the routes, Muon's first."""
+        key = (muon, adamw)
+        if key not in self._grad_lists:
+            grads = (list(self._keep[2]) if muon else []) + (list(self._keep_adam[3]) if adamw else [])
+            descs = [capi.DmuonGrad(g.numel(), g.data_ptr(), None, capi._grad_dtype(g), 0) for g in grads]
+            self._grad_lists[key] = capi.descriptor_array(descs, capi.DmuonGrad), len(descs)
+        return self._grad_lists[key]
+
+    def grad_norm(self, max_norm=None, norm=None, norms=None, coef=None, stream=None):
+        """2-norm of the registered gradients (Muon's, then AdamW's) together
+        into ``norm``, of each into ``norms`` and, with ``max_norm``,
+        min(1, max_norm / (norm + 1e-6)) into ``coef`` (fp32 on the device,
+        whichever are given; with none, ``norm`` is allocated).  Returns
+        ``norm``.  No gradient is written: ``coef`` is what the steps take as
+        ``grad_scale``."""
+        return self._grad_norm(self._mats is not None, self._vecs is not None, max_norm, norm, norms, coef, stream)
+
+    def _grad_norm(self, muon, adamw, max_norm, norm, norms, coef, stream):
+        if not muon and not adamw:
+            raise RuntimeError("set_muon() or set_adamw() first")
+        if coef is not None and max_norm is None:
+            raise ValueError("coef needs max_norm")
+        if norm is None and norms is None and coef is None:
+            norm = empty_on(stream, self.device, 1, dtype=torch.float32)
+        array, n = self._grad_list(muon, adamw)
+        capi._check(capi.load_library().dmuon_grad_norm(
+            self.ctx, array, n, 0.0 if max_norm is None else float(max_norm), self._one(norm, "norm"),
+            self._one(norms, "norms", n), self._one(coef, "coef"),
+            _raw_stream(self.device) if stream is None else capi._stream_handle(stream)))
+        return norm
 
     # ------------------------------------------------------ both routes
-    def step(self, muon, adamw, stream=None):
+    def step(self, muon, adamw, stream=None, max_norm=None, norm=None):
         """One optimizer step of every registered tensor: the Muon step on
         ``stream`` and, concurrently, the AdamW step on a side stream (the two
         share no workspace; AdamW is HBM-bound while the Newton-Schulz
         products are tensor-bound).  ``muon`` / ``adamw`` are keyword dicts for
-        muon_step / adamw_step (adamw may be None).  On return ``stream`` is
-        ordered after both."""
+        muon_step / adamw_step (either may be None: no step of that route).  On
+        return ``stream`` is ordered after both.
+
+        With ``max_norm`` the gradients of the routes that step count as
+        multiplied by min(1, max_norm / (their norm + 1e-6)); they are not
+        written.  ``norm`` (one fp32 on the device) then receives the norm."""
+        use_adamw = adamw is not None and self._vecs is not None
+        if muon is None and not use_adamw:
+            raise RuntimeError("step: no route to step")
+        if muon is not None and self._mats is None:
+            raise RuntimeError("set_muon() first")
+        if max_norm is None and norm is not None:
+            raise ValueError("step: norm without max_norm (grad_norm() gives it)")
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if adamw is None or self._vecs is None:
+        if max_norm is not None:
+            if "grad_scale" in (muon or {}) or "grad_scale" in (adamw or {}):
+                raise ValueError("step: max_norm and grad_scale")
+            if self._coef is None:
+                self._coef = empty_on(main, self.device, 1, dtype=torch.float32)
+            self._grad_norm(muon is not None, use_adamw, max_norm, norm, None, self._coef, main)
+            muon = muon if muon is None else dict(muon, grad_scale=self._coef)
+            adamw = adamw if adamw is None else dict(adamw, grad_scale=self._coef)
+        if muon is None:
+            self.adamw_step(stream=main, **adamw)
+            return
+        if not use_adamw:
             self.muon_step(stream=main, **muon)
             return
         if getattr(self, "_side", None) is None:
