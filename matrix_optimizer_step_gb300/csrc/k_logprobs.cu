@@ -27,6 +27,12 @@ __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000)
 //   ln p_t = -log1p(S / o),  entropy = log1p(S / o) - ln 2 (T - S (z_t - M)) / (S + o),
 // and both keep their digits however certain it is.  Blocks, widths and the
 // copy of dW's operand are as in ce_rows_kernel.
+//
+// Where a row's k largest logits are wanted, the same pass bounds them: a value T that
+// k of 256 groups of blocks reach with their maxima, found by bisection.  k entries
+// lie there or above, so only blocks that reach T (k and a few more, listed
+// for lp_top_kernel) hold one.  The maxima carry the product's rounding, for which
+// 2^-9 octaves and 2^-14 of the row's maximum are allowed.
 struct Sums {
   float m, s, t;
 };
@@ -45,10 +51,53 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   return r;
 }
 
+__device__ __forceinline__ float logit_slack(float top) { return 0x1p-9f + fabsf(top) * 0x1p-14f; }
+
+// A value that at least k of the warp's values reach (PER of them a lane) and, unless
+// values crowd there, not many more; -inf where k of them are not above it.
+template <int PER>
+__device__ __forceinline__ float reached_by(const float (&v)[PER], int k) {
+  float top = v[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  auto reach = [&](float at) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n += v[i] >= at ? 1 : 0;
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  float step = 2.f, above = top, at = top - step;
+  int n = reach(at);
+  while (n < k) {
+    if (step > 1e6f) return minus_inf();
+    above = at;
+    step *= 2.f;
+    at = top - step;
+    n = reach(at);
+  }
+  for (int i = 0; i < 10 && n > k + 2; ++i) {
+    const float mid = 0.5f * (at + above);
+    const int m = reach(mid);
+    if (m >= k) {
+      at = mid;
+      n = m;
+    } else {
+      above = mid;
+    }
+  }
+  return at;
+}
+
+constexpr int kGroups = 256;
+
 template <bool VEC>
 __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R, int row_blocks) {
   __shared__ Sums part[kRowWarps][8];
   __shared__ double dots[kRowWarps];
+  __shared__ float groups[8][kGroups + 1], reached[8], slack[8];
+  __shared__ int found[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = R.width;
   pdl_launch();
   pdl_wait();
@@ -71,8 +120,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R,
   Sums sum = {minus_inf(), 0.f, 0.f};
   const int64_t own_row = base + (lane & (width - 1));
   const int per_warp = 32 / width, stride = kRowWarps * per_warp;
+  const int first_block = warp * per_warp + lane / width;
+  float group[8];  // maxima of the blocks that are first, second, ... of eight
+#pragma unroll
+  for (int k = 0; k < 8; ++k) group[k] = minus_inf();
   if (own_row < R.rows) {
-    for (int b = warp * per_warp + lane / width; b < R.n_blocks; b += 8 * stride) {
+    for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
       Sums q[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -80,6 +133,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R,
         const bool in = b + k * stride < R.n_blocks;
         const float2 ms = in ? R.stats[at] : make_float2(minus_inf(), 0.f);
         q[k] = Sums{ms.x, ms.y, in ? R.weighted[at] : 0.f};
+        group[k] = fmaxf(group[k], ms.x);
       }
       // The eight against their common maximum.
       Sums eight = {q[0].m, 0.f, 0.f};
@@ -104,11 +158,57 @@ __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R,
     sum = lane & o ? join(other, sum) : join(sum, other);
   }
   if (lane < width) part[warp][lane] = sum;
+  if (R.k > 0) {
+    // Eight, four or one group of this thread: 256 of a row.
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      if (o >= width)
+#pragma unroll
+        for (int k = 0; k < o; ++k) group[k] = fmaxf(group[k], group[k + o]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < width) groups[lane & (width - 1)][(first_block * width + k)] = group[k];
+    if (threadIdx.x < 8) found[threadIdx.x] = 0;
+  }
   if (dot_target >= 0) {
     const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
     if (lane == 0) dots[warp] = d;
   }
   __syncthreads();
+  if (R.k > 0) {
+    if (warp < width) {
+      float g[kGroups / 32];
+#pragma unroll
+      for (int i = 0; i < kGroups / 32; ++i) g[i] = groups[warp][lane + 32 * i];
+      float top = g[0];
+#pragma unroll
+      for (int i = 1; i < kGroups / 32; ++i) top = fmaxf(top, g[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float at = reached_by<kGroups / 32>(g, R.k), off = logit_slack(top);
+      if (lane == 0) {
+        reached[warp] = at - off;
+        slack[warp] = off;
+      }
+    }
+    __syncthreads();
+    if (own_row < R.rows) {
+      const float from = reached[lane & (width - 1)], off = slack[lane & (width - 1)];
+      for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
+        float m[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          m[k] = b + k * stride < R.n_blocks ? R.stats[static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row].x : minus_inf();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (b + k * stride >= R.n_blocks || m[k] + off < from) continue;
+          const int at = atomicAdd(&found[lane & (width - 1)], 1);
+          if (at < kTopBlocks) R.top_blocks[own_row * kTopBlocks + at] = TopBlock{b + k * stride, m[k]};
+        }
+      }
+    }
+    __syncthreads();
+  }
   const int64_t r = base + lane;
   if (warp != 0 || lane >= width || r >= R.rows) return;
   Sums all = part[0][lane];
@@ -118,6 +218,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R,
   const int t = R.tokens.p ? load_id(R.tokens, i, &bad) : -1;
   if (bad) atomicCAS(R.err, 0, kErrBadIndex);
   LpRow o = {};
+  if (R.k > 0) {
+    o.reached = reached[lane];
+    o.blocks = found[lane];
+  }
   o.target = t;
   o.scored = !R.tokens.p || t >= 0;
   float lse = 0.f, entropy = 0.f;
@@ -157,53 +261,25 @@ __global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R,
 
 // ---------------------------------------------------------- most likely entries
 // The k largest logits of a row, equal ones by their numbers, in the order that
-// sums of 64 bits give.  A block takes a row; the logs (16-bit distances to the
-// blocks' maxima) bound each logit from both sides, and only entries that may be
-// among the k are multiplied out again:
-//   1. the k-th largest of the blocks' maxima: k entries lie there or above, so
-//      blocks further below hold none;
-//   2. of the others' entries the k-th largest lower bound;
-//   3. entries whose upper bound reaches it, k and one or two more: their logits
-//      as sums of exact products, in two floats each, put in order.
-// What a bound allows for besides the log's own half step is the product's
-// rounding, taken as 2^-9 octaves and 2^-14 of the row's maximum.
-// More candidates than there is room for (equal or nearly equal logits) are taken a few
-// blocks at a time; a row of zeros, all of whose logits are equal, is known without.
-constexpr int kCandidates = 256;
-
-// Lane i holds the i-th largest value so far; `least` is the k-th.
-struct WarpTop {
-  float q, least;
-  __device__ __forceinline__ WarpTop() : q(minus_inf()), least(minus_inf()) {}
-  // Takes each lane's value.
-  __device__ __forceinline__ void add(float v, int k, int lane) {
-    unsigned more = __ballot_sync(0xffffffffu, v > least);
-    while (more) {
-      const float c = __shfl_sync(0xffffffffu, v, __ffs(more) - 1);
-      more &= more - 1;
-      if (c <= least) continue;
-      const int at = __popc(__ballot_sync(0xffffffffu, q >= c));
-      const float above = __shfl_up_sync(0xffffffffu, q, 1);
-      q = lane < at ? q : lane == at ? c : above;
-      least = __shfl_sync(0xffffffffu, q, k - 1);
-    }
-  }
-};
-
-// The k-th largest of all warps' values.
-template <int WARPS>
-__device__ __forceinline__ float block_least(const WarpTop& mine, int k, float (&lists)[WARPS][kTopMost], float* result) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  lists[warp][lane] = mine.q;
-  __syncthreads();
-  if (warp == 0) {
-    WarpTop all;
-    for (int w = 0; w < WARPS; ++w) all.add(lane < k ? lists[w][lane] : minus_inf(), k, lane);
-    if (lane == 0) *result = all.least;
-  }
-  __syncthreads();
-  return *result;
-}
+// sums of 64 bits give.  The row pass has bounded them from below and listed the
+// blocks that may hold one.  The logs (16- or 8-bit distances to the blocks' maxima)
+// bound each logit from both sides, to half a step and the product's rounding, and
+// only entries that may be among the k are multiplied out again:
+//   1. of the listed blocks' entries those whose upper bound reaches the row's, and of
+//      these the ones that reach the k-th largest lower bound: k and a few more;
+//   2. their logits as sums of fp32, with a bound of their error; those that lie
+//      closer to another than both errors again, exact to about 48 bits.
+// A block takes a row.  Up to 1000 rows its latency counts: with 16 warps a call of
+// 300 x 50257 x 768 takes 54 us, with 4 65, of 64 x 128256 x 4096 211 and 232, of
+// 1000 x 128256 x 4096 685 each.  More rows need little of each: 2000 x 50257 x 768 162 us
+// with 16 warps, 146 with 4, 4096 292 and 265 (1 and 2 warps: 266).
+// For 4096 x 50257 x 768 the pass takes 60 us with 20 alternatives and 20 with one: two thirds are the
+// candidates' rows of w, from L2, and their products.
+//
+// More candidates than there is room for (equal or nearly equal logits) are taken
+// kWindow entries at a time; a row of zeros, all of whose logits are equal, is known without.
+constexpr int kWindow = 128;     // candidate entries
+constexpr int64_t kTopFew = 1000;
 
 // a + p without loss: the sum in a, what it rounds away in `lost` (Knuth's two-sum).
 __device__ __forceinline__ void add_exactly(float& a, float& lost, float p) {
@@ -212,24 +288,19 @@ __device__ __forceinline__ void add_exactly(float& a, float& lost, float p) {
   a = s;
 }
 
-// Dot product of two bf16 rows to about 48 bits, the same in every lane.
-__device__ __forceinline__ double warp_dot_exact(const uint16_t* a, const uint16_t* b, int n, int lane) {
+// Dot product of two bf16 rows on 16-byte boundaries to about 48 bits, the same in every lane.
+__device__ __noinline__ double warp_dot_exact(const uint16_t* a, const uint16_t* b, int n, int lane) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
-  int done = 0;
-  if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
-    done = n & ~7;
-#pragma unroll 4
-    for (int c = lane; c < n >> 3; c += 32) {
-      const uint4 p = reinterpret_cast<const uint4*>(a)[c], q = reinterpret_cast<const uint4*>(b)[c];
-      const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
+  for (int c = lane; c < n >> 3; c += 32) {
+    const uint4 p = reinterpret_cast<const uint4*>(a)[c], q = reinterpret_cast<const uint4*>(b)[c];
+    const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        add_exactly(sum[i], lost[i], __fmul_rn(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16)));
-        add_exactly(sum[i], lost[i], __fmul_rn(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u)));
-      }
+    for (int i = 0; i < 4; ++i) {
+      add_exactly(sum[i], lost[i], __fmul_rn(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16)));
+      add_exactly(sum[i], lost[i], __fmul_rn(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u)));
     }
   }
-  for (int c = done + lane; c < n; c += 32) add_exactly(sum[0], lost[0], __fmul_rn(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c])));
+  for (int c = (n & ~7) + lane; c < n; c += 32) add_exactly(sum[0], lost[0], __fmul_rn(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c])));
   double d = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -239,23 +310,93 @@ __device__ __forceinline__ double warp_dot_exact(const uint16_t* a, const uint16
   return warp_sum(d);
 }
 
-template <int WARPS>
+// Sum of each of N values over the warp's lanes; lane l has that of value l % N.
+template <int N>
+__device__ __forceinline__ float sum_values(float (&v)[N], int lane) {
+#pragma unroll
+  for (int d = N / 2; d > 0; d >>= 1) {
+    const bool up = (lane & d) != 0;
+#pragma unroll
+    for (int j = 0; j < d; ++j) {
+      const float keep = up ? v[j + d] : v[j], send = up ? v[j] : v[j + d];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+    }
+  }
+#pragma unroll
+  for (int d = N; d < 32; d <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+  return v[0];
+}
+
+// Dot products of x with N rows of w (all on 16-byte boundaries) in fp32, four chains a lane (64-bit sums of all
+// candidates took a quarter of this kernel's time: an SM adds two a cycle), and the sums of
+// the products' absolute values: no dot product is off by more than a roundoff of that for
+// each step of its longest chain.  Lane l returns those of row l % N.
+struct DotBound {
+  float z, error;
+};
+template <int N>
+__device__ __forceinline__ DotBound warp_dots(const uint16_t* x, const uint16_t* const (&w)[N], int n, int lane) {
+  float sum[N][4], size[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    size[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[r][i] = 0.f;
+  }
+  auto add = [&](int r, int i, float p, float q) {
+    sum[r][i] = fmaf(p, q, sum[r][i]);
+    size[r] = fmaf(fabsf(p), fabsf(q), size[r]);
+  };
+#pragma unroll 2
+  for (int c = lane; c < n >> 3; c += 32) {
+    uint4 q[N];
+    const uint4 p = reinterpret_cast<const uint4*>(x)[c];
+#pragma unroll
+    for (int r = 0; r < N; ++r) q[r] = reinterpret_cast<const uint4*>(w[r])[c];
+    const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const uint32_t v[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        add(r, i, __uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16));
+        add(r, i, __uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u));
+      }
+    }
+  }
+  for (int c = (n & ~7) + lane; c < n; c += 32)
+#pragma unroll
+    for (int r = 0; r < N; ++r) add(r, 0, bf16_bits_to_f32(x[c]), bf16_bits_to_f32(w[r][c]));
+  float z[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) z[r] = (sum[r][0] + sum[r][1]) + (sum[r][2] + sum[r][3]);
+  DotBound d;
+  d.z = sum_values(z, lane);
+  // Two steps for each vector of a lane, one for its last element, seven between chains and lanes.  `size` itself is a sum of at most
+  // four times as many steps; a part in 2^10 more than covers what that may take from it.
+  const int steps = 2 * ((n >> 3) / 32 + 1) + 8;
+  d.error = sum_values(size, lane) * (static_cast<float>(steps) * (0x1p-24f + 0x1p-34f));
+  return d;
+}
+
 struct TopShared {
-  float lists[WARPS][kTopMost];
-  double z[kTopMost + kCandidates];
-  int32_t id[kTopMost + kCandidates];
+  double z[kWindow + kTopMost];     // where some were close: all of them, those exact
+  float near[kWindow + kTopMost], error[kWindow + kTopMost];
+  int32_t id[kWindow + kTopMost];
+  uint8_t again[kWindow + kTopMost], rank[kWindow + kTopMost];
+  float upper[kWindow], lower[kWindow];
+  int32_t entry[kWindow];
   double best_z[kTopMost];
   int32_t best_id[kTopMost];
-  float least;
-  int32_t count;
-  int32_t nonzero;
+  int32_t n_entries, n_ids, close;
 };
 
 template <int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) lp_top_kernel(const LpTop T) {
-  __shared__ TopShared<WARPS> S;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch();
+__global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
+  constexpr int kThreads = 32 * WARPS;
+  constexpr int kDots = 2;                    // candidates that a warp takes at a time
+  __shared__ TopShared S;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, thread = threadIdx.x;
   pdl_wait();
   const int64_t row = blockIdx.x;
   const LpRow R = T.rows_in[row];
@@ -268,97 +409,97 @@ __global__ void __launch_bounds__(WARPS * 32) lp_top_kernel(const LpTop T) {
     if (T.logprobs) T.logprobs[row * k + rank] = logprob;
   };
   // A row that is not scored, or has no distribution (NaN, or infinite logits).
-  const bool ok = isfinite(R.top) && isfinite(R.log_sum);
-  if (!R.scored || !ok) {
-    if (threadIdx.x < k) put(threadIdx.x, -1, R.scored ? __int_as_float(0x7fc00000) : 0.f);
+  if (!R.scored || !isfinite(R.top) || !isfinite(R.log_sum)) {
+    if (thread < k) put(thread, -1, R.scored ? __int_as_float(0x7fc00000) : 0.f);
     return;
   }
-  const float2* stats = T.stats + row;
-  const uint16_t* logs = T.block + row * T.ld_block;
+  const uint8_t* logs = static_cast<const uint8_t*>(T.block) + row * T.ld_block * (T.coarse ? 1 : 2);
   const uint16_t* x = T.x + row * T.ld_x;
-  const float slack = 0x1p-9f + fabsf(R.top) * 0x1p-14f;
-  const int per_lane = (1 << T.stats_shift) / 32;
+  const float slack = logit_slack(R.top);
   auto logprob = [&](double z, int32_t id) {
     return id == R.target ? R.logprob : kLn2 * (static_cast<float>(z * T.logit_scale_log2 - R.top) - R.log_sum);
   };
+  if (thread == 0) S.n_entries = S.n_ids = S.close = 0;
+  __syncthreads();
 
-  // Maxima of the blocks [b0, b1), those at or above `from`, each with a whole warp.
-  auto for_blocks = [&](int b0, int b1, float from, auto&& take) {
-    for (int b = b0 + warp * 32; b < b1; b += WARPS * 32) {
-      const float m = b + lane < b1 ? stats[static_cast<int64_t>(b + lane) * T.stats_ld].x : minus_inf();
-      unsigned more = __ballot_sync(0xffffffffu, b + lane < b1 && m >= from);
-      while (more) {
-        const int at = __ffs(more) - 1;
-        more &= more - 1;
-        take(b + at, __shfl_sync(0xffffffffu, m, at));
-      }
-    }
-  };
-  // Entries of block b, one a lane at a time: number and log; 65535: further off than logs go, or no logit.
-  auto for_entries = [&](int b, auto&& take) {
+  // This lane's logs of a block, all ones (further off than logs go, or none) past the vocabulary.
+  const int per_lane = (1 << T.stats_shift) / 32;
+  auto load_entries = [&](int b) {
     const int c0 = (b << T.stats_shift) + lane * per_lane;
-    uint16_t q[4] = {65535, 65535, 65535, 65535};
+    uint2 w = make_uint2(0xffffffffu, 0xffffffffu);
     if (c0 < T.vocab) {
-      if (per_lane == 4) {
-        const uint2 w = *reinterpret_cast<const uint2*>(logs + c0);
-        q[0] = static_cast<uint16_t>(w.x);
-        q[1] = static_cast<uint16_t>(w.x >> 16);
-        q[2] = static_cast<uint16_t>(w.y);
-        q[3] = static_cast<uint16_t>(w.y >> 16);
+      if (T.coarse)
+        w.x = *reinterpret_cast<const uint32_t*>(logs + c0);
+      else if (per_lane == 4)
+        w = *reinterpret_cast<const uint2*>(logs + 2 * c0);
+      else
+        w.x = *reinterpret_cast<const uint16_t*>(logs + 2 * c0);
+    }
+    return w;
+  };
+  // take(entry, upper and lower bound) for this lane's entries of a block with maximum m whose upper bound reaches the row's.
+  auto for_entries = [&](int b, float m, uint2 w, auto&& take) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= per_lane) break;
+      const int c = (b << T.stats_shift) + lane * per_lane + j;
+      float z, wide;
+      bool far;
+      if (T.coarse) {
+        // Sign, four bits of exponent (bias 7), three of mantissa: as an fp32's, times 2^120; what is below the first exponent stays exact.
+        const uint32_t q = w.x >> (8 * j) & 0x7fu;
+        const float d = __uint_as_float(q << 20) * 0x1p120f;
+        z = m - d;
+        wide = slack + fmaf(d, 0x1p-4f, 0x1p-10f);
+        far = q >= 0x7eu;
       } else {
-        q[0] = logs[c0];
+        const uint32_t q = ((j & 2) ? w.y : w.x) >> (16 * (j & 1)) & 0xffffu;
+        z = m - static_cast<float>(q) * (1.f / kCeLogUnits);
+        wide = slack + 0.5f / kCeLogUnits;
+        far = q == 65535u;
+      }
+      if (z + wide >= R.reached && c < T.vocab && c != R.target) take(c, z + wide, far ? minus_inf() : z - wide);
+    }
+  };
+  // Logits of n candidates, then the first k of them in order: take(rank, z, id).
+  auto in_order = [&](int n, auto&& take) {
+    for (int i = warp * kDots; i < n; i += WARPS * kDots) {
+      const uint16_t* w[kDots];
+#pragma unroll
+      for (int u = 0; u < kDots; ++u) w[u] = T.w + S.id[min(i + u, n - 1)] * T.ld_w;
+      const DotBound d = warp_dots(x, w, T.dim, lane);
+      if (lane < kDots && i + lane < n) {
+        S.near[i + lane] = d.z;
+        S.error[i + lane] = d.error;
       }
     }
-    for (int j = 0; j < per_lane; ++j) take(c0 + j, q[j]);
-  };
-
-  WarpTop maxima;
-  for (int b = warp * 32; b < T.n_blocks; b += WARPS * 32)
-    maxima.add(b + lane < T.n_blocks ? stats[static_cast<int64_t>(b + lane) * T.stats_ld].x : minus_inf(), k, lane);
-  const float from = block_least<WARPS>(maxima, k, S.lists, &S.least) - 2.f * slack;
-
-  WarpTop lower;
-  for_blocks(0, T.n_blocks, from, [&](int b, float m) {
-    for_entries(b, [&](int c, uint16_t q) {
-      const bool in = c < T.vocab && c != R.target && q != 65535;
-      lower.add(in ? m - (static_cast<float>(q) + 0.5f) * (1.f / kCeLogUnits) - slack : minus_inf(), k, lane);
-    });
-  });
-  __syncthreads();  // S.least has been read
-  const float reach = block_least<WARPS>(lower, k, S.lists, &S.least);
-
-  // Candidates of the blocks [b0, b1) into S.id; their number.
-  auto collect = [&](int b0, int b1) {
     __syncthreads();
-    if (threadIdx.x == 0) S.count = 0;
-    __syncthreads();
-    for_blocks(b0, b1, from, [&](int b, float m) {
-      for_entries(b, [&](int c, uint16_t q) {
-        const float upper = m - (static_cast<float>(q) - 0.5f) * (1.f / kCeLogUnits) + slack;
-        if (c < T.vocab && c != R.target && upper >= reach) {
-          const int at = atomicAdd(&S.count, 1);
-          if (at < kCandidates) S.id[at] = c;
-        }
-      });
-    });
-    // The given token's log is not kept.
-    if (threadIdx.x == 0 && R.target >= 0 && R.target >> T.stats_shift >= b0 && R.target >> T.stats_shift < b1) {
-      const int at = atomicAdd(&S.count, 1);
-      if (at < kCandidates) S.id[at] = R.target;
+    for (int i = thread; i < n; i += kThreads) {
+      const float z = S.near[i], e = S.error[i];
+      bool close = !isfinite(z);
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const float other = S.near[j];
+        rank += other > z;
+        close = close || (j != i && fabsf(z - other) <= e + S.error[j]);
+      }
+      S.again[i] = close;
+      S.rank[i] = rank;
+      if (close) S.close = 1;
     }
     __syncthreads();
-    return S.count;
-  };
-  auto multiply = [&](int n) {
+    if (!S.close) {
+      for (int i = thread; i < n; i += kThreads)
+        if (S.rank[i] < k) take(S.rank[i], static_cast<double>(S.near[i]), S.id[i]);
+      return;
+    }
+    // Closer to another than both errors: once more, exact.
     for (int i = warp; i < n; i += WARPS) {
-      const double z = warp_dot_exact(x, T.w + S.id[i] * T.ld_w, T.dim, lane);
+      const double z = S.again[i] ? warp_dot_exact(x, T.w + S.id[i] * T.ld_w, T.dim, lane) : static_cast<double>(S.near[i]);
       if (lane == 0) S.z[i] = z;
     }
     __syncthreads();
-  };
-  // The first k of n in order: take(rank, z, id).
-  auto in_order = [&](int n, auto&& take) {
-    for (int i = threadIdx.x; i < n; i += WARPS * 32) {
+    for (int i = thread; i < n; i += kThreads) {
       const double z = S.z[i];
       const int32_t id = S.id[i];
       int rank = 0;
@@ -367,33 +508,81 @@ __global__ void __launch_bounds__(WARPS * 32) lp_top_kernel(const LpTop T) {
     }
   };
 
-  const int found = collect(0, T.n_blocks);
-  if (found <= kCandidates) {
-    multiply(found);
-    in_order(found, [&](int rank, double z, int32_t id) { put(rank, id, logprob(z, id)); });
-    return;
+  bool fits = R.blocks <= kTopBlocks;
+  if (fits) {
+    constexpr int kLoads = WARPS >= 16 ? 2 : 8;
+    const TopBlock* list = T.top_blocks + row * kTopBlocks;
+    for (int i = warp; i < R.blocks; i += kLoads * WARPS) {
+      TopBlock b[kLoads];
+      uint2 w[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) b[u] = list[min(i + u * WARPS, R.blocks - 1)];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) w[u] = load_entries(b[u].block);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (i + u * WARPS < R.blocks)
+          for_entries(b[u].block, b[u].max, w[u], [&](int c, float upper, float lower) {
+            const int at = atomicAdd(&S.n_entries, 1);
+            if (at < kWindow) {
+              S.entry[at] = c;
+              S.upper[at] = upper;
+              S.lower[at] = lower;
+            }
+          });
+    }
+    __syncthreads();
+    const int n = S.n_entries;
+    fits = n <= kWindow;
+    if (fits) {
+      if (warp == 0) {
+        float v[kWindow / 32];
+#pragma unroll
+        for (int i = 0; i < kWindow / 32; ++i) v[i] = lane + 32 * i < n ? S.lower[lane + 32 * i] : minus_inf();
+        const float reach = reached_by<kWindow / 32>(v, k);
+        int count = R.target >= 0 ? 1 : 0;  // its log is not kept
+        if (R.target >= 0 && lane == 0) S.id[0] = R.target;
+#pragma unroll
+        for (int i = 0; i < kWindow / 32; ++i) {
+          const bool in = lane + 32 * i < n && S.upper[lane + 32 * i] >= reach;
+          const unsigned who = __ballot_sync(0xffffffffu, in);
+          if (in) S.id[count + __popc(who & ((1u << lane) - 1u))] = S.entry[lane + 32 * i];
+          count += __popc(who);
+        }
+        if (lane == 0) S.n_ids = count;
+      }
+      __syncthreads();
+      in_order(S.n_ids, [&](int rank, double z, int32_t id) {
+        pdl_launch();  // not earlier: blocks of a next call's product would wait for this kernel's room (300 x 50257 x 768 54 us for 49)
+        put(rank, id, logprob(z, id));
+      });
+      return;
+    }
   }
-  if (threadIdx.x == 0) S.nonzero = 0;
-  __syncthreads();
   bool any = false;
-  for (int c = threadIdx.x; c < T.dim; c += WARPS * 32) any = any || (x[c] & 0x7fffu) != 0;
-  if (any) S.nonzero = 1;
-  __syncthreads();
-  if (!S.nonzero) {
-    if (threadIdx.x < k) put(threadIdx.x, threadIdx.x, logprob(0.0, threadIdx.x));
+  for (int c = lane; c < T.dim; c += 32) any = any || (x[c] & 0x7fffu) != 0;
+  if (!__any_sync(0xffffffffu, any)) {
+    if (thread < k) put(thread, thread, logprob(0.0, thread));
     return;
   }
   // A few blocks at a time, each joined with the best before it.
-  const int step = kCandidates >> T.stats_shift;
+  const int step = kWindow >> T.stats_shift;
   int best = 0;
   for (int b0 = 0; b0 < T.n_blocks; b0 += step) {
-    const int n = collect(b0, min(b0 + step, T.n_blocks));
-    if (n == 0) continue;
-    multiply(n);
-    if (threadIdx.x < best) {
-      S.z[n + threadIdx.x] = S.best_z[threadIdx.x];
-      S.id[n + threadIdx.x] = S.best_id[threadIdx.x];
+    __syncthreads();
+    if (thread == 0) S.n_ids = S.close = 0;
+    __syncthreads();
+    for (int b = b0 + warp; b < min(b0 + step, T.n_blocks); b += WARPS) {
+      const float m = T.stats[static_cast<int64_t>(b) * T.stats_ld + row].x;
+      if (m + slack < R.reached) continue;
+      for_entries(b, m, load_entries(b), [&](int c, float, float) { S.id[atomicAdd(&S.n_ids, 1)] = c; });
     }
+    if (thread == 0 && R.target >= 0 && R.target >> T.stats_shift >= b0 && R.target >> T.stats_shift < b0 + step)
+      S.id[atomicAdd(&S.n_ids, 1)] = R.target;
+    __syncthreads();
+    const int n = S.n_ids;
+    if (n == 0) continue;
+    if (thread < best) S.id[n + thread] = S.best_id[thread];
     __syncthreads();
     in_order(n + best, [&](int rank, double z, int32_t id) {
       S.best_z[rank] = z;
@@ -402,7 +591,7 @@ __global__ void __launch_bounds__(WARPS * 32) lp_top_kernel(const LpTop T) {
     best = min(k, n + best);
   }
   __syncthreads();
-  if (threadIdx.x < best) put(threadIdx.x, S.best_id[threadIdx.x], logprob(S.best_z[threadIdx.x], S.best_id[threadIdx.x]));
+  if (thread < best) put(thread, S.best_id[thread], logprob(S.best_z[thread], S.best_id[thread]));
 }
 
 // ------------------------------------------------------------------- d logits
@@ -455,15 +644,17 @@ cudaError_t launch_lp_rows(const LpRows& R, cudaStream_t st) {
   const int64_t row_blocks = (R.rows + R.width - 1) / R.width;
   const int64_t copy_blocks = R.x_copy ? (R.rows + kRowWarps - 1) / kRowWarps : 0;
   const bool vec = R.dim % 8 == 0 && R.ld_x % 8 == 0 && (reinterpret_cast<uintptr_t>(R.x) & 15u) == 0;
-  return launch_after(vec ? lp_rows_kernel<true> : lp_rows_kernel<false>, dim3(static_cast<unsigned>(row_blocks + copy_blocks)),
-                      dim3(kRowWarps * 32), 0, st, R, static_cast<int>(row_blocks));
+  // Not before the product has ended: blocks that wait beside it cost it more than
+  // the launch that they save (64 x 128256 x 4096 scores 177 us for 171, 600 x 128256 x 1024 126 for 114).
+  return launch_ordered(false, vec ? lp_rows_kernel<true> : lp_rows_kernel<false>, dim3(static_cast<unsigned>(row_blocks + copy_blocks)),
+                        dim3(kRowWarps * 32), 0, st, R, static_cast<int>(row_blocks));
 }
 
 cudaError_t launch_lp_top(const LpTop& T, cudaStream_t st) {
   if (T.k < 1 || T.k > kTopMost || T.k > T.vocab) return cudaErrorInvalidValue;
-  // Few rows: more warps for each, since only their latency counts.
-  if (T.rows <= 304) return launch_after(lp_top_kernel<32>, dim3(static_cast<unsigned>(T.rows)), dim3(1024), 0, st, T);
-  return launch_after(lp_top_kernel<8>, dim3(static_cast<unsigned>(T.rows)), dim3(256), 0, st, T);
+  const dim3 grid(static_cast<unsigned>(T.rows));
+  if (T.rows <= kTopFew) return launch_after(lp_top_kernel<16>, grid, dim3(512), 0, st, T);
+  return launch_after(lp_top_kernel<4>, grid, dim3(128), 0, st, T);
 }
 
 cudaError_t launch_lp_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_shift,

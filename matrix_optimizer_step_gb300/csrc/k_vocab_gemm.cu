@@ -216,8 +216,16 @@ __device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
 // time of the whole product at 4096 x 50257 x 768.
 // `target`: of this thread's row, -1 for none.  Calls `release` once the last
 // column has left the TMEM.
+// Two distances as 8-bit floats.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
 // ENT: also the sum of 2^(z - m) (z - m), of which the entropy is made; a z of -inf has no part in it.
-template <bool ENT, class Args, class Release>
+// COARSE: VocabLogTop's logs.
+template <bool ENT, bool COARSE, class Args, class Release>
 __device__ __forceinline__ void logits_epilogue(const Args& G, uint32_t t_lane, int row, int target, int col0,
                                                 Release release) {
   const float c = G.logit_scale_log2;
@@ -243,7 +251,8 @@ __device__ __forceinline__ void logits_epilogue(const Args& G, uint32_t t_lane, 
   const float ref = m == minus_inf ? 0.f : m;
   const bool row_ok = row < G.M;
   const int at = target >= 0 ? target - col0 : -1;
-  uint16_t* logs = G.logs && row_ok ? G.logs + static_cast<int64_t>(row) * G.ld_logs + col0 : nullptr;
+  constexpr int kLogBytes = COARSE ? 1 : 2;
+  char* logs = G.logs && row_ok ? reinterpret_cast<char*>(G.logs) + (static_cast<int64_t>(row) * G.ld_logs + col0) * kLogBytes : nullptr;
   const int stored = static_cast<int>(min(static_cast<int64_t>(kCeBlock), G.ld_logs - col0));  // a multiple of 64
   // A distance is rounded to the nearest unit by adding 2^23, whose low
   // mantissa bits then are the integer; past 64 octaves it stays at the largest.
@@ -257,6 +266,7 @@ __device__ __forceinline__ void logits_epilogue(const Args& G, uint32_t t_lane, 
         if (at == 32 * i + j) q[j] = 0xff800000u;  // -inf
     }
     mask_columns(q, col0 + 32 * i, n);
+    uint32_t coarse[8];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       uint32_t w[8];
@@ -271,10 +281,20 @@ __device__ __forceinline__ void logits_epilogue(const Args& G, uint32_t t_lane, 
           t[k & 3] = fmaf(e_lo, fmaxf(lo, kNoLogit), t[k & 3]);
           t[k & 3] = fmaf(e_hi, fmaxf(hi, kNoLogit), t[k & 3]);
         }
-        w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),
-                           __float_as_uint(fminf(fmaf(hi, -kCeLogUnits, magic), most)), 0x5410);
+        if constexpr (COARSE) {
+          const uint32_t two = pack_e4m3x2(-lo, -hi);
+          coarse[4 * p + (k >> 1)] = k & 1 ? __byte_perm(coarse[4 * p + (k >> 1)], two, 0x5410) : two;
+        } else {
+          w[k] = __byte_perm(__float_as_uint(fminf(fmaf(lo, -kCeLogUnits, magic), most)),
+                             __float_as_uint(fminf(fmaf(hi, -kCeLogUnits, magic), most)), 0x5410);
+        }
       }
-      if (logs && 32 * i < stored) st_global_32(logs + 32 * i + 16 * p, w);
+      if constexpr (!COARSE) {
+        if (logs && 32 * i < stored) st_global_32(logs + 64 * i + 32 * p, w);
+      }
+    }
+    if constexpr (COARSE) {
+      if (logs && 32 * i < stored) st_global_32(logs + 32 * i, coarse);
     }
   };
   // The next chunk's load is in flight while one is worked on.
@@ -464,8 +484,8 @@ __device__ __forceinline__ const CUtensorMap* operand_map(const VocabGrad& G, in
 __device__ __forceinline__ bool a_is_mn(const VocabLogits&, int) { return false; }
 __device__ __forceinline__ bool a_is_mn(const VocabGrad& G, int p) { return G.p[p].a_mn != 0; }
 
-// Args: VocabLogits or VocabLogProbs (B is vocabulary x width, K-contiguous), or
-// VocabGrad (B is N-contiguous).
+// Args: VocabLogits, VocabLogProbs or VocabLogTop (B is vocabulary x width,
+// K-contiguous), or VocabGrad (B is N-contiguous).
 template <class Args, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Args G) {
@@ -680,7 +700,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         continue;
       }
       if constexpr (LOGITS) {
-        logits_epilogue<std::is_same<Args, VocabLogProbs>::value>(G, t_lane, warp_row0 + lane, target, col0, release);
+        constexpr bool kCoarse = std::is_same<Args, VocabLogTop>::value;
+        logits_epilogue<kCoarse || std::is_same<Args, VocabLogProbs>::value, kCoarse>(G, t_lane, warp_row0 + lane, target, col0, release);
       } else {
         const VgProduct& P = G.p[T.product];
         uint32_t r[4][32];
@@ -758,6 +779,10 @@ cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t 
 
 cudaError_t launch_vocab_logits(const VocabLogProbs& G, int n_pairs, cudaStream_t st) {
   return launch<VocabLogProbs, false>(G, G.grid.count(), n_pairs, st);
+}
+
+cudaError_t launch_vocab_logits(const VocabLogTop& G, int n_pairs, cudaStream_t st) {
+  return launch<VocabLogTop, false>(G, G.grid.count(), n_pairs, st);
 }
 
 cudaError_t launch_vocab_grad(const VocabGrad& G, int n_pairs, cudaStream_t st) {

@@ -363,7 +363,8 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   // Rows of one pass: what is held for each (its logs, or without gradients and alternatives its
   // statistics) stays within the limit, and tiles are numbered in 32 bits.
   const int64_t ld_block = round_up(v, 64);
-  const int64_t row_bytes = keep_logs ? (halves ? 4 : 2) * ld_block : (P ? 12 : 8) * ((v + kCeBlock - 1) / kCeBlock);
+  const bool thin_logits = thin_logits_pay(n, v, d, keep_logs), coarse = n_top > 0 && !grads && !thin_logits;
+  const int64_t row_bytes = keep_logs ? (halves ? 4 : coarse ? 1 : 2) * ld_block : (P ? 12 : 8) * ((v + kCeBlock - 1) / kCeBlock);
   const int64_t most = std::max<int64_t>(kVgTile, std::min(ctx->tune.ce_block_bytes / row_bytes,
                                                            (int64_t(1) << 30) / tiles_of(v) * kVgTile) / kVgTile * kVgTile);
   int64_t rows = n;
@@ -373,7 +374,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   }
   const bool one_pass = rows >= n;
   const int64_t token_rows = halves ? 2 * rows : rows;
-  const bool thin_logits = thin_logits_pay(n, v, d, keep_logs), thin_x = C.dx && thin_dx(token_rows, v, d);
+  const bool thin_x = C.dx && thin_dx(token_rows, v, d);
   const int stats_shift = thin_logits ? kCeThinShift : kCeShift, stats_block = 1 << stats_shift;
   const bool rows_make_dlogits = !P && halves && ce_rows_make_dlogits(n);
   const int n_blocks = static_cast<int>((v + stats_block - 1) / stats_block);
@@ -399,8 +400,9 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   const size_t off_partial = C.total ? L.take(static_cast<size_t>((n + width - 1) / width) * sizeof(double2)) : 0;
   size_t off_block = 0, off_rows = 0, off_alpha = 0, off_masked = 0, off_dx = 0, off_dw = 0;
   Target dx, dw;
-  if (keep_logs) off_block = L.take(static_cast<size_t>(token_rows * ld_block) * 2);
+  if (keep_logs) off_block = L.take(static_cast<size_t>(token_rows * ld_block) * (coarse ? 1 : 2));
   if (grads || P) off_rows = L.take(static_cast<size_t>(rows) * (P ? sizeof(LpRow) : sizeof(CeRow)));
+  const size_t off_top = n_top > 0 ? L.take(static_cast<size_t>(rows) * kTopBlocks * sizeof(TopBlock)) : 0;
   if (grads) {
     off_alpha = L.take(4);
     bool dx_part = false, dw_part = false;
@@ -515,7 +517,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       if (first) G.norm = norm;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
     } else {
-      VocabLogProbs G = {};
+      VocabLogTop G = {};
       G.M = static_cast<int32_t>(nr);
       G.N = static_cast<int32_t>(v);
       G.grid.set(nr, v, d, 1, kLogitsGroup);
@@ -533,7 +535,9 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       G.weighted = weighted;
       G.drawn = G.grid.kb_total >= kDrawnBlocks;
       DM_TRY(timed_launch(ctx, -1, s, [&] {
-        return P ? launch_vocab_logits(G, pairs, s) : launch_vocab_logits(static_cast<const VocabLogits&>(G), pairs, s);
+        return coarse ? launch_vocab_logits(G, pairs, s)
+               : P    ? launch_vocab_logits(static_cast<const VocabLogProbs&>(G), pairs, s)
+                      : launch_vocab_logits(static_cast<const VocabLogits&>(G), pairs, s);
       }));
     }
 
@@ -564,10 +568,13 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       R.width = width;
       R.counters = counters;
       R.err = err;
+      R.k = n_top;
+      R.top_blocks = reinterpret_cast<TopBlock*>(ws + off_top);
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_rows(R, s); }));
       if (n_top > 0) {
         LpTop T = {};
         T.block = block;
+        T.coarse = coarse;
         T.ld_block = ld_block;
         T.stats = stats;
         T.stats_ld = stats_ld;
@@ -575,6 +582,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
         T.stats_shift = stats_shift;
         T.vocab = static_cast<int32_t>(v);
         T.rows_in = lp_info;
+        T.top_blocks = R.top_blocks;
         T.rows = nr;
         T.x = R.x;
         T.w = w;

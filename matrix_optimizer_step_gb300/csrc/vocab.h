@@ -9,11 +9,8 @@
 
 namespace dmuon {
 
-// Launch that may begin while the kernel before it on the stream ends: every
-// kernel of the vocabulary operators calls pdl_wait before it touches memory,
-// so only its set-up (barriers, TMEM, launch latency) runs early.
 template <class... P, class... A>
-inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+inline cudaError_t launch_ordered(bool early, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -23,8 +20,16 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Launch that may begin while the kernel before it on the stream ends: every
+// kernel of the vocabulary operators calls pdl_wait before it touches memory,
+// so only its set-up (barriers, TMEM, launch latency) runs early.
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  return launch_ordered(true, kernel, grid, block, smem, st, args...);
 }
 
 // One lane of a warp whose lanes are all here, the same one every time.  The
@@ -234,6 +239,12 @@ struct VocabLogProbs : VocabLogits {
 };
 cudaError_t launch_vocab_logits(const VocabLogProbs& G, int n_pairs, cudaStream_t st);
 
+// Where only a row's largest logits are wanted, `logs` holds the distances in octaves as 8-bit
+// floats (e4m3, from 448 on its largest), `ld_logs` bytes a row: they bound a logit to a sixteenth of its distance,
+// which leaves as few candidates as 16 bits do, at half the bytes and fewer instructions.
+struct VocabLogTop : VocabLogProbs {};
+cudaError_t launch_vocab_logits(const VocabLogTop& G, int n_pairs, cudaStream_t st);
+
 // One gradient product D (M x N) = alpha A B: B is k x n with contiguous
 // columns, A is m x k, or k x m with a_mn.
 struct VgProduct {
@@ -353,7 +364,13 @@ cudaError_t launch_ce_finish(const float* part, int64_t ld_part, int64_t part_st
                              int64_t rows, int32_t cols, cudaStream_t st);
 
 // ---- k_logprobs.cu
-constexpr int kTopMost = 32;  // alternatives of a row at most
+constexpr int kTopMost = 32;    // alternatives of a row at most
+constexpr int kTopBlocks = 96;  // vocabulary blocks that may hold one of them, more are looked for again
+
+struct TopBlock {
+  int32_t block;
+  float max;
+};
 
 // A row's distribution, as the passes after the sums read it.  Octaves unless said otherwise.
 struct LpRow {
@@ -363,6 +380,10 @@ struct LpRow {
   float target_dz;     // and of the given token
   int32_t target;      // -1: none
   int32_t scored;
+  // Of the k largest logits none is below `reached`, and none is in another block than the listed ones
+  // (`blocks` of them; above kTopBlocks the list is not whole).
+  float reached;
+  int32_t blocks;
 };
 
 struct LpRows {
@@ -389,16 +410,20 @@ struct LpRows {
   int32_t width;           // rows of a block: ce_rows_width(n)
   uint32_t* counters;      // the products' two tile counters, set to zero
   int* err;
+  int32_t k;               // alternatives wanted, or 0
+  TopBlock* top_blocks;    // of row row0, kTopBlocks a row
 };
 cudaError_t launch_lp_rows(const LpRows& R, cudaStream_t st);
 
 struct LpTop {
-  const uint16_t* block;   // logs of row row0
+  const void* block;       // logs of row row0
+  int32_t coarse;          // VocabLogTop's
   int64_t ld_block;
   const float2* stats;
   int64_t stats_ld;
   int32_t n_blocks, stats_shift, vocab;
   const LpRow* rows_in;
+  const TopBlock* top_blocks;
   int64_t rows;
   const uint16_t* x;       // of row row0
   const uint16_t* w;
