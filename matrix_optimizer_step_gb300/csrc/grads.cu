@@ -127,16 +127,24 @@ int check_list(dmuon_context* ctx, const char* op, const dmuon_grad* gs, int n, 
   return DMUON_OK;
 }
 
-// Elements of a chunk: few enough that small calls reach every SM several times.
-int32_t chunk_elems(const dmuon_grad* gs, int n) {
+// Elements of a chunk, by the number of chunks wanted.
+int32_t chunk_elems(const dmuon_grad* gs, int n, int64_t wanted) {
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += gs[i].numel;
-  const int64_t even = round_up(total / (152 * 16) + 1, 2048);
-  int64_t chunk = std::min<int64_t>(even, 65536);
+  int64_t chunk = std::min<int64_t>(round_up(total / wanted + 1, 2048), 65536);
   // Chunks are numbered in 31 bits.
   while (total / chunk + n >= (int64_t(1) << 30)) chunk *= 2;
   return static_cast<int32_t>(chunk);
 }
+
+// An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 65536 do (their ends are what a
+// small call waits for), then eight.  Scaling: at least four rounds, so that its last one is a small part.
+constexpr int64_t kRound = 152 * 8;
+int32_t norm_chunk(const dmuon_grad* gs, int n) {
+  const int32_t one = chunk_elems(gs, n, std::max<int64_t>(kRound - n, kRound / 8));
+  return one < 65536 ? one : chunk_elems(gs, n, kRound * 8);
+}
+int32_t scale_chunk(const dmuon_grad* gs, int n) { return chunk_elems(gs, n, kRound * 4); }
 
 int64_t chunks_of(const dmuon_grad& g, int32_t chunk) { return (g.numel + chunk - 1) / chunk; }
 
@@ -161,8 +169,10 @@ int norm_launches(dmuon_context* ctx, const dmuon_grad* gs, int n, int32_t chunk
   for (int i = 0; i < std::max(n, 1); i += CAP) {
     GradBatch<CAP> B;
     fill_batch(B, gs + i, std::min(CAP, n - i), chunk);
-    if (B.first[B.n] > 0) DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_grad_squares(B, G, chunk0, s); }));
-    DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_grad_join(B, G, chunk0, i, s); }));
+    const int32_t chunks = B.first[B.n];
+    const bool whole = n <= CAP && chunks > 0 && chunks <= kGradWhole && n <= kGradWholeTensors;
+    if (chunks > 0) DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_grad_squares(B, G, chunk0, whole, s); }));
+    if (!whole) DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_grad_join(B, G, chunk0, i, s); }));
     chunk0 += B.first[B.n];
   }
   return DMUON_OK;
@@ -180,14 +190,14 @@ int scale_launches(dmuon_context* ctx, const dmuon_grad* gs, int n, int32_t chun
 }
 
 int scale_impl(dmuon_context* ctx, const dmuon_grad* gs, int n, const float* coef, cudaStream_t s) {
-  const int32_t chunk = chunk_elems(gs, n);
+  const int32_t chunk = scale_chunk(gs, n);
   return n <= kGradFew ? scale_launches<kGradFew>(ctx, gs, n, chunk, coef, s) : scale_launches<kGradBatch>(ctx, gs, n, chunk, coef, s);
 }
 
 // Norms into the given results; with `scale` the outs too.
 int norm_impl(dmuon_context* ctx, const dmuon_grad* gs, int n, float max_norm, float* norm, float* norms, float* coef, bool scale,
               cudaStream_t s) {
-  const int32_t chunk = chunk_elems(gs, n);
+  const int32_t chunk = norm_chunk(gs, n);
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) chunks += chunks_of(gs[i], chunk);
   const size_t at_squares = static_cast<size_t>(chunks) * sizeof(double), at_coef = at_squares + static_cast<size_t>(n) * sizeof(double);

@@ -33,9 +33,11 @@ struct GradNorm {
   uint32_t* ticket;     // zero before and after
 };
 
-// Sums of squares of a batch's chunks into G.partial + chunk0.
+// Sums of squares of a batch's chunks into G.partial + chunk0; with `whole` (one batch,
+// kGradWhole chunks and kGradWholeTensors tensors at most) the last block joins them too.
+constexpr int kGradWhole = 2048, kGradWholeTensors = kGradBatch;
 template <int CAP>
-cudaError_t launch_grad_squares(const GradBatch<CAP>& B, const GradNorm& G, int64_t chunk0, cudaStream_t st);
+cudaError_t launch_grad_squares(const GradBatch<CAP>& B, const GradNorm& G, int64_t chunk0, bool whole, cudaStream_t st);
 // Joins them: tensors [tensor0, tensor0 + B.n) of the call; the last block of the call's
 // last batch writes what concerns all.
 template <int CAP>

@@ -40,6 +40,26 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return s;
 }
 
+// Whether this is the last of n blocks to get here; what the others wrote before is then visible.
+__device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t n) {
+  __shared__ bool last;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(ticket, 1u) == n - 1u;
+  }
+  __syncthreads();
+  if (last) __threadfence();
+  return last;
+}
+
+// What concerns all tensors, from the sum of all squares; the ticket is handed back.
+__device__ __forceinline__ void put_norm(const GradNorm& G, double squares) {
+  const double norm = sqrt(squares), c = static_cast<double>(G.max_norm) / (norm + 1e-6);
+  if (G.norm) *G.norm = static_cast<float>(norm);
+  if (G.coef) *G.coef = c > 1.0 || isinf(G.max_norm) ? 1.f : static_cast<float>(c);  // NaN stays
+  *G.ticket = 0u;
+}
+
 __device__ __forceinline__ void square(uint32_t pair, float scale, float& a, float& b) {
   const float lo = __uint_as_float(pair << 16) * scale, hi = __uint_as_float(pair & 0xFFFF0000u) * scale;
   a = fmaf(lo, lo, a);
@@ -91,13 +111,27 @@ __device__ __forceinline__ float squares(const void* p, int n, float scale, uint
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// A chunk's sum, a thread's share of it in fp32.  Where it leaves the range in which squares keep their
+// Sum over the block of one fp32 value a thread, in a fixed order, in every thread.  (In 64 bits, of which an
+// SM adds two a cycle, the blocks of a small call spent more time here than on their data.)
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  static_assert(kThreads == 256, "eight warps");
+  return ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+}
+
+// A chunk's sum in fp32.  Where it leaves the range in which squares keep their
 // digits (infinite, or below 2^-80 without all elements being zeros) the chunk is
 // read again with a power of two that brings it back; the result is in 64 bits, so the call's
 // sum neither overflows nor loses small tensors.
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ GradBatch<CAP> B, double* partial) {
-  __shared__ double red[kThreads / 32];
+//
+// WHOLE: few chunks, whose sums the last block joins, which saves a launch.
+template <int CAP, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ GradBatch<CAP> B, const GradNorm G, double* partial) {
+  __shared__ float red[kThreads / 32];
   pdl_launch();
   pdl_wait();
   const int t = tensor_of(B, blockIdx.x);
@@ -106,14 +140,48 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
   const bool bf16 = B.in_bf16[t] != 0;
   const void* p = static_cast<const char*>(B.in[t]) + start * (bf16 ? 2 : 4);
   uint32_t bits = 0;
-  auto sum = [&](float scale) {
-    return block_sum(static_cast<double>(bf16 ? squares<true>(p, n, scale, bits) : squares<false>(p, n, scale, bits)), red);
-  };
-  double s = sum(1.f);
-  const bool large = isinf(s), small = s < 0x1p-80;
+  auto sum = [&](float scale) { return block_sum(bf16 ? squares<true>(p, n, scale, bits) : squares<false>(p, n, scale, bits), red); };
+  const float plain = sum(1.f);
+  double s = plain;
+  const bool large = isinf(plain), small = plain < 0x1p-80f;
   if (large || (small && __syncthreads_or((bits & (bf16 ? 0x7fff7fffu : 0x7fffffffu)) != 0u)))
     s = large ? sum(0x1p-80f) * 0x1p160 : sum(0x1p100f) * 0x1p-200;
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  if constexpr (WHOLE) {
+    __shared__ double all[kGradWhole], of_tensor[kGradWholeTensors];
+    __shared__ int first[kGradWholeTensors + 1];
+    if (!last_block(G.ticket, gridDim.x)) return;
+    for (int c = threadIdx.x; c < static_cast<int>(gridDim.x); c += kThreads) all[c] = __ldcg(partial + c);
+    for (int i = threadIdx.x; i <= B.n; i += kThreads) first[i] = B.first[i];
+    __syncthreads();
+    // A thread a tensor of few chunks, a warp one of many.
+    constexpr int kFew = 8;
+    for (int i = threadIdx.x; i < B.n; i += kThreads) {
+      const int c0 = first[i], c1 = first[i + 1];
+      double q = 0.0;
+      if (c1 - c0 <= kFew)
+        for (int c = c0; c < c1; ++c) q += all[c];
+      of_tensor[i] = q;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < B.n; i += kThreads / 32) {
+      const int c0 = first[i], c1 = first[i + 1];
+      if (c1 - c0 <= kFew) continue;
+      double q = 0.0;
+      for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) q += all[c];
+      q = warp_sum(q);
+      if ((threadIdx.x & 31) == 0) of_tensor[i] = q;
+    }
+    __syncthreads();
+    if (G.norms)
+      for (int i = threadIdx.x; i < B.n; i += kThreads) G.norms[i] = static_cast<float>(sqrt(of_tensor[i]));
+    if (threadIdx.x < 32) {
+      double total = 0.0;
+      for (int i = threadIdx.x; i < B.n; i += 32) total += of_tensor[i];
+      total = warp_sum(total);
+      if (threadIdx.x == 0) put_norm(G, total);
+    }
+  }
 }
 
 // A block a tensor; the last block of the call joins the tensors.
@@ -121,7 +189,6 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads) grad_join_kernel(const __grid_constant__ GradBatch<CAP> B, const GradNorm G,
                                                              int64_t chunk0, int tensor0) {
   __shared__ double red[kThreads / 32];
-  __shared__ bool last;
   pdl_launch();
   pdl_wait();
   const int t = blockIdx.x;
@@ -135,22 +202,11 @@ __global__ void __launch_bounds__(kThreads) grad_join_kernel(const __grid_consta
       if (G.norms) G.norms[tensor0 + t] = static_cast<float>(sqrt(s));
     }
   }
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(G.ticket, 1u) == static_cast<uint32_t>(max(G.n_total, 1)) - 1u;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+  if (!last_block(G.ticket, static_cast<uint32_t>(max(G.n_total, 1)))) return;
   double s = 0.0;
   for (int i = threadIdx.x; i < G.n_total; i += kThreads) s += __ldcg(G.squares + i);
   s = block_sum(s, red);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(s), c = static_cast<double>(G.max_norm) / (norm + 1e-6);
-    if (G.norm) *G.norm = static_cast<float>(norm);
-    if (G.coef) *G.coef = c > 1.0 || isinf(G.max_norm) ? 1.f : static_cast<float>(c);  // NaN stays
-    *G.ticket = 0u;
-  }
+  if (threadIdx.x == 0) put_norm(G, s);
 }
 
 template <bool IN_BF16, bool OUT_BF16>
@@ -230,8 +286,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
 }  // namespace
 
 template <int CAP>
-cudaError_t launch_grad_squares(const GradBatch<CAP>& B, const GradNorm& G, int64_t chunk0, cudaStream_t st) {
-  return launch_after(grad_squares_kernel<CAP>, dim3(static_cast<unsigned>(B.first[B.n])), dim3(kThreads), 0, st, B, G.partial + chunk0);
+cudaError_t launch_grad_squares(const GradBatch<CAP>& B, const GradNorm& G, int64_t chunk0, bool whole, cudaStream_t st) {
+  if (whole && B.first[B.n] > kGradWhole) return cudaErrorInvalidValue;
+  return launch_after(whole ? grad_squares_kernel<CAP, true> : grad_squares_kernel<CAP, false>, dim3(static_cast<unsigned>(B.first[B.n])),
+                      dim3(kThreads), 0, st, B, G, G.partial + chunk0);
 }
 
 template <int CAP>
@@ -244,8 +302,8 @@ cudaError_t launch_grad_scale(const GradBatch<CAP>& B, const float* coef, cudaSt
   return launch_after(grad_scale_kernel<CAP>, dim3(static_cast<unsigned>(B.first[B.n])), dim3(kThreads), 0, st, B, coef);
 }
 
-template cudaError_t launch_grad_squares(const GradBatch<kGradFew>&, const GradNorm&, int64_t, cudaStream_t);
-template cudaError_t launch_grad_squares(const GradBatch<kGradBatch>&, const GradNorm&, int64_t, cudaStream_t);
+template cudaError_t launch_grad_squares(const GradBatch<kGradFew>&, const GradNorm&, int64_t, bool, cudaStream_t);
+template cudaError_t launch_grad_squares(const GradBatch<kGradBatch>&, const GradNorm&, int64_t, bool, cudaStream_t);
 template cudaError_t launch_grad_join(const GradBatch<kGradFew>&, const GradNorm&, int64_t, int, cudaStream_t);
 template cudaError_t launch_grad_join(const GradBatch<kGradBatch>&, const GradNorm&, int64_t, int, cudaStream_t);
 template cudaError_t launch_grad_scale(const GradBatch<kGradFew>&, const float*, cudaStream_t);

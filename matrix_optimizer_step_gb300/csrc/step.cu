@@ -381,12 +381,17 @@ int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr,
   AdamPlan& A = ctx->adam;
   if (key != A.key) {
     A.release();
+    // Small lists in shorter chunks, so that the blocks' last round is a small part of all (a chunk's
+    // length changes no element): 4e7 elements 195 us with 65536, 170 with 8192.
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += ts[i].numel;
+    const int64_t chunk = std::max<int64_t>(2048, std::min<int64_t>(kChunkElems, round_up(total / (152 * 32) + 1, 2048)));
     for (int i = 0; i < n; ++i)
-      for (int64_t e = 0; e < ts[i].numel; e += kChunkElems) {
+      for (int64_t e = 0; e < ts[i].numel; e += chunk) {
         Chunk ch;
         ch.slice = i;
         ch.start = e;
-        ch.count = static_cast<int32_t>(std::min<int64_t>(kChunkElems, ts[i].numel - e));
+        ch.count = static_cast<int32_t>(std::min<int64_t>(chunk, ts[i].numel - e));
         A.chunks.push_back(ch);
       }
     if (A.chunks.size() > size_t(INT32_MAX)) return set_error(DMUON_ERR_SHAPE, "too many chunks");
