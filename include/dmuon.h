@@ -340,7 +340,7 @@ DMUON_API int dmuon_adamw_step_scaled(dmuon_context* ctx, const dmuon_vector* ts
  * In place with a factor of exactly 1 nothing is written.
  * Uses the vocabulary operators' scratch (below): the same holds for streams,
  * host threads and captured graphs.  Errors: DMUON_ERR_INVALID_ARG (null or
- * overlapping memory, no output, bad max_norm), DMUON_ERR_SHAPE (numel),
+ * overlapping memory, no output, bad max_norm), DMUON_ERR_SHAPE (numel, n above 2^24),
  * DMUON_ERR_DTYPE, DMUON_ERR_NOMEM, DMUON_ERR_CUDA, DMUON_ERR_UNSUPPORTED.
  */
 typedef struct dmuon_grad {

@@ -364,7 +364,8 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   // statistics) stays within the limit, and tiles are numbered in 32 bits.
   const int64_t ld_block = round_up(v, 64);
   const bool thin_logits = thin_logits_pay(n, v, d, keep_logs), coarse = n_top > 0 && !grads && !thin_logits;
-  const int64_t row_bytes = keep_logs ? (halves ? 4 : coarse ? 1 : 2) * ld_block : (P ? 12 : 8) * ((v + kCeBlock - 1) / kCeBlock);
+  const int64_t row_bytes = (keep_logs ? (halves ? 4 : coarse ? 1 : 2) * ld_block : (P ? 12 : 8) * ((v + kCeBlock - 1) / kCeBlock)) +
+                            (n_top > 0 ? static_cast<int64_t>(kTopBlocks * sizeof(TopBlock)) : 0);
   const int64_t most = std::max<int64_t>(kVgTile, std::min(ctx->tune.ce_block_bytes / row_bytes,
                                                            (int64_t(1) << 30) / tiles_of(v) * kVgTile) / kVgTile * kVgTile);
   int64_t rows = n;

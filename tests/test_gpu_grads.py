@@ -1,8 +1,9 @@
 """Gradient norms, clipping and the clipped step on the GPU.
 
-Tolerances.  A thread adds up to 512 squares (of chunks as the sizes here make them), four chains, each addition and
-product off by 2^-24 of the running sum at most, and the rest is added in 64 bits: a sum of squares is within 130 * 2 * 2^-24
-of itself, its root within half of that, and the result is rounded once.  A scaled value is the rounded product of
+Tolerances.  A thread adds up to 512 squares (of chunks as the sizes here make them) in four chains of fused steps, 128
+each, and a block's threads are joined in ten more additions; each step is off by 2^-24 of the running sum at most, and the
+rest is added in 64 bits: a sum of squares is within 2 * 130 * 2^-24 of itself, its root within half of that, and the
+result is rounded once.  A scaled value is the rounded product of
 the factor (its own error: the norm's, and one rounding) and the gradient, 2^-24, then rounded to its type."""
 
 import math

@@ -63,7 +63,7 @@ GRAD_BAD = [
     (INV, dict(grad=None), {}), (INV, dict(out=None), {}),
     (INV, dict(grad=BASE + 0x10001, out=BASE + 0x10001), {}), (INV, dict(out=BASE + 0x50001), {}),
     (INV, {}, dict(max_norm=0.0)), (INV, {}, dict(max_norm=-1.0)), (INV, {}, dict(max_norm=float("nan"))),
-    (INV, {}, dict(n=-1)), (INV, {}, dict(array=None)),
+    (INV, {}, dict(n=-1)), (INV, {}, dict(array=None)), ("ERR_SHAPE", {}, dict(n=(1 << 24) + 1)),
 ]
 
 
