@@ -14,43 +14,7 @@ namespace {
 
 __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
 
-// ------------------------------------------------------------------- row sums
-// Joins a row's blocks, each with its maximum m_b, its sum s_b of 2^(z - m_b)
-// and its sum t_b of 2^(z - m_b) (z - m_b), octaves, without the given token's:
-//   M = max m_b,  S = sum_b s_b 2^(m_b - M),  T = sum_b 2^(m_b - M) (t_b + s_b (m_b - M)).
-// With the given token's logit z_t, summed here in 64 bits as in the cross
-// entropy, and o = 2^(z_t - M):
-//   ln p_t  = ln(o / (S + o)),
-//   entropy = ln 2 (log2(S + o) - (T + o (z_t - M)) / (S + o)),
-// where every term of the second is positive but for the rounding of M, so that
-// nothing cancels.  A token that holds more than half is the reference itself:
-//   ln p_t = -log1p(S / o),  entropy = log1p(S / o) - ln 2 (T - S (z_t - M)) / (S + o),
-// and both keep their digits however certain it is.  Blocks, widths and the
-// copy of dW's operand are as in ce_rows_kernel.
-//
-// Where a row's k largest logits are wanted, the same pass bounds them: a value T that
-// k of 256 groups of blocks reach with their maxima, found by bisection.  k entries
-// lie there or above, so only blocks that reach T (k and a few more, listed
-// for lp_top_kernel) hold one.  The maxima carry the product's rounding, for which
-// 2^-9 octaves and 2^-14 of the row's maximum are allowed.
-struct Sums {
-  float m, s, t;
-};
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  if (r.m == minus_inf()) {  // nothing yet, or NaN
-    r.s = a.s + b.s;
-    r.t = a.t + b.t;
-    return r;
-  }
-  const float da = fmaxf(a.m - r.m, kNoLogit), db = fmaxf(b.m - r.m, kNoLogit);
-  const float fa = exp2f(da), fb = exp2f(db);
-  r.s = a.s * fa + b.s * fb;
-  r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
-  return r;
-}
-
+// What the product's rounding may do to a logit, in octaves.
 __device__ __forceinline__ float logit_slack(float top) { return 0x1p-9f + fabsf(top) * 0x1p-14f; }
 
 // A value that at least k of the warp's values reach (PER of them a lane) and, unless
@@ -88,175 +52,6 @@ __device__ __forceinline__ float reached_by(const float (&v)[PER], int k) {
     }
   }
   return at;
-}
-
-constexpr int kGroups = 256;
-
-template <bool VEC>
-__global__ void __launch_bounds__(kRowWarps * 32) lp_rows_kernel(const LpRows R, int row_blocks) {
-  __shared__ Sums part[kRowWarps][8];
-  __shared__ double dots[kRowWarps];
-  __shared__ float groups[8][kGroups + 1], reached[8], slack[8];
-  __shared__ int found[8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = R.width;
-  pdl_launch();
-  pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= row_blocks) {
-    const int64_t warps = static_cast<int64_t>(gridDim.x - row_blocks) * kRowWarps;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x - row_blocks) * kRowWarps + warp; r < R.rows; r += warps) {
-      bool bad = false;
-      const bool keep = !R.tokens.p || load_id(R.tokens, R.row0 + r, &bad) >= 0;
-      for (int k = 0; k < R.copies; ++k)
-        copy_row<VEC>(R.x + r * R.ld_x, R.x_copy + (r + k * R.rows) * R.ld_copy, R.dim, static_cast<int>(R.ld_copy), keep, lane);
-    }
-    return;
-  }
-  if (blockIdx.x == 0 && threadIdx.x < 2) R.counters[threadIdx.x] = 0u;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * width;
-  const int shares = kRowWarps / width;
-  const int64_t dot_row = base + warp / shares;
-  bool bad = false;
-  const int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
-  Sums sum = {minus_inf(), 0.f, 0.f};
-  const int64_t own_row = base + (lane & (width - 1));
-  const int per_warp = 32 / width, stride = kRowWarps * per_warp;
-  const int first_block = warp * per_warp + lane / width;
-  float group[8];  // maxima of the blocks that are first, second, ... of eight
-#pragma unroll
-  for (int k = 0; k < 8; ++k) group[k] = minus_inf();
-  if (own_row < R.rows) {
-    for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
-      Sums q[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row;
-        const bool in = b + k * stride < R.n_blocks;
-        const float2 ms = in ? R.stats[at] : make_float2(minus_inf(), 0.f);
-        q[k] = Sums{ms.x, ms.y, in ? R.weighted[at] : 0.f};
-        group[k] = fmaxf(group[k], ms.x);
-      }
-      // The eight against their common maximum.
-      Sums eight = {q[0].m, 0.f, 0.f};
-#pragma unroll
-      for (int k = 1; k < 8; ++k) eight.m = fmaxf(eight.m, q[k].m);
-      const float ref = eight.m == minus_inf() ? 0.f : eight.m;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = fmaxf(q[k].m - ref, kNoLogit), f = exp2f(d);
-        eight.s += f * q[k].s;
-        eight.t += f * fmaf(q[k].s, d, q[k].t);
-      }
-      sum = join(sum, eight);
-    }
-  }
-  for (int o = width; o < 32; o <<= 1) {
-    Sums other;
-    other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
-    other.s = __shfl_xor_sync(0xffffffffu, sum.s, o);
-    other.t = __shfl_xor_sync(0xffffffffu, sum.t, o);
-    // Both lanes join in the same order.
-    sum = lane & o ? join(other, sum) : join(sum, other);
-  }
-  if (lane < width) part[warp][lane] = sum;
-  if (R.k > 0) {
-    // Eight, four or one group of this thread: 256 of a row.
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-      if (o >= width)
-#pragma unroll
-        for (int k = 0; k < o; ++k) group[k] = fmaxf(group[k], group[k + o]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < width) groups[lane & (width - 1)][(first_block * width + k)] = group[k];
-    if (threadIdx.x < 8) found[threadIdx.x] = 0;
-  }
-  if (dot_target >= 0) {
-    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
-    if (lane == 0) dots[warp] = d;
-  }
-  __syncthreads();
-  if (R.k > 0) {
-    if (warp < width) {
-      float g[kGroups / 32];
-#pragma unroll
-      for (int i = 0; i < kGroups / 32; ++i) g[i] = groups[warp][lane + 32 * i];
-      float top = g[0];
-#pragma unroll
-      for (int i = 1; i < kGroups / 32; ++i) top = fmaxf(top, g[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float at = reached_by<kGroups / 32>(g, R.k), off = logit_slack(top);
-      if (lane == 0) {
-        reached[warp] = at - off;
-        slack[warp] = off;
-      }
-    }
-    __syncthreads();
-    if (own_row < R.rows) {
-      const float from = reached[lane & (width - 1)], off = slack[lane & (width - 1)];
-      for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
-        float m[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          m[k] = b + k * stride < R.n_blocks ? R.stats[static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row].x : minus_inf();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (b + k * stride >= R.n_blocks || m[k] + off < from) continue;
-          const int at = atomicAdd(&found[lane & (width - 1)], 1);
-          if (at < kTopBlocks) R.top_blocks[own_row * kTopBlocks + at] = TopBlock{b + k * stride, m[k]};
-        }
-      }
-    }
-    __syncthreads();
-  }
-  const int64_t r = base + lane;
-  if (warp != 0 || lane >= width || r >= R.rows) return;
-  Sums all = part[0][lane];
-#pragma unroll
-  for (int w = 1; w < kRowWarps; ++w) all = join(all, part[w][lane]);
-  const int64_t i = R.row0 + r;
-  const int t = R.tokens.p ? load_id(R.tokens, i, &bad) : -1;
-  if (bad) atomicCAS(R.err, 0, kErrBadIndex);
-  LpRow o = {};
-  if (R.k > 0) {
-    o.reached = reached[lane];
-    o.blocks = found[lane];
-  }
-  o.target = t;
-  o.scored = !R.tokens.p || t >= 0;
-  float lse = 0.f, entropy = 0.f;
-  if (o.scored) {
-    float own = 0.f, dz = kNoLogit;
-    if (t >= 0) {
-      double z = 0.0;
-      for (int k = 0; k < shares; ++k) z += dots[lane * shares + k];
-      dz = static_cast<float>(z * R.logit_scale_log2 - all.m);
-      own = exp2f(dz);
-    }
-    const float whole = all.s + own;
-    o.top = all.m;
-    o.log_sum = log2f(whole);
-    lse = kLn2 * (all.m + o.log_sum);
-    if (own > all.s) {
-      o.logprob = -log1pf(all.s / own);
-      entropy = -o.logprob - kLn2 * fmaf(-all.s, dz, all.t) / whole;
-    } else {
-      o.logprob = t >= 0 ? kLn2 * (dz - o.log_sum) : 0.f;
-      entropy = kLn2 * (o.log_sum - fmaf(own, fmaxf(dz, kNoLogit), all.t) / whole);
-    }
-    const float g = R.dlogprobs ? R.dlogprobs[i] : 0.f, h = R.dentropy ? R.dentropy[i] : 0.f;
-    o.a = fmaf(h, entropy, g);
-    o.b = kLn2 * h;
-    const float p = own / whole;
-    o.target_dz = g * (all.s / whole);
-    // Of a token with no probability p ln p is 0.
-    if (h != 0.f) o.target_dz -= p > 0.f ? h * p * (o.logprob + entropy) : 0.f;
-    if (g == 0.f && h == 0.f) o.a = o.b = o.target_dz = 0.f;
-  }
-  if (R.logprobs) R.logprobs[i] = o.logprob;
-  if (R.lse) R.lse[i] = lse;
-  if (R.entropy) R.entropy[i] = entropy;
-  R.out[r] = o;
 }
 
 // ---------------------------------------------------------- most likely entries
@@ -347,7 +142,8 @@ __device__ __forceinline__ DotBound warp_dots(const uint16_t* x, const uint16_t*
     sum[r][i] = fmaf(p, q, sum[r][i]);
     size[r] = fmaf(fabsf(p), fabsf(q), size[r]);
   };
-#pragma unroll 2
+  constexpr int kAhead = N > 1 ? 2 : 8;
+#pragma unroll kAhead
   for (int c = lane; c < n >> 3; c += 32) {
     uint4 q[N];
     const uint4 p = reinterpret_cast<const uint4*>(x)[c];
@@ -391,15 +187,12 @@ struct TopShared {
   int32_t n_entries, n_ids, close;
 };
 
+// By all WARPS of the block; `list`: the row's listed blocks, in either memory.
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
+__device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const LpRow& R, const TopBlock* list, TopShared& S) {
   constexpr int kThreads = 32 * WARPS;
-  constexpr int kDots = 2;                    // candidates that a warp takes at a time
-  __shared__ TopShared S;
+  constexpr int kDots = WARPS >= 16 ? 1 : 2;  // candidates that a warp takes at a time
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, thread = threadIdx.x;
-  pdl_wait();
-  const int64_t row = blockIdx.x;
-  const LpRow R = T.rows_in[row];
   const int k = T.k;
   auto put = [&](int rank, int32_t id, float logprob) {
     if (T.ids64)
@@ -511,7 +304,6 @@ __global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
   bool fits = R.blocks <= kTopBlocks;
   if (fits) {
     constexpr int kLoads = WARPS >= 16 ? 2 : 8;
-    const TopBlock* list = T.top_blocks + row * kTopBlocks;
     for (int i = warp; i < R.blocks; i += kLoads * WARPS) {
       TopBlock b[kLoads];
       uint2 w[kLoads];
@@ -594,6 +386,248 @@ __global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
   if (thread < best) put(thread, S.best_id[thread], logprob(S.best_z[thread], S.best_id[thread]));
 }
 
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
+  __shared__ TopShared S;
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const LpRow R = T.rows_in[row];
+  top_of_row<WARPS>(T, row, R, T.top_blocks + row * kTopBlocks, S);
+}
+
+// ------------------------------------------------------------------- row sums
+// Joins a row's blocks, each with its maximum m_b, its sum s_b of 2^(z - m_b)
+// and its sum t_b of 2^(z - m_b) (z - m_b), octaves, without the given token's:
+//   M = max m_b,  S = sum_b s_b 2^(m_b - M),  T = sum_b 2^(m_b - M) (t_b + s_b (m_b - M)).
+// With the given token's logit z_t, summed here in 64 bits as in the cross
+// entropy, and o = 2^(z_t - M):
+//   ln p_t  = ln(o / (S + o)),
+//   entropy = ln 2 (log2(S + o) - (T + o (z_t - M)) / (S + o)),
+// where every term of the second is positive but for the rounding of M, so that
+// nothing cancels.  A token that holds more than half is the reference itself:
+//   ln p_t = -log1p(S / o),  entropy = log1p(S / o) - ln 2 (T - S (z_t - M)) / (S + o),
+// and both keep their digits however certain it is.  Blocks, widths and the
+// copy of dW's operand are as in ce_rows_kernel.
+//
+// Where a row's k largest logits are wanted, the same pass bounds them: a value T that
+// k of 256 groups of blocks reach with their maxima, found by bisection.  k entries
+// lie there or above, so only blocks that reach T (k and a few more, listed
+// for lp_top_kernel) hold one.  The maxima carry the product's rounding, for which
+// 2^-9 octaves and 2^-14 of the row's maximum are allowed.
+struct Sums {
+  float m, s, t;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+  Sums r;
+  r.m = fmaxf(a.m, b.m);
+  if (r.m == minus_inf()) {  // nothing yet, or NaN
+    r.s = a.s + b.s;
+    r.t = a.t + b.t;
+    return r;
+  }
+  const float da = fmaxf(a.m - r.m, kNoLogit), db = fmaxf(b.m - r.m, kNoLogit);
+  const float fa = exp2f(da), fb = exp2f(db);
+  r.s = a.s * fa + b.s * fb;
+  r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
+  return r;
+}
+
+// Joined over lanes `step`, 2 step, ... 16 apart; both lanes of a pair join in the same order.
+__device__ __forceinline__ Sums join_lanes(Sums sum, int step, int lane) {
+  for (int o = step; o < 32; o <<= 1) {
+    Sums other;
+    other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
+    other.s = __shfl_xor_sync(0xffffffffu, sum.s, o);
+    other.t = __shfl_xor_sync(0xffffffffu, sum.t, o);
+    sum = lane & o ? join(other, sum) : join(sum, other);
+  }
+  return sum;
+}
+
+// Few rows: 16 warps a row (WARPS), and where alternatives are wanted (TOP) the block goes on
+// to them, without a launch and a way through memory.
+template <bool VEC, int WARPS, bool TOP>
+__global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, const LpTop T, int row_blocks) {
+  constexpr int kGroups = 32 * WARPS, kWidth = WARPS > kRowWarps ? 1 : 8;  // groups of a row, and rows at most
+  __shared__ Sums part[WARPS][kWidth];
+  __shared__ double dots[WARPS];
+  __shared__ float groups[kWidth][kGroups + 1], reached[kWidth], slack[kWidth];
+  __shared__ int found[kWidth];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = kWidth == 1 ? 1 : R.width;
+  if (!TOP) pdl_launch();  // else with the last of it
+  pdl_wait();
+  if (static_cast<int>(blockIdx.x) >= row_blocks) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x - row_blocks) * WARPS;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x - row_blocks) * WARPS + warp; r < R.rows; r += warps) {
+      bool bad = false;
+      const bool keep = !R.tokens.p || load_id(R.tokens, R.row0 + r, &bad) >= 0;
+      for (int k = 0; k < R.copies; ++k)
+        copy_row<VEC>(R.x + r * R.ld_x, R.x_copy + (r + k * R.rows) * R.ld_copy, R.dim, static_cast<int>(R.ld_copy), keep, lane);
+    }
+    return;
+  }
+  // The candidate blocks go to memory, or with TOP stay here.
+  __shared__ TopBlock here[TOP ? kTopBlocks : 1];
+  TopBlock* const list = TOP ? here : R.top_blocks;
+  const int64_t list_rows = TOP ? 0 : kTopBlocks;
+  if (blockIdx.x == 0 && threadIdx.x < 2) R.counters[threadIdx.x] = 0u;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * width;
+  const int shares = WARPS / width;
+  const int64_t dot_row = base + warp / shares;
+  bool bad = false;
+  const int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
+  Sums sum = {minus_inf(), 0.f, 0.f};
+  const int64_t own_row = base + (lane & (width - 1));
+  const int per_warp = 32 / width, stride = WARPS * per_warp;
+  const int first_block = warp * per_warp + lane / width;
+  float group[8];  // maxima of the blocks that are first, second, ... of eight
+#pragma unroll
+  for (int k = 0; k < 8; ++k) group[k] = minus_inf();
+  Sums q[8];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row;
+      const bool in = own_row < R.rows && b + k * stride < R.n_blocks;
+      const float2 ms = in ? R.stats[at] : make_float2(minus_inf(), 0.f);
+      q[k] = Sums{ms.x, ms.y, in ? R.weighted[at] : 0.f};
+    }
+  };
+  load(first_block);  // under way while the given token's logit is summed
+  if (dot_target >= 0) {
+    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
+    if (lane == 0) dots[warp] = d;
+  }
+  if (own_row < R.rows) {
+    for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
+      if (b != first_block) load(b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) group[k] = fmaxf(group[k], q[k].m);
+      // The eight against their common maximum.
+      Sums eight = {q[0].m, 0.f, 0.f};
+#pragma unroll
+      for (int k = 1; k < 8; ++k) eight.m = fmaxf(eight.m, q[k].m);
+      const float ref = eight.m == minus_inf() ? 0.f : eight.m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = fmaxf(q[k].m - ref, kNoLogit), f = exp2f(d);
+        eight.s += f * q[k].s;
+        eight.t += f * fmaf(q[k].s, d, q[k].t);
+      }
+      sum = join(sum, eight);
+    }
+  }
+  sum = join_lanes(sum, width, lane);
+  if (lane < width) part[warp][lane] = sum;
+  if (R.k > 0) {
+    // Eight, four or one group of this thread: as many of a row as the block has threads.
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      if (o >= width)
+#pragma unroll
+        for (int k = 0; k < o; ++k) group[k] = fmaxf(group[k], group[k + o]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < kWidth && k < width) groups[lane & (width - 1)][(first_block * width + k)] = group[k];
+    if (threadIdx.x < kWidth) found[threadIdx.x] = 0;
+  }
+  __syncthreads();
+  if (R.k > 0) {
+    if (warp < width) {
+      float g[kGroups / 32];
+#pragma unroll
+      for (int i = 0; i < kGroups / 32; ++i) g[i] = groups[warp][lane + 32 * i];
+      float top = g[0];
+#pragma unroll
+      for (int i = 1; i < kGroups / 32; ++i) top = fmaxf(top, g[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float at = reached_by<kGroups / 32>(g, R.k), off = logit_slack(top);
+      if (lane == 0) {
+        reached[warp] = at - off;
+        slack[warp] = off;
+      }
+    }
+    __syncthreads();
+    if (own_row < R.rows) {
+      const float from = reached[lane & (width - 1)], off = slack[lane & (width - 1)];
+      for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
+        float m[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          m[k] = b + k * stride < R.n_blocks ? R.stats[static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row].x : minus_inf();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (b + k * stride >= R.n_blocks || m[k] + off < from) continue;
+          const int at = atomicAdd(&found[lane & (width - 1)], 1);
+          if (at < kTopBlocks) list[own_row * list_rows + at] = TopBlock{b + k * stride, m[k]};
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t r = base + lane;
+  __shared__ LpRow info;
+  auto finish = [&](const Sums& all) {
+    const int64_t i = R.row0 + r;
+    const int t = R.tokens.p ? load_id(R.tokens, i, &bad) : -1;
+    if (bad) atomicCAS(R.err, 0, kErrBadIndex);
+    LpRow o = {};
+    if (R.k > 0) {
+      o.reached = reached[lane];
+      o.blocks = found[lane];
+    }
+    o.target = t;
+    o.scored = !R.tokens.p || t >= 0;
+    float lse = 0.f, entropy = 0.f;
+    if (o.scored) {
+      float own = 0.f, dz = kNoLogit;
+      if (t >= 0) {
+        double z = 0.0;
+        for (int k = 0; k < shares; ++k) z += dots[lane * shares + k];
+        dz = static_cast<float>(z * R.logit_scale_log2 - all.m);
+        own = exp2f(dz);
+      }
+      const float whole = all.s + own;
+      o.top = all.m;
+      o.log_sum = log2f(whole);
+      lse = kLn2 * (all.m + o.log_sum);
+      if (own > all.s) {
+        o.logprob = -log1pf(all.s / own);
+        entropy = -o.logprob - kLn2 * fmaf(-all.s, dz, all.t) / whole;
+      } else {
+        o.logprob = t >= 0 ? kLn2 * (dz - o.log_sum) : 0.f;
+        entropy = kLn2 * (o.log_sum - fmaf(own, fmaxf(dz, kNoLogit), all.t) / whole);
+      }
+      const float g = R.dlogprobs ? R.dlogprobs[i] : 0.f, h = R.dentropy ? R.dentropy[i] : 0.f;
+      o.a = fmaf(h, entropy, g);
+      o.b = kLn2 * h;
+      const float p = own / whole;
+      o.target_dz = g * (all.s / whole);
+      // Of a token with no probability p ln p is 0.
+      if (h != 0.f) o.target_dz -= p > 0.f ? h * p * (o.logprob + entropy) : 0.f;
+      if (g == 0.f && h == 0.f) o.a = o.b = o.target_dz = 0.f;
+    }
+    if (R.logprobs) R.logprobs[i] = o.logprob;
+    if (R.lse) R.lse[i] = lse;
+    if (R.entropy) R.entropy[i] = entropy;
+    if (TOP) info = o;
+    R.out[r] = o;
+  };
+  if (warp == 0) {
+    Sums all = {minus_inf(), 0.f, 0.f};
+    for (int w = lane / width; w < WARPS; w += 32 / width) all = join(all, part[w][lane & (width - 1)]);
+    all = join_lanes(all, width, lane);
+    if (lane < width && r < R.rows) finish(all);
+  }
+  if constexpr (TOP) {
+    __shared__ TopShared S;
+    __syncthreads();
+    const LpRow o = info;
+    top_of_row<WARPS>(T, base, o, here, S);
+  }
+}
+
 // ------------------------------------------------------------------- d logits
 //   dz_v = g ([v = t] - p_v) - h p_v (ln p_v + H) = g [v = t] - p_v (a + b log2 p_v)
 // with a = g + h H and b = h ln 2; the given token's comes from the row pass.
@@ -640,14 +674,21 @@ __global__ void __launch_bounds__(kDlThreads) lp_dlogits_kernel(uint16_t* block,
 
 }  // namespace
 
-cudaError_t launch_lp_rows(const LpRows& R, cudaStream_t st) {
+cudaError_t launch_lp_rows(const LpRows& R, const LpTop& T, bool* top_done, cudaStream_t st) {
+  const bool few = R.width == 1 && R.rows <= kTopFew, top = few && T.k > 0;
+  *top_done = top;
+  if (T.k < 0 || T.k > kTopMost || T.k > T.vocab) return cudaErrorInvalidValue;
+  const int warps = few ? 16 : kRowWarps;
   const int64_t row_blocks = (R.rows + R.width - 1) / R.width;
-  const int64_t copy_blocks = R.x_copy ? (R.rows + kRowWarps - 1) / kRowWarps : 0;
+  const int64_t copy_blocks = R.x_copy ? (R.rows + warps - 1) / warps : 0;
   const bool vec = R.dim % 8 == 0 && R.ld_x % 8 == 0 && (reinterpret_cast<uintptr_t>(R.x) & 15u) == 0;
+  auto kernel = top   ? (vec ? lp_rows_kernel<true, 16, true> : lp_rows_kernel<false, 16, true>)
+                : few ? (vec ? lp_rows_kernel<true, 16, false> : lp_rows_kernel<false, 16, false>)
+                      : (vec ? lp_rows_kernel<true, kRowWarps, false> : lp_rows_kernel<false, kRowWarps, false>);
   // Not before the product has ended: blocks that wait beside it cost it more than
   // the launch that they save (64 x 128256 x 4096 scores 177 us for 171, 600 x 128256 x 1024 126 for 114).
-  return launch_ordered(false, vec ? lp_rows_kernel<true> : lp_rows_kernel<false>, dim3(static_cast<unsigned>(row_blocks + copy_blocks)),
-                        dim3(kRowWarps * 32), 0, st, R, static_cast<int>(row_blocks));
+  return launch_ordered(false, kernel, dim3(static_cast<unsigned>(row_blocks + copy_blocks)), dim3(32 * warps), 0, st, R, T,
+                        static_cast<int>(row_blocks));
 }
 
 cudaError_t launch_lp_top(const LpTop& T, cudaStream_t st) {

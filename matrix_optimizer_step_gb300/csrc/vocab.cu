@@ -571,32 +571,31 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       R.err = err;
       R.k = n_top;
       R.top_blocks = reinterpret_cast<TopBlock*>(ws + off_top);
-      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_rows(R, s); }));
-      if (n_top > 0) {
-        LpTop T = {};
-        T.block = block;
-        T.coarse = coarse;
-        T.ld_block = ld_block;
-        T.stats = stats;
-        T.stats_ld = stats_ld;
-        T.n_blocks = n_blocks;
-        T.stats_shift = stats_shift;
-        T.vocab = static_cast<int32_t>(v);
-        T.rows_in = lp_info;
-        T.top_blocks = R.top_blocks;
-        T.rows = nr;
-        T.x = R.x;
-        T.w = w;
-        T.ld_x = ld_x;
-        T.ld_w = ld_w;
-        T.dim = R.dim;
-        T.logit_scale_log2 = scale_log2;
-        T.k = n_top;
-        T.ids64 = P->top_dtype == DMUON_INDEX_I64;
-        T.ids = static_cast<char*>(P->top_ids) + r0 * n_top * (T.ids64 ? 8 : 4);
-        T.logprobs = P->top_logprobs ? P->top_logprobs + r0 * n_top : nullptr;
-        DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_top(T, s); }));
-      }
+      LpTop T = {};
+      T.block = block;
+      T.coarse = coarse;
+      T.ld_block = ld_block;
+      T.stats = stats;
+      T.stats_ld = stats_ld;
+      T.n_blocks = n_blocks;
+      T.stats_shift = stats_shift;
+      T.vocab = static_cast<int32_t>(v);
+      T.rows_in = lp_info;
+      T.top_blocks = R.top_blocks;
+      T.rows = nr;
+      T.x = R.x;
+      T.w = w;
+      T.ld_x = ld_x;
+      T.ld_w = ld_w;
+      T.dim = R.dim;
+      T.logit_scale_log2 = scale_log2;
+      T.k = n_top;
+      T.ids64 = P->top_dtype == DMUON_INDEX_I64;
+      if (n_top > 0) T.ids = static_cast<char*>(P->top_ids) + r0 * n_top * (T.ids64 ? 8 : 4);
+      T.logprobs = P->top_logprobs ? P->top_logprobs + r0 * n_top : nullptr;
+      bool top_done = false;
+      DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_rows(R, T, &top_done, s); }));
+      if (n_top > 0 && !top_done) DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_lp_top(T, s); }));
       if (!grads) continue;
       DM_TRY(timed_launch(ctx, -1, s, [&] {
         return launch_lp_dlogits(block, ld_block, nr, static_cast<int32_t>(v), stats_shift, stats, stats_ld, lp_info,

@@ -413,7 +413,6 @@ struct LpRows {
   int32_t k;               // alternatives wanted, or 0
   TopBlock* top_blocks;    // of row row0, kTopBlocks a row
 };
-cudaError_t launch_lp_rows(const LpRows& R, cudaStream_t st);
 
 struct LpTop {
   const void* block;       // logs of row row0
@@ -435,6 +434,8 @@ struct LpTop {
   int32_t ids64;
   float* logprobs;         // of row row0, k a row, or null
 };
+// The row pass; for few rows with T.k > 0 it finds the alternatives too (*top_done), else launch_lp_top does.
+cudaError_t launch_lp_rows(const LpRows& R, const LpTop& T, bool* top_done, cudaStream_t st);
 cudaError_t launch_lp_top(const LpTop& T, cudaStream_t st);
 
 // Fixed-point logs -> bf16 d logits in place, as launch_ce_dlogits.
