@@ -64,17 +64,16 @@ __device__ __forceinline__ float reached_by(const float (&v)[PER], int k) {
 //      these the ones that reach the k-th largest lower bound: k and a few more;
 //   2. their logits as sums of fp32, with a bound of their error; those that lie
 //      closer to another than both errors again, exact to about 48 bits.
-// A block takes a row.  Up to 1000 rows its latency counts: with 16 warps a call of
-// 300 x 50257 x 768 takes 54 us, with 4 65, of 64 x 128256 x 4096 211 and 232, of
-// 1000 x 128256 x 4096 685 each.  More rows need little of each: 2000 x 50257 x 768 162 us
-// with 16 warps, 146 with 4, 4096 292 and 265 (1 and 2 warps: 266).
-// For 4096 x 50257 x 768 the pass takes 60 us with 20 alternatives and 20 with one: two thirds are the
-// candidates' rows of w, from L2, and their products.
+// A block takes a row.  Below 512 rows, where its latency counts, it has the row pass's
+// 16 warps; from there on 4: 600 x 128256 x 1024 with 20 alternatives 146 us (16 warps: 150),
+// 4096 x 50257 x 768 251 (8: 278, 2: 265), 8192 x 32000 x 2048 760 (8: 821, 2: 859).
+// For 4096 x 50257 x 768 the pass takes 54 us with 20 alternatives, 20 with one, for 8192 x 32000 x 2048
+// 175 and 57: most of it is the candidates' rows of w, from L2 and memory (5.6 TB/s in the second case),
+// so neither more rows at a time nor fewer instructions make it shorter.
 //
 // More candidates than there is room for (equal or nearly equal logits) are taken
 // kWindow entries at a time; a row of zeros, all of whose logits are equal, is known without.
 constexpr int kWindow = 128;     // candidate entries
-constexpr int64_t kTopFew = 1000;
 
 // a + p without loss: the sum in a, what it rounds away in `lost` (Knuth's two-sum).
 __device__ __forceinline__ void add_exactly(float& a, float& lost, float p) {
@@ -122,26 +121,34 @@ __device__ __forceinline__ float sum_values(float (&v)[N], int lane) {
   return v[0];
 }
 
+// Two fp32 side by side, and two multiply-adds in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t pair_of_bf16(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ void fma_pair(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float sum_of_pair(uint64_t v) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  return a + b;
+}
+
 // Dot products of x with N rows of w (all on 16-byte boundaries) in fp32, four chains a lane (64-bit sums of all
-// candidates took a quarter of this kernel's time: an SM adds two a cycle), and the sums of
-// the products' absolute values: no dot product is off by more than a roundoff of that for
-// each step of its longest chain.  Lane l returns those of row l % N.
+// candidates took a quarter of this kernel's time: an SM adds two a cycle).  No dot product is off by more than a roundoff of
+// sum |x_k w_k| <= |x| |w| for each step of its longest chain; the norms cost less than that sum.
+// Lane l returns what concerns row l % N.
 struct DotBound {
   float z, error;
 };
 template <int N>
 __device__ __forceinline__ DotBound warp_dots(const uint16_t* x, const uint16_t* const (&w)[N], int n, int lane) {
-  float sum[N][4], size[N];
+  uint64_t sum[N][2], ww[N], xx = 0;  // all bits zero: 0.f twice
 #pragma unroll
-  for (int r = 0; r < N; ++r) {
-    size[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[r][i] = 0.f;
-  }
-  auto add = [&](int r, int i, float p, float q) {
-    sum[r][i] = fmaf(p, q, sum[r][i]);
-    size[r] = fmaf(fabsf(p), fabsf(q), size[r]);
-  };
+  for (int r = 0; r < N; ++r) sum[r][0] = sum[r][1] = ww[r] = 0;
   constexpr int kAhead = N > 1 ? 2 : 8;
 #pragma unroll kAhead
   for (int c = lane; c < n >> 3; c += 32) {
@@ -149,29 +156,46 @@ __device__ __forceinline__ DotBound warp_dots(const uint16_t* x, const uint16_t*
     const uint4 p = reinterpret_cast<const uint4*>(x)[c];
 #pragma unroll
     for (int r = 0; r < N; ++r) q[r] = reinterpret_cast<const uint4*>(w[r])[c];
-    const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+    const uint64_t u[4] = {pair_of_bf16(p.x), pair_of_bf16(p.y), pair_of_bf16(p.z), pair_of_bf16(p.w)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fma_pair(xx, u[i], u[i]);
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      const uint32_t v[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
+      const uint64_t v[4] = {pair_of_bf16(q[r].x), pair_of_bf16(q[r].y), pair_of_bf16(q[r].z), pair_of_bf16(q[r].w)};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        add(r, i, __uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16));
-        add(r, i, __uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u));
+        fma_pair(sum[r][i & 1], u[i], v[i]);
+        fma_pair(ww[r], v[i], v[i]);
       }
     }
   }
-  for (int c = (n & ~7) + lane; c < n; c += 32)
+  for (int c = (n & ~7) + lane; c < n; c += 32) {
+    const uint64_t u = pair(bf16_bits_to_f32(x[c]), 0.f);
+    fma_pair(xx, u, u);
 #pragma unroll
-    for (int r = 0; r < N; ++r) add(r, 0, bf16_bits_to_f32(x[c]), bf16_bits_to_f32(w[r][c]));
-  float z[N];
+    for (int r = 0; r < N; ++r) {
+      const uint64_t v = pair(bf16_bits_to_f32(w[r][c]), 0.f);
+      fma_pair(sum[r][0], u, v);
+      fma_pair(ww[r], v, v);
+    }
+  }
+  float z[N], norm[N];
 #pragma unroll
-  for (int r = 0; r < N; ++r) z[r] = (sum[r][0] + sum[r][1]) + (sum[r][2] + sum[r][3]);
+  for (int r = 0; r < N; ++r) {
+    z[r] = sum_of_pair(sum[r][0]) + sum_of_pair(sum[r][1]);
+    norm[r] = sum_of_pair(ww[r]);
+  }
+  float x2 = sum_of_pair(xx);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x2 += __shfl_xor_sync(0xffffffffu, x2, o);
   DotBound d;
   d.z = sum_values(z, lane);
-  // Two steps for each vector of a lane, one for its last element, seven between chains and lanes.  `size` itself is a sum of at most
-  // four times as many steps; a part in 2^10 more than covers what that may take from it.
+  const float w2 = sum_values(norm, lane);
+  // Two steps for each vector of a lane, one for its last element, seven between chains and lanes.  A part in 2^8 more than covers
+  // what the norms' own sums round away.  Squares that leave the range of fp32 bound nothing.
   const int steps = 2 * ((n >> 3) / 32 + 1) + 8;
-  d.error = sum_values(size, lane) * (static_cast<float>(steps) * (0x1p-24f + 0x1p-34f));
+  const bool known = x2 > 1e-30f && w2 > 1e-30f;
+  d.error = known ? sqrtf(x2) * sqrtf(w2) * (static_cast<float>(steps) * (0x1p-24f + 0x1p-32f)) : __int_as_float(0x7f800000);
   return d;
 }
 
@@ -231,11 +255,26 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
     return w;
   };
   // take(entry, upper and lower bound) for this lane's entries of a block with maximum m whose upper bound reaches the row's.
+  // Few do, so their logs are compared as they are with what the bound leaves room for, a little more than it.
   auto for_entries = [&](int b, float m, uint2 w, auto&& take) {
+    const int c0 = (b << T.stats_shift) + lane * per_lane;
+    const float room = m + slack - R.reached;
+    uint32_t some = 0;  // bit j: entry j
+    if (T.coarse) {
+      // d (1 - 1/16) - 2^-10 <= room; codes without their sign are in the order of what they stand for, and NaN's is the last.
+      const uint32_t most = pack_e4m3x2(fmaf(room, 1.25f, 0x1p-6f), 0.f) & 0x7fu;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= per_lane) break;
-      const int c = (b << T.stats_shift) + lane * per_lane + j;
+      for (int j = 0; j < 4; ++j) some |= ((w.x >> (8 * j)) & 0x7fu) <= most ? 1u << j : 0u;
+    } else {
+      const float most = fmaf(room, kCeLogUnits, 2.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < per_lane) some |= static_cast<float>(((j & 2) ? w.y : w.x) >> (16 * (j & 1)) & 0xffffu) > most ? 0u : 1u << j;  // NaN: all
+    }
+    while (some) {
+      const int j = __ffs(some) - 1;
+      some &= some - 1;
+      const int c = c0 + j;
       float z, wide;
       bool far;
       if (T.coarse) {
@@ -675,7 +714,7 @@ __global__ void __launch_bounds__(kDlThreads) lp_dlogits_kernel(uint16_t* block,
 }  // namespace
 
 cudaError_t launch_lp_rows(const LpRows& R, const LpTop& T, bool* top_done, cudaStream_t st) {
-  const bool few = R.width == 1 && R.rows <= kTopFew, top = few && T.k > 0;
+  const bool few = R.width == 1, top = few && T.k > 0;
   *top_done = top;
   if (T.k < 0 || T.k > kTopMost || T.k > T.vocab) return cudaErrorInvalidValue;
   const int warps = few ? 16 : kRowWarps;
@@ -693,9 +732,7 @@ cudaError_t launch_lp_rows(const LpRows& R, const LpTop& T, bool* top_done, cuda
 
 cudaError_t launch_lp_top(const LpTop& T, cudaStream_t st) {
   if (T.k < 1 || T.k > kTopMost || T.k > T.vocab) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(T.rows));
-  if (T.rows <= kTopFew) return launch_after(lp_top_kernel<16>, grid, dim3(512), 0, st, T);
-  return launch_after(lp_top_kernel<4>, grid, dim3(128), 0, st, T);
+  return launch_after(lp_top_kernel<4>, dim3(static_cast<unsigned>(T.rows)), dim3(128), 0, st, T);
 }
 
 cudaError_t launch_lp_dlogits(uint16_t* block, int64_t ld, int64_t rows, int32_t vocab, int32_t stats_shift,

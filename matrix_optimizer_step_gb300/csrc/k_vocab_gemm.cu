@@ -216,13 +216,6 @@ __device__ __forceinline__ float max_of(const uint32_t (&r)[32]) {
 // time of the whole product at 4096 x 50257 x 768.
 // `target`: of this thread's row, -1 for none.  Calls `release` once the last
 // column has left the TMEM.
-// Two distances as 8-bit floats.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t v;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
-  return v;
-}
-
 // ENT: also the sum of 2^(z - m) (z - m), of which the entropy is made; a z of -inf has no part in it.
 // COARSE: VocabLogTop's logs.
 template <bool ENT, bool COARSE, class Args, class Release>

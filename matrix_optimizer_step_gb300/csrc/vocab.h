@@ -103,6 +103,13 @@ constexpr float kCeLogUnits = 1024.f;
 // Stands for a distance of -inf where one is multiplied: 2^it is 0.
 constexpr float kNoLogit = -256.f;
 
+// Two distances as 8-bit floats.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
 // Division by a constant of the launch: n / d for 0 <= n < 2^31, by the rounded-up
 // reciprocal 2^32 + mul and a shift (Granlund and Montgomery, "Division by invariant
 // integers using multiplication", 1994).
