@@ -332,8 +332,9 @@ DMUON_API int dmuon_adamw_step_scaled(dmuon_context* ctx, const dmuon_vector* ts
  *            is written
  *   norm, coef   one fp32 each in device memory, norms n of them (written);
  *            each may be NULL (not all three for dmuon_grad_norm)
- * Squares are summed in fp32, a few hundred of them, and on from there in 64
- * bits; a chunk whose squares leave the range of fp32 is summed again at
+ * Squares are summed in fp32 over 128 KB of a tensor at most (no sum is off by
+ * more than 2e-5 of itself, whatever the order of magnitude of its terms), and
+ * on from there in 64 bits; what leaves the range of fp32 is summed again at
  * another scale, so that no element is too large or too small.  A norm that is
  * not finite gives the factor that the formula gives: 0 for an infinite one (0
  * times the infinite elements is NaN), NaN for NaN.
@@ -587,7 +588,7 @@ DMUON_API int dmuon_token_logprobs(dmuon_context* ctx, const dmuon_logprobs* arg
  * fp32 each, at any row pitch >= dim; rows on 16-byte boundaries with
  * dim % 8 = 0 move as 16-byte vectors.  Errors as dmuon_cross_entropy.
  *
- * The vocabulary operators share scratch of the context, apart from the Muon
+ * The vocabulary and the gradient operators share scratch of the context, apart from the Muon
  * step's: a call on another stream than the last one's waits for that one.
  * A context's calls are made by one host thread at a time.  A call whose
  * scratch has its size already (any earlier call of the sizes) can be captured
@@ -669,8 +670,9 @@ DMUON_API int dmuon_selftest_wait_timeout(dmuon_context* ctx, int32_t timeout_us
  *          tiles average at least `value` 64-deep k-blocks runs 256 x 512
  *          tiles wherever two adjacent column blocks exist (0..1e6, default
  *          128; 0 = never).  Results do not depend on the setting.
- *   key 14: dmuon_cross_entropy: the block of 16-bit logs (without gradients:
- *          of statistics) that is held at a time is at most `value` MiB
+ *   key 14: dmuon_cross_entropy and dmuon_token_logprobs: the block of 8- or
+ *          16-bit logs (without gradients and alternatives: of statistics) that
+ *          is held at a time is at most `value` MiB
  *          (1..65536, default 2048; at least 256 tokens' worth).  A call whose tokens do not fit runs
  *          in passes; their number only moves the rounding of dW's fp32 sums.
  * Results never depend on keys 3, 4, 6, 8, 9, 10, 11 and 12 (bit for bit);

@@ -15,6 +15,8 @@ namespace {
     if (st_ != DMUON_OK) return st_;    \
   } while (0)
 
+constexpr int64_t kLongChunk = 131072;  // bytes of a chunk of a large call
+
 int64_t elem_size(int32_t dtype) { return dtype == DMUON_DTYPE_BF16 ? 2 : 4; }
 
 int validate_grads(const char* op, const dmuon_grad* gs, int32_t n, bool outs) {
@@ -131,27 +133,30 @@ int check_list(dmuon_context* ctx, const char* op, const dmuon_grad* gs, int n, 
   return DMUON_OK;
 }
 
-// Elements of a chunk (a multiple of `least`), by the number of chunks wanted.
-int32_t chunk_elems(const dmuon_grad* gs, int n, int64_t wanted, int64_t least) {
+// Bytes of a chunk (a multiple of `least`), by the number of chunks wanted.
+int32_t chunk_bytes(const dmuon_grad* gs, int n, int64_t wanted, int64_t least) {
   int64_t total = 0;
-  for (int i = 0; i < n; ++i) total += gs[i].numel;
-  int64_t chunk = std::min<int64_t>(round_up(total / wanted + 1, least), 65536);
+  for (int i = 0; i < n; ++i) total += gs[i].numel * elem_size(gs[i].grad_dtype);
+  int64_t chunk = std::min<int64_t>(round_up(total / wanted + 1, least), kLongChunk);
   // Chunks are numbered in 31 bits.
   while (total / chunk + n >= (int64_t(1) << 30)) chunk *= 2;
   return static_cast<int32_t>(chunk);
 }
 
-// An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 65536 do (their ends are what a
-// small call waits for: 1.5e6 elements 8.1 us in chunks of 2048, 7.0 of 8192), then eight.  Scaling: at least four
+// An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 128 KB do (their ends are what a
+// small call waits for: 1.5e6 elements 8.1 us in chunks of 4 KB, 7.0 of 16), then eight.  Scaling: at least four
 // rounds, so that its last one is a small part (1e8 elements 167 us with one and a quarter, 149 with five).
 constexpr int64_t kRound = 152 * 8;
 int32_t norm_chunk(const dmuon_grad* gs, int n) {
-  const int32_t one = chunk_elems(gs, n, std::max<int64_t>(kRound - n, kRound / 8), 8192);
-  return one < 65536 ? one : chunk_elems(gs, n, kRound * 8, 8192);
+  const int32_t one = chunk_bytes(gs, n, std::max<int64_t>(kRound - n, kRound / 8), 16384);
+  return one < kLongChunk ? one : chunk_bytes(gs, n, kRound * 8, 16384);
 }
-int32_t scale_chunk(const dmuon_grad* gs, int n) { return chunk_elems(gs, n, kRound * 4, 2048); }
+int32_t scale_chunk(const dmuon_grad* gs, int n) { return chunk_bytes(gs, n, kRound * 4, 4096); }
 
-int64_t chunks_of(const dmuon_grad& g, int32_t chunk) { return (g.numel + chunk - 1) / chunk; }
+int64_t chunks_of(const dmuon_grad& g, int32_t chunk) {
+  const int64_t length = chunk / elem_size(g.grad_dtype);
+  return (g.numel + length - 1) / length;
+}
 
 template <int CAP>
 void fill_batch(GradBatch<CAP>& B, const dmuon_grad* gs, int n, int32_t chunk) {

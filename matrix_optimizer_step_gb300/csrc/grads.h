@@ -17,7 +17,7 @@ struct GradBatch {
   int32_t first[CAP + 1];   // first chunk of each tensor, from the batch's first on
   uint8_t in_bf16[CAP], out_bf16[CAP];
   int32_t n;
-  int32_t chunk;            // elements, a multiple of 8
+  int32_t chunk;            // bytes of a chunk of `in`, a multiple of 32
 };
 constexpr int kGradBatch = 512, kGradFew = 32;  // two sizes of argument lists
 

@@ -135,9 +135,10 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
   pdl_launch();
   pdl_wait();
   const int t = tensor_of(B, blockIdx.x);
-  const int64_t start = static_cast<int64_t>(blockIdx.x - B.first[t]) * B.chunk;
-  const int n = static_cast<int>(min(static_cast<int64_t>(B.chunk), B.numel[t] - start));
   const bool bf16 = B.in_bf16[t] != 0;
+  const int length = B.chunk >> (bf16 ? 1 : 2);
+  const int64_t start = static_cast<int64_t>(blockIdx.x - B.first[t]) * length;
+  const int n = static_cast<int>(min(static_cast<int64_t>(length), B.numel[t] - start));
   const void* p = static_cast<const char*>(B.in[t]) + start * (bf16 ? 2 : 4);
   uint32_t bits = 0;
   auto sum = [&](float scale) { return block_sum(bf16 ? squares<true>(p, n, scale, bits) : squares<false>(p, n, scale, bits), red); };
@@ -272,9 +273,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   const int c = static_cast<int>(gridDim.x - 1u - blockIdx.x);
   const int t = tensor_of(B, c);
   if (f == 1.f && B.in[t] == B.out[t]) return;
-  const int64_t start = static_cast<int64_t>(c - B.first[t]) * B.chunk;
-  const int n = static_cast<int>(min(static_cast<int64_t>(B.chunk), B.numel[t] - start));
   const bool in16 = B.in_bf16[t] != 0, out16 = B.out_bf16[t] != 0;
+  const int length = B.chunk >> (in16 ? 1 : 2);
+  const int64_t start = static_cast<int64_t>(c - B.first[t]) * length;
+  const int n = static_cast<int>(min(static_cast<int64_t>(length), B.numel[t] - start));
   const void* in = static_cast<const char*>(B.in[t]) + start * (in16 ? 2 : 4);
   void* out = static_cast<char*>(B.out[t]) + start * (out16 ? 2 : 4);
   if (in16)
