@@ -333,7 +333,7 @@ DMUON_API int dmuon_adamw_step_scaled(dmuon_context* ctx, const dmuon_vector* ts
  *   norm, coef   one fp32 each in device memory, norms n of them (written);
  *            each may be NULL (not all three for dmuon_grad_norm)
  * Squares are summed in fp32 over 128 KB of a tensor at most (no sum is off by
- * more than 2e-5 of itself, whatever the order of magnitude of its terms), and
+ * more than 5e-6 of itself, whatever the order of magnitude of its terms), and
  * on from there in 64 bits; what leaves the range of fp32 is summed again at
  * another scale, so that no element is too large or too small.  A norm that is
  * not finite gives the factor that the formula gives: 0 for an infinite one (0
@@ -527,10 +527,11 @@ DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void
  * are dmuon_cross_entropy's: a policy gradient's loss gives dlogprobs and
  * dentropy from a first call's outputs, and a second call turns them into
  * gradients (its logits are multiplied out again).  Both may be one call where
- * the coefficients are known before.  The alternatives are found among the
- * entries that the matrix instruction's sums put within 2^-8 octaves and 2^-13
- * of the row's maximum of the last place, and their order is that of logits
- * summed to 48 bits or more.
+ * the coefficients are known before.  The alternatives' order is that of logits
+ * summed to 48 bits or more.  They are found among the entries that the matrix
+ * instruction's sums leave, for whose rounding four roundoffs of the given
+ * token's sum_k |x_ik w_tk| are allowed for each 16 of its terms (without tokens, of some other
+ * row's of w), and 2^-9 octaves besides.
  *
  *   x, w        as in dmuon_cross_entropy
  *   tokens      n_tokens ids of token_dtype; below zero: the row is not scored (its

@@ -14,8 +14,12 @@ namespace {
 
 __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
 
-// What the product's rounding may do to a logit, in octaves.
-__device__ __forceinline__ float logit_slack(float top) { return 0x1p-9f + fabsf(top) * 0x1p-14f; }
+// What the product's rounding may do to a logit, in octaves: a roundoff, taken four times, of its sum of
+// absolute products for each of the matrix instruction's 16-term steps, `size` standing for that sum (in octaves
+// too); and for small ones 2^-9 octaves and 2^-14 of the row's maximum.
+__device__ __forceinline__ float logit_slack(float top, float size, int dim) {
+  return 0x1p-9f + fabsf(top) * 0x1p-14f + size * (static_cast<float>(dim / 16 + 8) * 0x1p-22f);
+}
 
 // A value that at least k of the warp's values reach (PER of them a lane) and, unless
 // values crowd there, not many more; -inf where k of them are not above it.
@@ -232,7 +236,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   }
   const uint8_t* logs = static_cast<const uint8_t*>(T.block) + row * T.ld_block * (T.coarse ? 1 : 2);
   const uint16_t* x = T.x + row * T.ld_x;
-  const float slack = logit_slack(R.top);
+  const float slack = R.slack;
   auto logprob = [&](double z, int32_t id) {
     return id == R.target ? R.logprob : kLn2 * (static_cast<float>(z * T.logit_scale_log2 - R.top) - R.log_sum);
   };
@@ -451,8 +455,8 @@ __global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
 // Where a row's k largest logits are wanted, the same pass bounds them: a value T that
 // k of 256 groups of blocks reach with their maxima, found by bisection.  k entries
 // lie there or above, so only blocks that reach T (k and a few more, listed
-// for lp_top_kernel) hold one.  The maxima carry the product's rounding, for which
-// 2^-9 octaves and 2^-14 of the row's maximum are allowed.
+// for lp_top_kernel) hold one.  The maxima carry the product's rounding (logit_slack), whose
+// size the row's products with its given token stand for, or with some other row of w.
 struct Sums {
   float m, s, t;
 };
@@ -490,6 +494,7 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   constexpr int kGroups = 32 * WARPS, kWidth = WARPS > kRowWarps ? 1 : 8;  // groups of a row, and rows at most
   __shared__ Sums part[WARPS][kWidth];
   __shared__ double dots[WARPS];
+  __shared__ float sizes[WARPS];
   __shared__ float groups[kWidth][kGroups + 1], reached[kWidth], slack[kWidth];
   __shared__ int found[kWidth];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = kWidth == 1 ? 1 : R.width;
@@ -514,7 +519,8 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   const int shares = WARPS / width;
   const int64_t dot_row = base + warp / shares;
   bool bad = false;
-  const int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
+  int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
+  if (!R.tokens.p && R.k > 0 && dot_row < R.rows) dot_target = static_cast<int>((R.row0 + dot_row) % R.vocab);
   Sums sum = {minus_inf(), 0.f, 0.f};
   const int64_t own_row = base + (lane & (width - 1));
   const int per_warp = 32 / width, stride = WARPS * per_warp;
@@ -534,8 +540,12 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   };
   load(first_block);  // under way while the given token's logit is summed
   if (dot_target >= 0) {
-    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane);
-    if (lane == 0) dots[warp] = d;
+    float size;
+    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane, &size);
+    if (lane == 0) {
+      dots[warp] = d;
+      sizes[warp] = size;
+    }
   }
   if (own_row < R.rows) {
     for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
@@ -572,6 +582,10 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   }
   __syncthreads();
   if (R.k > 0) {
+    auto scored = [&](int64_t r) {
+      bool past = false;
+      return r < R.rows && load_id(R.tokens, R.row0 + r, &past) >= 0;
+    };
     if (warp < width) {
       float g[kGroups / 32];
 #pragma unroll
@@ -581,7 +595,11 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
       for (int i = 1; i < kGroups / 32; ++i) top = fmaxf(top, g[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float at = reached_by<kGroups / 32>(g, R.k), off = logit_slack(top);
+      float size = 0.f;
+      if (!R.tokens.p || scored(base + warp))
+        for (int i = 0; i < shares; ++i) size += sizes[warp * shares + i];
+      const float off = logit_slack(top, size * static_cast<float>(R.logit_scale_log2), R.dim);
+      const float at = reached_by<kGroups / 32>(g, R.k);
       if (lane == 0) {
         reached[warp] = at - off;
         slack[warp] = off;
@@ -614,6 +632,7 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
     LpRow o = {};
     if (R.k > 0) {
       o.reached = reached[lane];
+      o.slack = slack[lane];
       o.blocks = found[lane];
     }
     o.target = t;

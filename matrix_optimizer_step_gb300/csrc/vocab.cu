@@ -558,6 +558,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       R.ld_x = ld_x;
       R.ld_w = ld_w;
       R.dim = static_cast<int32_t>(d);
+      R.vocab = static_cast<int32_t>(v);
       R.logit_scale_log2 = scale_log2;
       R.logprobs = P->logprobs;
       R.lse = P->lse;

@@ -389,7 +389,7 @@ struct LpRow {
   int32_t scored;
   // Of the k largest logits none is below `reached`, and none is in another block than the listed ones
   // (`blocks` of them; above kTopBlocks the list is not whole).
-  float reached;
+  float reached, slack;  // slack: what the products' rounding may do to one
   int32_t blocks;
 };
 
@@ -405,7 +405,7 @@ struct LpRows {
   const uint16_t* x;       // of row row0
   const uint16_t* w;
   int64_t ld_x, ld_w;
-  int32_t dim;
+  int32_t dim, vocab;
   double logit_scale_log2;
   float* logprobs;         // of row 0, or null
   float* lse;

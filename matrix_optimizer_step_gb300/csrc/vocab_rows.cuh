@@ -40,9 +40,11 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int col
 }
 
 // This warp's share (of `shares`) of the dot product of two bf16 rows: a lane's
-// part in fp32, their sum in 64 bits, the same in every lane.
-__device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane) {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+// part in fp32, their sum in 64 bits, the same in every lane.  `size`, if wanted: the
+// sum of the products' absolute values.
+__device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane,
+                                           float* size = nullptr) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, abs_sum = 0.f;
   const int start = share * 32 + lane, step = shares * 32;
   int done = 0;
   if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
@@ -55,10 +57,22 @@ __device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b,
       for (int i = 0; i < 4; ++i) {
         acc[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), acc[i]);
         acc[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc[i]);
+        if (size) {
+          abs_sum = fmaf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(v[i] << 16)), abs_sum);
+          abs_sum = fmaf(fabsf(__uint_as_float(u[i] & 0xFFFF0000u)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u)), abs_sum);
+        }
       }
     }
   }
-  for (int c = done + start; c < n; c += step) acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
+  for (int c = done + start; c < n; c += step) {
+    acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
+    if (size) abs_sum = fmaf(fabsf(bf16_bits_to_f32(a[c])), fabsf(bf16_bits_to_f32(b[c])), abs_sum);
+  }
+  if (size) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) abs_sum += __shfl_xor_sync(0xffffffffu, abs_sum, o);
+    *size = abs_sum;
+  }
   return warp_sum(static_cast<double>((acc[0] + acc[1]) + (acc[2] + acc[3])));
 }
 

@@ -65,7 +65,7 @@ def reference(x, w, t, s=1.0, k=0, dlp=None, dent=None, grad_scale=1.0, halves=T
            "entropy": (torch.where(scored, H, 0.0), eH * scored)}
     if k:
         # Which of two logits is larger is decided by sums in 64 bits of the operands alone, laid out the same for all ids.
-        exact = torch.cat([(X[i][None, :] * W).sum(1)[None] for i in range(n)]) if n * v * d < 3e9 else z
+        exact = torch.cat([(X[i][None, :] * W).sum(1)[None] for i in range(n)]) if n * v * d < 8e9 else z
         ids = torch.sort(exact, dim=1, descending=True, stable=True).indices[:, :k]
         out["top_ids"] = (torch.where(scored[:, None], ids, -1), None)
         out["top_logprobs"] = (torch.where(scored[:, None], logp.gather(1, ids), 0.0), (tol * scored)[:, None].expand(-1, k))
@@ -299,6 +299,23 @@ def test_nearly_equal_logits(ops, n, v):
     ops.sync()
     assert bool((out["top_ids"][:, 0::2] == out["top_ids"][:, 1::2] + 1).all())
     check(out, reference(x, w, t, 1.0, 20))
+
+
+@pytest.mark.parametrize("tokens", [True, False])
+@pytest.mark.parametrize("n", [4, 40, 600])
+def test_logits_that_cancel(ops, n, tokens):
+    # Two terms of 300 that cancel but for their rounding, the first and the last of 4096: what the matrix instruction's sums round
+    # away is that of a sum of 300 at each step, next to logits of a few units.
+    x, w, t, _, _ = inputs(n, 3000, 4096, seed=16)
+    x[:, 0] = x[:, 4095] = 17.25
+    w[:, 0] = 17.0
+    w[:, 4095] = -17.0
+    out = outputs(x, w, 20)
+    if not tokens:
+        del out["logprobs"]
+    ops.token_logprobs(x, w, t if tokens else None, **out)
+    ops.sync()
+    check(out, reference(x, w, t if tokens else None, 1.0, 20))
 
 
 @pytest.mark.parametrize("spread", [30.0, 0.0])
