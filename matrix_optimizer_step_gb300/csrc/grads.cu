@@ -144,8 +144,8 @@ int32_t chunk_bytes(const dmuon_grad* gs, int n, int64_t wanted, int64_t least) 
 }
 
 // An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 128 KB do (their ends are what a
-// small call waits for: 1.5e6 elements 8.1 us in chunks of 4 KB, 7.0 of 16), then eight.  Scaling: at least four
-// rounds, so that its last one is a small part (1e8 elements 167 us with one and a quarter, 149 with five).
+// small call waits for: three tensors of a small model 8.2 us in chunks of 4 KB, 7.1 of 16), then eight.  Scaling: at least four
+// rounds, so that its last one is a small part (clipping 1e8 elements 152 us with one or two, 147 with four).
 constexpr int64_t kRound = 152 * 8;
 int32_t norm_chunk(const dmuon_grad* gs, int n) {
   const int32_t one = chunk_bytes(gs, n, std::max<int64_t>(kRound - n, kRound / 8), 16384);

@@ -69,11 +69,11 @@ __device__ __forceinline__ float reached_by(const float (&v)[PER], int k) {
 //   2. their logits as sums of fp32, with a bound of their error; those that lie
 //      closer to another than both errors again, exact to about 48 bits.
 // A block takes a row.  Below 512 rows, where its latency counts, it has the row pass's
-// 16 warps; from there on 4: 600 x 128256 x 1024 with 20 alternatives 146 us (16 warps: 150),
-// 4096 x 50257 x 768 251 (8: 278, 2: 265), 8192 x 32000 x 2048 760 (8: 821, 2: 859).
-// For 4096 x 50257 x 768 the pass takes 54 us with 20 alternatives, 20 with one, for 8192 x 32000 x 2048
-// 175 and 57: most of it is the candidates' rows of w, from L2 and memory (5.6 TB/s in the second case),
-// so neither more rows at a time nor fewer instructions make it shorter.
+// 16 warps and no launch of its own (4 warps in one: 207 us for 184 with 1 row at 128256 x 4096, 50 for 43
+// with 128 at 50257 x 768); from there on 4.  Calls with 20 alternatives: 600 x 128256 x 1024 148 us (2 warps:
+// 159, 8: 145, 16: 152), 4096 x 50257 x 768 256 (2: 252, 8: 271, 16: 311), 8192 x 32000 x 2048 765 (2: 773,
+// 8: 827, 16: 872).  At 4096 x 50257 x 768 the pass itself takes 58 us from cold caches, with half of the
+// issue slots and a sixth of the memory's rate in use.
 //
 // More candidates than there is room for (equal or nearly equal logits) are taken
 // kWindow entries at a time; a row of zeros, all of whose logits are equal, is known without.
@@ -362,7 +362,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   };
   if (R.blocks <= kTopBlocks) {
     // Where fewer than k blocks or many close logits leave the row's bound low: a better one from the
-    // largest lower bounds of each thread's entries (2162 x 1292 x 3264 with 20 alternatives 3.2 ms without).
+    // largest lower bounds of each thread's entries (2162 x 1292 x 3264 with 20 alternatives 118 us, 3.2 ms without).
     float from = R.reached;
     for (int attempt = from == minus_inf() ? 1 : 0; attempt < 2; ++attempt) {
       if (attempt > 0) {
@@ -406,7 +406,9 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
       }
       __syncthreads();
       in_order(S.n_ids, [&](int rank, double z, int32_t id) {
-        pdl_launch();  // not earlier: blocks of a next call's product would wait for this kernel's room (300 x 50257 x 768 54 us for 49)
+        // Not earlier, for the smallest calls: at the start 1 row takes 184.2 us for 183.3 (128256 x 4096) and 128
+        // 44.0 for 42.8 (50257 x 768), though 300 rows 47.6 for 52.9 with one alternative and 53.6 for 55.2 with five.
+        pdl_launch();
         put(rank, id, logprob(z, id));
       });
       return;

@@ -382,7 +382,7 @@ int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr,
   if (key != A.key) {
     A.release();
     // Small lists in shorter chunks, so that the blocks' last round is a small part of all (a chunk's
-    // length changes no element): 4e7 elements 195 us with 65536, 170 with 8192.
+    // length changes no element): a clipped step of 52 tensors, 3.9e7 elements, 219 us with 65536, 190 with 8192.
     int64_t total = 0;
     for (int i = 0; i < n; ++i) total += ts[i].numel;
     const int64_t chunk = std::max<int64_t>(2048, std::min<int64_t>(kChunkElems, round_up(total / (152 * 32) + 1, 2048)));
