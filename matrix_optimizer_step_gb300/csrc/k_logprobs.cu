@@ -406,8 +406,9 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
       }
       __syncthreads();
       in_order(S.n_ids, [&](int rank, double z, int32_t id) {
-        // Not earlier, for the smallest calls: at the start 1 row takes 184.2 us for 183.3 (128256 x 4096) and 128
-        // 44.0 for 42.8 (50257 x 768), though 300 rows 47.6 for 52.9 with one alternative and 53.6 for 55.2 with five.
+        // Not at the start: over 100 to 511 rows of 50257 x 768, 32000 x 2048 and 128256 x 1024 with 1 and 20
+        // alternatives that is 3.4 % faster to 3.4 % slower, without a rule in the sizes, and on average slower
+        // (1 row of 128256 x 4096 184.2 us for 183.3; 300 of 50257 x 768 with one 47.6 for 52.9).
         pdl_launch();
         put(rank, id, logprob(z, id));
       });
