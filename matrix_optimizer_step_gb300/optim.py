@@ -39,7 +39,6 @@ class OwnerStep:
         self._n_vecs = 0
         self._keep = []
         self._grad_lists = {}
-        self._coef = None
 
     # -------------------------------------------------------------- Muon
     def set_muon(self, masters, momenta, grads, params=None):
@@ -161,11 +160,12 @@ class OwnerStep:
         if max_norm is not None:
             if "grad_scale" in (muon or {}) or "grad_scale" in (adamw or {}):
                 raise ValueError("step: max_norm and grad_scale")
-            if self._coef is None:
-                self._coef = empty_on(main, self.device, 1, dtype=torch.float32)
-            self._grad_norm(muon is not None, use_adamw, max_norm, norm, None, self._coef, main)
-            muon = muon if muon is None else dict(muon, grad_scale=self._coef)
-            adamw = adamw if adamw is None else dict(adamw, grad_scale=self._coef)
+            # Of this call alone, taken on the stream that its last reader is ordered before: steps of different
+            # routes may run on two streams, and nothing orders one's norm behind the other's reads.
+            coef = empty_on(main, self.device, 1, dtype=torch.float32)
+            self._grad_norm(muon is not None, use_adamw, max_norm, norm, None, coef, main)
+            muon = muon if muon is None else dict(muon, grad_scale=coef)
+            adamw = adamw if adamw is None else dict(adamw, grad_scale=coef)
         if muon is None:
             self.adamw_step(stream=main, **adamw)
             return
@@ -178,10 +178,12 @@ class OwnerStep:
             self._ev_join = torch.cuda.Event()
         self._ev_fork.record(main)
         self._side.wait_event(self._ev_fork)
-        self.adamw_step(stream=self._side, **adamw)
-        self.muon_step(stream=main, **muon)
-        self._ev_join.record(self._side)
-        main.wait_event(self._ev_join)
+        try:
+            self.adamw_step(stream=self._side, **adamw)
+            self.muon_step(stream=main, **muon)
+        finally:
+            self._ev_join.record(self._side)
+            main.wait_event(self._ev_join)
 
     # ------------------------------------------------- host-side buffers
     def set_host_io(self, grads_host, params_host=None, v_grads_host=None, v_params_host=None):

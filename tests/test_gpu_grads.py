@@ -349,6 +349,32 @@ def test_clipped_step_replayed(cuda_lib):
     b.close()
 
 
+def test_clipped_steps_of_two_routes_on_two_streams(cuda_lib):
+    # Each route's step behind a long wait on its own stream, with norms far apart, against the same steps in order.
+    g = torch.Generator(device=DEV).manual_seed(11)
+    grads = [torch.randn(s, generator=g, device=DEV) for s in MATS]
+    v_grads = [torch.randn(n, generator=g, device=DEV) * 1e3 for n in VECS]
+    a, sa = owner(cuda_lib, grads, v_grads)
+    b, sb = owner(cuda_lib, grads, v_grads)
+    norms = [torch.empty(1, device=DEV) for _ in range(4)]
+    b.step(MUON, None, max_norm=0.5, norm=norms[2])
+    b.sync()
+    b.step(None, ADAMW, max_norm=0.5, norm=norms[3])
+    b.sync()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(one):
+        torch.cuda._sleep(20_000_000)
+    a.step(MUON, None, stream=one, max_norm=0.5, norm=norms[0])
+    a.step(None, ADAMW, stream=two, max_norm=0.5, norm=norms[1])
+    torch.cuda.synchronize()
+    assert torch.equal(norms[0], norms[2]) and torch.equal(norms[1], norms[3])
+    for k in sa:
+        assert all(torch.equal(p, q) for p, q in zip(sa[k], sb[k])), k
+    a.close()
+    b.close()
+
+
 def test_policy_step(cuda_lib):
     # The operators together, as a policy-gradient step uses them: scores, a loss in torch, gradients, the clipped step.
     ops = cuda_lib.VocabOps(0)

@@ -156,3 +156,39 @@ def test_python_refusals(mos):
         owner.step(dict(lr=0.1, momentum=0.9, wd=0.0, grad_scale=1), None, stream=object(), max_norm=1.0)
     with pytest.raises(ValueError):
         owner.step(dict(lr=0.1, momentum=0.9, wd=0.0), None, stream=object(), norm=torch.zeros(1))
+
+
+class _Stream:
+    def wait_event(self, event):
+        pass
+
+
+class _Event:
+    def record(self, stream):
+        pass
+
+
+def test_a_clipped_step_has_a_factor_of_its_own(mos, monkeypatch):
+    # The Muon route on one stream and the AdamW route on another share no tensor, so either's norm may be written
+    # while the other's step has yet to read its factor.
+    import torch
+
+    from matrix_optimizer_step_gb300 import optim
+
+    taken, calls = [], []
+    monkeypatch.setattr(optim, "empty_on", lambda stream, *a, **kw: taken.append((stream, torch.empty(1))) or taken[-1][1])
+    step = optim.OwnerStep(0)
+    step._mats = step._vecs = ()
+    step._side, step._ev_fork, step._ev_join = _Stream(), _Event(), _Event()
+    monkeypatch.setattr(step, "_grad_norm", lambda muon, adamw, max_norm, norm, norms, coef, stream: calls.append((stream, coef)))
+    monkeypatch.setattr(step, "muon_step", lambda stream, grad_scale: calls.append((stream, grad_scale)))
+    monkeypatch.setattr(step, "adamw_step", lambda stream, grad_scale: calls.append((stream, grad_scale)))
+    streams = [_Stream() for _ in range(3)]
+    step.step({}, None, stream=streams[0], max_norm=1.0)
+    step.step(None, {}, stream=streams[1], max_norm=1.0)
+    step.step({}, {}, stream=streams[2], max_norm=1.0)
+    step.close()
+    assert [s for s, _ in taken] == streams
+    where = {id(t): i for i, (_, t) in enumerate(taken)}
+    assert [where[id(t)] for _, t in calls] == [0, 0, 1, 1, 2, 2, 2]
+    assert len({t.data_ptr() for _, t in taken}) == 3
