@@ -529,9 +529,9 @@ DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void
  * gradients (its logits are multiplied out again).  Both may be one call where
  * the coefficients are known before.  The alternatives' order is that of logits
  * summed to 48 bits or more.  They are found among the entries that the matrix
- * instruction's sums leave, for whose rounding four roundoffs of the given
- * token's sum_k |x_ik w_tk| are allowed for each 16 of its terms (without tokens, of some other
- * row's of w), and 2^-9 octaves besides.
+ * instruction's sums leave, for whose rounding 13 roundoffs (2^-24) of |x_i| |w_v| are
+ * allowed for each 16 of its terms, |w_v| being the largest norm in a block of w's rows: more than
+ * such a sum can be off by, whatever its terms, so no entry is left out.
  *
  *   x, w        as in dmuon_cross_entropy
  *   tokens      n_tokens ids of token_dtype; below zero: the row is not scored (its

@@ -14,11 +14,26 @@ namespace {
 
 __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
 
-// What the product's rounding may do to a logit, in octaves: a roundoff, taken four times, of its sum of
-// absolute products for each of the matrix instruction's 16-term steps, `size` standing for that sum (in octaves
-// too); and for small ones 2^-9 octaves and 2^-14 of the row's maximum.
-__device__ __forceinline__ float logit_slack(float top, float size, int dim) {
-  return 0x1p-9f + fabsf(top) * 0x1p-14f + size * (static_cast<float>(dim / 16 + 8) * 0x1p-22f);
+// What the product's rounding may do to a logit, in octaves.  A step of the matrix instruction adds 16 products to the running
+// sum: it lines the 17 up to the largest, keeps what reaches 2^-25 of that, and cuts the result off to 24 bits (measured
+// with a term of 2^p and small ones beside it, before it or behind it: a small one of 1 counts whole to p = 25 and not at
+// all from 26 on, and a sum past 2^23 loses its halves towards zero).  No product and no running sum is larger than |x| |w|
+// (Cauchy and Schwarz), so a step is off by at most (17 2^-25 + 2^-23) |x| |w|, 10.5 roundoffs of it, whatever the signs of its
+// terms; 13 are taken, which covers the rounding of the norms.  Joined parts, the scale and the fixed-point logs: 32 more and 2^-9 octaves.
+__device__ __forceinline__ float slack_unit(float x_squares, double logit_scale_log2, int dim) {
+  const float norm = sqrtf(fmaxf(x_squares, 1e-30f));
+  return norm * static_cast<float>(logit_scale_log2) * (static_cast<float>(13 * ((dim + 15) / 16) + 32) * 0x1p-24f);
+}
+// Largest norm of the rows of w of statistics block b.
+__device__ __forceinline__ float block_norm(const float* norms, int stats_shift, int b) {
+  if (stats_shift == kCeThinShift) return norms[b];
+  const float4 q = reinterpret_cast<const float4*>(norms)[b];
+  return fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
+}
+// Of a logit with a row of w of that norm.
+__device__ __forceinline__ float logit_slack(float unit, float norm) {
+  const float s = fmaf(unit, norm, 0x1p-9f);
+  return s < __int_as_float(0x7f800000) ? s : __int_as_float(0x7f800000);  // 0 times infinity
 }
 
 // A value that at least k of the warp's values reach (PER of them a lane) and, unless
@@ -237,7 +252,6 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   }
   const uint8_t* logs = static_cast<const uint8_t*>(T.block) + row * T.ld_block * (T.coarse ? 1 : 2);
   const uint16_t* x = T.x + row * T.ld_x;
-  const float slack = R.slack;
   auto logprob = [&](double z, int32_t id) {
     return id == R.target ? R.logprob : kLn2 * (static_cast<float>(z * T.logit_scale_log2 - R.top) - R.log_sum);
   };
@@ -260,8 +274,9 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
     return w;
   };
   // take(entry, upper and lower bound) for this lane's entries of a block with maximum m whose upper bound reaches `from`.
-  // Few do, so their logs are compared as they are with what the bound leaves room for, a little more than it.
-  auto for_entries = [&](int b, float m, uint2 w, float from, auto&& take) {
+  // Few do, so their logs are compared as they are with what the bound leaves room for, a little more than it.  An infinite slack
+  // (rows of w with infinities) leaves no bound, and none is below `from`.
+  auto for_entries = [&](int b, float m, float slack, uint2 w, float from, auto&& take) {
     const int c0 = (b << T.stats_shift) + lane * per_lane;
     const float room = m + slack - from;
     uint32_t some = 0;  // bit j: entry j
@@ -295,7 +310,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
         wide = slack + 0.5f / kCeLogUnits;
         far = q == 65535u;
       }
-      if (z + wide >= from && c < T.vocab && c != R.target) take(c, z + wide, far ? minus_inf() : z - wide);
+      if (!(z + wide < from) && c < T.vocab && c != R.target) take(c, z + wide, far ? minus_inf() : z - wide);
     }
   };
   // Logits of n candidates, then the first k of them in order: take(rank, z, id).
@@ -357,7 +372,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
       for (int u = 0; u < kLoads; ++u) w[u] = load_entries(b[u].block);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        if (i + u * WARPS < R.blocks) for_entries(b[u].block, b[u].max, w[u], from, take);
+        if (i + u * WARPS < R.blocks) for_entries(b[u].block, b[u].max, b[u].slack, w[u], from, take);
     }
   };
   if (R.blocks <= kTopBlocks) {
@@ -397,7 +412,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
         if (R.target >= 0 && lane == 0) S.id[0] = R.target;
 #pragma unroll
         for (int i = 0; i < kWindow / 32; ++i) {
-          const bool in = lane + 32 * i < n && S.upper[lane + 32 * i] >= reach;
+          const bool in = lane + 32 * i < n && !(S.upper[lane + 32 * i] < reach);
           const unsigned who = __ballot_sync(0xffffffffu, in);
           if (in) S.id[count + __popc(who & ((1u << lane) - 1u))] = S.entry[lane + 32 * i];
           count += __popc(who);
@@ -429,9 +444,9 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
     if (thread == 0) S.n_ids = S.close = 0;
     __syncthreads();
     for (int b = b0 + warp; b < min(b0 + step, T.n_blocks); b += WARPS) {
-      const float m = T.stats[static_cast<int64_t>(b) * T.stats_ld + row].x;
+      const float m = T.stats[static_cast<int64_t>(b) * T.stats_ld + row].x, slack = logit_slack(R.unit, block_norm(T.norms, T.stats_shift, b));
       if (m + slack < R.reached) continue;
-      for_entries(b, m, load_entries(b), R.reached, [&](int c, float, float) { S.id[atomicAdd(&S.n_ids, 1)] = c; });
+      for_entries(b, m, slack, load_entries(b), R.reached, [&](int c, float, float) { S.id[atomicAdd(&S.n_ids, 1)] = c; });
     }
     if (thread == 0 && R.target >= 0 && R.target >> T.stats_shift >= b0 && R.target >> T.stats_shift < b0 + step)
       S.id[atomicAdd(&S.n_ids, 1)] = R.target;
@@ -450,8 +465,9 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   if (thread < best) put(thread, S.best_id[thread], logprob(S.best_z[thread], S.best_id[thread]));
 }
 
+// Eight blocks an SM (72 registers, seven blocks: 8192 x 32000 x 2048 779 us for 750).
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
+__global__ void __launch_bounds__(32 * WARPS, 8) lp_top_kernel(const LpTop T) {
   __shared__ TopShared S;
   pdl_wait();
   const int64_t row = blockIdx.x;
@@ -476,8 +492,9 @@ __global__ void __launch_bounds__(32 * WARPS) lp_top_kernel(const LpTop T) {
 // Where a row's k largest logits are wanted, the same pass bounds them: a value T that
 // k of 256 groups of blocks reach with their maxima, found by bisection.  k entries
 // lie there or above, so only blocks that reach T (k and a few more, listed
-// for lp_top_kernel) hold one.  The maxima carry the product's rounding (logit_slack), whose
-// size the row's products with its given token stand for, or with some other row of w.
+// for lp_top_kernel) hold one.  The maxima carry the product's rounding (slack_unit): a
+// group counts with what its maximum is at least, a block reaches T with what its own is at most.  A thread takes the largest norm
+// of its blocks for all of them.
 struct Sums {
   float m, s, t;
 };
@@ -509,14 +526,15 @@ __device__ __forceinline__ Sums join_lanes(Sums sum, int step, int lane) {
 }
 
 // Few rows: 16 warps a row (WARPS), and where alternatives are wanted (TOP) the block goes on
-// to them, without a launch and a way through memory.
+// to them, without a launch and a way through memory.  1024 threads an SM: with the 79 registers that it would take, 4096 x 50257 x 768
+// runs 270 us for 266 and 8192 x 32000 x 2048 754 for 745, but 600 x 128256 x 1024 163 for 167.
 template <bool VEC, int WARPS, bool TOP>
-__global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, const LpTop T, int row_blocks) {
+__global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows_kernel(const LpRows R, const LpTop T, int row_blocks) {
   constexpr int kGroups = 32 * WARPS, kWidth = WARPS > kRowWarps ? 1 : 8;  // groups of a row, and rows at most
   __shared__ Sums part[WARPS][kWidth];
   __shared__ double dots[WARPS];
-  __shared__ float sizes[WARPS];
-  __shared__ float groups[kWidth][kGroups + 1], reached[kWidth], slack[kWidth];
+  __shared__ float squares[WARPS];
+  __shared__ float groups[kWidth][kGroups + 1], reached[kWidth];
   __shared__ int found[kWidth];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, width = kWidth == 1 ? 1 : R.width;
   if (!TOP) pdl_launch();  // else with the last of it
@@ -540,8 +558,7 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   const int shares = WARPS / width;
   const int64_t dot_row = base + warp / shares;
   bool bad = false;
-  int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
-  if (!R.tokens.p && R.k > 0 && dot_row < R.rows) dot_target = static_cast<int>((R.row0 + dot_row) % R.vocab);
+  const int dot_target = R.tokens.p && dot_row < R.rows ? load_id(R.tokens, R.row0 + dot_row, &bad) : -1;
   Sums sum = {minus_inf(), 0.f, 0.f};
   const int64_t own_row = base + (lane & (width - 1));
   const int per_warp = 32 / width, stride = WARPS * per_warp;
@@ -560,12 +577,18 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
     }
   };
   load(first_block);  // under way while the given token's logit is summed
-  if (dot_target >= 0) {
-    float size;
-    const double d = warp_dot(R.x + dot_row * R.ld_x, R.w + dot_target * R.ld_w, R.dim, warp % shares, shares, lane, &size);
+  float norm = 0.f;  // largest of this thread's blocks
+  if (R.k > 0) {
+#pragma unroll 8
+    for (int b = first_block; b < R.n_blocks; b += stride) norm = fmaxf(norm, block_norm(R.norms, R.stats_shift, b));
+  }
+  if (dot_row < R.rows && (dot_target >= 0 || R.k > 0)) {
+    const uint16_t* x = R.x + dot_row * R.ld_x;
+    float sq;
+    const double d = warp_dot(x, dot_target >= 0 ? R.w + dot_target * R.ld_w : x, R.dim, warp % shares, shares, lane, &sq);
     if (lane == 0) {
       dots[warp] = d;
-      sizes[warp] = size;
+      squares[warp] = sq;
     }
   }
   if (own_row < R.rows) {
@@ -589,7 +612,12 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
   }
   sum = join_lanes(sum, width, lane);
   if (lane < width) part[warp][lane] = sum;
+  float unit = 0.f, slack = 0.f;
   if (R.k > 0) {
+    __syncthreads();  // squares
+    for (int i = 0; i < shares; ++i) unit += squares[(lane & (width - 1)) * shares + i];
+    unit = slack_unit(unit, R.logit_scale_log2, R.dim);
+    slack = logit_slack(unit, norm);
     // Eight, four or one group of this thread: as many of a row as the block has threads.
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
@@ -598,37 +626,21 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
         for (int k = 0; k < o; ++k) group[k] = fmaxf(group[k], group[k + o]);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < kWidth && k < width) groups[lane & (width - 1)][(first_block * width + k)] = group[k];
+      if (k < kWidth && k < width) groups[lane & (width - 1)][(first_block * width + k)] = group[k] - slack;
     if (threadIdx.x < kWidth) found[threadIdx.x] = 0;
   }
   __syncthreads();
   if (R.k > 0) {
-    auto scored = [&](int64_t r) {
-      bool past = false;
-      return r < R.rows && load_id(R.tokens, R.row0 + r, &past) >= 0;
-    };
     if (warp < width) {
       float g[kGroups / 32];
 #pragma unroll
       for (int i = 0; i < kGroups / 32; ++i) g[i] = groups[warp][lane + 32 * i];
-      float top = g[0];
-#pragma unroll
-      for (int i = 1; i < kGroups / 32; ++i) top = fmaxf(top, g[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float size = 0.f;
-      if (!R.tokens.p || scored(base + warp))
-        for (int i = 0; i < shares; ++i) size += sizes[warp * shares + i];
-      const float off = logit_slack(top, size * static_cast<float>(R.logit_scale_log2), R.dim);
       const float at = reached_by<kGroups / 32>(g, R.k);
-      if (lane == 0) {
-        reached[warp] = at - off;
-        slack[warp] = off;
-      }
+      if (lane == 0) reached[warp] = at;
     }
     __syncthreads();
     if (own_row < R.rows) {
-      const float from = reached[lane & (width - 1)], off = slack[lane & (width - 1)];
+      const float from = reached[lane & (width - 1)];
       for (int b = first_block; b < R.n_blocks; b += 8 * stride) {
         float m[8];
 #pragma unroll
@@ -636,9 +648,9 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
           m[k] = b + k * stride < R.n_blocks ? R.stats[static_cast<int64_t>(b + k * stride) * R.stats_ld + own_row].x : minus_inf();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if (b + k * stride >= R.n_blocks || m[k] + off < from) continue;
+          if (b + k * stride >= R.n_blocks || m[k] + slack < from) continue;
           const int at = atomicAdd(&found[lane & (width - 1)], 1);
-          if (at < kTopBlocks) list[own_row * list_rows + at] = TopBlock{b + k * stride, m[k]};
+          if (at < kTopBlocks) list[own_row * list_rows + at] = TopBlock{b + k * stride, m[k], slack};
         }
       }
     }
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(WARPS * 32) lp_rows_kernel(const LpRows R, con
     LpRow o = {};
     if (R.k > 0) {
       o.reached = reached[lane];
-      o.slack = slack[lane];
+      o.unit = unit;  // warp 0's lanes below `width` have their own rows
       o.blocks = found[lane];
     }
     o.target = t;

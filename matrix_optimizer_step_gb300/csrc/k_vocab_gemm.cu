@@ -31,6 +31,12 @@
 // microsecond, so short tiles (vocab.cu says which) have fixed shares: drawn,
 // 24 x 128256 x 4096 took 671 us for 620.
 //
+// Where a row's largest logits are wanted, four more warps of each CTA read its half of W's rows in shared memory beside
+// the MMA, a row a lane, in the tiles of the first 256 tokens, and leave the largest norm of each 32: what
+// bounds the rounding of a logit (k_logprobs.cu).  The producer of W waits for them in those tiles.  At 1000 x
+// 128256 x 4096 a call with alternatives takes 620 us for 619 without the norms, and 750 with a kernel of its own that reads W
+// beside the product (795 behind it); with 64 tokens 233 for 226.
+//
 // Every wait is bounded; after a timeout the CTA records the error, stops
 // issuing, and both CTAs meet at the final cluster barrier before the pair
 // frees its TMEM.
@@ -43,6 +49,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "vocab.h"
+#include "vocab_rows.cuh"
 
 namespace dmuon {
 namespace {
@@ -53,14 +60,24 @@ constexpr int STAGES = 5;  // with 4: 16.4 ms for 15.6 at 8192 x 128256 x 4096, 
 constexpr int EPI = 8;  // epilogue warps: two per TMEM lane quarter, 128 columns each
 constexpr int kSchedWarp = 3 + EPI;
 constexpr int kThreads = (4 + EPI) * 32;
+constexpr int kNormWarp = 4 + EPI, kNormWarps = 4;  // the first of the warps that take norms
 constexpr uint32_t HALF_BYTES = 128 * BK * 2;
 constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
 constexpr uint32_t MN_BOX_BYTES = 64 * 64 * 2;
 constexpr uint32_t kStaging = 2 * 4096;  // two boxes of 32 rows x 128 bytes per epilogue warp
 constexpr int kMail = 2;  // tile numbers on their way to the roles
-constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1 + 2 * kMail;
+constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1 + 2 * kMail + 2 * STAGES;
 // Threads that read a tile number: both producers and the epilogue warps of two CTAs, and the MMA issuer.
 constexpr uint32_t kReaders = 2 * (2 + EPI) + 1;
+template <class Args>
+constexpr bool kCanNorm = std::is_base_of<VocabLogProbs, Args>::value;
+template <class Args>
+__host__ __device__ inline float* norms_of(const Args& G) {
+  if constexpr (kCanNorm<Args>)
+    return G.norms;
+  else
+    return nullptr;
+}
 constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + EPI * kStaging + kNumBars * 8 + 8 + 4 * kMail;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -480,7 +497,7 @@ __device__ __forceinline__ bool a_is_mn(const VocabGrad& G, int p) { return G.p[
 // Args: VocabLogits, VocabLogProbs or VocabLogTop (B is vocabulary x width,
 // K-contiguous), or VocabGrad (B is N-contiguous).
 template <class Args, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (kCanNorm<Args> ? 32 * kNormWarps : 0), 1)
     vocab_gemm_kernel(const __grid_constant__ Args G) {
   constexpr bool LOGITS = !B_MN;
   constexpr int kProducerBWarp = 2 + EPI;
@@ -501,6 +518,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t drain = bar0 + 8u * (2 * STAGES + 4);
   auto mail_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + i); };
   auto mail_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + kMail + i); };  // the leader's is used
+  // A stage whose rows of W the norms' warps may read, and have read: in the tiles that they take norms in.
+  auto readable = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + 2 * kMail + s); };
+  auto read = [&](int s) { return bar0 + 8u * (3 * STAGES + 5 + 2 * kMail + s); };
+  const bool norms = norms_of(G) != nullptr;
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -511,6 +532,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // one arrival per operand producer of the leader
       mbar_init(empty(s), 1);
+      mbar_init(readable(s), 1);
+      mbar_init(read(s), kNormWarps);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
@@ -519,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     for (int i = 0; i < kMail; ++i) {
       mbar_init(mail_full(i), 1);
-      mbar_init(mail_empty(i), kReaders);
+      mbar_init(mail_empty(i), kReaders + (norms ? 2 * kNormWarps : 0));
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -562,10 +585,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t leader_full0 = mapa_shared(full(0), 0);
     int stage = 0, filled = 0;
     uint32_t phase = 0;
+    uint32_t to_read = 0, read_phase = 0;  // by stages
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Tile T = next_tile(i, false);
       if (T.product < 0) break;
+      const bool has_norms = norms && is_b && T.m0 == 0;
       const CUtensorMap* map = operand_map(G, T.product, is_b);
       const bool mn = is_b ? B_MN : a_is_mn(G, T.product);
       const int row0 = (is_b ? T.n0 : T.m0) + 128 * static_cast<int>(rank);
@@ -573,6 +598,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded_cluster(empty(stage), phase ^ 1u, abort_flag, G.err, kErrTimeoutProducer)) {
           ok = false;
           break;
+        }
+        if constexpr (kCanNorm<Args>) {
+          const uint32_t bit = 1u << stage;
+          if (to_read & bit) {
+            if (!mbar_wait_bounded(read(stage), read_phase & bit ? 1u : 0u, abort_flag, G.err, kErrTimeoutProducer)) {
+              ok = false;
+              break;
+            }
+            read_phase ^= bit;
+          }
+          to_read = has_norms ? to_read | bit : to_read & ~bit;
         }
         const uint32_t leader_full = leader_full0 + 8u * stage;
         if (leader) mbar_expect_tx(full(stage), 2 * HALF_BYTES);
@@ -628,6 +664,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
+          // Both CTAs' copies have landed: tells the norms' warps so, once the MMAs of the stage before are done.
+          if (kCanNorm<Args> && norms && T.m0 == 0) umma_commit_pair_multicast(readable(stage), 0x3);
           const uint64_t ad = a0 + static_cast<uint32_t>(stage) * (STAGE_BYTES >> 4);
           const uint64_t bd = b0 + static_cast<uint32_t>(stage) * (STAGE_BYTES >> 4);
           umma_bf16_pair(d_tmem, ad, bd, idesc, kb != T.kb0 ? 1u : 0u);
@@ -712,6 +750,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
+  } else if (kCanNorm<Args> && warp >= kNormWarp) {
+    // --------------------------------------------------------------- norms
+    const int row = 32 * (warp - kNormWarp) + lane;  // of this CTA's half of the tile's rows of W
+    int stage = 0;
+    uint32_t phases = 0;  // by stages
+    bool ok = norms;
+    for (int i = 0; ok; ++i) {
+      const Tile T = next_tile(i, true);
+      if (T.product < 0) break;
+      if (T.m0 != 0) {
+        stage = (stage + T.kb1 - T.kb0) % STAGES;
+        continue;
+      }
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int kb = T.kb0; kb < T.kb1; ++kb) {
+        const uint32_t bit = 1u << stage;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded_cluster(readable(stage), phases & bit ? 1u : 0u, abort_flag, G.err, kErrTimeoutEpilogue));
+        if (!ok) break;
+        phases ^= bit;
+        add_row_squares(smem + stage * STAGE_BYTES + HALF_BYTES, row, s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(read(stage));
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+      }
+      const float most = warp_max((s[0] + s[1]) + (s[2] + s[3]));  // rows past the vocabulary are zeros
+      const int v0 = T.n0 + 128 * static_cast<int>(rank) + row - lane;
+      if constexpr (kCanNorm<Args>) {
+        // Whole blocks of statistics, the last one's rows past the vocabulary too.
+        if (ok && lane == 0 && v0 < (G.N + kCeBlock - 1) / kCeBlock * kCeBlock) G.norms[v0 / kNormRows] = largest_norm(most);
+      }
+    }
   }
 
   if (warp == kSchedWarp && !leader && blockIdx.x == 1) {
@@ -761,7 +830,8 @@ cudaError_t launch(const Args& G, int64_t tiles, int n_pairs, cudaStream_t st) {
   }
   if (tiles <= 0 || n_pairs <= 0) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < n_pairs ? tiles : n_pairs);
-  return launch_after(vocab_gemm_kernel<Args, B_MN>, dim3(2 * pairs), dim3(kThreads), kSmem, st, G);
+  const int threads = kThreads + (norms_of(G) ? 32 * kNormWarps : 0);
+  return launch_after(vocab_gemm_kernel<Args, B_MN>, dim3(2 * pairs), dim3(threads), kSmem, st, G);
 }
 
 }  // namespace

@@ -25,12 +25,13 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "vocab.h"
+#include "vocab_rows.cuh"
 
 namespace dmuon {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 7 * 32;
+constexpr int kThreads = 7 * 32, kNormThreads = kThreads + 4 * 32;
 constexpr uint32_t A_BYTES = BM * BK * 2;
 constexpr uint32_t MN_BOX_BYTES = 64 * 64 * 2;
 constexpr int kMaxStages = 12;
@@ -132,8 +133,11 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
 }
 
 // ENT: with what the entropy takes (VocabLogProbs).
-template <bool LOGITS, bool ENT>
-__global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_constant__ VocabThin G) {
+// NORMS: four more warps read each stage of W's rows in shared memory, a row a lane, and leave the largest
+// norm of each 32.  Memory still sets the pace: a stage's 16 KB arrive in 680 cycles, of which the MMA, the copy and these
+// warps take 128 of shared memory each.  A call with 24 tokens of 128256 x 4096 takes 225 us for 217 without.
+template <bool LOGITS, bool ENT, bool NORMS>
+__global__ void __launch_bounds__(NORMS ? kNormThreads : kThreads, 1) vocab_thin_kernel(const __grid_constant__ VocabThin G) {
   constexpr bool A_MN = !LOGITS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(empty(s), NORMS ? 5 : 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
@@ -281,6 +285,30 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, &no_abort, G.err, kErrTimeoutDrain);
     }
+  } else if (NORMS && warp >= 7) {
+    // ----------------------------------------------------------------- norms
+    const int quarter = warp - 7;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = 0; t < n_tiles && ok; ++t) {
+      const Tile T = tile_at(t);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int kb = T.kb0; kb < T.kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(stage), phase, abort_flag, G.err, kErrTimeoutEpilogue));
+        if (!ok) break;
+        add_row_squares(smem + stage * stage_bytes, 32 * quarter + lane, s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(stage));
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      const float most = warp_max((s[0] + s[1]) + (s[2] + s[3]));  // rows past the vocabulary are zeros
+      const int row0 = T.m0 + 32 * quarter;
+      if (ok && lane == 0 && row0 < G.M) G.norms[row0 / kNormRows] = largest_norm(most);
+    }
   } else {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;
@@ -327,18 +355,18 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_thin_kernel(const __grid_co
   if (warp == 1) tmem_dealloc(tmem_base, tmem_cols);
 }
 
-template <bool LOGITS, bool ENT>
+template <bool LOGITS, bool ENT, bool NORMS>
 cudaError_t launch_variant(const VocabThin& G, int n_ctas, cudaStream_t st) {
   static unsigned long long attr_mask = 0;
   if (attr_needed_on_current_device(&attr_mask)) {
-    cudaError_t e = cudaFuncSetAttribute(vocab_thin_kernel<LOGITS, ENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(vocab_thin_kernel<LOGITS, ENT, NORMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
     attr_note_current_device(&attr_mask);
   }
   const int64_t tiles = static_cast<int64_t>(G.tiles_m) * G.splits;
-  return launch_after(vocab_thin_kernel<LOGITS, ENT>, dim3(static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas)), dim3(kThreads),
-                      kSmem, st, G);
+  return launch_after(vocab_thin_kernel<LOGITS, ENT, NORMS>, dim3(static_cast<unsigned>(tiles < n_ctas ? tiles : n_ctas)),
+                      dim3(NORMS ? kNormThreads : kThreads), kSmem, st, G);
 }
 
 }  // namespace
@@ -347,8 +375,9 @@ cudaError_t launch_vocab_thin(bool logits, const VocabThin& G, int n_ctas, cudaS
   if (G.M <= 0 || G.tokens <= 0 || G.np < G.tokens || G.np > kThinRows || G.np % 16 != 0 || G.groups < 1 ||
       2 * G.np * G.groups > 512 || n_ctas <= 0)
     return cudaErrorInvalidValue;
-  if (!logits) return launch_variant<false, false>(G, n_ctas, st);
-  return G.weighted ? launch_variant<true, true>(G, n_ctas, st) : launch_variant<true, false>(G, n_ctas, st);
+  if (!logits) return launch_variant<false, false, false>(G, n_ctas, st);
+  if (G.norms) return launch_variant<true, true, true>(G, n_ctas, st);
+  return G.weighted ? launch_variant<true, true, false>(G, n_ctas, st) : launch_variant<true, false, false>(G, n_ctas, st);
 }
 
 }  // namespace dmuon

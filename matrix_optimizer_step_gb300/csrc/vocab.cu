@@ -404,6 +404,8 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   if (keep_logs) off_block = L.take(static_cast<size_t>(token_rows * ld_block) * (coarse ? 1 : 2));
   if (grads || P) off_rows = L.take(static_cast<size_t>(rows) * (P ? sizeof(LpRow) : sizeof(CeRow)));
   const size_t off_top = n_top > 0 ? L.take(static_cast<size_t>(rows) * kTopBlocks * sizeof(TopBlock)) : 0;
+  const int32_t norm_groups = static_cast<int32_t>(round_up((v + kNormRows - 1) / kNormRows, 4));
+  const size_t off_norms = n_top > 0 ? L.take(static_cast<size_t>(norm_groups) * sizeof(float)) : 0;
   if (grads) {
     off_alpha = L.take(4);
     bool dx_part = false, dw_part = false;
@@ -470,6 +472,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
   float* weighted = reinterpret_cast<float*>(ws + off_weighted);
   CeRow* row_info = reinterpret_cast<CeRow*>(ws + off_rows);
   LpRow* lp_info = reinterpret_cast<LpRow*>(ws + off_rows);
+  float* norms = n_top > 0 ? reinterpret_cast<float*>(ws + off_norms) : nullptr;
   float* alpha = reinterpret_cast<float*>(ws + off_alpha);
   uint16_t* masked = reinterpret_cast<uint16_t*>(ws + off_masked);
   uint32_t* counters = static_cast<uint32_t*>(ctx->vocab_ticket.p);  // two tile counters, one ticket
@@ -515,6 +518,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       G.stats_ld = stats_ld;
       G.targets = here;
       if (P) G.weighted = weighted;
+      G.norms = norms;
       if (first) G.norm = norm;
       DM_TRY(timed_launch(ctx, -1, s, [&] { return launch_vocab_thin(true, G, ctx->num_sms, s); }));
     } else {
@@ -534,6 +538,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       G.counter = counters;
       if (first) G.norm = norm;
       G.weighted = weighted;
+      G.norms = first ? norms : nullptr;
       G.drawn = G.grid.kb_total >= kDrawnBlocks;
       DM_TRY(timed_launch(ctx, -1, s, [&] {
         return coarse ? launch_vocab_logits(G, pairs, s)
@@ -572,6 +577,8 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       R.err = err;
       R.k = n_top;
       R.top_blocks = reinterpret_cast<TopBlock*>(ws + off_top);
+      R.norms = norms;
+      R.stats_shift = stats_shift;
       LpTop T = {};
       T.block = block;
       T.coarse = coarse;
@@ -583,6 +590,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       T.vocab = static_cast<int32_t>(v);
       T.rows_in = lp_info;
       T.top_blocks = R.top_blocks;
+      T.norms = norms;
       T.rows = nr;
       T.x = R.x;
       T.w = w;

@@ -239,10 +239,15 @@ struct VocabLogits {
 };
 cudaError_t launch_vocab_logits(const VocabLogits& G, int n_pairs, cudaStream_t st);
 
+// Rows of w of which the largest norm is left: the smaller blocks of statistics, and a quarter of the larger.
+constexpr int kNormRows = 32;
+static_assert(kNormRows == kCeThinBlock && 4 * kNormRows == kCeBlock, "blocks of statistics are one or four groups");
+
 // The same with what the entropy takes: a block's sum of 2^(z - maximum) (z - maximum), again
 // without the target's.  `targets.p` may be null.
 struct VocabLogProbs : VocabLogits {
   float* weighted;                    // [block][row], as stats
+  float* norms;                       // the largest norm in each kNormRows rows of w, or null: not wanted
 };
 cudaError_t launch_vocab_logits(const VocabLogProbs& G, int n_pairs, cudaStream_t st);
 
@@ -298,6 +303,7 @@ struct VocabThin {
   int64_t stats_ld;
   IdList targets;
   float* weighted;                    // as in VocabLogProbs, or null: not wanted
+  float* norms;                       // as in VocabLogProbs (with `weighted`), or null: not wanted
   CeNorm norm;
   // dX: fp32 partials [split][token][ld_part]
   float* part;
@@ -376,7 +382,7 @@ constexpr int kTopBlocks = 96;  // vocabulary blocks that may hold one of them, 
 
 struct TopBlock {
   int32_t block;
-  float max;
+  float max, slack;
 };
 
 // A row's distribution, as the passes after the sums read it.  Octaves unless said otherwise.
@@ -389,7 +395,8 @@ struct LpRow {
   int32_t scored;
   // Of the k largest logits none is below `reached`, and none is in another block than the listed ones
   // (`blocks` of them; above kTopBlocks the list is not whole).
-  float reached, slack;  // slack: what the products' rounding may do to one
+  float reached;
+  float unit;            // what the products' rounding may do to a logit, for each unit of its row of w's norm
   int32_t blocks;
 };
 
@@ -419,6 +426,8 @@ struct LpRows {
   int* err;
   int32_t k;               // alternatives wanted, or 0
   TopBlock* top_blocks;    // of row row0, kTopBlocks a row
+  const float* norms;      // VocabLogProbs's, up to a whole block of statistics (0 past the last row)
+  int32_t stats_shift;
 };
 
 struct LpTop {
@@ -430,6 +439,7 @@ struct LpTop {
   int32_t n_blocks, stats_shift, vocab;
   const LpRow* rows_in;
   const TopBlock* top_blocks;
+  const float* norms;
   int64_t rows;
   const uint16_t* x;       // of row row0
   const uint16_t* w;

@@ -40,11 +40,11 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, uint16_t* d, int col
 }
 
 // This warp's share (of `shares`) of the dot product of two bf16 rows: a lane's
-// part in fp32, their sum in 64 bits, the same in every lane.  `size`, if wanted: the
-// sum of the products' absolute values.
+// part in fp32, their sum in 64 bits, the same in every lane.  `squares`, if wanted: the sum of
+// the squares of a's share.
 __device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b, int n, int share, int shares, int lane,
-                                           float* size = nullptr) {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, abs_sum = 0.f;
+                                           float* squares = nullptr) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sq = 0.f;
   const int start = share * 32 + lane, step = shares * 32;
   int done = 0;
   if (((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0) {
@@ -57,24 +57,48 @@ __device__ __forceinline__ double warp_dot(const uint16_t* a, const uint16_t* b,
       for (int i = 0; i < 4; ++i) {
         acc[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), acc[i]);
         acc[i] = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc[i]);
-        if (size) {
-          abs_sum = fmaf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(v[i] << 16)), abs_sum);
-          abs_sum = fmaf(fabsf(__uint_as_float(u[i] & 0xFFFF0000u)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u)), abs_sum);
+        if (squares) {
+          sq = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(u[i] << 16), sq);
+          sq = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(u[i] & 0xFFFF0000u), sq);
         }
       }
     }
   }
   for (int c = done + start; c < n; c += step) {
     acc[0] = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), acc[0]);
-    if (size) abs_sum = fmaf(fabsf(bf16_bits_to_f32(a[c])), fabsf(bf16_bits_to_f32(b[c])), abs_sum);
+    if (squares) sq = fmaf(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(a[c]), sq);
   }
-  if (size) {
+  if (squares) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) abs_sum += __shfl_xor_sync(0xffffffffu, abs_sum, o);
-    *size = abs_sum;
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    *squares = sq;
   }
   return warp_sum(static_cast<double>((acc[0] + acc[1]) + (acc[2] + acc[3])));
 }
+
+// Adds the squares of this lane's row of a stage of W in shared memory (64 columns, 128-byte swizzle): its eight
+// 16-byte pieces in an order in which eight lanes read all banks.
+__device__ __forceinline__ void add_row_squares(const uint8_t* stage, int row, float (&s)[4]) {
+  const uint4* p = reinterpret_cast<const uint4*>(stage + row * 128);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 q = p[c ^ (row & 7)];
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
+      s[i] = fmaf(hi, hi, fmaf(lo, lo, s[i]));
+    }
+  }
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Norm of the row of w with the largest sum of squares.  Squares below fp32's range count for nothing, so none is taken below 1e-15.
+__device__ __forceinline__ float largest_norm(float squares) { return sqrtf(fmaxf(squares, 1e-30f)); }
 
 constexpr int kDlThreads = 256;
 constexpr int kDlCols = kDlThreads * 8 * 4;

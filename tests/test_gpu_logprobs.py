@@ -318,6 +318,47 @@ def test_logits_that_cancel(ops, n, tokens):
     check(out, reference(x, w, t if tokens else None, 1.0, 20))
 
 
+@pytest.mark.parametrize("tokens", [True, False])
+@pytest.mark.parametrize("big", [17.0, 64.0])
+@pytest.mark.parametrize("n", [4, 40, 600])
+def test_logits_that_cancel_beside_rows_of_zeros(ops, n, big, tokens):
+    # As above, but every second row of w alone has the two terms, and the given tokens' rows (without tokens: the first ones)
+    # are zeros: what a sum rounds away goes by its own row of w, and no other tells of it.
+    x, w, t, _, _ = inputs(n, 3000, 4096, seed=17)
+    x[:, 0] = x[:, 4095] = big
+    w[:, 0] = w[:, 4095] = 0
+    w[1::2, 0] = big
+    w[1::2, 4095] = -big
+    w[t[t >= 0] if tokens else torch.arange(n, device=DEV)] = 0
+    out = outputs(x, w, 20)
+    if not tokens:
+        del out["logprobs"]
+    ops.token_logprobs(x, w, t if tokens else None, **out)
+    ops.sync()
+    check(out, reference(x, w, t if tokens else None, 1.0, 20))
+
+
+@pytest.mark.parametrize("n", [6, 300])
+def test_infinities_in_the_head(ops, n):
+    # Entries shut out by an infinity in their row of w: no probability, and no bound on what else their blocks hold.
+    x, w, t, _, _ = inputs(n, 900, 64, seed=18)
+    x[:, 7] = x[:, 7].abs() + 1
+    out_of = torch.arange(3, 900, 90, device=DEV)
+    w[out_of, 7] = float("-inf")
+    t[torch.isin(t, out_of)] = -1
+    out = outputs(x, w, 32)
+    ops.token_logprobs(x, w, t, **out)
+    ops.sync()
+    keep = torch.ones(900, dtype=torch.bool, device=DEV)
+    keep[out_of] = False
+    place = keep.nonzero().squeeze(1)
+    u = torch.where(t >= 0, (torch.cumsum(keep, 0) - 1)[t.clamp(min=0)], t)
+    want = reference(x, w[keep], u, 1.0, 32)
+    ids, _ = want["top_ids"]
+    want["top_ids"] = (torch.where(ids >= 0, place[ids.clamp(min=0)], ids), None)
+    check(out, want)
+
+
 @pytest.mark.parametrize("spread", [30.0, 0.0])
 def test_far_and_equal_logits(ops, spread):
     # Logits hundreds apart: the alternatives lie under the logs' cut.
