@@ -532,6 +532,7 @@ DMUON_API int dmuon_cross_entropy(dmuon_context* ctx, const dmuon_ce* args, void
  * instruction's sums leave, for whose rounding 13 roundoffs (2^-24) of |x_i| |w_v| are
  * allowed for each 16 of its terms, |w_v| being the largest norm in a block of w's rows: more than
  * such a sum can be off by, whatever its terms, so no entry is left out.
+ * None of their log probabilities is above 0.
  *
  *   x, w        as in dmuon_cross_entropy
  *   tokens      n_tokens ids of token_dtype; below zero: the row is not scored (its

@@ -252,8 +252,14 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   }
   const uint8_t* logs = static_cast<const uint8_t*>(T.block) + row * T.ld_block * (T.coarse ? 1 : 2);
   const uint16_t* x = T.x + row * T.ld_x;
+  // An entry that holds more than half is the row's maximum: its share of the sum, which is 1, is taken out and the rest set
+  // against its own logit, so that what the product's sum rounded away of it takes no probability above 1.
   auto logprob = [&](double z, int32_t id) {
-    return id == R.target ? R.logprob : kLn2 * (static_cast<float>(z * T.logit_scale_log2 - R.top) - R.log_sum);
+    if (id == R.target) return R.logprob;
+    const float d = static_cast<float>(z * T.logit_scale_log2 - R.top), own = exp2f(d);
+    if (!(own > 0.5f * R.sum)) return kLn2 * (d - R.log_sum);
+    const float share = T.stats_shift == kCeThinShift ? exp2f(-fabsf(R.top) * kThinAbove) : 1.f;
+    return -log1pf(fmaxf(R.sum - share, 0.f) / own);
   };
   if (thread == 0) S.n_entries = S.n_ids = S.close = 0;
   __syncthreads();
@@ -681,6 +687,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows
       }
       const float whole = all.s + own;
       o.top = all.m;
+      o.sum = whole;
       o.log_sum = log2f(whole);
       lse = kLn2 * (all.m + o.log_sum);
       if (own > all.s) {

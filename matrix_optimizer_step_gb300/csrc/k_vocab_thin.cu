@@ -102,7 +102,7 @@ __device__ __forceinline__ void thin_logits(const VocabThin& G, uint32_t (&r)[16
   const float top = reduce16(t, lane, [](float a, float b) { return fmaxf(a, b); });
   // Above every z by more than the rounding of the products below.
   float m = top * c;  // c > 0
-  if (m != minus_inf) m += fabsf(m) * 2.4e-7f;
+  if (m != minus_inf) m += fabsf(m) * kThinAbove;
   const float ref = m == minus_inf ? 0.f : m;  // only -inf and NaN: as in k_vocab_gemm.cu
   const int token = token0 + (lane & 15);
   int target = -1;

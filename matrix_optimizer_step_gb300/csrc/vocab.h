@@ -100,6 +100,9 @@ static_assert(kCeBlock == 1 << kCeShift && kCeThinBlock == 1 << kCeThinShift, "b
 // maximum in units of 2^-10 octaves, cut off at 64 octaves.
 constexpr float kCeLogUnits = 1024.f;
 
+// k_vocab_thin.cu's maxima lie above the largest logit by this part of themselves.
+constexpr float kThinAbove = 2.4e-7f;
+
 // Stands for a distance of -inf where one is multiplied: 2^it is 0.
 constexpr float kNoLogit = -256.f;
 
@@ -388,6 +391,7 @@ struct TopBlock {
 // A row's distribution, as the passes after the sums read it.  Octaves unless said otherwise.
 struct LpRow {
   float top, log_sum;  // maximum, and log2 of the sum relative to it
+  float sum;           // that sum
   float logprob;       // of the given token, natural
   float a, b;          // d logit of entry v: -p_v (a + b log2 p_v); both 0: none for this row
   float target_dz;     // and of the given token

@@ -399,6 +399,33 @@ def test_certain_tokens_keep_their_digits(ops, n):
     assert bool(((out["entropy"].double() - entropy).abs() <= 2 * tol * entropy).all())
 
 
+@pytest.mark.parametrize("n", [3, 40, 600])
+def test_certain_alternatives_without_tokens(ops, n):
+    # No token given, logits of 4 to 30 over a sum of 4096 terms, which the matrix instruction's sums cut off towards zero: no
+    # probability above 1, falling, and next to 1 off by what the others' share is off by (2 ez of itself, as in `reference`),
+    # by the sum's additions and by the rounding of a logit, the product's and its scale's (4 F of it in octaves).
+    v, d = 3000, 4096
+    g = torch.Generator(device=DEV).manual_seed(19)
+    w = (torch.randn(v, d, generator=g, device=DEV) * 0.02).to(torch.bfloat16)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    raise_by = torch.linspace(4, 30, n, device=DEV)[:, None]
+    x = (torch.randn(n, d, generator=g, device=DEV) * 0.5 + raise_by * w[t].float() / w[t].float().square().sum(1, keepdim=True)).to(torch.bfloat16)
+    out = outputs(x, w, 4)
+    del out["logprobs"]
+    ops.token_logprobs(x, w, None, **out)
+    ops.sync()
+    check(out, reference(x, w, None, 1.0, 4))
+    got = out["top_logprobs"].double()
+    assert bool((got <= 0).all()) and bool((got[:, :-1] >= got[:, 1:]).all())
+    z = x.double() @ w.double().T
+    top, at = z.max(dim=1)
+    rest = torch.exp(z - top[:, None]).scatter(1, at[:, None], 0.0).sum(1)
+    ez = (d / 16 + 8) * 4 * F * float((x.double().abs() @ w.double().abs().T).max())
+    tol = 2 * ez * rest + 64 * F + 4 * F * top * 1.4427
+    sure = rest < 0.9
+    assert bool(sure.any()) and bool((((got[:, 0] + torch.log1p(rest)).abs() <= tol) | ~sure).all())
+
+
 def test_ids_past_the_vocabulary(cuda_lib):
     one = cuda_lib.VocabOps(0)
     x, w, t, dlp, _ = inputs(50, 300, 64, seed=11)
