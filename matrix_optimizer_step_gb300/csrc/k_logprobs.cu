@@ -697,6 +697,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows
         o.logprob = t >= 0 ? kLn2 * (dz - o.log_sum) : 0.f;
         entropy = kLn2 * (o.log_sum - fmaf(own, fmaxf(dz, kNoLogit), all.t) / whole);
       }
+      // The rounding of M may leave the entropy of a nearly certain row that much below 0.  NaN stays.
+      if (entropy < 0.f) entropy = 0.f;
       const float g = R.dlogprobs ? R.dlogprobs[i] : 0.f, h = R.dentropy ? R.dentropy[i] : 0.f;
       o.a = fmaf(h, entropy, g);
       o.b = kLn2 * h;

@@ -416,7 +416,7 @@ def test_certain_alternatives_without_tokens(ops, n):
     ops.sync()
     check(out, reference(x, w, None, 1.0, 4))
     got = out["top_logprobs"].double()
-    assert bool((got <= 0).all()) and bool((got[:, :-1] >= got[:, 1:]).all())
+    assert bool((got <= 0).all()) and bool((got[:, :-1] >= got[:, 1:]).all()) and bool((out["entropy"] >= 0).all())
     z = x.double() @ w.double().T
     top, at = z.max(dim=1)
     rest = torch.exp(z - top[:, None]).scatter(1, at[:, None], 0.0).sum(1)
