@@ -146,12 +146,13 @@ int32_t chunk_bytes(const dmuon_grad* gs, int n, int64_t wanted, int64_t least) 
 // An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 128 KB do (their ends are what a
 // small call waits for: three tensors of a small model 8.2 us in chunks of 4 KB, 7.1 of 16), then eight.  Scaling: at least four
 // rounds, so that its last one is a small part (clipping 1e8 elements 152 us with one or two, 147 with four).
-constexpr int64_t kRound = 152 * 8;
-int32_t norm_chunk(const dmuon_grad* gs, int n) {
-  const int32_t one = chunk_bytes(gs, n, std::max<int64_t>(kRound - n, kRound / 8), 16384);
-  return one < kLongChunk ? one : chunk_bytes(gs, n, kRound * 8, 16384);
+int64_t round_of(const dmuon_context* ctx) { return int64_t(ctx->num_sms) * 8; }
+int32_t norm_chunk(const dmuon_context* ctx, const dmuon_grad* gs, int n) {
+  const int64_t round = round_of(ctx);
+  const int32_t one = chunk_bytes(gs, n, std::max<int64_t>(round - n, round / 8), 16384);
+  return one < kLongChunk ? one : chunk_bytes(gs, n, round * 8, 16384);
 }
-int32_t scale_chunk(const dmuon_grad* gs, int n) { return chunk_bytes(gs, n, kRound * 4, 4096); }
+int32_t scale_chunk(const dmuon_context* ctx, const dmuon_grad* gs, int n) { return chunk_bytes(gs, n, round_of(ctx) * 4, 4096); }
 
 int64_t chunks_of(const dmuon_grad& g, int32_t chunk) {
   const int64_t length = chunk / elem_size(g.grad_dtype);
@@ -200,14 +201,14 @@ int scale_launches(dmuon_context* ctx, const dmuon_grad* gs, int n, int32_t chun
 }
 
 int scale_impl(dmuon_context* ctx, const dmuon_grad* gs, int n, const float* coef, cudaStream_t s) {
-  const int32_t chunk = scale_chunk(gs, n);
+  const int32_t chunk = scale_chunk(ctx, gs, n);
   return n <= kGradFew ? scale_launches<kGradFew>(ctx, gs, n, chunk, coef, s) : scale_launches<kGradBatch>(ctx, gs, n, chunk, coef, s);
 }
 
 // Norms into the given results; with `scale` the outs too.
 int norm_impl(dmuon_context* ctx, const dmuon_grad* gs, int n, float max_norm, float* norm, float* norms, float* coef, bool scale,
               cudaStream_t s) {
-  const int32_t chunk = norm_chunk(gs, n);
+  const int32_t chunk = norm_chunk(ctx, gs, n);
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) chunks += chunks_of(gs[i], chunk);
   const size_t at_squares = static_cast<size_t>(chunks) * sizeof(double), at_coef = at_squares + static_cast<size_t>(n) * sizeof(double);

@@ -385,7 +385,7 @@ int adamw_step_impl(dmuon_context* ctx, const dmuon_vector* ts, int n, float lr,
     // length changes no element): a clipped step of 52 tensors, 3.9e7 elements, 219 us with 65536, 190 with 8192.
     int64_t total = 0;
     for (int i = 0; i < n; ++i) total += ts[i].numel;
-    const int64_t chunk = std::max<int64_t>(2048, std::min<int64_t>(kChunkElems, round_up(total / (152 * 32) + 1, 2048)));
+    const int64_t chunk = std::max<int64_t>(2048, std::min<int64_t>(kChunkElems, round_up(total / (ctx->num_sms * 32) + 1, 2048)));
     for (int i = 0; i < n; ++i)
       for (int64_t e = 0; e < ts[i].numel; e += chunk) {
         Chunk ch;
