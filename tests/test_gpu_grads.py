@@ -95,6 +95,22 @@ def test_norms_of_large_and_small_values(ops, value, dtype):
     assert abs(float(both[1]) - 3.0) <= NORM_TOL * 3
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [1.9921875, 1.1015625, 1.3359375])
+@pytest.mark.parametrize("n", [70_000_000, 700_000_000])
+def test_norms_keep_the_bound_of_the_longest_chunks(ops, n, value, dtype):
+    # A chunk is 128 KB at most: 256 squares of a bf16 chunk a thread, in four chains of 64, then two joins in the thread, five in the
+    # warp and three in the block, 74 steps of 2^-24 each: a sum within 5e-6 of itself, a norm within 2.5e-6 and its rounding.
+    # Equal values, whose sums are rounded the same way again and again.  The lengths have chunks of just under 128 KB and of all of it.
+    if dtype == F32:
+        value, n = value + 2.0 ** -12 + 2.0 ** -19, n // 2
+    g = torch.full((n,), value, device=DEV, dtype=dtype)
+    norm = ops.norm([g])
+    ops.sync()
+    want = float(g[0].double()) * math.sqrt(n)
+    assert 74 * F <= 5e-6 and abs(float(norm) - want) <= (2.5e-6 + F) * want
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 def test_norms_that_are_not_finite(ops, bad):
     grads = make([5000, 300], seed=3)
