@@ -19,10 +19,12 @@ __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000)
 // with a term of 2^p and small ones beside it, before it or behind it: a small one of 1 counts whole to p = 25 and not at
 // all from 26 on, and a sum past 2^23 loses its halves towards zero).  No product and no running sum is larger than |x| |w|
 // (Cauchy and Schwarz), so a step is off by at most (17 2^-25 + 2^-23) |x| |w|, 10.5 roundoffs of it, whatever the signs of its
-// terms; 13 are taken, which covers the rounding of the norms.  Joined parts, the scale and the fixed-point logs: 32 more and 2^-9 octaves.
-__device__ __forceinline__ float slack_unit(float x_squares, double logit_scale_log2, int dim) {
+// terms; 13 are taken, which covers the rounding of the norms.  Where the width is cut into sums of their own, each is off by as many of
+// its parts' norms, whose products add up to |x| |w| at most: `steps` are those of one.  Joined sums, the scale and the fixed-point
+// logs: 32 more and 2^-9 octaves.
+__device__ __forceinline__ float slack_unit(float x_squares, double logit_scale_log2, int steps) {
   const float norm = sqrtf(fmaxf(x_squares, 1e-30f));
-  return norm * static_cast<float>(logit_scale_log2) * (static_cast<float>(13 * ((dim + 15) / 16) + 32) * 0x1p-24f);
+  return norm * static_cast<float>(logit_scale_log2) * (static_cast<float>(13 * steps + 32) * 0x1p-24f);
 }
 // Largest norm of the rows of w of statistics block b.
 __device__ __forceinline__ float block_norm(const float* norms, int stats_shift, int b) {
@@ -256,10 +258,10 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   // against its own logit, so that what the product's sum rounded away of it takes no probability above 1.
   auto logprob = [&](double z, int32_t id) {
     if (id == R.target) return R.logprob;
-    const float d = static_cast<float>(z * T.logit_scale_log2 - R.top), own = exp2f(d);
-    if (!(own > 0.5f * R.sum)) return kLn2 * (d - R.log_sum);
+    const float d = static_cast<float>(z * T.logit_scale_log2 - R.top);
+    if (!(d > R.log_sum - 1.f)) return kLn2 * (d - R.log_sum);
     const float share = T.stats_shift == kCeThinShift ? exp2f(-fabsf(R.top) * kThinAbove) : 1.f;
-    return -log1pf(fmaxf(R.sum - share, 0.f) / own);
+    return -log1pf(fmaxf(exp2f(R.log_sum) - share, 0.f) / exp2f(d));
   };
   if (thread == 0) S.n_entries = S.n_ids = S.close = 0;
   __syncthreads();
@@ -585,8 +587,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows
   load(first_block);  // under way while the given token's logit is summed
   float norm = 0.f;  // largest of this thread's blocks
   if (R.k > 0) {
+    // Shared among the lanes that have the same blocks, of other rows.
 #pragma unroll 8
-    for (int b = first_block; b < R.n_blocks; b += stride) norm = fmaxf(norm, block_norm(R.norms, R.stats_shift, b));
+    for (int b = first_block + (lane & (width - 1)) * stride; b < R.n_blocks; b += width * stride)
+      norm = fmaxf(norm, block_norm(R.norms, R.stats_shift, b));
+    for (int o = 1; o < width; o <<= 1) norm = fmaxf(norm, __shfl_xor_sync(0xffffffffu, norm, o));
   }
   if (dot_row < R.rows && (dot_target >= 0 || R.k > 0)) {
     const uint16_t* x = R.x + dot_row * R.ld_x;
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows
   if (R.k > 0) {
     __syncthreads();  // squares
     for (int i = 0; i < shares; ++i) unit += squares[(lane & (width - 1)) * shares + i];
-    unit = slack_unit(unit, R.logit_scale_log2, R.dim);
+    unit = slack_unit(unit, R.logit_scale_log2, R.steps);
     slack = logit_slack(unit, norm);
     // Eight, four or one group of this thread: as many of a row as the block has threads.
 #pragma unroll
@@ -687,7 +692,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kRowWarps ? 2 : 4) lp_rows
       }
       const float whole = all.s + own;
       o.top = all.m;
-      o.sum = whole;
       o.log_sum = log2f(whole);
       lse = kLn2 * (all.m + o.log_sum);
       if (own > all.s) {

@@ -498,6 +498,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
     const bool first = r0 == 0, last = r0 + rows >= n;
     const int64_t k_rows = halves ? 2 * nr : nr;  // rows of d logits
     IdList here = ids;
+    int32_t steps = static_cast<int32_t>((d + 15) / 16);
     if (ids.p) here.p = static_cast<const char*>(ids.p) + r0 * (ids.is64 ? 8 : 4);
     if (thin_logits) {
       VocabThin G = {};
@@ -508,6 +509,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       G.splits = 1;
       G.kb_total = G.kb_step = static_cast<int32_t>((d + 63) / 64);
       G.groups = std::max(1, std::min({4, G.kb_total / 16, 256 / G.np}));
+      steps = 4 * ((G.kb_total + G.groups - 1) / G.groups);
       G.err = err;
       DM_TRY(encode_2d(enc, &G.map_a, w, d, v, ld_w, 64, 128));
       DM_TRY(encode_2d(enc, &G.map_b, x, d, nr, ld_x, 64, static_cast<uint32_t>(G.np)));
@@ -579,6 +581,7 @@ int head_impl(dmuon_context* ctx, const dmuon_ce& C, const dmuon_logprobs* P, cu
       R.top_blocks = reinterpret_cast<TopBlock*>(ws + off_top);
       R.norms = norms;
       R.stats_shift = stats_shift;
+      R.steps = steps;
       LpTop T = {};
       T.block = block;
       T.coarse = coarse;

@@ -391,7 +391,6 @@ struct TopBlock {
 // A row's distribution, as the passes after the sums read it.  Octaves unless said otherwise.
 struct LpRow {
   float top, log_sum;  // maximum, and log2 of the sum relative to it
-  float sum;           // that sum
   float logprob;       // of the given token, natural
   float a, b;          // d logit of entry v: -p_v (a + b log2 p_v); both 0: none for this row
   float target_dz;     // and of the given token
@@ -432,6 +431,7 @@ struct LpRows {
   TopBlock* top_blocks;    // of row row0, kTopBlocks a row
   const float* norms;      // VocabLogProbs's, up to a whole block of statistics (0 past the last row)
   int32_t stats_shift;
+  int32_t steps;           // 16-term steps of one of a logit's sums
 };
 
 struct LpTop {
