@@ -145,7 +145,8 @@ int32_t chunk_bytes(const dmuon_grad* gs, int n, int64_t wanted, int64_t least) 
 
 // An SM holds eight blocks.  Sums: one round of blocks as long as chunks of 128 KB do (their ends are what a
 // small call waits for: three tensors of a small model 8.2 us in chunks of 4 KB, 7.1 of 16), then eight.  Scaling: at least four
-// rounds, so that its last one is a small part (clipping 1e8 elements 152 us with one or two, 147 with four).
+// rounds, so that its last one is a small part (clipping 1e8 bf16 elements 109 us with two, 107.4 with four, 3e7 of fp32 into bf16 56.3
+// and 55.3; 120 small tensors, 1.9e7 elements, 33.0 and 34.0).
 int64_t round_of(const dmuon_context* ctx) { return int64_t(ctx->num_sms) * 8; }
 int32_t norm_chunk(const dmuon_context* ctx, const dmuon_grad* gs, int n) {
   const int64_t round = round_of(ctx);

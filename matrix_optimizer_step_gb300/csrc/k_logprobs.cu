@@ -89,8 +89,8 @@ __device__ __forceinline__ float reached_by(const float (&v)[PER], int k) {
 // 16 warps and no launch of its own (4 warps in one: 207 us for 184 with 1 row at 128256 x 4096, 50 for 43
 // with 128 at 50257 x 768); from there on 4.  Calls with 20 alternatives: 600 x 128256 x 1024 148 us (2 warps:
 // 159, 8: 145, 16: 152), 4096 x 50257 x 768 256 (2: 252, 8: 271, 16: 311), 8192 x 32000 x 2048 765 (2: 773,
-// 8: 827, 16: 872).  At 4096 x 50257 x 768 the pass itself takes 58 us from cold caches, with half of the
-// issue slots and a sixth of the memory's rate in use.
+// 8: 827, 16: 872), all before the norms of w's rows were taken.  At 4096 x 50257 x 768 the pass itself takes 60 us from cold caches,
+// with half of the issue slots and a sixth of the memory's rate in use.
 //
 // More candidates than there is room for (equal or nearly equal logits) are taken
 // kWindow entries at a time; a row of zeros, all of whose logits are equal, is known without.

@@ -33,9 +33,9 @@
 //
 // Where a row's largest logits are wanted, four more warps of each CTA read its half of W's rows in shared memory beside
 // the MMA, a row a lane, in the tiles of the first 256 tokens, and leave the largest norm of each 32: what
-// bounds the rounding of a logit (k_logprobs.cu).  The producer of W waits for them in those tiles.  At 1000 x
-// 128256 x 4096 a call with alternatives takes 620 us for 619 without the norms, and 750 with a kernel of its own that reads W
-// beside the product (795 behind it); with 64 tokens 233 for 226.
+// bounds the rounding of a logit (k_logprobs.cu).  The producer of W waits for them in those tiles.  A call with
+// alternatives takes 630 us for 616 without the norms at 1000 x 128256 x 4096, and 750 with a kernel of its own that reads W
+// beside the product (795 behind it); with 64 tokens 232 for 223.
 //
 // Every wait is bounded; after a timeout the CTA records the error, stops
 // issuing, and both CTAs meet at the final cluster barrier before the pair

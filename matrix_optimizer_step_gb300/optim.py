@@ -148,7 +148,10 @@ class OwnerStep:
 
         With ``max_norm`` the gradients of the routes that step count as
         multiplied by min(1, max_norm / (their norm + 1e-6)); they are not
-        written.  ``norm`` (one fp32 on the device) then receives the norm."""
+        written.  ``norm`` (one fp32 on the device) then receives the norm.
+        That is the norm of what is registered here and steps: a rank that
+        owns a part of a model would clip to that part's
+        (``DistributedOwnerStep.local_step`` says what to do there)."""
         use_adamw = adamw is not None and self._vecs is not None
         if muon is None and not use_adamw:
             raise RuntimeError("step: no route to step")

@@ -358,7 +358,13 @@ class DistributedOwnerStep:
     def local_step(self, muon, adamw, stream=None):
         """The owner's step of its tensors and its sharded piece (no
         communication).  ``muon`` / ``adamw``: keyword dicts of
-        OwnerStep.muon_step / adamw_step."""
+        OwnerStep.muon_step / adamw_step.
+
+        No norm is taken over the ranks here.  To clip to the whole model's,
+        sum the squares of the norms of what each rank steps (``GradOps.norm``)
+        over the ranks after ``reduce_grads``, and give
+        min(1, max_norm / (root + 1e-6)), one fp32 on the device, as
+        ``grad_scale`` in both dicts."""
         if not self._registered:
             self._register()
         if self._mine_muon:
