@@ -255,13 +255,19 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   const uint8_t* logs = static_cast<const uint8_t*>(T.block) + row * T.ld_block * (T.coarse ? 1 : 2);
   const uint16_t* x = T.x + row * T.ld_x;
   // An entry that holds more than half is the row's maximum: its share of the sum, which is 1, is taken out and the rest set
-  // against its own logit, so that what the product's sum rounded away of it takes no probability above 1.
-  auto logprob = [&](double z, int32_t id) {
+  // against its own logit, so that what the product's sum rounded away of it takes no probability above 1.  Not below a half
+  // then: the value falls with the logit from one formula to the other.  Beside the given token's logprob, whose
+  // logit is summed apart, the others keep their places.  z_t: its z here, -inf where it is not among them.
+  auto logprob = [&](double z, int32_t id, double z_t) {
     if (id == R.target) return R.logprob;
     const float d = static_cast<float>(z * T.logit_scale_log2 - R.top);
-    if (!(d > R.log_sum - 1.f)) return kLn2 * (d - R.log_sum);
-    const float share = T.stats_shift == kCeThinShift ? exp2f(-fabsf(R.top) * kThinAbove) : 1.f;
-    return -log1pf(fmaxf(exp2f(R.log_sum) - share, 0.f) / exp2f(d));
+    float v = kLn2 * (d - R.log_sum);
+    if (d > R.log_sum - 1.f) {
+      const float share = T.stats_shift == kCeThinShift ? exp2f(-fabsf(R.top) * kThinAbove) : 1.f;
+      v = fmaxf(-log1pf(fmaxf(exp2f(R.log_sum) - share, 0.f) / exp2f(d)), -kLn2);
+    }
+    if (R.target < 0) return v;
+    return z > z_t || (z == z_t && id < R.target) ? fmaxf(v, R.logprob) : fminf(v, R.logprob);
   };
   if (thread == 0) S.n_entries = S.n_ids = S.close = 0;
   __syncthreads();
@@ -433,7 +439,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
         // alternatives that is 3.4 % faster to 3.4 % slower, without a rule in the sizes, and on average slower
         // (1 row of 128256 x 4096 184.2 us for 183.3; 300 of 50257 x 768 with one 47.6 for 52.9).
         pdl_launch();
-        put(rank, id, logprob(z, id));
+        put(rank, id, logprob(z, id, S.close ? S.z[0] : static_cast<double>(S.near[0])));  // the given token comes first
       });
       return;
     }
@@ -441,7 +447,7 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
   bool any = false;
   for (int c = lane; c < T.dim; c += 32) any = any || (x[c] & 0x7fffu) != 0;
   if (!__any_sync(0xffffffffu, any)) {
-    if (thread < k) put(thread, thread, logprob(0.0, thread));
+    if (thread < k) put(thread, thread, logprob(0.0, thread, 0.0));
     return;
   }
   // A few blocks at a time, each joined with the best before it.
@@ -470,7 +476,10 @@ __device__ __forceinline__ void top_of_row(const LpTop& T, int64_t row, const Lp
     best = min(k, n + best);
   }
   __syncthreads();
-  if (thread < best) put(thread, S.best_id[thread], logprob(S.best_z[thread], S.best_id[thread]));
+  double z_t = static_cast<double>(minus_inf());
+  for (int i = 0; i < best; ++i)
+    if (S.best_id[i] == R.target) z_t = S.best_z[i];
+  if (thread < best) put(thread, S.best_id[thread], logprob(S.best_z[thread], S.best_id[thread], z_t));
 }
 
 // Eight blocks an SM (72 registers, seven blocks: 8192 x 32000 x 2048 779 us for 750).

@@ -426,6 +426,42 @@ def test_certain_alternatives_without_tokens(ops, n):
     assert bool(sure.any()) and bool((((got[:, 0] + torch.log1p(rest)).abs() <= tol) | ~sure).all())
 
 
+@pytest.mark.parametrize("tokens", [True, False])
+@pytest.mark.parametrize("n", [20, 300, 900])
+def test_log_probabilities_of_alternatives_fall(ops, n, tokens):
+    # A few entries share a row, 0.02 and less apart, and the first two hold terms of 4096 that cancel, for which the matrix
+    # instruction's sum loses 0.06: more than lies between them.  With tokens, entries 2 and 3 are next to 0 and 1, closer than the
+    # fp32 sum of the given token's logit tells apart.  The values stay in the order of the ids, at 0 or below, and the given
+    # token's is its log probability.
+    v, d, k, few = 8, 4096, 6, 4 if tokens else 3
+    g = torch.Generator(device=DEV).manual_seed(20)
+    x = torch.randn(n, d, generator=g, device=DEV)
+    w = (torch.randn(1, d, generator=g, device=DEV) * 0.01).expand(v, d).clone()
+    x[:, 0] = x[:, d - 1] = 64.0
+    w[:, 0] = w[:, d - 1] = 0
+    w[:2, 0] = 64.0
+    w[:2, d - 1] = -64.0
+    x[:, 10] = 8.0
+    w[:few, 10] = 4.0
+    w[:, 1:4] = 0
+    for i in range(few):
+        w[i, 1 + (i % 2 if tokens else i)] = 0.02 + (2.0 ** -12 if i >= 2 else 0.0)
+    x, w = x.to(torch.bfloat16), w.to(torch.bfloat16)
+    t = torch.randint(0, few, (n,), generator=g, device=DEV)
+    out = outputs(x, w, k)
+    if not tokens:
+        del out["logprobs"]
+    for s in (0.5, 1.0, 2.0):
+        ops.token_logprobs(x, w, t if tokens else None, logit_scale=s, **out)
+        ops.sync()
+        check(out, reference(x, w, t if tokens else None, s, k))
+        lp = out["top_logprobs"]
+        assert bool((lp <= 0).all()) and bool((lp[:, :-1] >= lp[:, 1:]).all())
+        if tokens:
+            row, at = (out["top_ids"] == t[:, None]).nonzero(as_tuple=True)
+            assert len(row) == n and torch.equal(lp[row, at], out["logprobs"][row])
+
+
 def test_ids_past_the_vocabulary(cuda_lib):
     one = cuda_lib.VocabOps(0)
     x, w, t, dlp, _ = inputs(50, 300, 64, seed=11)
